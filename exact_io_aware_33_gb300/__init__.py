@@ -12,9 +12,12 @@ The functions carry the C entry points' names:
     fa_bwd_workspace_bytes(B, H, N, d)
     fa_fwd_ex(q, k, v, causal=False, window=0, scale=None) -> (o, lse)
     fa_decode_splitkv(q, k, v, causal=False, window=0, scale=None, n_splits=0) -> (o, lse)
+    fa_paged_append(cache, batch, k, v, q=None, rope=None) -> rotated q
+    fa_paged_attn(cache, batch, q, window=0, scale=None, n_splits=0) -> (o, lse)
     fa_strerror(code), fa_get_last_device_status(), fa_version()
 
-fa_fwd_ex and fa_decode_splitkv take Nq queries [B, H, Nq, d] over Nk keys
+The paged forms work on a PagedCache (a pool of e4m3 pages) and a PagedBatch
+(the sequences of a step); the paged module documents them. fa_fwd_ex and fa_decode_splitkv take Nq queries [B, H, Nq, d] over Nk keys
 [B, H, Nk, d] (causal queries are the last Nq positions) and an optional
 sliding window.
 
@@ -41,6 +44,7 @@ FA_ERR_UNSUPPORTED = -2
 FA_ERR_LAUNCH = -3
 FA_ERR_TIMEOUT = -4
 FA_ERR_WORKSPACE = -5
+FA_ERR_INDEX = -6
 
 # Every symbol include/fa.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
@@ -48,6 +52,7 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
 _U64 = ctypes.c_ulonglong
+_L = ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F]),
     "fa_fwd_stream": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
@@ -66,6 +71,10 @@ SIGNATURES = {
     "fa_fwd_dropout": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _U64, _U64, _P]),
     "fa_bwd_dropout": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _U64, _U64,
                             _P, _S, _P]),
+    "fa_paged_append": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _P]),
+    "fa_paged_attn": (_I, [_P, _P, _P, _L, _P, _P, _I, _I, _F, _I, _P, _S, _P]),
+    "fa_paged_attn_num_splits": (_I, [_P, _P, _I, _I]),
+    "fa_paged_attn_workspace_bytes": (_S, [_P, _P, _I, _I]),
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_get_last_device_status": (_I, []),
     "fa_version": (_I, []),
@@ -393,3 +402,7 @@ def fa_bwd_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, offset: int
                                 ctypes.c_size_t(workspace.numel()), _stream_handle(stream, q.device))
     _check(rc, "fa_bwd_dropout")
     return dq, dk, dv
+
+
+from .paged import (PagedBatch, PagedCache, fa_paged_append, fa_paged_attn,  # noqa: E402,F401
+                    fa_paged_attn_num_splits, fa_paged_attn_workspace_bytes)

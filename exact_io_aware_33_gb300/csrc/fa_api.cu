@@ -21,7 +21,7 @@ __device__ int g_status_word;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kSmemSlots = 20;
+constexpr int kSmemSlots = 32;
 
 struct DeviceState {
   bool probed = false;
@@ -116,6 +116,22 @@ bool make_map_bhnd(CUtensorMap* map, const void* ptr, int BH, int N, int d, int 
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d),
+                                 static_cast<cuuint64_t>(rows) * static_cast<cuuint64_t>(d)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int current_device_status() {
   DeviceState* st = nullptr;
   return current_device(&st);
@@ -163,6 +179,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_LAUNCH: return "a CUDA call failed (launch, attribute or tensor map)";
     case FA_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
+    case FA_ERR_INDEX: return "a page, length, row range or position read on the device was out of range";
     default: return "unknown error code";
   }
 }
@@ -427,6 +444,129 @@ int fa_decode_splitkv(const void* q, const void* k, const void* v, void* o, floa
                                 static_cast<cudaStream_t>(cuda_stream));
 }
 
+namespace {
+
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks of the cache and the batch that both paged entry points share; fills
+// the internal forms. *empty: no sequence or no row, nothing is read.
+int check_paged(const fa_paged_cache* c, const fa_paged_batch* b, fa::PagedPool* pool,
+                fa::PagedBatchDev* dev, bool* empty) {
+  *empty = false;
+  if (c == nullptr || b == nullptr) return FA_ERR_INVALID;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  const int ps = c->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128) return FA_ERR_UNSUPPORTED;
+  if (c->num_pages < 0 || c->num_heads <= 0 || b->B < 0 || b->T < 0 || b->max_q < 1 || b->max_pages < 0 ||
+      b->max_kv < 0)
+    return FA_ERR_INVALID;
+  if (b->B == 0 || b->T == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  if (b->cu_q == nullptr && (b->T != b->B || b->max_q != 1)) return FA_ERR_INVALID;
+  if (c->num_pages == 0 || b->max_pages == 0) return FA_ERR_INVALID;
+  // tensor-map coordinates and positions are 32-bit
+  if (static_cast<long long>(c->num_pages) * c->num_heads > 0x7fffffffLL) return FA_ERR_INVALID;
+  if (static_cast<long long>(b->max_pages) * ps > 0x7fffffffLL - 256) return FA_ERR_INVALID;
+  if (!fa::aligned16(c->k_pages) || !fa::aligned16(c->v_pages) || !aligned4(c->k_scales) ||
+      !aligned4(c->v_scales) || !aligned4(b->block_table) || !aligned4(b->kv_lens) ||
+      (b->cu_q != nullptr && !aligned4(b->cu_q)))
+    return FA_ERR_INVALID;
+  *pool = fa::PagedPool{c->k_pages, c->v_pages, c->k_scales, c->v_scales,
+                        c->num_pages, c->num_heads, ps, c->d};
+  int shift = 4;
+  while ((1 << shift) < ps) ++shift;
+  *dev = fa::PagedBatchDev{b->block_table, b->kv_lens, b->cu_q, b->B, b->T, b->max_q, b->max_pages,
+                           ps, shift, c->num_pages};
+  return FA_OK;
+}
+
+// Rows of `heads` x d elements, `stride` elements apart, read in 16-byte words.
+bool row_stride_ok(long long stride, int heads, int d) {
+  return stride >= static_cast<long long>(heads) * d && stride % 8 == 0 && stride <= (1LL << 40);
+}
+
+int paged_max_kv(const fa_paged_cache* c, const fa_paged_batch* b) {
+  const long long most = static_cast<long long>(b->max_pages) * c->page_size;
+  return static_cast<int>(b->max_kv > 0 && b->max_kv < most ? b->max_kv : most);
+}
+
+}  // namespace
+
+int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* k,
+                    long long k_stride, const void* v, long long v_stride, const void* q,
+                    long long q_stride, void* q_out, long long q_out_stride, int Hq, const float* cos,
+                    const float* sin, int max_pos, int rot, int interleaved, void* cuda_stream) {
+  fa::PagedPool pool;
+  fa::PagedBatchDev dev;
+  bool empty = false;
+  int rc = check_paged(cache, batch, &pool, &dev, &empty);
+  if (rc != FA_OK) return rc;
+  const int d = cache->d;
+  if (Hq < 0 || rot < 0 || rot > d || max_pos < 0) return FA_ERR_INVALID;
+  if (rot % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (empty) return FA_OK;
+  if (!fa::aligned16(k) || !fa::aligned16(v) || !row_stride_ok(k_stride, pool.num_heads, d) ||
+      !row_stride_ok(v_stride, pool.num_heads, d))
+    return FA_ERR_INVALID;
+  if (Hq > 0 && (!fa::aligned16(q) || !fa::aligned16(q_out) || !row_stride_ok(q_stride, Hq, d) ||
+                 !row_stride_ok(q_out_stride, Hq, d)))
+    return FA_ERR_INVALID;
+  if (rot > 0 && (!fa::aligned16(cos) || !fa::aligned16(sin) || max_pos == 0)) return FA_ERR_INVALID;
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  const fa::PagedAppend p{k, v, q, q_out, k_stride, v_stride, q_stride, q_out_stride, Hq,
+                          cos, sin, max_pos, rot, interleaved ? 1 : 0};
+  return fa::launch_paged_append(pool, dev, p, static_cast<cudaStream_t>(cuda_stream));
+}
+
+int fa_paged_attn_num_splits(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq, int n_splits) {
+  fa::PagedPool pool;
+  fa::PagedBatchDev dev;
+  bool empty = false;
+  if (check_paged(cache, batch, &pool, &dev, &empty) != FA_OK || empty || Hq <= 0 || Hq % cache->num_heads != 0)
+    return 0;
+  return fa::paged_attn_split(pool, dev, Hq, paged_max_kv(cache, batch), n_splits, sm_count()).splits;
+}
+
+size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq,
+                                     int n_splits) {
+  fa::PagedPool pool;
+  fa::PagedBatchDev dev;
+  bool empty = false;
+  if (check_paged(cache, batch, &pool, &dev, &empty) != FA_OK || empty || Hq <= 0 || Hq % cache->num_heads != 0)
+    return 0;
+  return fa::paged_attn_split(pool, dev, Hq, paged_max_kv(cache, batch), n_splits, sm_count()).workspace_bytes;
+}
+
+int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
+                  long long q_stride, void* o, float* lse, int Hq, int window, float scale, int n_splits,
+                  void* workspace, size_t ws_bytes, void* cuda_stream) {
+  fa::PagedPool pool;
+  fa::PagedBatchDev dev;
+  bool empty = false;
+  int rc = check_paged(cache, batch, &pool, &dev, &empty);
+  if (rc != FA_OK) return rc;
+  if (Hq <= 0 || Hq % cache->num_heads != 0 || window < 0) return FA_ERR_INVALID;
+  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID;
+  if (empty) return FA_OK;
+  if (!fa::aligned16(q) || !fa::aligned16(o) || !aligned4(lse) || !row_stride_ok(q_stride, Hq, cache->d))
+    return FA_ERR_INVALID;
+  const int max_kv = paged_max_kv(cache, batch);
+  const fa::PagedSplit split = fa::paged_attn_split(pool, dev, Hq, max_kv, n_splits, sm_count());
+  if (split.workspace_bytes > 0 &&
+      (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+       ws_bytes < split.workspace_bytes))
+    return FA_ERR_WORKSPACE;
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  const fa::PagedAttn p{q, q_stride, o, lse, Hq, window, max_kv, scale};
+  return fa::launch_paged_attn(pool, dev, p, split, workspace, static_cast<cudaStream_t>(cuda_stream));
+}
+
 int fa_get_last_device_status(void) {
   fa::DeviceState* st = nullptr;
   if (fa::current_device(&st) != FA_OK) return FA_ERR_LAUNCH;
@@ -437,7 +577,7 @@ int fa_get_last_device_status(void) {
   const int zero = 0;
   if (cudaMemcpyToSymbol(fa::g_status_word, &zero, sizeof(int)) != cudaSuccess)
     return FA_ERR_LAUNCH;
-  return word == fa::kStatusTimeout ? FA_ERR_TIMEOUT : FA_OK;
+  return word == fa::kStatusTimeout ? FA_ERR_TIMEOUT : word == fa::kStatusIndex ? FA_ERR_INDEX : FA_OK;
 }
 
 }  // extern "C"

@@ -49,6 +49,11 @@ struct FwdProblem {
 // box_rows rows x 64 columns and 128-byte swizzle. Returns false on failure.
 bool make_map_bhnd(CUtensorMap* map, const void* ptr, int BH, int N, int d, int box_rows = 128);
 
+// Encodes a 3-D tiled TMA map over 8-bit pages [blocks, rows, d] (one block per
+// page and head) with boxes of box_rows rows x d bytes and a swizzle of d bytes
+// (64 or 128). Returns false on failure.
+bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows);
+
 // Size and scale checks shared by the entry points taking (B, H, N, d):
 // FA_OK or an error code; *empty is set when there is nothing to compute.
 int check_problem(int B, int H, int N, int d, float scale, bool* empty);
@@ -100,6 +105,65 @@ int launch_bwd_pre(const Problem& p, const void* o, const float* lse, const void
 int launch_bwd_main(const Problem& p, const void* dO, void* dk, void* dv, void* workspace,
                     cudaStream_t stream);
 int launch_bwd_post(const Problem& p, void* dq, const void* workspace, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged cache
+// The pool of an e4m3 cache: pages [num_pages, num_heads, page_size, d],
+// scales [num_pages, num_heads].
+struct PagedPool {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  int num_pages, num_heads, page_size, d;
+};
+
+// A packed batch on the device, with the host's bounds.
+struct PagedBatchDev {
+  const int* block_table;  // [B, max_pages]
+  const int* kv_lens;      // [B], new tokens included
+  const int* cu_q;         // [B + 1], or nullptr: one token per sequence
+  int B, T, max_q, max_pages;
+  int page_size, page_shift, num_pages;
+};
+
+struct PagedAppend {
+  const void* k;
+  const void* v;
+  const void* q;   // nullptr with Hq = 0
+  void* q_out;
+  long long k_stride, v_stride, q_stride, q_out_stride;  // elements between tokens
+  int Hq;
+  const float* cos;
+  const float* sin;
+  int max_pos, rot, interleaved;
+};
+
+struct PagedAttn {
+  const void* q;
+  long long q_stride;  // elements between tokens
+  void* o;             // [T, Hq, d]
+  float* lse;          // [T, Hq]
+  int Hq;
+  int window;
+  int max_kv;          // no sequence is expected to be longer (one that is takes longer)
+  float scale;
+};
+
+int launch_paged_append(const PagedPool& pool, const PagedBatchDev& batch, const PagedAppend& p,
+                        cudaStream_t stream);
+
+// How a launch cuts the key range: `splits` parts of `split_tiles` tiles of
+// 64 tokens, and the workspace that the parts' states take.
+struct PagedSplit {
+  int row_tiles;    // row tiles of a sequence and key head
+  int splits;
+  int split_tiles;
+  size_t workspace_bytes;
+};
+PagedSplit paged_attn_split(const PagedPool& pool, const PagedBatchDev& batch, int Hq, int max_kv,
+                            int n_splits, int sms);
+int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p,
+                      const PagedSplit& split, void* workspace, cudaStream_t stream);
 
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 

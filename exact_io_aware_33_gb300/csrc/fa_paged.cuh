@@ -1,0 +1,76 @@
+// What the kernels of the paged 8-bit key/value cache share: the packed
+// batch, its bounds checks, and e4m3 conversions.
+//
+// Pool layout: k_pages and v_pages are e4m3 [num_pages, heads, page_size, d],
+// so the tokens of one head in one page are one contiguous block (2 to 16
+// KiB) that a tiled copy fetches whole; k_scales and v_scales are fp32
+// [num_pages, heads]. A cached value is code * scale.
+//
+// Everything the device reads as an index (block_table, kv_lens, cu_q) is
+// checked against the sizes the host gave before it is used; what fails the
+// check is treated as absent and kStatusIndex is raised, so a bad table never
+// becomes a bad address.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fa_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+// One sequence of the batch: its packed rows [row0, row0 + n) and its length.
+struct PagedSeq {
+  int row0, n, len;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev& b, int seq, int* status) {
+  PagedSeq s;
+  bool bad = false;
+  if (b.cu_q != nullptr) {
+    const int c0 = b.cu_q[seq], c1 = b.cu_q[seq + 1];
+    bad = c0 < 0 || c1 < c0 || c1 > b.T || c1 - c0 > b.max_q;
+    s.row0 = min(max(c0, 0), b.T);
+    s.n = min(min(max(c1, s.row0), b.T) - s.row0, b.max_q);
+  } else {
+    s.row0 = seq;
+    s.n = 1;
+  }
+  s.len = b.kv_lens[seq];
+  // max_pages * page_size fits an int: checked on the host
+  const int most = b.max_pages << b.page_shift;
+  bad = bad || s.len < 0 || s.len > most;
+  s.len = min(max(s.len, 0), most);
+  if (bad) *status = kStatusIndex;
+  return s;
+}
+
+// The page that holds the tokens [idx * page_size, ...) of a sequence, or -1.
+__device__ __forceinline__ int paged_page(const PagedBatchDev& b, int seq, int idx, int* status) {
+  const int p = b.block_table[static_cast<long long>(seq) * b.max_pages + idx];
+  if (p >= 0 && p < b.num_pages) return p;
+  *status = kStatusIndex;
+  return -1;
+}
+
+// Two e4m3 codes (low byte first) to an f16 pair; exact, and a NaN code gives NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+
+// Two floats to two e4m3 codes, to nearest even, magnitudes above 448 to 448; `lo` in the low byte.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+}  // namespace fa

@@ -18,6 +18,7 @@ namespace fa {
 enum : int {
   kStatusOk = 0,
   kStatusTimeout = 1,       // a bounded wait ran out
+  kStatusIndex = 2,         // a page, length or position read on the device was out of range
 };
 
 // Wall-clock budget of a single wait, in nanoseconds (about one second; a

@@ -1,0 +1,277 @@
+"""The paged 8-bit key/value cache: appending rotated keys and values, and attention over it.
+
+Binding of ``fa_paged_append`` and ``fa_paged_attn`` (``include/fa.h`` states the operators). A serving
+step is two calls on one ``PagedCache`` and one ``PagedBatch``:
+
+    cache = fa.PagedCache.empty(num_pages, num_heads, page_size, d)
+    batch = fa.PagedBatch(block_table, kv_lens, cu_q, max_q=..., max_kv=...)   # or cu_q=None: decode
+    q = fa.fa_paged_append(cache, batch, k, v, q=q, rope=(cos, sin))
+    o, lse = fa.fa_paged_attn(cache, batch, q)
+
+Both objects only hold tensors of the caller and their checked sizes, so a decode loop makes them once
+and updates ``kv_lens`` and ``block_table`` in place between steps; the calls can be captured into a
+CUDA graph and replayed that way. All tensors of a call must be on one device, which need not be the
+current one. With ``stream`` the work is queued there and outputs and workspaces belong to that stream;
+tensors of other streams must be ready, and kept, by the caller.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+_PAGE_SIZES = (16, 32, 64, 128)
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("T", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("max_kv", ctypes.c_int)]
+
+
+def _require(t, name, dtype, dim, device=None):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+
+
+class PagedCache:
+    """A pool of e4m3 pages [num_pages, num_heads, page_size, d] with fp32 scales [num_pages, num_heads]."""
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales):
+        import torch
+        _require(k_pages, "k_pages", torch.float8_e4m3fn, 4)
+        dev = k_pages.device
+        _require(v_pages, "v_pages", torch.float8_e4m3fn, 4, dev)
+        P, H, page, d = k_pages.shape
+        if page not in _PAGE_SIZES:
+            raise ValueError(f"page size {page} is not one of {_PAGE_SIZES}")
+        if d not in (64, 128):
+            raise ValueError(f"head size {d} is not 64 or 128")
+        if v_pages.shape != k_pages.shape:
+            raise ValueError(f"v_pages has shape {tuple(v_pages.shape)}, expected {tuple(k_pages.shape)}")
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _require(t, name, torch.float32, 2, dev)
+            if tuple(t.shape) != (P, H):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(P, H)}")
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales),
+                        ("v_scales", v_scales)):
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.num_pages, self.num_heads, self.page_size, self.d = P, H, page, d
+        self.device = dev
+        self._index = dev.index
+        self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                    v_scales.data_ptr(), P, H, page, d)
+        self._address = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_heads: int, page_size: int, d: int, device="cuda"):
+        """A new pool. Its contents do not matter: only what was appended is ever read."""
+        import torch
+        shape = (num_pages, num_heads, page_size, d)
+        pages = [torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+        scales = [torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*pages, *scales)
+
+
+class PagedBatch:
+    """The sequences of a step: their pages, lengths (new tokens included) and packed rows.
+
+    ``cu_q`` None: one new token per sequence. ``max_q`` bounds the new tokens of a sequence, ``max_kv``
+    their lengths (0: what the block table can hold); both are host numbers, no tensor is read back."""
+
+    def __init__(self, block_table, kv_lens, cu_q=None, max_q: int = 1, max_kv: int = 0):
+        import torch
+        _require(block_table, "block_table", torch.int32, 2)
+        dev = block_table.device
+        _require(kv_lens, "kv_lens", torch.int32, 1, dev)
+        B, max_pages = block_table.shape
+        if kv_lens.shape[0] != B:
+            raise ValueError(f"kv_lens has {kv_lens.shape[0]} entries, block_table {B} rows")
+        if cu_q is not None:
+            _require(cu_q, "cu_q", torch.int32, 1, dev)
+            if cu_q.shape[0] != B + 1:
+                raise ValueError(f"cu_q has {cu_q.shape[0]} entries, expected {B + 1}")
+        elif max_q != 1:
+            raise ValueError("max_q must be 1 without cu_q")
+        if max_q < 1 or max_kv < 0:
+            raise ValueError("max_q must be at least 1 and max_kv at least 0")
+        for name, t in (("block_table", block_table), ("kv_lens", kv_lens), ("cu_q", cu_q)):
+            if t is not None and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        self.block_table, self.kv_lens, self.cu_q = block_table, kv_lens, cu_q
+        self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
+        self.device = dev
+        self._made = (-1, None, 0)
+
+    def _for_rows(self, T: int):
+        """(T, C struct, its address) for tensors of T rows."""
+        made = self._made
+        if made[0] != T:
+            if self.cu_q is None and T != self.B:
+                raise ValueError(f"{T} rows for {self.B} sequences of one token each")
+            s = _BatchStruct(self.block_table.data_ptr(), self.kv_lens.data_ptr(),
+                             0 if self.cu_q is None else self.cu_q.data_ptr(), self.B, T, self.max_q,
+                             self.max_pages, self.max_kv)
+            made = (T, s, ctypes.addressof(s))
+            self._made = made  # one assignment: another thread sees the old tuple or this one
+        return made
+
+
+def _rows(t, name, heads, d, device, torch):
+    """Checks a packed [T, heads, d] tensor whose tokens may lie apart; returns its token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [T, {heads or 'heads'}, {d}]")
+    st = t.stride()
+    if st[2] != 1 or (st[1] != d and shape[1] != 1):
+        raise ValueError(f"the heads and channels of {name} must lie side by side")
+    if shape[0] <= 1:
+        return shape[1] * d  # one row: whatever its stride says
+    return st[0]
+
+
+def _context(index, stream, torch):
+    """Where the call allocates and launches: the tensors' device, and `stream` where one is given."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != index:
+        return torch.cuda.device(index)
+    return None
+
+
+def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=None, interleaved: bool = False,
+                    q_out=None, stream=None):
+    """Writes k and v [T, num_heads, d] to the batch's pages, keys rotated; returns the rotated queries.
+
+    ``rope`` is (cos, sin), fp32 [max_pos, rot / 2] each, or None. Without ``q`` the result is None. Rows
+    of a new ``q_out`` behind the last sequence, or without a position, are not written."""
+    import torch
+    from . import _check, load_library
+    dev, d = cache.device, cache.d
+    if batch.device != dev:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
+    ks = _rows(k, "k", cache.num_heads, d, dev, torch)
+    vs = _rows(v, "v", cache.num_heads, d, dev, torch)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"v has {v.shape[0]} rows, k {T}")
+    cos = sin = None
+    max_pos = rot = 0
+    if rope is not None:
+        cos, sin = rope
+        _require(cos, "cos", torch.float32, 2, dev)
+        _require(sin, "sin", torch.float32, 2, dev)
+        if cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous and of one shape")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    made = batch._for_rows(T)
+    Hq = qs = os_ = 0
+    context = _context(cache._index, stream, torch)
+    with context or contextlib.nullcontext():
+        if q is not None:
+            qs = _rows(q, "q", 0, d, dev, torch)
+            Hq = q.shape[1]
+            if q.shape[0] != T:
+                raise ValueError(f"q has {q.shape[0]} rows, k {T}")
+            if q_out is None:
+                q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+                os_ = Hq * d
+            else:
+                os_ = _rows(q_out, "q_out", Hq, d, dev, torch)
+                if q_out.shape[0] != T:
+                    raise ValueError(f"q_out has {q_out.shape[0]} rows, q {T}")
+        rc = load_library().fa_paged_append(
+            cache._address, made[2], k.data_ptr(), ks, v.data_ptr(), vs, q.data_ptr() if Hq else 0, qs,
+            q_out.data_ptr() if Hq else 0, os_, Hq, cos.data_ptr() if rot else 0, sin.data_ptr() if rot else 0,
+            max_pos, rot, 1 if interleaved else 0, torch._C._cuda_getCurrentRawStream(cache._index))
+    if rc:
+        _check(rc, "fa_paged_append")
+    return q_out if q is not None else None
+
+
+def fa_paged_attn_num_splits(cache: PagedCache, batch: PagedBatch, Hq: int, T: int | None = None,
+                             n_splits: int = 0) -> int:
+    from . import load_library
+    made = batch._for_rows(batch.B if T is None else T)
+    return load_library().fa_paged_attn_num_splits(cache._address, made[2], Hq, n_splits)
+
+
+def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int, n_splits: int = 0) -> int:
+    """Workspace bytes of fa_paged_attn with these arguments; they do not depend on the number of rows."""
+    from . import load_library
+    made = batch._for_rows(batch.B)
+    return load_library().fa_paged_attn_workspace_bytes(cache._address, made[2], Hq, n_splits)
+
+
+def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scale: float | None = None,
+                  n_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [T, Hq, d] over the batch's cached tokens; (o bf16 [T, Hq, d], lse fp32 [T, Hq]).
+
+    Rows of a new ``out`` behind the last sequence are not written. Without ``workspace`` one is allocated
+    where the call needs it."""
+    import torch
+    from . import _check, load_library
+    dev, d = cache.device, cache.d
+    if batch.device != dev:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
+    qs = _rows(q, "q", 0, d, dev, torch)
+    T, Hq, _ = q.shape
+    made = batch._for_rows(T)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load_library()
+    context = _context(cache._index, stream, torch)
+    with context or contextlib.nullcontext():
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        elif out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous [{T}, {Hq}, {d}]")
+        else:
+            _rows(out, "out", Hq, d, dev, torch)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        else:
+            _require(lse, "lse", torch.float32, 2, dev)
+            if tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+                raise ValueError(f"lse must be contiguous [{T}, {Hq}]")
+        if workspace is None:
+            need = lib.fa_paged_attn_workspace_bytes(cache._address, made[2], Hq, n_splits)
+            ws = 0
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                ws = workspace.data_ptr()
+        else:
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous on {dev}")
+            need = workspace.numel() * workspace.element_size()
+            ws = workspace.data_ptr() if need else 0
+        rc = lib.fa_paged_attn(cache._address, made[2], q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq,
+                               window, scale, n_splits, ws, need,
+                               torch._C._cuda_getCurrentRawStream(cache._index))
+    if rc:
+        _check(rc, "fa_paged_attn")
+    return out, lse

@@ -62,6 +62,7 @@ extern "C" {
 #define FA_ERR_LAUNCH -3       /* a CUDA call failed (launch, attribute, map) */
 #define FA_ERR_TIMEOUT -4      /* a bounded wait in a kernel ran out          */
 #define FA_ERR_WORKSPACE -5    /* workspace missing or too small              */
+#define FA_ERR_INDEX -6        /* a page, length, row range or position read on the device was out of range */
 
 /*
  * Forward pass.
@@ -264,12 +265,137 @@ int fa_bwd_dropout(const void* q, const void* k, const void* v, const void* o, c
                    unsigned long long offset, void* workspace, size_t ws_bytes,
                    void* cuda_stream);
 
+/*
+ * The paged 8-bit key/value cache: a pool of pages that sequences of
+ * different lengths share, written by fa_paged_append and read by
+ * fa_paged_attn. The pages the library's method comes from name KV caching
+ * as the cost of decode-time history ("Flash Attention: IO-Aware Exact
+ * Attention", section "What changes in FlashAttention-2"); the paging, the
+ * 8-bit form and the rotation have no counterpart there.
+ *   k_pages, v_pages   : e4m3 [num_pages, num_heads, page_size, d]
+ *   k_scales, v_scales : fp32 [num_pages, num_heads]; a cached value is
+ *                        code * scale. Scales are positive; the append writes
+ *                        powers of two, the attention takes any.
+ *   num_heads          : key/value heads
+ *   page_size          : tokens per page: 16, 32, 64 or 128
+ *   d                  : 64 or 128 (FA_ERR_UNSUPPORTED otherwise, also for
+ *                        the page size)
+ * The struct is read during the call and not kept. Pages need no
+ * initialisation: no slot behind a sequence's length is ever used, whatever
+ * it holds.
+ */
+typedef struct fa_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  int num_pages;
+  int num_heads;
+  int page_size;
+  int d;
+} fa_paged_cache;
+
+/*
+ * The batch of a step: B sequences whose new tokens are packed row after row
+ * into tensors of T rows.
+ *   block_table : int32 [B, max_pages] on the device: the page that holds the
+ *                 tokens [i * page_size, (i + 1) * page_size) of sequence b.
+ *                 Only entries below ceil(kv_lens[b] / page_size) are read.
+ *   kv_lens     : int32 [B] on the device: each sequence's length with its
+ *                 new tokens
+ *   cu_q        : int32 [B + 1] on the device: sequence b's rows are
+ *                 cu_q[b] .. cu_q[b + 1] - 1, none allowed. NULL: one token
+ *                 per sequence (T = B, max_q = 1). Rows from cu_q[B] on are
+ *                 neither read nor written.
+ *   max_q       : at least every sequence's number of rows (1 or more)
+ *   max_kv      : an upper bound of kv_lens that the work is divided by; 0
+ *                 stands for max_pages * page_size. A longer sequence is
+ *                 computed all the same, only less evenly.
+ * Row i of sequence b sits at position kv_lens[b] - n_b + i. Rows with a
+ * negative position (n_b > kv_lens[b], as in a padded batch) are no tokens:
+ * the append skips them, the attention gives them O = 0 and LSE = -inf.
+ * The device checks what it reads: a page outside the pool, a length outside
+ * [0, max_pages * page_size], a row range outside [0, T] or longer than max_q
+ * and a position outside the angle tables raise FA_ERR_INDEX in the device
+ * status word; such a page is treated as absent, the others are clamped.
+ */
+typedef struct fa_paged_batch {
+  const int* block_table;
+  const int* kv_lens;
+  const int* cu_q;
+  int B;
+  int T;
+  int max_q;
+  int max_pages;
+  int max_kv;
+} fa_paged_batch;
+
+/*
+ * Appends the batch's new keys and values, with the rotation of positions
+ * applied to the keys, and rotates the queries with them.
+ *   k, v    : in,  bf16 [T, num_heads, d], rows k_stride / v_stride elements
+ *             apart (at least num_heads * d, a multiple of 8): a slice of a
+ *             fused projection is fine
+ *   q       : in,  bf16 [T, Hq, d], rows q_stride elements apart; NULL with
+ *             Hq = 0. Hq need not be related to num_heads here.
+ *   q_out   : out, bf16 [T, Hq, d], rows q_out_stride apart: the rotated
+ *             queries; may be q itself (with the same stride)
+ *   cos, sin: in,  fp32 [max_pos, rot / 2]: the angles of each position;
+ *             NULL with rot = 0 (no rotation)
+ *   rot     : channels that turn, a multiple of 16 up to d; pairs are
+ *             (c, c + rot / 2), or (2c, 2c + 1) when interleaved != 0:
+ *             (a, b) -> (a cos - b sin, b cos + a sin), in fp32. The other
+ *             channels stay.
+ * Scales: per page and head, the smallest power of two s (2^-126 or more; 1
+ * for zeros) with max |x| / s <= 448 over the page's new tokens, and no
+ * smaller than the page's scale where the page already held tokens of the
+ * sequence; when it is larger, the older codes are rounded again to it. Codes
+ * round to nearest even. Values that are not finite take no part in the
+ * scale: +-inf is stored as +-448 s, NaN as NaN.
+ * A page that is written must not be any other sequence's in the batch, nor
+ * its own twice (pages that are only read may be shared); two calls that
+ * write the same page must be ordered.
+ */
+int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* k,
+                    long long k_stride, const void* v, long long v_stride, const void* q,
+                    long long q_stride, void* q_out, long long q_out_stride, int Hq, const float* cos,
+                    const float* sin, int max_pos, int rot, int interleaved, void* cuda_stream);
+
+/*
+ * Attention of the batch's queries over the cached keys and values of their
+ * own sequences: causal (a query at position p sees the keys j <= p; its own
+ * key must have been appended), optionally with a window (keys
+ * p - window < j <= p; 0 = none), grouped heads (query head h reads key head
+ * h / (Hq / num_heads); Hq must be a multiple of num_heads).
+ *   q        : in,  bf16 [T, Hq, d], rows q_stride elements apart (a multiple of 8)
+ *   o        : out, bf16 [T, Hq, d] contiguous
+ *   lse      : out, fp32 [T, Hq], natural-log log-sum-exp
+ *   n_splits : parts of the key range, joined by a second kernel with the
+ *              rule of fa_decode_splitkv; <= 0 chooses from the sizes and the
+ *              device's SM count
+ *   workspace: at least fa_paged_attn_workspace_bytes(cache, batch, Hq,
+ *              n_splits) bytes (0: may be NULL), 256-byte aligned; nothing
+ *              in it outlives the call. Two calls in flight at once need two.
+ * A row that sees no key gives O = 0 and LSE = -inf. What lies in masked
+ * places (slots behind a length, keys outside the window) has no influence,
+ * NaN codes included. The library is free to sum in any order: results of
+ * different n_splits agree up to rounding; the same call gives the same bits.
+ */
+int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
+                  long long q_stride, void* o, float* lse, int Hq, int window, float scale, int n_splits,
+                  void* workspace, size_t ws_bytes, void* cuda_stream);
+int fa_paged_attn_num_splits(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq, int n_splits);
+size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq,
+                                     int n_splits);
+
 /* Static description of a return code. Never NULL. */
 const char* fa_strerror(int code);
 
 /*
  * Device status word of the current device: FA_OK, or FA_ERR_TIMEOUT when a
- * kernel launched since the last read gave up on a bounded wait. Reading
+ * kernel launched since the last read gave up on a bounded wait, or
+ * FA_ERR_INDEX when one of the paged cache's kernels read an index that was
+ * out of range (the last of several is kept). Reading
  * synchronises the device and clears the word. Returns FA_ERR_LAUNCH if the
  * word cannot be read.
  */

@@ -27,10 +27,14 @@ merge
 dropout
     Dropout on the probabilities with a keep mask drawn from Philox4x32-10,
     and the forward and backward for a given mask.
+paged
+    The paged 8-bit key/value cache: e4m3, appending with the rotation of
+    positions and power-of-two scales, attention over the pages.
 
 Pins (what fixes each function other than itself) live in
 ``tests/test_oracle_pins.py``, ``tests/test_oracle_general.py``,
-``tests/test_oracle_dropout.py`` and ``tests/test_oracle_philox.py``; each
+``tests/test_oracle_dropout.py``, ``tests/test_oracle_philox.py`` and
+``tests/test_oracle_paged.py``; each
 module's docstring names its pins.
 No function here is "parity unpinned".
 
@@ -40,6 +44,6 @@ Sources cited (title of the page, then its section):
   * "FlashAttention" (Road to Intelligence, Chapter 11)
 """
 
-from . import dense, tiled, finite_diff, general, merge, dropout  # noqa: F401
+from . import dense, tiled, finite_diff, general, merge, dropout, paged  # noqa: F401
 
-__all__ = ["dense", "tiled", "finite_diff", "general", "merge", "dropout"]
+__all__ = ["dense", "tiled", "finite_diff", "general", "merge", "dropout", "paged"]

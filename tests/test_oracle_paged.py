@@ -1,0 +1,193 @@
+"""The plain paged cache against facts about e4m3 and against dense attention, and the binding's host checks."""
+
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_33_gb300 as fa
+from oracle import dense, paged
+
+
+def test_every_code_has_the_value_that_torch_gives_it():
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes.copy()).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(paged.E4M3, want, equal_nan=True)
+
+
+def test_encode_rounds_to_nearest_even():
+    rng = np.random.default_rng(1)
+    x = np.concatenate([rng.standard_normal(4000) * s for s in (1e-3, 1e-2, 1.0, 60.0)]).astype(np.float32)
+    x = np.clip(x, -448, 448)
+    pos = paged.E4M3[:127]
+    mids = ((pos[:-1] + pos[1:]) / 2).astype(np.float32)   # every tie
+    x = np.concatenate([x, mids, -mids, pos.astype(np.float32)])
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(paged.encode(x), want)
+    assert np.array_equal(paged.encode(paged.E4M3[:127]), np.arange(127))
+    assert list(paged.encode([np.inf, -np.inf, 1e9, np.nan])) == [126, 254, 126, 127]
+
+
+@pytest.mark.parametrize("amax,want", [(448.0, 1.0), (448.5, 2.0), (224.0, 0.5), (1.0, 2.0 ** -8), (1.75, 2.0 ** -8),
+                                       (1.7500001, 2.0 ** -7), (2.0 ** -133, 2.0 ** -126), (0.0, 1.0)])
+def test_scales_are_the_smallest_power_of_two(amax, want):
+    assert paged.scale_of(amax) == want
+
+
+def test_rotation_keeps_pairs_lengths_and_relative_angles():
+    rng = np.random.default_rng(2)
+    for interleaved in (False, True):
+        x, y = rng.standard_normal((2, 64))
+        ang = lambda p: p * 10000.0 ** (-np.arange(16) / 16)  # noqa: E731
+        at = lambda v, p: paged.rotate(v, np.cos(ang(p)), np.sin(ang(p)), interleaved, np.float64)  # noqa: E731
+        assert math.isclose(np.linalg.norm(at(x, 77)), np.linalg.norm(x), rel_tol=1e-12)
+        assert np.array_equal(at(x, 77)[32:], x[32:])
+        assert math.isclose(at(x, 10) @ at(y, 3), at(x, 107) @ at(y, 100), rel_tol=1e-9)
+
+
+def test_a_growing_scale_rounds_the_older_codes_again():
+    c = paged.Cache(np.zeros((1, 1, 16, 64)), np.zeros((1, 1, 16, 64)), np.ones((1, 1)), np.ones((1, 1)))
+    table = [[0]]
+    x = np.full((1, 1, 64), 1.0)
+    c.append(table, [1], [0, 1], x, x)
+    assert c.scales["k"][0, 0] == 2.0 ** -8
+    c.append(table, [2], [0, 1], 100 * x, 100 * x)
+    assert c.scales["k"][0, 0] == 0.25
+    assert np.all(c.read("k", [0], 2)[0, :, 0] == [1.0, 96.0 if paged.E4M3[paged.encode(400.0)] == 384 else 104.0])
+    c.append(table, [3], [0, 1], x, x)   # smaller values do not shrink the scale
+    assert c.scales["k"][0, 0] == 0.25
+
+
+def test_attend_is_dense_attention_over_what_is_read():
+    rng = np.random.default_rng(3)
+    P, H, page, d, n = 4, 2, 16, 64, 40
+    codes = [paged.encode(rng.standard_normal((P, H, page, d)) * 50) for _ in range(2)]
+    scales = [2.0 ** rng.integers(-8, -4, (P, H)) for _ in range(2)]
+    c = paged.Cache(codes[0], codes[1], scales[0], scales[1])
+    table = [[2, 0, 3]]
+    q = rng.standard_normal((n, H, d)).astype(np.float32)  # the dense oracle reads its inputs as float32
+    o, lse = c.attend(table, [n], [0, n], q, 0.125)
+    k, v = c.read("k", table[0], n), c.read("v", table[0], n)
+    as_t = lambda x: torch.from_numpy(np.ascontiguousarray(x))[None]  # noqa: E731
+    want, want_lse = dense.forward(as_t(q.transpose(1, 0, 2)), as_t(k), as_t(v), True, 0.125)
+    assert np.allclose(o, want[0].transpose(1, 0, 2), atol=1e-12)
+    assert np.allclose(lse, want_lse[0].T, atol=1e-12)
+
+
+# ------------------------------------------------------------------ host checks, no device touched
+@pytest.fixture(scope="module")
+def lib():
+    from exact_io_aware_33_gb300 import build
+    build.build()
+    return fa.load_library()
+
+
+P = 0x100000  # never dereferenced: every call below fails its checks first or is empty
+
+
+def _cache(**kw):
+    from exact_io_aware_33_gb300.paged import _CacheStruct
+    f = dict(k_pages=P, v_pages=P, k_scales=P, v_scales=P, num_pages=8, num_heads=2, page_size=16, d=64)
+    f.update(kw)
+    return _CacheStruct(**f)
+
+
+def _batch(**kw):
+    from exact_io_aware_33_gb300.paged import _BatchStruct
+    f = dict(block_table=P, kv_lens=P, cu_q=P, B=2, T=9, max_q=8, max_pages=4, max_kv=0)
+    f.update(kw)
+    return _BatchStruct(**f)
+
+
+def _attn(lib, c, b, q=P, stride=4 * 64, o=P, lse=P, Hq=4, window=0, scale=0.125, n_splits=1, ws=0, bytes_=0):
+    return lib.fa_paged_attn(ctypes.addressof(c) if c else 0, ctypes.addressof(b) if b else 0, q, stride, o, lse, Hq,
+                             window, scale, n_splits, ws, bytes_, 0)
+
+
+def _append(lib, c, b, k=P, ks=2 * 64, v=P, vs=2 * 64, q=P, qs=4 * 64, qo=P, qos=4 * 64, Hq=4, cos=P, sin=P,
+            max_pos=9, rot=64):
+    return lib.fa_paged_append(ctypes.addressof(c) if c else 0, ctypes.addressof(b) if b else 0, k, ks, v, vs, q, qs,
+                               qo, qos, Hq, cos, sin, max_pos, rot, 0, 0)
+
+
+BOTH = [
+    (dict(d=96), {}, fa.FA_ERR_UNSUPPORTED),
+    (dict(d=256), {}, fa.FA_ERR_UNSUPPORTED),
+    (dict(page_size=48), {}, fa.FA_ERR_UNSUPPORTED),
+    (dict(page_size=256), {}, fa.FA_ERR_UNSUPPORTED),
+    (dict(num_heads=0), {}, fa.FA_ERR_INVALID),
+    (dict(num_pages=0), {}, fa.FA_ERR_INVALID),
+    (dict(num_pages=1 << 30, num_heads=4), {}, fa.FA_ERR_INVALID),
+    (dict(k_pages=0), {}, fa.FA_ERR_INVALID),
+    (dict(v_pages=P + 8), {}, fa.FA_ERR_INVALID),
+    (dict(k_scales=0), {}, fa.FA_ERR_INVALID),
+    (dict(v_scales=P + 2), {}, fa.FA_ERR_INVALID),
+    ({}, dict(B=-1), fa.FA_ERR_INVALID),
+    ({}, dict(T=-3), fa.FA_ERR_INVALID),
+    ({}, dict(max_q=0), fa.FA_ERR_INVALID),
+    ({}, dict(max_kv=-1), fa.FA_ERR_INVALID),
+    ({}, dict(max_pages=0), fa.FA_ERR_INVALID),
+    ({}, dict(max_pages=1 << 28), fa.FA_ERR_INVALID),
+    ({}, dict(block_table=0), fa.FA_ERR_INVALID),
+    ({}, dict(kv_lens=P + 1), fa.FA_ERR_INVALID),
+    ({}, dict(cu_q=0), fa.FA_ERR_INVALID),              # one token per sequence, but nine rows for two
+    ({}, dict(cu_q=0, T=2), fa.FA_ERR_INVALID),         # ... and max_q is not 1
+    ({}, dict(B=0), fa.FA_OK),
+    ({}, dict(T=0), fa.FA_OK),
+]
+
+
+@pytest.mark.parametrize("c,b,code", BOTH)
+def test_cache_and_batch_are_checked_on_the_host(lib, c, b, code):
+    assert _attn(lib, _cache(**c), _batch(**b)) == code
+    assert _append(lib, _cache(**c), _batch(**b)) == code
+
+
+def test_missing_structs_are_refused(lib):
+    assert _attn(lib, None, _batch()) == fa.FA_ERR_INVALID
+    assert _append(lib, _cache(), None) == fa.FA_ERR_INVALID
+    assert lib.fa_paged_attn_workspace_bytes(0, 0, 4, 0) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Hq=3), fa.FA_ERR_INVALID), (dict(Hq=0), fa.FA_ERR_INVALID), (dict(window=-1), fa.FA_ERR_INVALID),
+    (dict(scale=math.nan), fa.FA_ERR_INVALID), (dict(scale=-1.0), fa.FA_ERR_INVALID), (dict(q=0), fa.FA_ERR_INVALID),
+    (dict(q=P + 2), fa.FA_ERR_INVALID), (dict(o=0), fa.FA_ERR_INVALID), (dict(lse=0), fa.FA_ERR_INVALID),
+    (dict(stride=4 * 64 - 8), fa.FA_ERR_INVALID), (dict(stride=4 * 64 + 4), fa.FA_ERR_INVALID),
+    (dict(n_splits=4), fa.FA_ERR_WORKSPACE), (dict(n_splits=4, ws=P + 16, bytes_=1 << 30), fa.FA_ERR_WORKSPACE),
+    (dict(n_splits=4, ws=P, bytes_=64), fa.FA_ERR_WORKSPACE)])
+def test_attention_arguments_are_checked_on_the_host(lib, kw, code):
+    assert _attn(lib, _cache(page_size=128), _batch(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=0), fa.FA_ERR_INVALID), (dict(v=P + 4), fa.FA_ERR_INVALID), (dict(ks=2 * 64 - 8), fa.FA_ERR_INVALID),
+    (dict(vs=2 * 64 + 1), fa.FA_ERR_INVALID), (dict(Hq=-1), fa.FA_ERR_INVALID), (dict(q=0), fa.FA_ERR_INVALID),
+    (dict(qo=0), fa.FA_ERR_INVALID), (dict(qs=8), fa.FA_ERR_INVALID), (dict(qos=12), fa.FA_ERR_INVALID),
+    (dict(rot=80), fa.FA_ERR_INVALID), (dict(rot=-16), fa.FA_ERR_INVALID), (dict(rot=24), fa.FA_ERR_UNSUPPORTED),
+    (dict(cos=0), fa.FA_ERR_INVALID), (dict(sin=P + 4), fa.FA_ERR_INVALID), (dict(max_pos=0), fa.FA_ERR_INVALID)])
+def test_append_arguments_are_checked_on_the_host(lib, kw, code):
+    assert _append(lib, _cache(), _batch(), **kw) == code
+
+
+def test_split_counts_and_workspace(lib):
+    c, b = _cache(page_size=64, num_heads=2), _batch(B=3, T=3, cu_q=0, max_q=1, max_pages=100)
+    ca, ba = ctypes.addressof(c), ctypes.addressof(b)
+    for want in (1, 2, 7, 100, 1000):
+        n = lib.fa_paged_attn_num_splits(ca, ba, 8, want)
+        assert 1 <= n <= min(want, 100)
+        need = lib.fa_paged_attn_workspace_bytes(ca, ba, 8, want)
+        assert need == (0 if n == 1 else 3 * 2 * n * 16 * (64 + 1) * 4)  # 16 rows per (sequence, key head, split)
+    assert lib.fa_paged_attn_num_splits(ca, ba, 7, 0) == 0               # heads do not divide
+    assert lib.fa_paged_attn_num_splits(ca, ba, 8, 0) >= 1
+
+
+def test_binding_refuses_cpu_tensors():
+    pages = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn)
+    scales = torch.ones(4, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.PagedCache(pages, pages, scales, scales)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.PagedBatch(torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))

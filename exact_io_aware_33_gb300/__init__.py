@@ -13,7 +13,7 @@ The functions carry the C entry points' names:
     fa_fwd_ex(q, k, v, causal=False, window=0, scale=None) -> (o, lse)
     fa_decode_splitkv(q, k, v, causal=False, window=0, scale=None, n_splits=0) -> (o, lse)
     fa_paged_append(cache, batch, k, v, q=None, rope=None) -> rotated q
-    fa_paged_attn(cache, batch, q, window=0, scale=None, n_splits=0) -> (o, lse)
+    fa_paged_attn(cache, batch, q, window=0, scale=None) -> (o, lse)
     fa_strerror(code), fa_get_last_device_status(), fa_version()
 
 The paged forms work on a PagedCache (a pool of e4m3 pages) and a PagedBatch
@@ -72,9 +72,8 @@ SIGNATURES = {
     "fa_bwd_dropout": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _U64, _U64,
                             _P, _S, _P]),
     "fa_paged_append": (_I, [_P, _P, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _P]),
-    "fa_paged_attn": (_I, [_P, _P, _P, _L, _P, _P, _I, _I, _F, _I, _P, _S, _P]),
-    "fa_paged_attn_num_splits": (_I, [_P, _P, _I, _I]),
-    "fa_paged_attn_workspace_bytes": (_S, [_P, _P, _I, _I]),
+    "fa_paged_attn": (_I, [_P, _P, _P, _L, _P, _P, _I, _I, _F, _P, _S, _P]),
+    "fa_paged_attn_workspace_bytes": (_S, [_P, _P, _I]),
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_get_last_device_status": (_I, []),
     "fa_version": (_I, []),
@@ -405,4 +404,4 @@ def fa_bwd_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, offset: int
 
 
 from .paged import (PagedBatch, PagedCache, fa_paged_append, fa_paged_attn,  # noqa: E402,F401
-                    fa_paged_attn_num_splits, fa_paged_attn_workspace_bytes)
+                    fa_paged_attn_workspace_bytes)

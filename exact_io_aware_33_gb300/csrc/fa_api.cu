@@ -116,7 +116,7 @@ bool make_map_bhnd(CUtensorMap* map, const void* ptr, int BH, int N, int d, int 
   return r == CUDA_SUCCESS;
 }
 
-bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows) {
+bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
@@ -127,7 +127,8 @@ bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r =
       enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -487,6 +488,12 @@ bool row_stride_ok(long long stride, int heads, int d) {
   return stride >= static_cast<long long>(heads) * d && stride % 8 == 0 && stride <= (1LL << 40);
 }
 
+// SMs of the current device, looked up once; a GB300's where there is none.
+int paged_sms() {
+  const int sms = fa::device_sm_count();
+  return sms > 0 ? sms : 152;
+}
+
 int paged_max_kv(const fa_paged_cache* c, const fa_paged_batch* b) {
   const long long most = static_cast<long long>(b->max_pages) * c->page_size;
   return static_cast<int>(b->max_kv > 0 && b->max_kv < most ? b->max_kv : most);
@@ -522,27 +529,17 @@ int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, co
   return fa::launch_paged_append(pool, dev, p, static_cast<cudaStream_t>(cuda_stream));
 }
 
-int fa_paged_attn_num_splits(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq, int n_splits) {
+size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq) {
   fa::PagedPool pool;
   fa::PagedBatchDev dev;
   bool empty = false;
   if (check_paged(cache, batch, &pool, &dev, &empty) != FA_OK || empty || Hq <= 0 || Hq % cache->num_heads != 0)
     return 0;
-  return fa::paged_attn_split(pool, dev, Hq, paged_max_kv(cache, batch), n_splits, sm_count()).splits;
-}
-
-size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq,
-                                     int n_splits) {
-  fa::PagedPool pool;
-  fa::PagedBatchDev dev;
-  bool empty = false;
-  if (check_paged(cache, batch, &pool, &dev, &empty) != FA_OK || empty || Hq <= 0 || Hq % cache->num_heads != 0)
-    return 0;
-  return fa::paged_attn_split(pool, dev, Hq, paged_max_kv(cache, batch), n_splits, sm_count()).workspace_bytes;
+  return fa::paged_attn_plan(pool, dev, Hq, paged_max_kv(cache, batch), paged_sms()).workspace_bytes;
 }
 
 int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
-                  long long q_stride, void* o, float* lse, int Hq, int window, float scale, int n_splits,
+                  long long q_stride, void* o, float* lse, int Hq, int window, float scale,
                   void* workspace, size_t ws_bytes, void* cuda_stream) {
   fa::PagedPool pool;
   fa::PagedBatchDev dev;
@@ -554,17 +551,18 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   if (empty) return FA_OK;
   if (!fa::aligned16(q) || !fa::aligned16(o) || !aligned4(lse) || !row_stride_ok(q_stride, Hq, cache->d))
     return FA_ERR_INVALID;
-  const int max_kv = paged_max_kv(cache, batch);
-  const fa::PagedSplit split = fa::paged_attn_split(pool, dev, Hq, max_kv, n_splits, sm_count());
-  if (split.workspace_bytes > 0 &&
+  // packed (query, head) rows of a key head are counted in 32 bits
+  if (static_cast<long long>(batch->max_q) * Hq > 0x7fffffffLL) return FA_ERR_INVALID;
+  const fa::PagedPlan plan = fa::paged_attn_plan(pool, dev, Hq, paged_max_kv(cache, batch), paged_sms());
+  if (plan.workspace_bytes > 0 &&
       (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-       ws_bytes < split.workspace_bytes))
+       ws_bytes < plan.workspace_bytes))
     return FA_ERR_WORKSPACE;
   fa::DeviceState* st = nullptr;
   rc = fa::current_device(&st);
   if (rc != FA_OK) return rc;
-  const fa::PagedAttn p{q, q_stride, o, lse, Hq, window, max_kv, scale};
-  return fa::launch_paged_attn(pool, dev, p, split, workspace, static_cast<cudaStream_t>(cuda_stream));
+  const fa::PagedAttn p{q, q_stride, o, lse, Hq, window, scale};
+  return fa::launch_paged_attn(pool, dev, p, plan, workspace, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int fa_get_last_device_status(void) {

@@ -50,9 +50,9 @@ struct FwdProblem {
 bool make_map_bhnd(CUtensorMap* map, const void* ptr, int BH, int N, int d, int box_rows = 128);
 
 // Encodes a 3-D tiled TMA map over 8-bit pages [blocks, rows, d] (one block per
-// page and head) with boxes of box_rows rows x d bytes and a swizzle of d bytes
-// (64 or 128). Returns false on failure.
-bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows);
+// page and head) with boxes of box_rows rows x d bytes, with a swizzle of d bytes
+// (64 or 128) or none. Returns false on failure.
+bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int d, int box_rows, bool swizzle);
 
 // Size and scale checks shared by the entry points taking (B, H, N, d):
 // FA_OK or an error code; *empty is set when there is nothing to compute.
@@ -87,6 +87,33 @@ cudaError_t launch_overlapped(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Launches `kern` with the grid in clusters of `cluster` CTAs, with (as
+// launch_overlapped) or without programmatic stream serialization.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_with(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem_bytes, bool overlapped,
+                        int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem_bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (overlapped) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -145,25 +172,28 @@ struct PagedAttn {
   float* lse;          // [T, Hq]
   int Hq;
   int window;
-  int max_kv;          // no sequence is expected to be longer (one that is takes longer)
   float scale;
 };
 
 int launch_paged_append(const PagedPool& pool, const PagedBatchDev& batch, const PagedAppend& p,
                         cudaStream_t stream);
 
-// How a launch cuts the key range: `splits` parts of `split_tiles` tiles of
-// 64 tokens, and the workspace that the parts' states take.
-struct PagedSplit {
-  int row_tiles;    // row tiles of a sequence and key head
-  int splits;
-  int split_tiles;
-  size_t workspace_bytes;
+// How a launch divides its work (see fa_paged_attn.cu).
+struct PagedPlan {
+  int rows;                // (query, head) rows per CTA: 8 or 16
+  int row_tiles;           // tiles of that many rows of the longest packed sequence and a key head
+  long long items;         // sequences x key heads x row tiles
+  int cluster;             // CTAs per item in the cluster form; 0: the streaming form
+  bool chunk;              // many rows: the kernel of fa_paged_chunk.cu, nothing below
+  long long ctas;
+  size_t workspace_bytes;  // the pieces' states of the streaming form
 };
-PagedSplit paged_attn_split(const PagedPool& pool, const PagedBatchDev& batch, int Hq, int max_kv,
-                            int n_splits, int sms);
+PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, int Hq, int max_kv, int sms);
 int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p,
-                      const PagedSplit& split, void* workspace, cudaStream_t stream);
+                      const PagedPlan& plan, void* workspace, cudaStream_t stream);
+
+// Attention for many query rows (fa_paged_chunk.cu).
+int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, cudaStream_t stream);
 
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 

@@ -70,6 +70,23 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 0xff in each byte of w that holds a NaN code.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t z = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (z >> 7) * 255u;
+}
+
+// Whether the query at position p sees key j.
+__device__ __forceinline__ bool sees(int p, int j, int window) {
+  return j <= p && (window == 0 || j > p - window);
+}
+
 // 2^e as a float, e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 

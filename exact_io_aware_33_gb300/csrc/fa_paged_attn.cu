@@ -13,19 +13,31 @@
 // Precision. Queries are scaled per row by a power of two into f16's normal
 // range (exact for every bf16 value within 2^27 of the row's largest; below
 // that it would change S by less than 2^-38 of its bound). P is rounded to f16
-// (2^-12) and scaled by 2^15, so that weights down to 2^-29 of the largest
-// keep full precision and down to 2^-39 are not lost. The denominator adds
-// the weights before that rounding.
+// (2^-12 of it) after a factor of 2^6, so that weights down to 2^-20 of their
+// reference keep that precision and those down to 2^-31 still count; the
+// references lie between the largest weight so far and 2^-8 of it (as in the
+// forward). The denominator adds the weights before that rounding.
 //
 // What bounds it: at one token per sequence every cached byte is read once
 // for G = Hq / Hkv rows of arithmetic, far below the tensor core's rate, so
 // the kernel is a copy from HBM. It therefore is organised as one: a TMA warp
-// keeps a ring of tiles (64 tokens of K and V) full, as deep as two CTAs per
-// SM allow, and four warps take 16 tokens of each tile, each with an online
-// softmax of its own, so that no two warps wait for one another until the
-// end. Codes go from shared memory to registers and are widened there
-// (mma.sync takes its operands from registers; tcgen05 would want them
-// widened in shared memory first, which costs a second pass over it).
+// keeps a ring of tiles (64 tokens of K and V) full and four warps take 16
+// tokens of each tile, each with an online softmax of its own, so that no two
+// warps wait for one another until the end of an item. Codes go from shared
+// memory to registers and are widened there (mma.sync takes its operands from
+// registers; tcgen05 would want them widened in shared memory first, which
+// costs a second pass over it).
+//
+// Division of the work. An item is one sequence, key head and tile of 8 or 16
+// query rows. The streaming form cuts the tiles of all items, laid end to end, into
+// equal parts, one per CTA slot of the GPU: lengths differ by orders of
+// magnitude between the sequences of a batch, and a part may hold many short
+// items or a piece of a long one. The ring runs on across items. Items that
+// end up in one part are written at once; pieces go to the workspace (two per
+// part at most: one that it continues and one that it leaves) and a second
+// kernel joins them. Where the whole batch is so little that a second launch
+// would cost more than it divides, a cluster of CTAs takes an item instead
+// and joins its pieces through distributed shared memory.
 
 #include <cmath>
 
@@ -36,26 +48,36 @@ namespace {
 
 constexpr int kTile = 64;        // tokens per stage
 constexpr int kGroup = 16;       // tokens per warp of a stage
-constexpr int kRows = 16;        // query rows per CTA
 constexpr int kThreads = 160;    // four warps and the TMA warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPShift = 15.f;  // P is held as 2^15 P
+constexpr float kPShift = 6.f;   // P is held as 2^6 P
+constexpr float kSlack = 8.f;    // log2 units that a weight may pass its reference by
 
-template <int D>
+// Each item costs about this many tiles more than it has (its queries, the
+// joining of its four warps, the write-back).
+constexpr int kItemUnits = 2;
+
+// NB: blocks of eight query rows per CTA.
+template <int D, int NB>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 6 : 10;  // two CTAs per SM
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kCtasPerSm = NB == 1 ? 3 : 2;
   static constexpr int kTileBytes = kTile * D;
+  // the four warps' states at the end of an item: rows of d channels, then {m_s, m_t, l, -} each
+  static constexpr int kPitch = D + 4;
+  static constexpr int kStateBytes = 4 * kRows * (kPitch + 4) * 4;
+  // as many stages as leave room for the other CTAs of the SM
+  static constexpr int kRoom = 233472 / kCtasPerSm - 1024 - 1024 - 512 - kStateBytes;
+  static constexpr int kStages = kRoom / (2 * kTileBytes) < 10 ? kRoom / (2 * kTileBytes) : 10;
   static constexpr int kKOff = 0;
   static constexpr int kVOff = kStages * kTileBytes;
-  static constexpr int kScaleOff = 2 * kStages * kTileBytes;  // [stage][4] {sk, log2 sv}
+  static constexpr int kStateOff = 2 * kStages * kTileBytes;
+  static constexpr int kScaleOff = kStateOff + kStateBytes;  // [stage][4] {sk, log2 sv}
   static constexpr int kBarOff = kScaleOff + kStages * 4 * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + slack to align the base
-  // the warps' states at the end, in the ring's place
-  static constexpr int kPitch = D + 4;
-  static_assert(4 * kRows * (kPitch + 4) * 4 <= kScaleOff, "the warps' states must fit the ring");
-  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "the CTAs of an SM must fit");
 };
 
 struct AttnArgs {
@@ -64,47 +86,155 @@ struct AttnArgs {
   long long q_stride;
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;    // [item][split][16][d], normalised
-  float* part_lse;  // [item][split][16], log2 units
+  float* part_o;    // [part][2][16][d], normalised
+  float* part_lse;  // [part][2][16], log2 units
   const uint8_t* v_pages;  // the rare path that looks for NaN codes again
   const float* k_scales;
   const float* v_scales;
   int* status;
   int Hq, Hkv, G;
   int window;
-  int row_tiles, splits, split_tiles;
+  int row_tiles;   // cluster form: row tiles of the longest packed sequence
+  int cluster;     // CTAs per item (cluster form)
   float scale_log2;
 };
 
-// The rows of one CTA (16 of the n * G rows of a sequence and key head, query
-// by query) and the keys that they see.
-struct RowTile {
-  int rows, r0;
-  int p0;          // position of query 0
-  int p_lo, p_hi;  // positions of the first and last query of the tile
-  int lo, hi;      // keys that any of its rows sees: [lo, hi)
-  int t0, nt;      // as tiles of 64
-  int active;      // splits with work
+// One sequence's items: its tiles of R rows, and the tiles of 64 keys that any of
+// its queries sees.
+struct SeqGeo {
+  PagedSeq s;
+  int rows, rts;  // packed (query, head of the group) rows of a key head, and tiles of R of them
+  int p0;         // position of query 0
+  int t0, nt;
 };
 
-__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const PagedSeq& s, int rt) {
-  RowTile g;
-  g.rows = s.n * a.G;
-  g.r0 = rt * kRows;
-  g.p0 = s.len - s.n;
-  g.p_lo = g.p0 + g.r0 / a.G;
-  g.p_hi = g.p0 + (min(g.r0 + kRows, g.rows) - 1) / a.G;
-  g.hi = max(g.p_hi + 1, 0);
-  g.lo = a.window > 0 ? max(g.p_lo - a.window + 1, 0) : 0;
-  g.t0 = g.lo / kTile;
-  g.nt = g.hi > g.lo ? (g.hi + kTile - 1) / kTile - g.t0 : 0;
-  g.active = min((g.nt + a.split_tiles - 1) / a.split_tiles, a.splits);
+template <int R>
+__device__ __forceinline__ SeqGeo seq_geo(const AttnArgs& a, int seq) {
+  SeqGeo g;
+  g.s = paged_seq(a.batch, seq, a.status);
+  g.rows = g.s.n * a.G;
+  g.rts = (g.rows + R - 1) / R;
+  g.p0 = g.s.len - g.s.n;
+  const int hi = g.s.n > 0 ? g.s.len : 0;
+  const int lo = a.window > 0 ? max(g.p0 - a.window + 1, 0) : 0;
+  g.t0 = lo / kTile;
+  g.nt = hi > lo ? (hi + kTile - 1) / kTile - g.t0 : 0;
   return g;
 }
 
-__device__ __forceinline__ bool sees(int p, int j, int window) {
-  return j <= p && (window == 0 || j > p - window);
+__device__ __forceinline__ long long seq_units(const AttnArgs& a, const SeqGeo& g) {
+  return static_cast<long long>(a.Hkv) * g.rts * (g.nt + kItemUnits);
 }
+
+// The rows of an item and the keys [lo, hi) that any of them sees.
+struct RowTile {
+  int rows, r0;
+  int p0;
+  int p_lo, p_hi;  // positions of the first and last query of the tile
+  int lo, hi;
+};
+
+template <int R>
+__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqGeo& s, int rt) {
+  RowTile g;
+  g.rows = s.rows;
+  g.r0 = rt * R;
+  g.p0 = s.p0;
+  g.p_lo = g.p0 + g.r0 / a.G;
+  g.p_hi = g.p0 + (min(g.r0 + R, g.rows) - 1) / a.G;
+  g.hi = max(g.p_hi + 1, 0);
+  g.lo = a.window > 0 ? max(g.p_lo - a.window + 1, 0) : 0;
+  return g;
+}
+
+// First unit of part c of `parts` over `units` units, and the part of a unit.
+__device__ __forceinline__ long long part_start(long long units, int parts, int c) {
+  return units * c / parts;
+}
+
+// The units of the whole batch, by one warp.
+template <int R>
+__device__ __forceinline__ long long all_units(const AttnArgs& a) {
+  long long sum = 0;
+  for (int b = lane_id(); b < a.batch.B; b += 32) sum += seq_units(a, seq_geo<R>(a, b));
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  return sum;
+}
+
+// The sequence that holds unit u (below the total), and its first unit; by one warp.
+template <int R>
+__device__ __forceinline__ int find_seq(const AttnArgs& a, long long u, long long* first) {
+  long long before = 0;
+  for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
+    const int b = b0 + static_cast<int>(lane_id());
+    const long long own = b < a.batch.B ? seq_units(a, seq_geo<R>(a, b)) : 0;
+    long long end = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, end, m);
+      if (lane_id() >= static_cast<uint32_t>(m)) end += x;
+    }
+    end += before;
+    const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+    if (past) {
+      const int i = __ffs(past) - 1;
+      *first = __shfl_sync(0xffffffffu, end - own, i);
+      return b0 + i;
+    }
+    before = __shfl_sync(0xffffffffu, end, 31);
+  }
+  *first = before;  // not reached for u below the total
+  return a.batch.B;
+}
+
+// Walks the pieces of items that a CTA has, sequence by sequence: tiles
+// [v0, v1) of the sequence's tiles laid end to end, item after item (key head
+// by key head, row tile by row tile). A sequence whose rows see no key has
+// items [e0, e1) to be filled with zeros instead. Every warp walks alike.
+template <int R>
+struct Walk {
+  long long u0, u1;  // this CTA's units
+  long long base;    // first unit of sequence b
+  int b;
+
+  __device__ __forceinline__ void start(const AttnArgs& a, int part, int parts) {
+    const long long units = all_units<R>(a);
+    u0 = part_start(units, parts, part);
+    u1 = part_start(units, parts, part + 1);
+    b = a.batch.B;
+    base = 0;
+    if (u0 < u1) b = find_seq<R>(a, u0, &base);
+  }
+  // unit -> tile index in the sequence: the first kItemUnits of an item are not tiles
+  static __device__ __forceinline__ long long tile_of(long long u, int nt) {
+    const int per = nt + kItemUnits;
+    return u / per * nt + max(u % per - kItemUnits, 0LL);
+  }
+  __device__ __forceinline__ bool next(const AttnArgs& a, SeqGeo* g, long long* v0, long long* v1, int* e0,
+                                       int* e1) {
+    while (b < a.batch.B && base < u1) {
+      *g = seq_geo<R>(a, b);
+      const long long own = seq_units(a, *g);
+      const long long lo = max(u0 - base, 0LL), hi = min(u1 - base, own);
+      base += own;
+      ++b;
+      if (hi <= lo) continue;
+      *v0 = *v1 = 0;
+      *e0 = *e1 = 0;
+      if (g->nt > 0) {
+        *v0 = tile_of(lo, g->nt);
+        *v1 = tile_of(hi, g->nt);
+        if (*v1 > *v0) return true;
+      } else {
+        *e0 = static_cast<int>((lo + kItemUnits - 1) / kItemUnits);
+        *e1 = static_cast<int>((hi + kItemUnits - 1) / kItemUnits);
+        if (*e1 > *e0) return true;
+      }
+    }
+    return false;
+  }
+};
 
 // Whether every row of the tile sees every one of the 16 keys from j0 on.
 __device__ __forceinline__ bool all_see(const RowTile& g, int j0, int window) {
@@ -119,30 +249,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+// The transpose of an 8 x 8 block of 16-bit values, in the fragment layout of mma.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-// 0xff in each byte of w that holds a NaN code.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  const uint32_t z = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return (z >> 7) * 255u;
 }
 
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// Over the eight lanes of equal lane & 3.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
 // One row's D/4 consecutive queries of this lane, scaled into f16, and the
 // factor that undoes it (with the softmax scale). Four words of eight values
-// per 16 bytes; word pairs are the two halves of an mma step's A columns.
+// per 16 bytes; word pairs are the two halves of an mma step's k range.
 template <int D>
 __device__ __forceinline__ float load_query(const __nv_bfloat16* row, bool on, float scale_log2,
                                             uint32_t (&w)[D / 8]) {
@@ -171,21 +303,52 @@ __device__ __forceinline__ float load_query(const __nv_bfloat16* row, bool on, f
   return scale_log2 * pow2i(-k);
 }
 
-// kHalf: at most eight rows, the upper half of every m16 tile is zero and its
-// softmax left out.
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 2)
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// kCols channels from c0 on of row r of a key head.
+template <int D, int kCols>
+__device__ __forceinline__ void store_row(const AttnArgs& a, const SeqGeo& sg, int h, int r, int c0,
+                                          const float (&x)[kCols], float lse2) {
+  const long long at = static_cast<long long>(sg.s.row0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+  __nv_bfloat16* dst = a.o + at * D + c0;
+#pragma unroll
+  for (int i = 0; i < kCols; i += 4)
+    *reinterpret_cast<uint2*>(dst + i) = make_uint2(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]));
+  if (c0 == 0) a.lse[at] = kLn2 * lse2;
+}
+
+// kCluster: the cluster form (see the top of the file).
+//
+// The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys (and
+// channels) fill the 16 rows of an mma tile and queries its 8 columns, so that
+// eight query rows, the usual group, leave nothing idle, and a widened key or
+// value serves all NB blocks of them. P^T comes out of the softmax as the
+// transpose of what the second product takes, two 8 x 8 blocks per 16 keys.
+template <int D, int NB, bool kCluster>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const AttnArgs a) {
-  using C = Cfg<D>;
-  constexpr int kS = C::kStages;
-  constexpr int kNR = kHalf ? 1 : 2;  // row halves per lane
+  using C = Cfg<D, NB>;
+  constexpr int kS = C::kStages, R = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   const uint32_t full = sb + C::kBarOff, empty = full + 8 * kS;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
-  volatile int* nan_flag = abort_flag + 1;
+  volatile int* nan_flag = abort_flag + 1;  // two, taken in turn by the items
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -194,422 +357,664 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty + 8 * i, 4);
     }
     *abort_flag = 0;
-    *nan_flag = 0;
+    nan_flag[0] = nan_flag[1] = 0;
     mbar_fence_init();
   }
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
 
-  const int split = static_cast<int>(blockIdx.x % a.splits);
-  const long long item = blockIdx.x / a.splits;
-  const int rt = static_cast<int>(item % a.row_tiles);
-  const long long bh = item / a.row_tiles;
-  const int h = static_cast<int>(bh % a.Hkv), seq = static_cast<int>(bh / a.Hkv);
-  const PagedSeq s = paged_seq(a.batch, seq, a.status);
-  if (rt * kRows >= s.n * a.G) return;
-  const RowTile g = row_tile(a, s, rt);
-  if (split >= max(g.active, 1)) return;
-  const int ta = g.t0 + split * a.split_tiles;
-  const int tb = split == g.active - 1 ? g.t0 + g.nt : min(ta + a.split_tiles, g.t0 + g.nt);
-  const int tiles = g.nt > 0 ? tb - ta : 0;
+  // What this CTA does: a walk over its part (streaming), or its piece of one
+  // item (cluster; `rank` of `pieces` that have any tile).
+  Walk<R> walk;
+  SeqGeo sg;
+  long long v0 = 0, v1 = 0;
+  int e0 = 0, e1 = 0, rank = 0, pieces = 1;
+  bool more;
+  if constexpr (kCluster) {
+    rank = static_cast<int>(blockIdx.x % a.cluster);
+    const long long item = blockIdx.x / a.cluster;
+    const int rt = static_cast<int>(item % a.row_tiles);
+    const long long bh = item / a.row_tiles;
+    const int h = static_cast<int>(bh % a.Hkv);
+    sg = seq_geo<R>(a, static_cast<int>(bh / a.Hkv));
+    if (rt >= sg.rts) return;  // the whole cluster alike
+    walk.b = static_cast<int>(bh / a.Hkv) + 1;
+    const int own = h * sg.rts + rt;
+    const int per = (sg.nt + a.cluster - 1) / a.cluster;
+    pieces = sg.nt > 0 ? (sg.nt + per - 1) / per : 1;
+    if (rank >= pieces) return;  // nothing to do, and nothing that the others would read
+    v0 = static_cast<long long>(own) * sg.nt + min(rank * per, sg.nt);
+    v1 = static_cast<long long>(own) * sg.nt + min((rank + 1) * per, sg.nt);
+    if (sg.nt == 0) {
+      e0 = own;
+      e1 = own + 1;
+    }
+    more = true;
+  } else {
+    walk.start(a, blockIdx.x, gridDim.x);
+    more = walk.next(a, &sg, &v0, &v1, &e0, &e1);
+  }
+  uint32_t it = 0;  // tiles so far: the ring runs on across items and sequences
 
   if (warp == 4) {
     // ------------------------------------------------------------ TMA warp
-    // Lane i looks up the i-th of the next 32 groups of 16 keys: its page and
-    // scales, two dependent loads that are paid once for eight tiles.
+    // Lane i looks up the i-th of 32 groups of 16 keys (eight tiles, across
+    // items of a sequence): its page, then its scales. The next eight tiles'
+    // two dependent loads are under way while the present ones are issued.
     const int box_rows = min(a.batch.page_size, kTile);
     const int boxes = kTile / box_rows, groups_per_box = box_rows / kGroup;
-    int armed = 0;
-    for (int base = 0; base < tiles && !*abort_flag; base += 8) {
-      int page = -1;
-      float sk = -1.f, ev = 0.f;
-      const int j0 = (ta + base) * kTile + lane * kGroup;
-      if (base + lane / 4 < tiles && j0 < g.hi && j0 + kGroup > g.lo) {
-        page = paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status);
-        if (page >= 0) {
-          const long long at = static_cast<long long>(page) * a.Hkv + h;
-          sk = a.k_scales[at];
-          const float sv = a.v_scales[at];
-          const uint32_t bits = __float_as_uint(sv);
-          // exact for the powers of two that the append writes
-          ev = (bits & 0x7fffffu) ? log2f(sv) : bits == 0 ? -INFINITY : static_cast<float>(static_cast<int>(bits >> 23) - 127);
+    while (more) {
+      const int seq = walk.b - 1;
+      long long left = v1 - v0;  // tiles not looked up yet
+      int item = sg.nt > 0 ? static_cast<int>(v0 / sg.nt) : 0;
+      int tile = sg.nt > 0 ? static_cast<int>(v0 % sg.nt) : 0;
+      int page = -1, head = 0, key = 0, count = 0;
+      float sk = -1.f, sv = 1.f;
+      int n_page = -1, n_head = 0, n_key = 0, n_count = 0;
+      auto look = [&]() {  // the next (up to) eight tiles' pages
+        n_count = static_cast<int>(min(left, 8LL));
+        int ti = tile + (lane >> 2), ii = item;
+        while (ti >= sg.nt && sg.nt > 0) {
+          ti -= sg.nt;
+          ++ii;
         }
-      }
-      for (int i = 0; i < 8 && base + i < tiles; ++i) {
-        const int it = base + i, st = it % kS;
-        int pg[4];
+        n_page = -1;
+        if ((lane >> 2) < n_count) {
+          const RowTile g = row_tile<R>(a, sg, ii % sg.rts);
+          n_head = ii / sg.rts;
+          n_key = (sg.t0 + ti) * kTile;
+          const int j0 = n_key + (lane & 3) * kGroup;
+          if (j0 < g.hi && j0 + kGroup > g.lo)
+            n_page = paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status);
+        }
+        left -= n_count;
+        tile += n_count;
+        while (tile >= sg.nt && sg.nt > 0) {
+          tile -= sg.nt;
+          ++item;
+        }
+      };
+      float n_sk = -1.f, n_sv = 1.f;
+      auto scales = [&]() {
+        n_sk = -1.f;
+        if (n_page >= 0) {
+          const long long at = static_cast<long long>(n_page) * a.Hkv + n_head;
+          n_sk = a.k_scales[at];
+          n_sv = a.v_scales[at];
+        }
+      };
+      look();
+      scales();
+      while (n_count > 0) {
+        page = n_page;
+        head = n_head;
+        key = n_key;
+        count = n_count;
+        sk = n_sk;
+        sv = n_sv;
+        look();
+        for (int i = 0; i < count && !*abort_flag; ++i) {
+          const int st = it % kS;
+          int pg[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) pg[q] = __shfl_sync(0xffffffffu, page, 4 * i + q);
-        if (it >= kS && !mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag)) break;
-        if (lane / 4 == i)
-          *reinterpret_cast<float2*>(smem + C::kScaleOff + (st * 4 + (lane & 3)) * 8) = make_float2(sk, ev);
-        __syncwarp();
-        if (lane == 0) {
-          int n = 0;
-          int bp[4];
-          for (int b = 0; b < boxes; ++b) {
-            bp[b] = -1;
-            for (int q = 0; q < groups_per_box; ++q) bp[b] = max(bp[b], pg[b * groups_per_box + q]);
-            n += bp[b] >= 0;
+          for (int q = 0; q < 4; ++q) pg[q] = __shfl_sync(0xffffffffu, page, 4 * i + q);
+          const int hd = __shfl_sync(0xffffffffu, head, 4 * i), tok = __shfl_sync(0xffffffffu, key, 4 * i);
+          if (it >= kS && !mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag)) break;
+          // the copies need the pages only: they go out before the scales are waited for
+          uint32_t bytes = 0;
+          if (lane == 0) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              if (b >= boxes) break;
+              int bp = -1;
+              for (int q = 0; q < groups_per_box; ++q) {
+                const int x = b * groups_per_box + q;
+                bp = max(bp, x == 0 ? pg[0] : x == 1 ? pg[1] : x == 2 ? pg[2] : pg[3]);
+              }
+              if (bp < 0) continue;
+              const int slot = (tok + b * box_rows) & (a.batch.page_size - 1);
+              const int blk = bp * a.Hkv + hd;
+              const uint32_t off = st * C::kTileBytes + b * box_rows * D;
+              tma_load_3d(sb + C::kKOff + off, &tmK, full + 8 * st, 0, slot, blk);
+              tma_load_3d(sb + C::kVOff + off, &tmV, full + 8 * st, 0, slot, blk);
+              bytes += 2u * box_rows * D;
+            }
           }
-          mbar_arrive_expect_tx(full + 8 * st, 2u * n * box_rows * D);
-          const int tok = (ta + it) * kTile;
-          for (int b = 0; b < boxes; ++b) {
-            if (bp[b] < 0) continue;
-            const int slot = (tok + b * box_rows) & (a.batch.page_size - 1);
-            const int blk = bp[b] * a.Hkv + h;
-            const uint32_t off = st * C::kTileBytes + b * box_rows * D;
-            tma_load_3d(sb + C::kKOff + off, &tmK, full + 8 * st, 0, slot, blk);
-            tma_load_3d(sb + C::kVOff + off, &tmV, full + 8 * st, 0, slot, blk);
+          if (lane / 4 == i) {
+            const uint32_t bits = __float_as_uint(sv);
+            // exact for the powers of two that the append writes
+            const float ev = (bits & 0x7fffffu) ? log2f(sv)
+                             : bits == 0       ? -INFINITY
+                                               : static_cast<float>(static_cast<int>(bits >> 23) - 127);
+            *reinterpret_cast<float2*>(smem + C::kScaleOff + (st * 4 + (lane & 3)) * 8) = make_float2(sk, ev);
           }
+          __syncwarp();
+          // (bytes that have landed already count as well: the phase cannot end before this arrival)
+          if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+          if (i == min(3, count - 1)) scales();
+          ++it;
         }
-        armed = it + 1;
+        __syncwarp();
+        if (*abort_flag) break;
       }
-      __syncwarp();
+      if (*abort_flag) break;
+      more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
     }
     // let every copy in flight land before the CTA can end
-    for (int it = max(armed - kS, 0); it < armed; ++it) mbar_wait(full + 8 * (it % kS), (it / kS) & 1, nullptr);
+    for (uint32_t i = it > kS ? it - kS : 0; i < it; ++i) mbar_wait(full + 8 * (i % kS), (i / kS) & 1, nullptr);
     if (lane == 0 && *abort_flag) *a.status = kStatusTimeout;
+    if constexpr (kCluster) {
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
   // -------------------------------------------------------------- four compute warps
   const int n = lane >> 2, t = lane & 3;  // fragment row (or column) and quarter
-  uint32_t qa[D / 16][4];
-  float qf[2];
-  int p_row[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = g.r0 + n + 8 * r;
-    const bool on = row < g.rows && (r == 0 || !kHalf);
-    const int i = on ? row / a.G : 0, hd = h * a.G + (on ? row % a.G : 0);
-    p_row[r] = on ? g.p0 + i : g.p_hi;
-    uint32_t w[D / 8];
-    qf[r] = load_query<D>(a.q + static_cast<long long>(s.row0 + i) * a.q_stride + hd * D + t * (D / 4), on,
-                          a.scale_log2, w);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      qa[k][r] = w[2 * k];
-      qa[k][2 + r] = w[2 * k + 1];
-    }
-  }
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float ms[2] = {-INFINITY, -INFINITY}, mt[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  bool ok = true, saw_nan = false;
+  constexpr int kTpr = 128 / R;           // at the end of an item: threads per row,
+  constexpr int kCols = D / kTpr;         // and channels per thread
+  const int wrow = threadIdx.x / kTpr, c0 = threadIdx.x % kTpr * kCols;
+  float* so = reinterpret_cast<float*>(smem + C::kStateOff);  // [warp][row][kPitch]
+  float* sst = so + 4 * R * C::kPitch;                        // [warp][row][4]: m_s, m_t, l
+  bool ok = true;
+  int turn = 0;
 
-  for (int it = 0; it < tiles; ++it) {
-    const int st = it % kS;
-    ok = mbar_wait_w(full + 8 * st, (it / kS) & 1, abort_flag);
-    if (!ok) break;
-    const float2 sc = *reinterpret_cast<const float2*>(smem + C::kScaleOff + (st * 4 + warp) * 8);
-    if (!(sc.x < 0.f)) {  // below zero: no row sees these keys, or they have no page
-      const int j0 = (ta + it) * kTile + warp * kGroup;
-      const bool part = !all_see(g, j0, a.window);
-      const uint8_t* kb = smem + C::kKOff + st * C::kTileBytes;
-      const uint8_t* vb = smem + C::kVOff + st * C::kTileBytes;
-      // S = Q K^T: 16 rows x 16 keys. A lane holds D/4 consecutive channels of
-      // its key, four per mma step, in the order that its queries have.
-      float acc[2][4] = {};
-      uint4 kw[2][D / 64];
+  while (more) {
+    const int seq = walk.b - 1;
+    // items whose rows see no key
+    for (int e = e0; e < e1; ++e) {
+      const int r = e % sg.rts * R + wrow;
+      const float x[kCols] = {};
+      if (r < sg.rows) store_row<D>(a, sg, e / sg.rts, r, c0, x, -INFINITY);
+    }
+    int item = sg.nt > 0 ? static_cast<int>(v0 / sg.nt) : 0;
+    int tile = sg.nt > 0 ? static_cast<int>(v0 % sg.nt) : 0;
+    for (long long left = v1 - v0; left > 0;) {
+      // the piece [tile, tile_end) of this item
+      const int tile_end = static_cast<int>(min(static_cast<long long>(sg.nt), tile + left));
+      const int h = item / sg.rts;
+      const RowTile g = row_tile<R>(a, sg, item % sg.rts);
+      uint32_t qb[NB][D / 8];   // B operand of S^T: row n of each block, D/4 channels
+      float qf[NB][2];          // per column of the accumulators (rows 2t, 2t + 1 of a block)
+      int p_row[NB][2];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const int row = warp * kGroup + nb * 8 + n;
-        if constexpr (D == 128) {
-          kw[nb][0] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t) ^ (row & 7)) << 4));
-          kw[nb][1] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t + 1) ^ (row & 7)) << 4));
-        } else {
-          kw[nb][0] = *reinterpret_cast<const uint4*>(kb + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
+      for (int nb = 0; nb < NB; ++nb) {
+        const int row = g.r0 + nb * 8 + n;
+        const bool on = row < g.rows;
+        const int i = on ? row / a.G : 0, hd = h * a.G + (on ? row % a.G : 0);
+        const float f = load_query<D>(
+            a.q + static_cast<long long>(sg.s.row0 + i) * a.q_stride + hd * D + t * (D / 4), on, a.scale_log2, qb[nb]);
+        const int p = on ? g.p0 + i : g.p_hi;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qf[nb][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
+          p_row[nb][e] = __shfl_sync(0xffffffffu, p, 4 * (2 * t + e));
         }
       }
+      float o[NB][D / 16][4];
+      float ms[NB][2], mt[NB][2], l[NB][2];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int i = 0; i < D / 16; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
+        ms[nb][0] = ms[nb][1] = mt[nb][0] = mt[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.f;
+      }
+      bool saw_nan = false;
+
+      for (int ti = tile; ti < tile_end; ++ti, ++it) {
+        const int st = it % kS;
+        ok = ok && mbar_wait_w(full + 8 * st, (it / kS) & 1, abort_flag);
+        if (!ok) continue;
+        const float2 sc = *reinterpret_cast<const float2*>(smem + C::kScaleOff + (st * 4 + warp) * 8);
+        if (!(sc.x < 0.f)) {  // below zero: no row sees these keys, or they have no page
+          const int j0 = (sg.t0 + ti) * kTile + warp * kGroup;
+          const bool part = !all_see(g, j0, a.window);
+          const uint8_t* kb = smem + C::kKOff + st * C::kTileBytes;
+          const uint8_t* vb = smem + C::kVOff + st * C::kTileBytes;
+          // S^T = K Q^T: 16 keys x 8 NB rows. A lane holds D/4 consecutive
+          // channels of keys n and n + 8, four per mma step, in the order
+          // that its queries have.
+          constexpr int kChains = NB == 1 ? 2 : 1;  // of dependent products: with two blocks they alternate
+          float acc[NB][kChains][4] = {};
+          uint4 kw[2][D / 64];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            const uint32_t w = e == 0 ? kw[nb][c].x : e == 1 ? kw[nb][c].y : e == 2 ? kw[nb][c].z : kw[nb][c].w;
-            mma16816(acc[nb], qa[4 * c + e], e4m3x2_to_f16x2(static_cast<uint16_t>(w)),
-                     e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)));
+          for (int hh = 0; hh < 2; ++hh) {
+            const int row = warp * kGroup + hh * 8 + n;
+            if constexpr (D == 128) {
+              kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t) ^ (row & 7)) << 4));
+              kw[hh][1] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t + 1) ^ (row & 7)) << 4));
+            } else {
+              kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
+            }
           }
-        }
-      }
-      uint32_t pa[4] = {0u, 0u, 0u, 0u};
-      float alpha[2] = {1.f, 1.f};
 #pragma unroll
-      for (int r = 0; r < kNR; ++r) {
-        const float f = qf[r] * sc.x;
-        float x[4];
+          for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = acc[e >> 1][2 * r + (e & 1)] * f;
-          if (part && !sees(p_row[r], j0 + (e >> 1) * 8 + 2 * t + (e & 1), a.window)) x[e] = -INFINITY;
-        }
-        const float mx = quad_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-        const float ms_new = fmaxf(ms[r], mx), mt_new = fmaxf(mt[r], mx + sc.y);
-        // a row that has seen nothing yet has both at -infinity
-        const float su = ms_new == -INFINITY ? 0.f : ms_new, tu = mt_new == -INFINITY ? 0.f : mt_new;
-        const float ls = ex2(ms[r] - su);
-        alpha[r] = ex2(mt[r] - tu);
-        const float f2 = ex2(fminf(su + sc.y - tu + kPShift, 126.f));
-        float p[4], sum = 0.f;
+            for (int e = 0; e < 4; ++e) {
+              uint32_t ka[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2(x[e] - su);
-          sum += p[e];
-        }
-        l[r] = fmaf(l[r], ls, sum);
-        ms[r] = ms_new;
-        mt[r] = mt_new;
-        pa[r] = pack_f16(p[0] * f2, p[1] * f2);
-        pa[2 + r] = pack_f16(p[2] * f2, p[3] * f2);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || (!kHalf && alpha[1] != 1.f))) {
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t w = e == 0 ? kw[hh][c].x : e == 1 ? kw[hh][c].y : e == 2 ? kw[hh][c].z : kw[hh][c].w;
+                ka[hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w));
+                ka[2 + hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+              }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          if constexpr (!kHalf) {
-            o[i][2] *= alpha[1];
-            o[i][3] *= alpha[1];
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816(acc[nb][e % kChains], ka, qb[nb][2 * (4 * c + e)], qb[nb][2 * (4 * c + e) + 1]);
+            }
           }
-        }
-      }
-      // O += P V: lane (n, t) takes channels [n D/8, (n + 1) D/8) of keys 2t, 2t+1, 2t+8, 2t+9
-      uint32_t vw[4][D / 32];
+          // x[nb][2 hh + e]: key n + 8 hh, row 2t + e, in log2 units
+          float x[NB][4];
+          bool over = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = warp * kGroup + 2 * t + (e & 1) + 8 * (e >> 1);
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(vb + row * 128 + ((n ^ (row & 7)) << 4));
-          vw[e][0] = w.x; vw[e][1] = w.y; vw[e][2] = w.z; vw[e][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(vb + row * 64 + (((n >> 1) ^ ((row >> 1) & 3)) << 4) +
-                                                          ((n & 1) << 3));
-          vw[e][0] = w.x; vw[e][1] = w.y;
-        }
-      }
-      if (part) {
-        // keys that a row does not see have weight 0, and 0 x NaN is NaN: here
-        // NaN codes are taken out, and rows that do see one are mended at the end
+          for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
+              const float f = qf[nb][e] * sc.x;
+              const float bar = fminf(ms[nb][e], mt[nb][e] - sc.y) + kSlack;
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                float v = acc[nb][0][2 * hh + e];
+                if constexpr (kChains == 2) v += acc[nb][1][2 * hh + e];
+                v *= f;
+                if (part && !sees(p_row[nb][e], j0 + n + 8 * hh, a.window)) v = -INFINITY;
+                x[nb][2 * hh + e] = v;
+                over = over || v > bar;
+              }
+            }
+          }
+          // The references only move when a weight would pass them by more
+          // than 2^8; until then weights above 1 are summed as they are.
+          if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float alpha[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float mx = column_max(fmaxf(x[nb][e], x[nb][2 + e]));
+                const float ms_new = fmaxf(ms[nb][e], mx), mt_new = fmaxf(mt[nb][e], mx + sc.y);
+                // a row that has seen nothing yet has both at -infinity
+                l[nb][e] *= ex2(ms[nb][e] - (ms_new == -INFINITY ? 0.f : ms_new));
+                alpha[e] = ex2(mt[nb][e] - (mt_new == -INFINITY ? 0.f : mt_new));
+                ms[nb][e] = ms_new;
+                mt[nb][e] = mt_new;
+              }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[nb][i][0] *= alpha[0];
+                o[nb][i][1] *= alpha[1];
+                o[nb][i][2] *= alpha[0];
+                o[nb][i][3] *= alpha[1];
+              }
+            }
+          }
+          uint32_t pb[NB][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float su = ms[nb][e] == -INFINITY ? 0.f : ms[nb][e];
+              const float tu = mt[nb][e] == -INFINITY ? 0.f : mt[nb][e];
+              const float f2 = ex2(fminf(su + sc.y - tu + kPShift, 126.f));
+              const float p0 = ex2(x[nb][e] - su), p1 = ex2(x[nb][2 + e] - su);
+              l[nb][e] += p0 + p1;
+              w[e] = p0 * f2;
+              w[2 + e] = p1 * f2;
+            }
+            pb[nb][0] = transpose8x8(pack_f16(w[0], w[1]));
+            pb[nb][1] = transpose8x8(pack_f16(w[2], w[3]));
+          }
+          // O^T += V^T P^T: lane (n, t) takes channels [n D/8, (n + 1) D/8) of
+          // keys 2t, 2t+1, 2t+8, 2t+9; an mma tile's rows n and n + 8 are two
+          // neighbouring channels
+          uint32_t vw[4][D / 32];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = warp * kGroup + 2 * t + (e & 1) + 8 * (e >> 1);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vb + row * 128 + ((n ^ (row & 7)) << 4));
+              vw[e][0] = w.x; vw[e][1] = w.y; vw[e][2] = w.z; vw[e][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(
+                  vb + row * 64 + (((n >> 1) ^ ((row >> 1) & 3)) << 4) + ((n & 1) << 3));
+              vw[e][0] = w.x; vw[e][1] = w.y;
+            }
+          }
+          if (part) {
+            // keys that a row does not see have weight 0, and 0 x NaN is NaN: here
+            // NaN codes are taken out, and rows that do see one are mended at the end
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                const uint32_t z = nan_bytes(vw[e][i]);
+                saw_nan = saw_nan || z != 0;
+                vw[e][i] &= ~z;
+              }
+            }
+          }
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
-            const uint32_t z = nan_bytes(vw[e][i]);
-            saw_nan = saw_nan || z != 0;
-            vw[e][i] &= ~z;
+            // byte pairs of two neighbouring keys, channel by channel
+            const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+            const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+            const uint32_t va[2][4] = {
+                {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
+                 e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))},
+                {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
+                 e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))}};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(o[nb][2 * i], va[0], pb[nb][0], pb[nb][1]);
+              mma16816(o[nb][2 * i + 1], va[1], pb[nb][0], pb[nb][1]);
+            }
+          }
+        }
+        mbar_arrive_warp(empty + 8 * st);
+      }
+      if (saw_nan) nan_flag[turn] = 1;
+
+      // ---------------------------------------------------------- join the four warps
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = nb * 8 + 2 * t + e;
+          const float sum = column_sum(l[nb][e]);
+          float* dst = so + (warp * R + row) * C::kPitch + n * (D / 8);
+          // o[nb][i][2 c + e] is channel n D/8 + 2 i + c of row 2t + e
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =
+                make_float4(o[nb][i][e], o[nb][i][2 + e], o[nb][i + 1][e], o[nb][i + 1][2 + e]);
+          if (n == 0) {
+            float* s4 = sst + (warp * R + row) * 4;
+            s4[0] = ms[nb][e];
+            s4[1] = mt[nb][e];
+            s4[2] = sum;
           }
         }
       }
+      named_bar_sync(1, 128);
+      // a wait that ran out: no results, but every warp goes through the same barriers
+      const bool dead = *abort_flag != 0;
+      const bool whole = tile == 0 && tile_end == sg.nt;
+      float x[kCols] = {}, sum = 0.f, m = -INFINITY;
+      if (!dead && g.r0 + wrow < g.rows) {
+        float mv = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        // byte pairs of two neighbouring keys, channel by channel
-        const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-        const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-        mma16816(o[4 * i], pa, e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01)));
-        mma16816(o[4 * i + 1], pa, e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
-                 e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16)));
-        mma16816(o[4 * i + 2], pa, e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23)));
-        mma16816(o[4 * i + 3], pa, e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
-                 e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16)));
+        for (int w = 0; w < 4; ++w) {
+          m = fmaxf(m, sst[(w * R + wrow) * 4]);
+          mv = fmaxf(mv, sst[(w * R + wrow) * 4 + 1]);
+        }
+        const float mu = m == -INFINITY ? 0.f : m, vu = mv == -INFINITY ? 0.f : mv;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float* s4 = sst + (w * R + wrow) * 4;
+          sum += s4[2] * ex2(s4[0] - mu);
+          const float f = ex2(s4[1] - vu);
+          const float* src = so + (w * R + wrow) * C::kPitch + c0;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) x[i] = fmaf(src[i], f, x[i]);
+        }
+        // sum = 0: the row saw no key
+        const float f = sum == 0.f ? 0.f : ex2(vu - mu - kPShift) / sum;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) x[i] *= f;
+        if (nan_flag[turn]) {
+          const int p = g.p0 + (g.r0 + wrow) / a.G;
+          for (int j = max((sg.t0 + tile) * kTile, g.lo); j < min((sg.t0 + tile_end) * kTile, g.hi); ++j) {
+            if (all_see(g, j & ~(kGroup - 1), a.window) || !sees(p, j, a.window)) continue;
+            const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
+            if (page < 0) continue;
+            const uint8_t* code = a.v_pages +
+                                  ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
+                                   (j & (a.batch.page_size - 1))) * D + c0;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if ((code[i] & 0x7f) == 0x7f) x[i] = __int_as_float(0x7fffffff);
+          }
+        }
+        const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
+        if (kCluster ? pieces == 1 : whole) {
+          store_row<D>(a, sg, h, g.r0 + wrow, c0, x, lse2);
+        } else if constexpr (kCluster) {
+          // this thread alone read warp 0's part of these channels: the piece's state takes its place
+          float* dst = so + wrow * C::kPitch + c0;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) dst[i] = x[i];
+        } else {
+          // piece 0 of the part continues an item, piece 1 begins one
+          const long long at = (static_cast<long long>(blockIdx.x) * 2 + (tile == 0 ? 1 : 0)) * R + wrow;
+          float* dst = a.part_o + at * D + c0;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          if (c0 == 0) a.part_lse[at] = lse2;
+        }
+        m = lse2;
+      }
+      named_bar_sync(1, 128);  // the states have been read
+      if (threadIdx.x == 0) nan_flag[turn] = 0;  // next raised two items on, past two more barriers
+      turn ^= 1;
+      if constexpr (kCluster) {
+        if (c0 == 0) sst[wrow * 4] = dead ? -INFINITY : m;
+      }
+      left -= tile_end - tile;
+      tile = 0;
+      ++item;
+    }
+    more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
+  }
+  if (*abort_flag && threadIdx.x == 0) *a.status = kStatusTimeout;
+  if constexpr (kCluster) {
+    // Join the pieces: every CTA of the cluster takes a share of the rows.
+    cluster_sync();
+    if (pieces > 1 && v1 > v0) {
+      const int own = static_cast<int>(v0 / sg.nt);
+      const int r = own % sg.rts * R + wrow;
+      if (wrow % pieces == rank && r < sg.rows && !*abort_flag) {
+        float m = -INFINITY, sum = 0.f, x[kCols] = {};
+        for (int i = 0; i < pieces; ++i) m = fmaxf(m, ld_cluster(cluster_addr(smem_u32(sst + wrow * 4), i)));
+        const float mu = m == -INFINITY ? 0.f : m;
+        for (int i = 0; i < pieces; ++i) {
+          const float w = ex2(ld_cluster(cluster_addr(smem_u32(sst + wrow * 4), i)) - mu);
+          const uint32_t src = cluster_addr(smem_u32(so + wrow * C::kPitch + c0), i);
+          sum += w;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) x[c] = fmaf(w, ld_cluster(src + 4 * c), x[c]);
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) x[c] *= f;
+        store_row<D>(a, sg, own / sg.rts, r, c0, x, sum == 0.f ? -INFINITY : m + log2f(sum));
       }
     }
-    mbar_arrive_warp(empty + 8 * st);
+    cluster_sync();  // no CTA ends while another reads its state
   }
-  if (saw_nan) *nan_flag = 1;
-
-  // -------------------------------------------------------------- join the four warps
-  named_bar_sync(1, 128);  // every warp is done with the ring
-  if (*abort_flag) {
-    if (threadIdx.x == 0) *a.status = kStatusTimeout;
-    return;  // all 128 threads alike: the flag is only raised by a wait, and all waits are over
-  }
-  float* so = reinterpret_cast<float*>(smem);               // [warp][row][kPitch]
-  float* sst = so + 4 * kRows * C::kPitch;                  // [warp][row][4]: m_s, m_t, l
-#pragma unroll
-  for (int r = 0; r < kNR; ++r) {
-    const int row = n + 8 * r;
-    const float sum = quad_sum(l[r]);
-    float* dst = so + (warp * kRows + row) * C::kPitch + t * (D / 4);
-    // o[i][2r + e] is channel (D/8) (2t + e) + i
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int i = 0; i < D / 8; i += 4)
-        *reinterpret_cast<float4*>(dst + e * (D / 8) + i) =
-            make_float4(o[i][2 * r + e], o[i + 1][2 * r + e], o[i + 2][2 * r + e], o[i + 3][2 * r + e]);
-    if (t == 0) {
-      float* st = sst + (warp * kRows + row) * 4;
-      st[0] = ms[r];
-      st[1] = mt[r];
-      st[2] = sum;
-    }
-  }
-  named_bar_sync(1, 128);
-  constexpr int kCols = D / 8;  // per thread, eight threads per row
-  const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * kCols;
-  if (g.r0 + row >= g.rows) return;
-  float m = -INFINITY, mv = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    m = fmaxf(m, sst[(w * kRows + row) * 4]);
-    mv = fmaxf(mv, sst[(w * kRows + row) * 4 + 1]);
-  }
-  const float mu = m == -INFINITY ? 0.f : m, vu = mv == -INFINITY ? 0.f : mv;
-  float sum = 0.f, x[kCols] = {};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float* st = sst + (w * kRows + row) * 4;
-    sum += st[2] * ex2(st[0] - mu);
-    const float f = ex2(st[1] - vu);
-    const float* src = so + (w * kRows + row) * C::kPitch + c0;
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) x[i] = fmaf(src[i], f, x[i]);
-  }
-  // sum = 0: the row saw no key
-  const float f = sum == 0.f ? 0.f : ex2(vu - mu - kPShift) / sum;
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) x[i] *= f;
-  const int qi = (g.r0 + row) / a.G, hd = h * a.G + (g.r0 + row) % a.G;
-  if (*nan_flag) {
-    const int p = g.p0 + qi;
-    for (int j = max(ta * kTile, g.lo); j < min(tb * kTile, g.hi); ++j) {
-      if (all_see(g, j & ~(kGroup - 1), a.window) || !sees(p, j, a.window)) continue;
-      const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
-      if (page < 0) continue;
-      const uint8_t* code = a.v_pages +
-                            ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
-                             (j & (a.batch.page_size - 1))) * D + c0;
-#pragma unroll
-      for (int i = 0; i < kCols; ++i)
-        if ((code[i] & 0x7f) == 0x7f) x[i] = __int_as_float(0x7fffffff);
-    }
-  }
-  if (g.active > 1) {
-    const long long at = (item * a.splits + split) * kRows + row;
-    float* dst = a.part_o + at * D + c0;
-#pragma unroll
-    for (int i = 0; i < kCols; i += 4)
-      *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-    if (c0 == 0) a.part_lse[at] = sum == 0.f ? -INFINITY : m + log2f(sum);
-    return;
-  }
-  const long long at = static_cast<long long>(s.row0 + qi) * a.Hq + hd;
-  uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c0);
-#pragma unroll
-  for (int i = 0; i < kCols; i += 8)
-    dst[i / 8] = make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
-                            pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
-  if (c0 == 0) a.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (m + log2f(sum));
 }
 
-// Joins the splits' states of 16 rows: LSE = log sum_s exp(LSE_s), O = sum_s
-// exp(LSE_s - LSE) O_s ("FlashAttention -- the same attention, made
-// memory-aware", section 03). Eight threads per row.
-template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const AttnArgs a) {
-  constexpr int kCols = D / 8;
+// Joins the pieces of an item that parts c, c + 1, ... of the streaming form
+// share: LSE = log sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s ("FlashAttention
+// -- the same attention, made memory-aware", section 03). Block c has something
+// to do when part c begins an item that it does not end. kShare warps per row,
+// each taking every kShare-th run of kRun parts with their states all in
+// flight: one warp and runs of four for a batch of many items, which have few
+// parts each and want small blocks, many to an SM; up to four warps and runs of
+// 16 for few items of many parts.
+template <int D, int NB, int kShare>
+__global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const AttnArgs a, int parts) {
+  constexpr int R = 8 * NB, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
+  __shared__ float s_x[R][kShare][D];
+  __shared__ float s_m[R][kShare], s_sum[R][kShare];
   grid_dep_wait();
   grid_dep_launch();
-  const long long item = blockIdx.x;
-  const int rt = static_cast<int>(item % a.row_tiles);
-  const long long bh = item / a.row_tiles;
-  const int h = static_cast<int>(bh % a.Hkv), seq = static_cast<int>(bh / a.Hkv);
-  const PagedSeq s = paged_seq(a.batch, seq, a.status);
-  if (rt * kRows >= s.n * a.G) return;
-  const RowTile g = row_tile(a, s, rt);
-  if (g.active <= 1) return;  // written by the split itself
-  const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * kCols;
-  if (g.r0 + row >= g.rows) return;
-  const float* pl = a.part_lse + item * a.splits * kRows + row;
-  const float* po = a.part_o + (item * a.splits * kRows + row) * D + c0;
-  float m = -INFINITY;
-  for (int i = 0; i < g.active; ++i) m = fmaxf(m, pl[i * kRows]);
-  const float mu = m == -INFINITY ? 0.f : m;
-  float sum = 0.f, x[kCols] = {};
-  for (int i = 0; i < g.active; ++i) {
-    const float w = ex2(pl[i * kRows] - mu);
-    sum += w;
-    const float* src = po + static_cast<long long>(i) * kRows * D;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wrow = warp / kShare, share = warp % kShare;
+  const long long units = all_units<R>(a);
+  const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
+  if (u0 >= u1) return;
+  long long base;
+  const int seq = find_seq<R>(a, u1 - 1, &base);
+  const SeqGeo sg = seq_geo<R>(a, seq);
+  const int per = sg.nt + kItemUnits;
+  const int item = static_cast<int>((u1 - 1 - base) / per);
+  const long long first = base + static_cast<long long>(item) * per + kItemUnits;  // unit of the item's tile 0
+  const long long end = u1 - first;                                                  // tiles up to here
+  if (u0 > first || end <= 0 || end >= sg.nt) return;
+  const int r = item % sg.rts * R + wrow;
+  const bool live = r < sg.rows;
+  // part k > c holds tiles of the item when it starts before the item's end; it continues it (piece 0)
+  float m = -INFINITY, sum = 0.f, x[kCols] = {};
+  for (int k0 = c + share * kRun; live && k0 < parts; k0 += kShare * kRun) {
+    const int k = k0 + lane;
+    const long long s0 = lane < kRun && k < parts ? part_start(units, parts, k) : units;
+    const bool in = lane < kRun && k < parts && s0 - first < sg.nt;
+    if (!__any_sync(0xffffffffu, in)) break;
+    const bool on = in && s0 < part_start(units, parts, k + 1);  // (with fewer units than parts some are empty)
+    const long long at = (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * R + wrow;
+    const float ls = on ? a.part_lse[at] : -INFINITY;
+    float v[kRun][kCols];
 #pragma unroll
-    for (int c = 0; c < kCols; c += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src + c);
-      x[c] = fmaf(w, v.x, x[c]);
-      x[c + 1] = fmaf(w, v.y, x[c + 1]);
-      x[c + 2] = fmaf(w, v.z, x[c + 2]);
-      x[c + 3] = fmaf(w, v.w, x[c + 3]);
+    for (int j = 0; j < kRun; ++j) {
+      // a part without a state: part c's stands in, with weight 0
+      const int kj = __shfl_sync(0xffffffffu, on ? k : c, j);
+      const float* src = a.part_o + ((static_cast<long long>(kj) * 2 + (kj == c ? 1 : 0)) * R + wrow) * D + lane * kCols;
+      if constexpr (kCols == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[j][0] = f.x; v[j][1] = f.y;
+      }
+    }
+    float mx = fmaxf(m, ls);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float mu = mx == -INFINITY ? 0.f : mx, alpha = ex2(m - mu);
+    const float w = on ? ex2(ls - mu) : 0.f;
+    sum *= alpha;
+    m = mx;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) x[i] *= alpha;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const bool has = __shfl_sync(0xffffffffu, on ? 1 : 0, j) != 0;
+      sum += wj;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) x[i] = has ? fmaf(wj, v[j][i], x[i]) : x[i];
     }
   }
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) s_x[wrow][share][lane * kCols + i] = x[i];
+  if (lane == 0) {
+    s_m[wrow][share] = m;
+    s_sum[wrow][share] = sum;
+  }
+  __syncthreads();
+  if (share != 0 || !live) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kShare; ++i) m = fmaxf(m, s_m[wrow][i]);
+  const float mu = m == -INFINITY ? 0.f : m;
+  sum = 0.f;
+#pragma unroll
+  for (int c2 = 0; c2 < kCols; ++c2) x[c2] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kShare; ++i) {
+    const float w = ex2(s_m[wrow][i] - mu);
+    sum = fmaf(s_sum[wrow][i], w, sum);
+#pragma unroll
+    for (int c2 = 0; c2 < kCols; ++c2) x[c2] = fmaf(s_x[wrow][i][lane * kCols + c2], w, x[c2]);
+  }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const long long at = static_cast<long long>(sg.s.row0 + r / a.G) * a.Hq + item / sg.rts * a.G + r % a.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + at * D + lane * kCols);
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) x[i] *= f;
-  const long long at = static_cast<long long>(s.row0 + (g.r0 + row) / a.G) * a.Hq + h * a.G + (g.r0 + row) % a.G;
-  uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c0);
-#pragma unroll
-  for (int i = 0; i < kCols; i += 8)
-    dst[i / 8] = make_uint4(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]),
-                            pack_bf16(x[i + 4], x[i + 5]), pack_bf16(x[i + 6], x[i + 7]));
-  if (c0 == 0) a.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (m + log2f(sum));
+  for (int i = 0; i < kCols; i += 2) dst[i / 2] = pack_bf16(x[i] * f, x[i + 1] * f);
+  if (lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (m + log2f(sum));
 }
 
-template <int D>
-int launch_rows(const PagedPool& pool, const AttnArgs& a, long long items, cudaStream_t stream) {
-  using C = Cfg<D>;
+template <int D, int NB, bool kCluster>
+int launch_rows(const PagedPool& pool, const AttnArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  using C = Cfg<D, NB>;
   CUtensorMap mk, mv;
   const int box = pool.page_size < kTile ? pool.page_size : kTile;
   const int blocks = pool.num_pages * pool.num_heads;
-  if (!make_map_pages(&mk, pool.k_pages, blocks, pool.page_size, D, box) ||
-      !make_map_pages(&mv, pool.v_pages, blocks, pool.page_size, D, box))
+  if (!make_map_pages(&mk, pool.k_pages, blocks, pool.page_size, D, box, true) ||
+      !make_map_pages(&mv, pool.v_pages, blocks, pool.page_size, D, box, true))
     return -3;
-  const bool half = a.batch.max_q * a.G <= 8;
-  auto kern = half ? paged_rows_kernel<D, true> : paged_rows_kernel<D, false>;
-  // attribute slots 20 to 23
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, 20 + (D == 128 ? 2 : 0) + (half ? 1 : 0)))
-    return -3;
-  const long long grid = items * a.splits;
-  if (grid > 0x7fffffffLL) return -1;
-  cudaError_t e = launch_overlapped(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), C::kSmemBytes,
-                                    stream, mk, mv, a);
+  auto kern = paged_rows_kernel<D, NB, kCluster>;
+  // attribute slots 20 to 27
+  constexpr int kSlot = 20 + (D == 128 ? 4 : 0) + (NB == 1 ? 2 : 0) + (kCluster ? 1 : 0);
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, kSlot)) return -3;
+  const dim3 grid(static_cast<unsigned>(plan.ctas)), block(kThreads);
+  cudaError_t e;
+  // The streaming form fills every SM's shared memory and does not start under
+  // the kernel before it: on SMs whose shared memory that kernel had set up
+  // smaller, fewer of its CTAs would fit for the whole run (B = 8, 32 heads,
+  // 8192 keys, one call after another: 119 us overlapped, 92 us not).
+  if (kCluster)
+    e = launch_with(kern, grid, block, C::kSmemBytes, true, plan.cluster, stream, mk, mv, a);
+  else
+    e = launch_with(kern, grid, block, C::kSmemBytes, false, 1, stream, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
-  if (a.splits > 1) {
-    e = launch_overlapped(paged_merge_kernel<D>, dim3(static_cast<unsigned>(items)), dim3(128), 0, stream, a);
+  if (!kCluster && plan.ctas > 1) {
+    // fewer items than SMs: several parts to most of them
+    constexpr int kShare = 4 / NB;
+    auto join = plan.items < plan.ctas / C::kCtasPerSm ? paged_join_kernel<D, NB, kShare> : paged_join_kernel<D, NB, 1>;
+    const int threads = 256 * NB * (plan.items < plan.ctas / C::kCtasPerSm ? kShare : 1);
+    e = launch_overlapped(join, dim3(static_cast<unsigned>(plan.ctas - 1)), dim3(threads), 0, stream, a,
+                          static_cast<int>(plan.ctas));
     if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
   }
   return 0;
 }
 
+template <int D>
+int launch_rows_d(const PagedPool& pool, const AttnArgs& a, const PagedPlan& plan, cudaStream_t stream) {
+  if (plan.cluster > 0)
+    return plan.rows == 8 ? launch_rows<D, 1, true>(pool, a, plan, stream) : launch_rows<D, 2, true>(pool, a, plan, stream);
+  return plan.rows == 8 ? launch_rows<D, 1, false>(pool, a, plan, stream) : launch_rows<D, 2, false>(pool, a, plan, stream);
+}
+
 }  // namespace
 
-PagedSplit paged_attn_split(const PagedPool& pool, const PagedBatchDev& batch, int Hq, int max_kv,
-                            int n_splits, int sms) {
-  PagedSplit r{};
-  const int G = Hq / pool.num_heads;
-  r.row_tiles = static_cast<int>((static_cast<long long>(batch.max_q) * G + kRows - 1) / kRows);
-  const long long items = static_cast<long long>(batch.B) * pool.num_heads * r.row_tiles;
-  const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + kTile - 1) / kTile : 1;
-  long long per = tiles;  // tiles per split
-  if (n_splits > 0) {
-    per = (tiles + n_splits - 1) / n_splits;
-  } else {
-    const long long slots = 2LL * sms;
-    const long long total = items * tiles;
-    per = total <= slots ? 1 : total < 8 * slots ? (total + slots - 1) / slots
-                                                 : (total + 3 * slots - 1) / (3 * slots);
-    if (total >= 8 * slots && per < 8) per = 8;
-    if (per > tiles) per = tiles;
+PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, const int Hq, int max_kv, int sms) {
+  PagedPlan r{};
+  const long long rows = static_cast<long long>(batch.max_q) * (Hq / pool.num_heads);
+  if (rows > 64) {
+    r.chunk = true;
+    return r;
   }
-  r.split_tiles = static_cast<int>(per);
-  r.splits = static_cast<int>((tiles + per - 1) / per);
-  r.workspace_bytes =
-      r.splits > 1 ? static_cast<size_t>(items) * r.splits * kRows * (pool.d + 1) * sizeof(float) : 0;
+  r.rows = rows <= 8 ? 8 : 16;
+  r.row_tiles = static_cast<int>((rows + r.rows - 1) / r.rows);
+  const long long items = static_cast<long long>(batch.B) * pool.num_heads * r.row_tiles;
+  r.items = items;
+  const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + kTile - 1) / kTile : 1;
+  const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
+  // The cluster form while every CTA of a cluster of up to eight has a slot and
+  // at most eight tiles.
+  long long want = 1;
+  while (want < 8 && 2 * want < tiles) want *= 2;
+  if (items * want <= slots && tiles <= 8 * want) {
+    r.cluster = static_cast<int>(want);
+    r.ctas = items * want;
+    return r;
+  }
+  r.ctas = slots;
+  r.workspace_bytes = static_cast<size_t>(slots) * 2 * r.rows * (pool.d + 1) * sizeof(float);
   return r;
 }
 
 int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p,
-                      const PagedSplit& split, void* workspace, cudaStream_t stream) {
+                      const PagedPlan& plan, void* workspace, cudaStream_t stream) {
+  if (plan.chunk) return launch_paged_chunk(pool, batch, p, stream);
   AttnArgs a{};
   a.batch = batch;
   a.q = static_cast<const __nv_bfloat16*>(p.q);
@@ -625,16 +1030,14 @@ int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const P
   a.Hkv = pool.num_heads;
   a.G = p.Hq / pool.num_heads;
   a.window = p.window;
-  a.row_tiles = split.row_tiles;
-  a.splits = split.splits;
-  a.split_tiles = split.split_tiles;
+  a.row_tiles = plan.row_tiles;
+  a.cluster = plan.cluster;
   // scale 0 (uniform weights) runs as a tiny positive scale, as in the forward
   const float sl2 = p.scale * kLog2e;
   a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
-  const long long items = static_cast<long long>(batch.B) * pool.num_heads * split.row_tiles;
   a.part_o = static_cast<float*>(workspace);
-  a.part_lse = a.part_o + (split.splits > 1 ? items * split.splits * kRows * pool.d : 0);
-  return pool.d == 64 ? launch_rows<64>(pool, a, items, stream) : launch_rows<128>(pool, a, items, stream);
+  a.part_lse = a.part_o + (plan.workspace_bytes > 0 ? plan.ctas * 2 * plan.rows * pool.d : 0);
+  return pool.d == 64 ? launch_rows_d<64>(pool, a, plan, stream) : launch_rows_d<128>(pool, a, plan, stream);
 }
 
 }  // namespace fa

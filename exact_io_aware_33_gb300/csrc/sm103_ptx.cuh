@@ -362,6 +362,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, bo
          | ((M >> 4) << 24);            // M / 16
 }
 
+// The same with f16 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle. `addr` is the shared
 // address of the (1024-byte aligned) swizzle atom the operand starts in,
 // possibly advanced along K inside the atom; lbo / sbo are byte offsets.

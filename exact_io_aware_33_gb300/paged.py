@@ -17,11 +17,23 @@ tensors of other streams must be ready, and kept, by the caller.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
 _PAGE_SIZES = (16, 32, 64, 128)
+
+torch = None  # set, like _library, with the first object: the package loads neither torch nor libfa.so by itself
+_library = _fail = None
+
+
+def _load():
+    global torch, _library, _fail
+    if torch is None:
+        import torch as t
+
+        from . import _check, load_library
+        load_library()
+        torch, _library, _fail = t, load_library, _check
 
 
 class _CacheStruct(ctypes.Structure):
@@ -37,7 +49,6 @@ class _BatchStruct(ctypes.Structure):
 
 
 def _require(t, name, dtype, dim, device=None):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -54,7 +65,7 @@ class PagedCache:
     """A pool of e4m3 pages [num_pages, num_heads, page_size, d] with fp32 scales [num_pages, num_heads]."""
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales):
-        import torch
+        _load()
         _require(k_pages, "k_pages", torch.float8_e4m3fn, 4)
         dev = k_pages.device
         _require(v_pages, "v_pages", torch.float8_e4m3fn, 4, dev)
@@ -77,6 +88,7 @@ class PagedCache:
         self.num_pages, self.num_heads, self.page_size, self.d = P, H, page, d
         self.device = dev
         self._index = dev.index
+        self._scale = 1.0 / math.sqrt(d)
         self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
                                     v_scales.data_ptr(), P, H, page, d)
         self._address = ctypes.addressof(self._struct)
@@ -84,7 +96,7 @@ class PagedCache:
     @classmethod
     def empty(cls, num_pages: int, num_heads: int, page_size: int, d: int, device="cuda"):
         """A new pool. Its contents do not matter: only what was appended is ever read."""
-        import torch
+        _load()
         shape = (num_pages, num_heads, page_size, d)
         pages = [torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
         scales = [torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
@@ -98,7 +110,7 @@ class PagedBatch:
     their lengths (0: what the block table can hold); both are host numbers, no tensor is read back."""
 
     def __init__(self, block_table, kv_lens, cu_q=None, max_q: int = 1, max_kv: int = 0):
-        import torch
+        _load()
         _require(block_table, "block_table", torch.int32, 2)
         dev = block_table.device
         _require(kv_lens, "kv_lens", torch.int32, 1, dev)
@@ -119,6 +131,7 @@ class PagedBatch:
         self.block_table, self.kv_lens, self.cu_q = block_table, kv_lens, cu_q
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
         self.device = dev
+        self._index = dev.index
         self._made = (-1, None, 0)
 
     def _for_rows(self, T: int):
@@ -135,7 +148,7 @@ class PagedBatch:
         return made
 
 
-def _rows(t, name, heads, d, device, torch):
+def _rows(t, name, heads, d, device):
     """Checks a packed [T, heads, d] tensor whose tokens may lie apart; returns its token stride."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
@@ -154,11 +167,12 @@ def _rows(t, name, heads, d, device, torch):
     return st[0]
 
 
-def _context(index, stream, torch):
-    """Where the call allocates and launches: the tensors' device, and `stream` where one is given."""
+def _elsewhere(index, stream):
+    """None when the call may allocate and launch as things stand; else the context to do it in: `stream`
+    where one is given, the tensors' device where it is not the current one."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         return torch.cuda.device(index)
     return None
 
@@ -169,109 +183,107 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
 
     ``rope`` is (cos, sin), fp32 [max_pos, rot / 2] each, or None. Without ``q`` the result is None. Rows
     of a new ``q_out`` behind the last sequence, or without a position, are not written."""
-    import torch
-    from . import _check, load_library
+    index = cache._index
+    elsewhere = _elsewhere(index, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return fa_paged_append(cache, batch, k, v, q, rope, interleaved, q_out)
     dev, d = cache.device, cache.d
-    if batch.device != dev:
+    if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    ks = _rows(k, "k", cache.num_heads, d, dev, torch)
-    vs = _rows(v, "v", cache.num_heads, d, dev, torch)
+    ks = _rows(k, "k", cache.num_heads, d, dev)
+    vs = _rows(v, "v", cache.num_heads, d, dev)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"v has {v.shape[0]} rows, k {T}")
-    cos = sin = None
-    max_pos = rot = 0
+    cos = sin = max_pos = rot = Hq = qp = qs = op = os_ = 0
     if rope is not None:
-        cos, sin = rope
-        _require(cos, "cos", torch.float32, 2, dev)
-        _require(sin, "sin", torch.float32, 2, dev)
-        if cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+        c, s = rope
+        _require(c, "cos", torch.float32, 2, dev)
+        _require(s, "sin", torch.float32, 2, dev)
+        max_pos, rot = c.shape
+        rot *= 2
+        if c.shape != s.shape or not c.is_contiguous() or not s.is_contiguous():
             raise ValueError("cos and sin must be contiguous and of one shape")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    made = batch._for_rows(T)
-    Hq = qs = os_ = 0
-    context = _context(cache._index, stream, torch)
-    with context or contextlib.nullcontext():
-        if q is not None:
-            qs = _rows(q, "q", 0, d, dev, torch)
-            Hq = q.shape[1]
-            if q.shape[0] != T:
-                raise ValueError(f"q has {q.shape[0]} rows, k {T}")
-            if q_out is None:
-                q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-                os_ = Hq * d
-            else:
-                os_ = _rows(q_out, "q_out", Hq, d, dev, torch)
-                if q_out.shape[0] != T:
-                    raise ValueError(f"q_out has {q_out.shape[0]} rows, q {T}")
-        rc = load_library().fa_paged_append(
-            cache._address, made[2], k.data_ptr(), ks, v.data_ptr(), vs, q.data_ptr() if Hq else 0, qs,
-            q_out.data_ptr() if Hq else 0, os_, Hq, cos.data_ptr() if rot else 0, sin.data_ptr() if rot else 0,
-            max_pos, rot, 1 if interleaved else 0, torch._C._cuda_getCurrentRawStream(cache._index))
+        if rot:
+            cos, sin = c.data_ptr(), s.data_ptr()
+    if q is not None:
+        qs = _rows(q, "q", 0, d, dev)
+        Hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError(f"q has {q.shape[0]} rows, k {T}")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            os_ = Hq * d
+        else:
+            os_ = _rows(q_out, "q_out", Hq, d, dev)
+            if q_out.shape[0] != T:
+                raise ValueError(f"q_out has {q_out.shape[0]} rows, q {T}")
+        if Hq:
+            qp, op = q.data_ptr(), q_out.data_ptr()
+    else:
+        q_out = None
+    rc = _library().fa_paged_append(cache._address, batch._for_rows(T)[2], k.data_ptr(), ks, v.data_ptr(), vs, qp, qs,
+                                    op, os_, Hq, cos, sin, max_pos, rot, 1 if interleaved else 0,
+                                    torch._C._cuda_getCurrentRawStream(index))
     if rc:
-        _check(rc, "fa_paged_append")
-    return q_out if q is not None else None
+        _fail(rc, "fa_paged_append")
+    return q_out
 
 
-def fa_paged_attn_num_splits(cache: PagedCache, batch: PagedBatch, Hq: int, T: int | None = None,
-                             n_splits: int = 0) -> int:
-    from . import load_library
-    made = batch._for_rows(batch.B if T is None else T)
-    return load_library().fa_paged_attn_num_splits(cache._address, made[2], Hq, n_splits)
-
-
-def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int, n_splits: int = 0) -> int:
+def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int) -> int:
     """Workspace bytes of fa_paged_attn with these arguments; they do not depend on the number of rows."""
-    from . import load_library
-    made = batch._for_rows(batch.B)
-    return load_library().fa_paged_attn_workspace_bytes(cache._address, made[2], Hq, n_splits)
+    elsewhere = _elsewhere(cache._index, None)
+    if elsewhere is not None:
+        with elsewhere:
+            return fa_paged_attn_workspace_bytes(cache, batch, Hq)
+    return _library().fa_paged_attn_workspace_bytes(cache._address, batch._for_rows(batch.B)[2], Hq)
 
 
 def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scale: float | None = None,
-                  n_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
+                  out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [T, Hq, d] over the batch's cached tokens; (o bf16 [T, Hq, d], lse fp32 [T, Hq]).
 
     Rows of a new ``out`` behind the last sequence are not written. Without ``workspace`` one is allocated
     where the call needs it."""
-    import torch
-    from . import _check, load_library
+    index = cache._index
+    elsewhere = _elsewhere(index, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return fa_paged_attn(cache, batch, q, window, scale, out, lse, workspace)
     dev, d = cache.device, cache.d
-    if batch.device != dev:
+    if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    qs = _rows(q, "q", 0, d, dev, torch)
+    qs = _rows(q, "q", 0, d, dev)
     T, Hq, _ = q.shape
-    made = batch._for_rows(T)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    lib = load_library()
-    context = _context(cache._index, stream, torch)
-    with context or contextlib.nullcontext():
-        if out is None:
-            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        elif out.shape != q.shape or not out.is_contiguous():
+    struct = batch._for_rows(T)[2]
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _rows(out, "out", Hq, d, dev)
+        if out.shape[0] != T or not out.is_contiguous():
             raise ValueError(f"out must be contiguous [{T}, {Hq}, {d}]")
-        else:
-            _rows(out, "out", Hq, d, dev, torch)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        else:
-            _require(lse, "lse", torch.float32, 2, dev)
-            if tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
-                raise ValueError(f"lse must be contiguous [{T}, {Hq}]")
-        if workspace is None:
-            need = lib.fa_paged_attn_workspace_bytes(cache._address, made[2], Hq, n_splits)
-            ws = 0
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                ws = workspace.data_ptr()
-        else:
-            if workspace.device != dev or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be contiguous on {dev}")
-            need = workspace.numel() * workspace.element_size()
-            ws = workspace.data_ptr() if need else 0
-        rc = lib.fa_paged_attn(cache._address, made[2], q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq,
-                               window, scale, n_splits, ws, need,
-                               torch._C._cuda_getCurrentRawStream(cache._index))
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _require(lse, "lse", torch.float32, 2, dev)
+        if tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{T}, {Hq}]")
+    lib = _library()
+    if workspace is None:
+        ws = 0
+        need = lib.fa_paged_attn_workspace_bytes(cache._address, struct, Hq)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        need = workspace.numel() * workspace.element_size()
+        ws = workspace.data_ptr() if need else 0
+    rc = lib.fa_paged_attn(cache._address, struct, q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq, window,
+                           cache._scale if scale is None else scale, ws, need,
+                           torch._C._cuda_getCurrentRawStream(index))
     if rc:
-        _check(rc, "fa_paged_attn")
+        _fail(rc, "fa_paged_attn")
     return out, lse

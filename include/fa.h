@@ -370,23 +370,20 @@ int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, co
  *   q        : in,  bf16 [T, Hq, d], rows q_stride elements apart (a multiple of 8)
  *   o        : out, bf16 [T, Hq, d] contiguous
  *   lse      : out, fp32 [T, Hq], natural-log log-sum-exp
- *   n_splits : parts of the key range, joined by a second kernel with the
- *              rule of fa_decode_splitkv; <= 0 chooses from the sizes and the
- *              device's SM count
- *   workspace: at least fa_paged_attn_workspace_bytes(cache, batch, Hq,
- *              n_splits) bytes (0: may be NULL), 256-byte aligned; nothing
- *              in it outlives the call. Two calls in flight at once need two.
+ *   workspace: at least fa_paged_attn_workspace_bytes(cache, batch, Hq)
+ *              bytes (0: may be NULL), 256-byte aligned; nothing in it
+ *              outlives the call. Two calls in flight at once need two.
+ * Long key ranges are divided among the SMs and the parts' states joined with
+ * the rule of fa_decode_splitkv; how depends on the lengths, so the same
+ * inputs give the same bits.
  * A row that sees no key gives O = 0 and LSE = -inf. What lies in masked
  * places (slots behind a length, keys outside the window) has no influence,
- * NaN codes included. The library is free to sum in any order: results of
- * different n_splits agree up to rounding; the same call gives the same bits.
+ * NaN codes included.
  */
 int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
-                  long long q_stride, void* o, float* lse, int Hq, int window, float scale, int n_splits,
+                  long long q_stride, void* o, float* lse, int Hq, int window, float scale,
                   void* workspace, size_t ws_bytes, void* cuda_stream);
-int fa_paged_attn_num_splits(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq, int n_splits);
-size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq,
-                                     int n_splits);
+size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq);
 
 /* Static description of a return code. Never NULL. */
 const char* fa_strerror(int code);

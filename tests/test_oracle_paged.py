@@ -101,9 +101,9 @@ def _batch(**kw):
     return _BatchStruct(**f)
 
 
-def _attn(lib, c, b, q=P, stride=4 * 64, o=P, lse=P, Hq=4, window=0, scale=0.125, n_splits=1, ws=0, bytes_=0):
+def _attn(lib, c, b, q=P, stride=4 * 64, o=P, lse=P, Hq=4, window=0, scale=0.125, ws=0, bytes_=0):
     return lib.fa_paged_attn(ctypes.addressof(c) if c else 0, ctypes.addressof(b) if b else 0, q, stride, o, lse, Hq,
-                             window, scale, n_splits, ws, bytes_, 0)
+                             window, scale, ws, bytes_, 0)
 
 
 def _append(lib, c, b, k=P, ks=2 * 64, v=P, vs=2 * 64, q=P, qs=4 * 64, qo=P, qos=4 * 64, Hq=4, cos=P, sin=P,
@@ -148,7 +148,7 @@ def test_cache_and_batch_are_checked_on_the_host(lib, c, b, code):
 def test_missing_structs_are_refused(lib):
     assert _attn(lib, None, _batch()) == fa.FA_ERR_INVALID
     assert _append(lib, _cache(), None) == fa.FA_ERR_INVALID
-    assert lib.fa_paged_attn_workspace_bytes(0, 0, 4, 0) == 0
+    assert lib.fa_paged_attn_workspace_bytes(0, 0, 4) == 0
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -156,10 +156,10 @@ def test_missing_structs_are_refused(lib):
     (dict(scale=math.nan), fa.FA_ERR_INVALID), (dict(scale=-1.0), fa.FA_ERR_INVALID), (dict(q=0), fa.FA_ERR_INVALID),
     (dict(q=P + 2), fa.FA_ERR_INVALID), (dict(o=0), fa.FA_ERR_INVALID), (dict(lse=0), fa.FA_ERR_INVALID),
     (dict(stride=4 * 64 - 8), fa.FA_ERR_INVALID), (dict(stride=4 * 64 + 4), fa.FA_ERR_INVALID),
-    (dict(n_splits=4), fa.FA_ERR_WORKSPACE), (dict(n_splits=4, ws=P + 16, bytes_=1 << 30), fa.FA_ERR_WORKSPACE),
-    (dict(n_splits=4, ws=P, bytes_=64), fa.FA_ERR_WORKSPACE)])
+    (dict(), fa.FA_ERR_WORKSPACE), (dict(ws=P + 16, bytes_=1 << 30), fa.FA_ERR_WORKSPACE),
+    (dict(ws=P, bytes_=64), fa.FA_ERR_WORKSPACE)])
 def test_attention_arguments_are_checked_on_the_host(lib, kw, code):
-    assert _attn(lib, _cache(page_size=128), _batch(), **kw) == code
+    assert _attn(lib, _cache(), _batch(max_pages=100000), **kw) == code
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -172,16 +172,14 @@ def test_append_arguments_are_checked_on_the_host(lib, kw, code):
     assert _append(lib, _cache(), _batch(), **kw) == code
 
 
-def test_split_counts_and_workspace(lib):
-    c, b = _cache(page_size=64, num_heads=2), _batch(B=3, T=3, cu_q=0, max_q=1, max_pages=100)
-    ca, ba = ctypes.addressof(c), ctypes.addressof(b)
-    for want in (1, 2, 7, 100, 1000):
-        n = lib.fa_paged_attn_num_splits(ca, ba, 8, want)
-        assert 1 <= n <= min(want, 100)
-        need = lib.fa_paged_attn_workspace_bytes(ca, ba, 8, want)
-        assert need == (0 if n == 1 else 3 * 2 * n * 16 * (64 + 1) * 4)  # 16 rows per (sequence, key head, split)
-    assert lib.fa_paged_attn_num_splits(ca, ba, 7, 0) == 0               # heads do not divide
-    assert lib.fa_paged_attn_num_splits(ca, ba, 8, 0) >= 1
+def test_workspace(lib):
+    c, b = _cache(page_size=64, num_heads=2), _batch(B=3, T=3, cu_q=0, max_q=1, max_pages=100000)
+    need = lib.fa_paged_attn_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), 8)
+    # the states of two pieces of 8 rows (d + 1 floats each) for several CTAs on each of at least 100 SMs
+    assert need % (2 * 8 * (64 + 1) * 4) == 0 and need >= 200 * 2 * 8 * (64 + 1) * 4
+    b.max_kv = 100   # so little that a cluster takes each sequence and head
+    assert lib.fa_paged_attn_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), 8) == 0
+    assert lib.fa_paged_attn_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), 7) == 0  # heads do not divide
 
 
 def test_binding_refuses_cpu_tensors():

@@ -101,51 +101,59 @@ def check_attn(w, cu, o, lse, q, scale, window=0):
 
 # ------------------------------------------------------------------ attention
 DECODE = [
-    # lens, Hq, Hkv, d, page, splits
-    ([1], 4, 4, 64, 16, 1),
-    ([1, 2, 15, 16, 17], 8, 2, 128, 16, 0),
-    ([64, 63, 65, 300], 6, 2, 64, 32, 0),
-    ([1000, 0, 127, 129], 8, 1, 128, 64, 0),         # a sequence of nothing; eight rows
-    ([1000, 513], 32, 2, 128, 128, 0),               # sixteen rows
-    ([700], 40, 1, 64, 16, 3),                       # three row tiles
-    ([4096, 5, 2049], 12, 12, 64, 64, 0),
-    ([2500, 1], 5, 1, 128, 32, 7),
-    ([333], 3, 3, 128, 16, 1000),                    # more splits asked than tiles
+    # lens, Hq, Hkv, d, page
+    ([1], 4, 4, 64, 16),
+    ([1, 2, 15, 16, 17], 8, 2, 128, 16),
+    ([64, 63, 65, 300], 6, 2, 64, 32),
+    ([1000, 0, 127, 129], 8, 1, 128, 64),         # a sequence of nothing; eight rows
+    ([1000, 513], 32, 2, 128, 128),               # sixteen rows
+    ([700], 40, 1, 64, 16),                       # three row tiles
+    ([4096, 5, 2049], 12, 12, 64, 64),
+    ([2500, 1], 5, 1, 128, 32),
+    ([333], 3, 3, 128, 16),
+    ([0, 0], 4, 2, 64, 16),
 ]
+STREAM = 1 << 20  # a length bound that large always divides the work among the SMs
 
 
-@pytest.mark.parametrize("lens,Hq,Hkv,d,page,splits", DECODE)
-def test_one_token_per_sequence(lens, Hq, Hkv, d, page, splits):
-    w = World(lens, Hkv, page, d, seed=sum(lens) + Hq).fill()
+@pytest.mark.parametrize("max_kv", [0, STREAM])
+@pytest.mark.parametrize("lens,Hq,Hkv,d,page", DECODE)
+def test_one_token_per_sequence(lens, Hq, Hkv, d, page, max_kv):
+    w = World(lens, Hkv, page, d, seed=sum(lens) + Hq, max_pages=STREAM // page if max_kv else None).fill()
     q = bf16(w.rng, len(lens), Hq, d)
     cu = np.arange(len(lens) + 1)
-    batch = fa.PagedBatch(torch.from_numpy(w.table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
-    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), n_splits=splits)
+    batch = fa.PagedBatch(torch.from_numpy(w.table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                          max_kv=max_kv)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
     done()
     check_attn(w, cu, o, lse, q, 1 / math.sqrt(d))
 
 
 SEVERAL = [
-    # lens, news, Hq, Hkv, d, page, window, splits
-    ([100, 40], [5, 1], 12, 4, 64, 16, 0, 0),
-    ([200, 200, 33], [3, 0, 8], 8, 2, 128, 32, 0, 0),          # a sequence without rows
-    ([70, 3], [70, 3], 4, 4, 128, 64, 0, 1),                   # fresh prompts
-    ([130, 257], [129, 200], 4, 2, 64, 128, 0, 2),
-    ([5, 2], [8, 4], 4, 1, 64, 16, 0, 0),                      # more rows than tokens: the first see nothing
-    ([500, 90], [40, 90], 8, 2, 128, 16, 17, 0),               # windows
-    ([500, 90], [4, 1], 8, 8, 64, 64, 1, 0),                   # ... of the own key alone
-    ([1500], [2], 16, 1, 128, 64, 1000, 4),
-    ([1100, 1], [300, 1], 6, 6, 64, 32, 64, 3),
-    ([640], [256], 8, 1, 128, 64, 0, 0),                       # 2048 rows of one key head
+    # lens, news, Hq, Hkv, d, page, window
+    ([100, 40], [5, 1], 12, 4, 64, 16, 0),
+    ([200, 200, 33], [3, 0, 8], 8, 2, 128, 32, 0),          # a sequence without rows
+    ([70, 3], [70, 3], 4, 4, 128, 64, 0),                   # fresh prompts
+    ([130, 257], [129, 200], 4, 2, 64, 128, 0),
+    ([5, 2], [8, 4], 4, 1, 64, 16, 0),                      # more rows than tokens: the first see nothing
+    ([0, 40], [4, 2], 4, 1, 64, 16, 0),                     # ... and all of a sequence's
+    ([500, 90], [40, 90], 8, 2, 128, 16, 17),               # windows
+    ([500, 90], [4, 1], 8, 8, 64, 64, 1),                   # ... of the own key alone
+    ([1500], [2], 16, 1, 128, 64, 1000),
+    ([1100, 1], [300, 1], 6, 6, 64, 32, 64),
+    ([640], [256], 8, 1, 128, 64, 0),                       # 2048 rows of one key head
+    ([200] * 40, [1, 2, 3, 0] * 10, 4, 2, 64, 16, 0),       # more sequences than a warp has lanes
 ]
 
 
-@pytest.mark.parametrize("lens,news,Hq,Hkv,d,page,window,splits", SEVERAL)
-def test_several_tokens_per_sequence(lens, news, Hq, Hkv, d, page, window, splits):
-    w = World(lens, Hkv, page, d, seed=sum(lens) + sum(news) + window).fill()
-    cu, batch = w.batch(news, max_kv=max(lens))
+@pytest.mark.parametrize("max_kv", [0, STREAM])
+@pytest.mark.parametrize("lens,news,Hq,Hkv,d,page,window", SEVERAL)
+def test_several_tokens_per_sequence(lens, news, Hq, Hkv, d, page, window, max_kv):
+    w = World(lens, Hkv, page, d, seed=sum(lens) + sum(news) + window,
+              max_pages=STREAM // page if max_kv else None).fill()
+    cu, batch = w.batch(news, max_kv=max_kv)
     q = bf16(w.rng, int(cu[-1]), Hq, d)
-    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), window=window, n_splits=splits)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), window=window)
     done()
     check_attn(w, cu, o, lse, q, 1 / math.sqrt(d), window)
 
@@ -202,16 +210,17 @@ def test_queries_of_any_size(size):
     assert (want[1] - got[1]).abs().max().item() <= 5e-4
 
 
-@pytest.mark.parametrize("news,splits", [([1], 1), ([1], 3), ([20], 1), ([150], 2)])
-def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, splits):
+@pytest.mark.parametrize("max_pages", [13, STREAM // 16])
+@pytest.mark.parametrize("news", [[1], [20], [150]])
+def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, max_pages):
     n = 200
-    w = World([n], 1, 16, 64, seed=7).fill()
+    w = World([n], 1, 16, 64, seed=7, max_pages=max_pages).fill()
     rows = news[0]
     for j, c in ((n - 1, 5), (n - rows // 2 - 1, 60)):   # the last key, and one that half of the rows see
         w.oracle.codes["v"][w.table[0, j // 16], 0, j % 16, c] = 0x7F if c == 5 else 0xFF
     cu, batch = w.batch(news)
     q = bf16(w.rng, rows, 4, 64)
-    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), n_splits=splits)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
     done()
     assert torch.isfinite(lse).all()
     o = o.float().cpu().numpy()
@@ -574,7 +583,7 @@ def test_indices_out_of_range_are_reported_and_touch_nothing():
 
 
 def test_arguments_that_the_binding_refuses():
-    w = World([20, 20], 2, 16, 64, seed=42, max_pages=13).fill()   # room for four tiles of 64 keys
+    w = World([20, 20], 2, 16, 64, seed=42, max_pages=100000).fill()   # a long table: a workspace is needed
     cache = w.to_gpu()
     cu, batch = w.batch([2, 1])
     q = bf16(w.rng, 3, 4, 64).cuda()
@@ -590,7 +599,7 @@ def test_arguments_that_the_binding_refuses():
     with pytest.raises(fa.FAError):
         fa.fa_paged_attn(cache, batch, q, window=-1)
     with pytest.raises(fa.FAError):
-        fa.fa_paged_attn(cache, batch, q, n_splits=2, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        fa.fa_paged_attn(cache, batch, q, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         fa.fa_paged_append(cache, batch, k, k[:2])
     with pytest.raises(ValueError):

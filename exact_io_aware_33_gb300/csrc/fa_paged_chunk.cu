@@ -54,12 +54,14 @@ constexpr float kPShift = 6.f;   // P is held as 2^6 P
 
 // What the softmax and the widening need to know of a tile.
 struct TileInfo {
-  float ek;             // 2^(largest exponent of the keys' scales)
-  float ev;             // log2 of the values' largest scale (its exponent)
-  int by_group;         // 1: scales applied group by group
-  int pad;
-  float kr[kGroups];    // scale of each group's keys relative to ek
-  float vr[kGroups];    // the same of the values (by_group: log2 of the scale); negative kr: group absent
+  float ek;               // 2^(largest exponent of the keys' scales)
+  float ev;               // log2 of the values' largest scale (its exponent)
+  int by_group;           // 1: scales applied group by group
+  int absent;             // 1: some group of 16 keys has no page to read
+  uint32_t kh[kGroups];   // what a group's widened codes are multiplied by (f16 pair): scale / largest
+  uint32_t vh[kGroups];
+  float kr[kGroups];      // by_group: the keys' scale relative to ek (below 0: group absent)
+  float vr[kGroups];      // and log2 of the values' scale
 };
 
 template <int D>
@@ -208,51 +210,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- TMA warp
       tma_prefetch_map(&tmK);
       tma_prefetch_map(&tmV);
+      // Lane i looks up the i-th of 32 groups of 16 keys (four tiles): its
+      // page, then its scales. The next four tiles' loads are under way while
+      // the present ones are issued.
       const int box_rows = min(a.batch.page_size, kBN), boxes = kBN / box_rows, per_box = box_rows / 16;
-      // lanes 0..7: the tile's groups of 16 keys
-      int page = -1;
-      float sk = 0.f, sv = 0.f;
-      bool ok = true, missing = false;
-      int k_copies = 0, v_copies = 0;
+      int n_page = -1;
+      float n_sk = 1.f, n_sv = 1.f;
+      bool n_want = false;
       auto look = [&](int step) {
-        const int j0 = (j_first + step) * kBN + (lane & 7) * 16;
-        page = -1;
-        missing = false;
-        if (lane < 8 && step < n_stream && j0 < key_end && j0 + 16 > key_lo) {
-          page = paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status);
-          missing = page < 0;
-          if (page >= 0) {
-            const long long at = static_cast<long long>(page) * a.Hkv + h;
-            sk = a.k_scales[at];
-            sv = a.v_scales[at];
-          }
+        const int j0 = (j_first + step) * kBN + lane * 16;
+        n_want = step + (lane >> 3) < n_stream && j0 < key_end && j0 + 16 > key_lo;
+        n_page = n_want ? paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status) : -1;
+      };
+      auto scales = [&]() {
+        n_sk = n_sv = 1.f;
+        if (n_page >= 0) {
+          const long long at = static_cast<long long>(n_page) * a.Hkv + h;
+          n_sk = a.k_scales[at];
+          n_sv = a.v_scales[at];
         }
       };
+      bool ok = true;
+      int k_copies = 0, v_copies = 0;
       look(0);
-      for (int jj = 0; jj < n_stream; ++jj) {
-        const bool on = page >= 0;
-        const int cur = page;
-        int bp[8];
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          bp[b] = -1;
-          if (b < boxes)
-            for (int q = 0; q < per_box; ++q) bp[b] = max(bp[b], __shfl_sync(0xffffffffu, cur, b * per_box + q));
-        }
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int b = 0; b < 8; ++b) bytes += bp[b] >= 0 ? static_cast<uint32_t>(box_rows * D) : 0u;
-        auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(full, bytes);
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (bp[b] >= 0)
-                tma_load_3d(dst + b * box_rows * D, map, full, 0, (b * box_rows) & (a.batch.page_size - 1),
-                            bp[b] * a.Hkv + h);
-          }
-        };
-        // the tile's scales
+      scales();
+      for (int base4 = 0; base4 < n_stream && ok; base4 += 4) {
+        const int page = n_page;
+        const float sk = n_sk, sv = n_sv;
+        const bool on = page >= 0, missing = n_want && !on;
+        look(base4 + 4);
+        // the four tiles' scales, eight lanes each
         const bool pow2 = (__float_as_uint(sk) & 0x7fffffu) == 0 && (__float_as_uint(sv) & 0x7fffffu) == 0 &&
                           sk > 0.f && sv > 0.f && sk < INFINITY && sv < INFINITY;
         const int ke = on ? exponent_of(sk) : -1000, ve = on ? exponent_of(sv) : -1000;
@@ -264,31 +251,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, d));
           vmin = min(vmin, __shfl_xor_sync(0xffffffffu, vmin, d));
         }
-        const bool odd = (on && !pow2) || missing;
-        const bool by_group = __any_sync(0xffffffffu, odd) || kmax - kmin > 8 || vmax - vmin > 8;
+        const uint32_t mine = 0xffu << (lane & 24);
+        const bool by_group = (__ballot_sync(0xffffffffu, (on && !pow2) || missing) & mine) != 0 ||
+                              kmax - kmin > 8 || vmax - vmin > 8;
+        const bool absent = (__ballot_sync(0xffffffffu, !on) & mine) != 0;
         kmax = min(max(kmax, -126), 126);
         vmax = min(max(vmax, -126), 126);
-        if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawKEmpty), (jj - 1) & 1, abort_flag);
-        if (!ok) break;
-        if (lane < 8) {
-          TileInfo& ti = infos[jj % kInfos];
-          const float ek = pow2i(kmax);
-          ti.kr[lane] = !on ? -1.f : by_group ? sk / ek : pow2i(ke - kmax);
-          ti.vr[lane] = by_group ? log2f(sv) : on ? pow2i(ve - vmax) : 0.f;
-          if (lane == 0) {
-            ti.ek = ek;
-            ti.ev = static_cast<float>(vmax);
-            ti.by_group = by_group ? 1 : 0;
+        const float ek = pow2i(kmax);
+        const float kh = by_group ? 1.f : on ? pow2i(ke - kmax) : 0.f, vh = by_group ? 1.f : on ? pow2i(ve - vmax) : 0.f;
+        const float kr = !on ? -1.f : sk / ek, vr = log2f(sv);
+        for (int i = 0; i < 4 && base4 + i < n_stream; ++i) {
+          const int jj = base4 + i;
+          if (i == 2) scales();
+          // lane b: the page of box b of the tile
+          int bp = __shfl_sync(0xffffffffu, page, 8 * i + (lane & 7) * per_box % 8);
+          for (int q = 1; q < per_box; ++q) bp = max(bp, __shfl_sync(0xffffffffu, page, 8 * i + ((lane & 7) * per_box + q) % 8));
+          const bool box = lane < boxes && bp >= 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * static_cast<uint32_t>(box_rows * D);
+          const int slot = (lane * box_rows) & (a.batch.page_size - 1), blk = bp * a.Hkv + h;
+          if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawKEmpty), (jj - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (box)
+            tma_load_3d(base + C::kRawKOff + lane * box_rows * D, &tmK, bar(C::kBarRawKFull), 0, slot, blk);
+          if ((lane >> 3) == i) {
+            TileInfo& ti = infos[jj % kInfos];
+            const int g = lane & 7;
+            ti.kh[g] = pack_f16(kh, kh);
+            ti.vh[g] = pack_f16(vh, vh);
+            ti.kr[g] = kr;
+            ti.vr[g] = vr;
+            if (g == 0) {
+              ti.ek = ek;
+              ti.ev = static_cast<float>(vmax);
+              ti.by_group = by_group ? 1 : 0;
+              ti.absent = absent ? 1 : 0;
+            }
           }
+          __syncwarp();
+          // (bytes that have landed already count as well: the phase cannot end before this arrival)
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull), bytes);
+          ++k_copies;
+          if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (jj - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (box)
+            tma_load_3d(base + C::kRawVOff + lane * box_rows * D, &tmV, bar(C::kBarRawVFull), 0, slot, blk);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawVFull), bytes);
+          ++v_copies;
         }
-        __syncwarp();
-        load(&tmK, base + C::kRawKOff, bar(C::kBarRawKFull));
-        ++k_copies;
-        look(jj + 1);  // while the values' buffer is waited for
-        if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (jj - 1) & 1, abort_flag);
-        if (!ok) break;
-        load(&tmV, base + C::kRawVOff, bar(C::kBarRawVFull));
-        ++v_copies;
+        if (base4 + 2 >= n_stream) break;  // (fewer than three tiles in this batch: none follows)
       }
       // Let the copies in flight land before the CTA can end, whoever gives up:
       // each buffer's last phase (over already unless someone did).
@@ -333,44 +344,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = t == 0 ? a0 : a1, y = t == 0 ? b0 : b1;
         return (jj >= x && jj < y) ? jj - x : -1;
       };
-      ensure_k(0);
-      if (ok) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (step_of(t, 0) == 0) issue_s(t, 0);
-        mma_commit_w(bar(C::kBarKEmpty + 0));
-      }
-      // P overwrites S: each tile's next QK^T is issued after its P.V
-      for (int jj = 0; jj < n_stream && ok; ++jj) {
-        ok = mbar_wait_w(bar(C::kBarVFull + jj % C::kStages), (jj / C::kStages) & 1, abort_flag);
-        tc_fence_after();
-#pragma unroll
+      // P overwrites S: each tile's next QK^T is issued after its P.V. Step
+      // jj: per tile, the P.V of key tile jj, then the QK^T of jj + 1 (the
+      // first step, -1, has none of the former). One copy of the code for
+      // both tiles: the loops of the four roles share the instruction cache.
+#pragma unroll 1
+      for (int jj = -1; jj < n_stream && ok; ++jj) {
+        if (jj >= 0) {
+          ok = mbar_wait_w(bar(C::kBarVFull + jj % C::kStages), (jj / C::kStages) & 1, abort_flag);
+          tc_fence_after();
+        }
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           const int u = step_of(t, jj);
-          if (!ok || u < 0) continue;
-          ok = mbar_wait_w(bar(C::kBarPFull + t), u & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(t, jj, u == 0);
-          if (jj + 1 < (t == 0 ? b0 : b1)) {
+          if (ok && u >= 0) {
+            ok = mbar_wait_w(bar(C::kBarPFull + t), u & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, jj, u == 0);
+            if (jj + 1 >= (t == 0 ? b0 : b1)) {
+              mma_commit_w(bar(C::kBarOFinal + t));
+              mbar_arrive_warp(bar(C::kBarOFinal + t));
+            }
+          }
+          if (ok && step_of(t, jj + 1) >= 0) {
             ensure_k(jj + 1);
             if (!ok) break;
             issue_s(t, jj + 1);
-          } else {
-            mma_commit_w(bar(C::kBarOFinal + t));
-            mbar_arrive_warp(bar(C::kBarOFinal + t));
           }
         }
         if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {  // a tile whose range starts at step jj + 1
-          if (!ok || step_of(t, jj + 1) != 0) continue;
-          ensure_k(jj + 1);
-          if (!ok) break;
-          issue_s(t, jj + 1);
-        }
-        if (!ok) break;
-        mma_commit_w(bar(C::kBarVEmpty + jj % C::kStages));
+        if (jj >= 0) mma_commit_w(bar(C::kBarVEmpty + jj % C::kStages));
         if (jj + 1 < n_stream) mma_commit_w(bar(C::kBarKEmpty + (jj + 1) % C::kStages));
       }
       // let every MMA this warp issued finish before TMEM is released
@@ -380,72 +384,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kWidenWarp) {
     regs_decrease<88>();
     // ------------------------------------------------------------ widening
-    // 16 codes per thread and step: two 16-byte units of the widened row. The
-    // eight lanes of a store phase hold 8 (d = 64: 4) chunks of one row (two
-    // rows); those of the upper half store their odd unit first, which keeps
-    // the phase's banks apart.
+    // Eight codes per thread and step become one 16-byte unit of the widened
+    // row. The eight lanes of a store phase hold the eight units of one row,
+    // which the swizzle spreads over all banks; a thread's rows are 16 apart,
+    // so its swizzle and all offsets are fixed.
     const int tid = threadIdx.x - 32 * kWidenWarp;
-    constexpr int kCpr = D / 16;            // 16-byte chunks of codes per row
-    constexpr int kRowsPerStep = 128 / kCpr;
-    constexpr int kSteps = kBN / kRowsPerStep;
-    const int row_in = tid / kCpr, chunk = tid % kCpr;
-    const int swap = D == 128 ? (chunk >> 2) : (row_in & 1);
+    const int unit = tid & 7, row0 = tid >> 3;
+    constexpr int kSteps = kBN / 16;
+    const uint32_t src0 = static_cast<uint32_t>(row0 * D + unit * 8);
+    const uint32_t dst0 = static_cast<uint32_t>(row0 * 128 + ((unit ^ (row0 & 7)) << 4));
     bool ok = true;
     bool saw_nan = false;
-    auto widen = [&](const uint8_t* raw, uint8_t* out, const TileInfo& ti, bool values, int key0) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int row = i * kRowsPerStep + row_in;
-        const int grp = row >> 4;  // one per warp
-        uint4 w = *reinterpret_cast<const uint4*>(raw + (row * kCpr + chunk) * 16);
-        const float kr = ti.kr[grp], r = values ? ti.vr[grp] : kr;
-        uint32_t ratio = 0x3c003c00u;
-        if (!ti.by_group) ratio = pack_f16(r, r);
-        if (kr < 0.f) w = make_uint4(0, 0, 0, 0);  // keys without a page: nothing was loaded
-        if (values) {
-          const int j0 = key0 + grp * 16;
-          if (j0 + 15 > full_hi || j0 < full_lo) {
-            // 0 x NaN is NaN: codes that some row does not see must not hold any
-            uint32_t z[4] = {nan_bytes(w.x), nan_bytes(w.y), nan_bytes(w.z), nan_bytes(w.w)};
-            saw_nan = saw_nan || (z[0] | z[1] | z[2] | z[3]) != 0;
-            w = make_uint4(w.x & ~z[0], w.y & ~z[1], w.z & ~z[2], w.w & ~z[3]);
-          }
-        }
-        uint32_t f[8];
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f[2 * q] = hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(in[q])), ratio);
-          f[2 * q + 1] = hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(in[q] >> 16)), ratio);
-        }
-        // channels 16 chunk ..: 64-column chunk, units 2 (chunk & 3) and + 1 of its row
-        uint8_t* dst = out + (chunk >> 2) * C::kChunkBytes + row * 128;
-        const int u0 = 2 * (chunk & 3), x = row & 7;
-        const uint4 first = make_uint4(f[0], f[1], f[2], f[3]), second = make_uint4(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint4*>(dst + (((u0 + swap) ^ x) << 4)) = swap ? second : first;
-        *reinterpret_cast<uint4*>(dst + (((u0 + 1 - swap) ^ x) << 4)) = swap ? first : second;
-      }
-    };
-    for (int jj = 0; jj < n_stream && ok; ++jj) {
-      const int st = jj % C::kStages;
-      const uint32_t ph = ((jj / C::kStages) + 1) & 1;
+#pragma unroll 1
+    for (int w2 = 0; w2 < 2 * n_stream && ok; ++w2) {  // keys and values in turn
+      const int jj = w2 >> 1, st = jj % C::kStages;
+      const bool values = w2 & 1;
       const TileInfo& ti = infos[jj % kInfos];
       const int key0 = (j_first + jj) * kBN;
-      ok = mbar_wait_w(bar(C::kBarRawKFull), jj & 1, abort_flag);
-      if (ok && jj >= C::kStages) ok = mbar_wait_w(bar(C::kBarKEmpty + st), ph, abort_flag);
+      const uint8_t* raw = smem + (values ? C::kRawVOff : C::kRawKOff) + src0;
+      uint8_t* out = smem + (values ? C::kVOff : C::kKOff) + st * C::kTileBytes + dst0;
+      ok = mbar_wait_w(bar(values ? C::kBarRawVFull : C::kBarRawKFull), jj & 1, abort_flag);
+      if (ok && jj >= C::kStages)
+        ok = mbar_wait_w(bar((values ? C::kBarVEmpty : C::kBarKEmpty) + st), ((jj / C::kStages) + 1) & 1, abort_flag);
       if (!ok) break;
-      widen(smem + C::kRawKOff, smem + C::kKOff + st * C::kTileBytes, ti, false, key0);
-      fence_async_smem();
-      mbar_arrive_warp(bar(C::kBarKFull + st));
-      mbar_arrive_warp(bar(C::kBarRawKEmpty));
-      ok = mbar_wait_w(bar(C::kBarRawVFull), jj & 1, abort_flag);
-      if (ok && jj >= C::kStages) ok = mbar_wait_w(bar(C::kBarVEmpty + st), ph, abort_flag);
-      if (!ok) break;
-      widen(smem + C::kRawVOff, smem + C::kVOff + st * C::kTileBytes, ti, true, key0);
+      const uint32_t* ratios = values ? ti.vh : ti.kh;
+      // Values of keys that some row does not see: 0 x NaN is NaN, so no code
+      // of theirs may be one. Groups without a page: nothing was loaded.
+      const bool check = ti.absent || (values && (key0 + kBN - 1 > full_hi || key0 < full_lo));
+      // Codes are fetched eight units ahead of the stores: the compiler cannot
+      // move a shared load above a shared store itself, and one unit at a time
+      // is all latency (115 cycles each, against about 12 instructions).
+      constexpr int kUnits = kSteps * C::kChunks, kBatch = 8;
+      uint2 w[kUnits];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
+#pragma unroll
+      for (int b = 0; b < kUnits; b += kBatch) {
+        if (b + kBatch < kUnits) {
+#pragma unroll
+          for (int i = b + kBatch; i < b + 2 * kBatch; ++i)
+            w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
+        }
+        uint32_t ratio[kBatch / C::kChunks];
+#pragma unroll
+        for (int i = 0; i < kBatch / C::kChunks; ++i) ratio[i] = ratios[b / C::kChunks + i];
+        if (check) {
+#pragma unroll
+          for (int i = b; i < b + kBatch; ++i) {
+            const int g = i / C::kChunks;
+            if (ti.kr[g] < 0.f) w[i] = make_uint2(0, 0);
+            if (values && (key0 + g * 16 + 15 > full_hi || key0 + g * 16 < full_lo)) {
+              const uint2 z = make_uint2(nan_bytes(w[i].x), nan_bytes(w[i].y));
+              saw_nan = saw_nan || (z.x | z.y) != 0;
+              w[i] = make_uint2(w[i].x & ~z.x, w[i].y & ~z.y);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = b; i < b + kBatch; ++i) {
+          const uint32_t r = ratio[(i - b) / C::kChunks];
+          *reinterpret_cast<uint4*>(out + i / C::kChunks * 2048 + i % C::kChunks * C::kChunkBytes) =
+              make_uint4(hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x)), r),
+                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x >> 16)), r),
+                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y)), r),
+                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y >> 16)), r));
+        }
+      }
       if (saw_nan) *nan_flag = 1;
       fence_async_smem();
-      mbar_arrive_warp(bar(C::kBarVFull + st));
-      mbar_arrive_warp(bar(C::kBarRawVEmpty));
+      mbar_arrive_warp(bar((values ? C::kBarVFull : C::kBarKFull) + st));
+      mbar_arrive_warp(bar(values ? C::kBarRawVEmpty : C::kBarRawKEmpty));
     }
   } else {
     regs_increase<184>();
@@ -518,34 +527,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 128; ++c)
           if (c >= lim_hi || c < lim_lo) x[c] = -INFINITY;
       }
-      float alpha;     // of the accumulator
-      bool moved;
-      uint32_t pk[32];
-      if (!by_group) {
-        const float m_tile = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96)) * sl2;
-        moved = m_tile > fminf(ms, mt - ev) + kSlack;
-        const float ms_old = ms, mt_old = mt;
-        if (moved) {
-          ms = fmaxf(ms, m_tile);
-          mt = fmaxf(mt, m_tile + ev);
-        }
-        const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
-        alpha = moved ? ex2(mt_old - tu) : 1.f;
-        const float als = moved ? ex2(ms_old - su) : 1.f;
+      const float m_tile = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96)) * sl2;
+      const float ms_old = ms, mt_old = mt;
+      bool moved = m_tile > fminf(ms, mt - ev) + kSlack;
+      if (moved && !by_group) {
+        ms = fmaxf(ms, m_tile);
+        mt = fmaxf(mt, m_tile + ev);
+      }
+      float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
+      // P = 2^(x sl2 + ev - m_t + 6); the denominator's terms are P 2^(m_t - ev - 6 - m_s),
+      // unless the two references lie too far apart for P not to underflow
+      if (!by_group && !__any_sync(0xffffffffu, su + ev - tu < -60.f)) {
         const float add = ev - tu + kPShift;
         const float2 sl2x2 = make_float2(sl2, sl2), add2 = make_float2(add, add);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        // P = 2^(x sl2 + ev - m_t + 6); the denominator's terms are P 2^(m_t - ev - 6 - m_s),
-        // unless that lies too far from 1 for P not to have underflowed
-        const bool apart = su + ev - tu < -60.f;
-        const float fl = ex2(tu - ev - kPShift - su);
-        float l_tile = 0.f;
-        if (__any_sync(0xffffffffu, apart)) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) l_tile += ex2(fmaf(x[c], sl2, -su));
-        }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const float2 e2 = __ffma2_rn(make_float2(x[64 * hf + 2 * c], x[64 * hf + 2 * c + 1]), sl2x2, add2);
@@ -556,46 +554,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st32(tS + 32 * hf, pk);
         }
-        l = fmaf(l, als, apart ? l_tile : ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * fl);
+        const float als = moved ? ex2(ms_old - su) : 1.f;
+        l = fmaf(l, als, ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * ex2(tu - ev - kPShift - su));
       } else {
-        // scales group by group: x in log2 units, numerators and denominators apart
-        float m_s = -INFINITY, m_t = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float f = sl2 * ti.kr[g];
-          const bool absent = ti.kr[g] < 0.f;  // no page: no key of it takes part
-          float m = -INFINITY;
+        // Group by group from tensor memory again, with the group's scales,
+        // numerators and denominators apart. P of group g takes columns
+        // 8 g .. 8 g + 7, which no later group's S lies in.
+        auto group = [&](int g, float (&y)[16], float* vlog) {
+          uint32_t w[16];
+          tmem_ld16(tS + 16 * g, w);
+          tmem_ld_wait(w);
+          const float kr = by_group ? ti.kr[g] : 1.f;
+          *vlog = by_group ? ti.vr[g] : ev;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            x[16 * g + c] = absent ? -INFINITY : x[16 * g + c] * f;
-            m = fmaxf(m, x[16 * g + c]);
+            const int j = key0 + 16 * g + c;
+            // (no page: no key of the group takes part)
+            y[c] = kr >= 0.f && sees(p, j, a.window) ? __uint_as_float(w[c]) * (sl2 * kr) : -INFINITY;
           }
-          m_s = fmaxf(m_s, m);
-          m_t = fmaxf(m_t, m + ti.vr[g]);
+        };
+        float vlog;
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+          float y[16], m = -INFINITY;
+          group(g, y, &vlog);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) m = fmaxf(m, y[c]);
+          ms = fmaxf(ms, m);
+          mt = fmaxf(mt, m + vlog);
         }
-        const float ms_old = ms, mt_old = mt;
-        ms = fmaxf(ms, m_s);
-        mt = fmaxf(mt, m_t);
-        moved = ms != ms_old || mt != mt_old;
-        const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
-        alpha = ex2(mt_old - tu);
+        moved = true;
+        su = ms == -INFINITY ? 0.f : ms;
+        tu = mt == -INFINITY ? 0.f : mt;
         l *= ex2(ms_old - su);
+#pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+          float y[16];
+          uint32_t pk[8];
+          group(g, y, &vlog);
+          const float add = vlog - tu + kPShift;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int e = 64 * hf + 2 * c;
-            const float add = ti.vr[e >> 4] - tu + kPShift;
-            l += ex2(x[e] - su) + ex2(x[e + 1] - su);
-            pk[c] = pack_f16(ex2(x[e] + add), ex2(x[e + 1] + add));
+          for (int c = 0; c < 8; ++c) {
+            l += ex2(y[2 * c] - su) + ex2(y[2 * c + 1] - su);
+            pk[c] = pack_f16(ex2(y[2 * c] + add), ex2(y[2 * c + 1] + add));
           }
-          tmem_st32(tS + 32 * hf, pk);
+          tmem_st8(tS + 8 * g, pk);
         }
       }
+      const float alpha = moved ? ex2(mt_old - tu) : 1.f;  // of the accumulator
       // O is settled: this tile's S was committed after the previous P.V
       if (u > 0 && __any_sync(0xffffffffu, moved)) {
         const float2 al2 = make_float2(alpha, alpha);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + c * 32, o);
@@ -627,31 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
         const float f = l == 0.f ? 0.f : ex2(tu - su - kPShift) / l;
-        const bool mend = *nan_flag != 0;
         // as in the forward: 32 rows x 64 columns at a time through this
         // warp's part of the Q tile (free by now), so that rows leave as whole lines
         uint8_t* blk = q_tile + (warp & 3) * 4096;
         uint8_t* mine = blk + lane * 128;
-#pragma unroll
+#pragma unroll 1
         for (int hh = 0; hh < D / 64; ++hh) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + hh * 64 + c * 32, o);
             tmem_ld_wait(o);
-            if (mend && live) {
-              for (int j = max(a.window > 0 ? p - a.window + 1 : 0, 0); j <= p; ++j) {
-                const int j0 = j & ~15;
-                if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
-                const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
-                if (page < 0) continue;
-                const uint8_t* code = a.v_pages + ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
-                                                   (j & (a.batch.page_size - 1))) * D + hh * 64 + c * 32;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if ((code[e] & 0x7f) == 0x7f) o[e] = 0x7fffffffu;
-              }
-            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t w[4];
@@ -674,6 +670,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (live) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (su + log2f(l));
+        if (*nan_flag && live) {
+          // a NaN code was taken out of a tile that not every row sees: put it into the rows that do
+#pragma unroll 1
+          for (int j = max(a.window > 0 ? p - a.window + 1 : 0, 0); j <= p; ++j) {
+            const int j0 = j & ~15;
+            if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
+            const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
+            if (page < 0) continue;
+            const uint8_t* code = a.v_pages + ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
+                                               (j & (a.batch.page_size - 1))) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; ++c)
+              if ((code[c] & 0x7f) == 0x7f) a.o[at * D + c] = __float2bfloat16(__int_as_float(0x7fffffff));
+          }
+        }
       }
     }
   }

@@ -22,18 +22,20 @@ import math
 
 _PAGE_SIZES = (16, 32, 64, 128)
 
-torch = None  # set, like _library, with the first object: the package loads neither torch nor libfa.so by itself
-_library = _fail = None
+# Set with the first object: the package loads neither torch nor libfa.so by itself. The functions are
+# bound here once because a step's small calls are bound by what the host does per call.
+torch = _lib = _fail = _empty = _bf16 = _raw_stream = _current = None
 
 
 def _load():
-    global torch, _library, _fail
+    global torch, _lib, _fail, _empty, _bf16, _raw_stream, _current
     if torch is None:
         import torch as t
 
         from . import _check, load_library
-        load_library()
-        torch, _library, _fail = t, load_library, _check
+        _lib, _fail, _empty, _bf16 = load_library(), _check, t.empty, t.bfloat16
+        _raw_stream, _current = t._C._cuda_getCurrentRawStream, t._C._cuda_getDevice
+        torch = t
 
 
 class _CacheStruct(ctypes.Structure):
@@ -49,16 +51,18 @@ class _BatchStruct(ctypes.Structure):
 
 
 def _require(t, name, dtype, dim, device=None):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dim and (
+            t.device == device if device is not None else t.is_cuda):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 class PagedCache:
@@ -148,33 +152,30 @@ class PagedBatch:
         return made
 
 
-def _rows(t, name, heads, d, device):
-    """Checks a packed [T, heads, d] tensor whose tokens may lie apart; returns its token stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != d or (heads and shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [T, {heads or 'heads'}, {d}]")
-    st = t.stride()
-    if st[2] != 1 or (st[1] != d and shape[1] != 1):
-        raise ValueError(f"the heads and channels of {name} must lie side by side")
-    if shape[0] <= 1:
-        return shape[1] * d  # one row: whatever its stride says
-    return st[0]
+def _stride(t, name, rows, heads, d, device):
+    """Checks a packed [rows, heads, d] tensor whose rows may lie apart (0: any number of them); the row stride."""
+    shape, st = t.shape, t.stride()
+    if (t.dtype is not _bf16 or t.device != device or len(shape) != 3 or shape[2] != d or st[2] != 1
+            or (st[1] != d and shape[1] != 1) or (rows and shape[0] != rows) or (heads and shape[1] != heads)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+        if t.dtype is not _bf16:
+            raise TypeError(f"{name} must be {_bf16}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if len(shape) == 3 and shape[2] == d and (not rows or shape[0] == rows) and (not heads or shape[1] == heads):
+            raise ValueError(f"the heads and channels of {name} must lie side by side")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows or 'T'}, {heads or 'heads'}, {d}]")
+    return st[0] if shape[0] > 1 else shape[1] * d  # (one row: whatever its stride says)
 
 
-def _elsewhere(index, stream):
-    """None when the call may allocate and launch as things stand; else the context to do it in: `stream`
-    where one is given, the tensors' device where it is not the current one."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if torch._C._cuda_getDevice() != index:
-        return torch.cuda.device(index)
-    return None
+def _elsewhere(device, stream):
+    """Where a call allocates and launches when not as things stand: `stream`, or the tensors' own device."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, expected {device}")
+    return torch.cuda.stream(stream)
 
 
 def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=None, interleaved: bool = False,
@@ -184,48 +185,43 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
     ``rope`` is (cos, sin), fp32 [max_pos, rot / 2] each, or None. Without ``q`` the result is None. Rows
     of a new ``q_out`` behind the last sequence, or without a position, are not written."""
     index = cache._index
-    elsewhere = _elsewhere(index, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or _current() != index:
+        with _elsewhere(cache.device, stream):
             return fa_paged_append(cache, batch, k, v, q, rope, interleaved, q_out)
-    dev, d = cache.device, cache.d
+    dev, d, H = cache.device, cache.d, cache.num_heads
     if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    ks = _rows(k, "k", cache.num_heads, d, dev)
-    vs = _rows(v, "v", cache.num_heads, d, dev)
+    ks = _stride(k, "k", 0, H, d, dev)
     T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"v has {v.shape[0]} rows, k {T}")
+    vs = _stride(v, "v", T, H, d, dev) if T else 0
+    made = batch._made
+    if made[0] != T:
+        made = batch._for_rows(T)
     cos = sin = max_pos = rot = Hq = qp = qs = op = os_ = 0
     if rope is not None:
         c, s = rope
         _require(c, "cos", torch.float32, 2, dev)
         _require(s, "sin", torch.float32, 2, dev)
-        max_pos, rot = c.shape
-        rot *= 2
-        if c.shape != s.shape or not c.is_contiguous() or not s.is_contiguous():
+        max_pos, rot = shape = c.shape
+        if shape != s.shape or not c.is_contiguous() or not s.is_contiguous():
             raise ValueError("cos and sin must be contiguous and of one shape")
         if rot:
+            rot *= 2
             cos, sin = c.data_ptr(), s.data_ptr()
     if q is not None:
-        qs = _rows(q, "q", 0, d, dev)
         Hq = q.shape[1]
-        if q.shape[0] != T:
-            raise ValueError(f"q has {q.shape[0]} rows, k {T}")
+        qs = _stride(q, "q", T, Hq, d, dev) if T else 0
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            q_out = _empty((T, Hq, d), dtype=_bf16, device=dev)
             os_ = Hq * d
         else:
-            os_ = _rows(q_out, "q_out", Hq, d, dev)
-            if q_out.shape[0] != T:
-                raise ValueError(f"q_out has {q_out.shape[0]} rows, q {T}")
+            os_ = _stride(q_out, "q_out", T, Hq, d, dev) if T else 0
         if Hq:
             qp, op = q.data_ptr(), q_out.data_ptr()
     else:
         q_out = None
-    rc = _library().fa_paged_append(cache._address, batch._for_rows(T)[2], k.data_ptr(), ks, v.data_ptr(), vs, qp, qs,
-                                    op, os_, Hq, cos, sin, max_pos, rot, 1 if interleaved else 0,
-                                    torch._C._cuda_getCurrentRawStream(index))
+    rc = _lib.fa_paged_append(cache._address, made[2], k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, op, os_, Hq, cos,
+                              sin, max_pos, rot, 1 if interleaved else 0, _raw_stream(index))
     if rc:
         _fail(rc, "fa_paged_append")
     return q_out
@@ -233,11 +229,10 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
 
 def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int) -> int:
     """Workspace bytes of fa_paged_attn with these arguments; they do not depend on the number of rows."""
-    elsewhere = _elsewhere(cache._index, None)
-    if elsewhere is not None:
-        with elsewhere:
+    if _current() != cache._index:
+        with _elsewhere(cache.device, None):
             return fa_paged_attn_workspace_bytes(cache, batch, Hq)
-    return _library().fa_paged_attn_workspace_bytes(cache._address, batch._for_rows(batch.B)[2], Hq)
+    return _lib.fa_paged_attn_workspace_bytes(cache._address, batch._for_rows(batch.B)[2], Hq)
 
 
 def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scale: float | None = None,
@@ -247,43 +242,40 @@ def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scal
     Rows of a new ``out`` behind the last sequence are not written. Without ``workspace`` one is allocated
     where the call needs it."""
     index = cache._index
-    elsewhere = _elsewhere(index, stream)
-    if elsewhere is not None:
-        with elsewhere:
+    if stream is not None or _current() != index:
+        with _elsewhere(cache.device, stream):
             return fa_paged_attn(cache, batch, q, window, scale, out, lse, workspace)
     dev, d = cache.device, cache.d
     if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    qs = _rows(q, "q", 0, d, dev)
+    qs = _stride(q, "q", 0, 0, d, dev)
     T, Hq, _ = q.shape
-    struct = batch._for_rows(T)[2]
+    made = batch._made
+    if made[0] != T:
+        made = batch._for_rows(T)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _rows(out, "out", Hq, d, dev)
-        if out.shape[0] != T or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous [{T}, {Hq}, {d}]")
+        out = _empty((T, Hq, d), dtype=_bf16, device=dev)
+    elif T and (_stride(out, "out", T, Hq, d, dev) < 0 or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous [{T}, {Hq}, {d}]")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((T, Hq), dtype=torch.float32, device=dev)
     else:
         _require(lse, "lse", torch.float32, 2, dev)
         if tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{T}, {Hq}]")
-    lib = _library()
+    ws = need = 0
     if workspace is None:
-        ws = 0
-        need = lib.fa_paged_attn_workspace_bytes(cache._address, struct, Hq)
+        need = _lib.fa_paged_attn_workspace_bytes(cache._address, made[2], Hq)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _empty(need, dtype=torch.uint8, device=dev)
             ws = workspace.data_ptr()
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
-        need = workspace.numel() * workspace.element_size()
+        need = workspace.nbytes
         ws = workspace.data_ptr() if need else 0
-    rc = lib.fa_paged_attn(cache._address, struct, q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq, window,
-                           cache._scale if scale is None else scale, ws, need,
-                           torch._C._cuda_getCurrentRawStream(index))
+    rc = _lib.fa_paged_attn(cache._address, made[2], q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq, window,
+                            cache._scale if scale is None else scale, ws, need, _raw_stream(index))
     if rc:
         _fail(rc, "fa_paged_attn")
     return out, lse

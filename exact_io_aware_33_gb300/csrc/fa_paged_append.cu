@@ -132,6 +132,11 @@ __device__ __forceinline__ float amax16(const float (&x)[16], float m) {
   return m;
 }
 
+// The largest of a warp's non-negative values: their bits order as the values do.
+__device__ __forceinline__ float warp_amax(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
 // Smallest power of two s (not below 2^-126) with amax / s <= 448 = 1.75 * 2^8; 1 for amax = 0.
 __device__ __forceinline__ float scale_of(float amax) {
   if (amax == 0.f) return 1.f;
@@ -331,15 +336,20 @@ __global__ void __launch_bounds__(1024) append_pages_kernel(const AppendArgs a) 
     const int h0 = (part - a.kv_parts) * kQHeadsPerBlock, h1 = min(h0 + kQHeadsPerBlock, a.Hq);
     const __nv_bfloat16* src = a.q + row * a.q_stride;
     __nv_bfloat16* dst = a.q_out + row * a.q_out_stride;
-    RawUnit next = load_raw(src + h0 * D, u);
     load_angles(a, u, p0 + slot, c, sn);
-    for (int h = h0; h < h1; ++h) {
-      const RawUnit w = next;
-      if (h + 1 < h1) next = load_raw(src + (h + 1) * D, u);
-      float x[16];
-      unpack(w, x);
-      rotate(a, u, c, sn, x);
-      store_query(dst + h * D, u, x);
+    for (int h = h0; h < h1; h += 2) {  // two heads in flight (four: 42 us instead of 38)
+      RawUnit w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (h + i < h1) w[i] = load_raw(src + (h + i) * D, u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (h + i >= h1) break;
+        float x[16];
+        unpack(w[i], x);
+        rotate(a, u, c, sn, x);
+        store_query(dst + (h + i) * D, u, x);
+      }
     }
     return;
   }
@@ -372,11 +382,8 @@ __global__ void __launch_bounds__(1024) append_pages_kernel(const AppendArgs a) 
       unpack(wv, xv);
       mv = amax16(xv, mv);
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, m));
-      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, m));
-    }
+    mk = warp_amax(mk);
+    mv = warp_amax(mv);
     float (&r)[2][32] = red[h & 1];  // two sets: the next head's writes need no second barrier
     if ((tid & 31) == 0) {
       r[0][tid >> 5] = mk;
@@ -388,10 +395,9 @@ __global__ void __launch_bounds__(1024) append_pages_kernel(const AppendArgs a) 
       v_old = a.v_scales[ph];
     }
     __syncthreads();
-    for (int w = 0; w < (threads >> 5); ++w) {
-      mk = fmaxf(mk, r[0][w]);
-      mv = fmaxf(mv, r[1][w]);
-    }
+    const int w = min(tid & 31, (threads >> 5) - 1);
+    mk = warp_amax(r[0][w]);
+    mv = warp_amax(r[1][w]);
     const float k_scale = fmaxf(scale_of(mk), k_old), v_scale = fmaxf(scale_of(mv), v_old);
     uint8_t* kb = a.k_pages + ph * ps * D;
     uint8_t* vb = a.v_pages + ph * ps * D;

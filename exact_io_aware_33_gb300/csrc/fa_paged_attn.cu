@@ -147,46 +147,67 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqGeo& s, 
   return g;
 }
 
+// x / y for x >= 0, y > 0: by 32 bits where they suffice, which takes a fifth of the time.
+__device__ __forceinline__ long long div_pos(long long x, int y) {
+  if (x >> 32) return x / y;
+  return static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+__device__ __forceinline__ void split_by(long long x, int y, int* quotient, int* remainder) {
+  const long long q = div_pos(x, y);
+  *quotient = static_cast<int>(q);
+  *remainder = static_cast<int>(x - q * y);
+}
+
 // First unit of part c of `parts` over `units` units, and the part of a unit.
 __device__ __forceinline__ long long part_start(long long units, int parts, int c) {
-  return units * c / parts;
+  return div_pos(units * c, parts);
 }
 
-// The units of the whole batch, by one warp.
+// The units of the sequences, by one warp: their total, and, kept from that
+// pass, the first 32 sequences' (what a batch of up to 32 needs no second
+// pass over the lengths for).
 template <int R>
-__device__ __forceinline__ long long all_units(const AttnArgs& a) {
-  long long sum = 0;
-  for (int b = lane_id(); b < a.batch.B; b += 32) sum += seq_units(a, seq_geo<R>(a, b));
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  return sum;
-}
+struct Units {
+  long long total;
+  long long own, end;  // of sequence lane_id(): its units, and the units up to its end
 
-// The sequence that holds unit u (below the total), and its first unit; by one warp.
-template <int R>
-__device__ __forceinline__ int find_seq(const AttnArgs& a, long long u, long long* first) {
-  long long before = 0;
-  for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
+  __device__ __forceinline__ void scan(const AttnArgs& a, int b0, long long before) {
     const int b = b0 + static_cast<int>(lane_id());
-    const long long own = b < a.batch.B ? seq_units(a, seq_geo<R>(a, b)) : 0;
-    long long end = own;
+    own = b < a.batch.B ? seq_units(a, seq_geo<R>(a, b)) : 0;
+    end = own;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, end, m);
       if (lane_id() >= static_cast<uint32_t>(m)) end += x;
     }
     end += before;
-    const uint32_t past = __ballot_sync(0xffffffffu, end > u);
-    if (past) {
-      const int i = __ffs(past) - 1;
-      *first = __shfl_sync(0xffffffffu, end - own, i);
-      return b0 + i;
-    }
-    before = __shfl_sync(0xffffffffu, end, 31);
   }
-  *first = before;  // not reached for u below the total
-  return a.batch.B;
-}
+  __device__ __forceinline__ void start(const AttnArgs& a) {
+    scan(a, 0, 0);
+    total = __shfl_sync(0xffffffffu, end, 31);
+    if (a.batch.B > 32) {
+      long long sum = 0;
+      for (int b = 32 + static_cast<int>(lane_id()); b < a.batch.B; b += 32) sum += seq_units(a, seq_geo<R>(a, b));
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      total += sum;
+    }
+  }
+  // The sequence that holds unit u (below the total), and its first unit.
+  __device__ __forceinline__ int find(const AttnArgs& a, long long u, long long* first) {
+    for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
+      if (b0 > 0) scan(a, b0, __shfl_sync(0xffffffffu, end, 31));
+      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        *first = __shfl_sync(0xffffffffu, end - own, i);
+        return b0 + i;
+      }
+    }
+    *first = 0;  // not reached for u below the total
+    return a.batch.B;
+  }
+};
 
 // Walks the pieces of items that a CTA has, sequence by sequence: tiles
 // [v0, v1) of the sequence's tiles laid end to end, item after item (key head
@@ -199,17 +220,19 @@ struct Walk {
   int b;
 
   __device__ __forceinline__ void start(const AttnArgs& a, int part, int parts) {
-    const long long units = all_units<R>(a);
-    u0 = part_start(units, parts, part);
-    u1 = part_start(units, parts, part + 1);
+    Units<R> units;
+    units.start(a);
+    u0 = part_start(units.total, parts, part);
+    u1 = part_start(units.total, parts, part + 1);
     b = a.batch.B;
     base = 0;
-    if (u0 < u1) b = find_seq<R>(a, u0, &base);
+    if (u0 < u1) b = units.find(a, u0, &base);
   }
   // unit -> tile index in the sequence: the first kItemUnits of an item are not tiles
   static __device__ __forceinline__ long long tile_of(long long u, int nt) {
-    const int per = nt + kItemUnits;
-    return u / per * nt + max(u % per - kItemUnits, 0LL);
+    int item, rest;
+    split_by(u, nt + kItemUnits, &item, &rest);
+    return static_cast<long long>(item) * nt + max(rest - kItemUnits, 0);
   }
   __device__ __forceinline__ bool next(const AttnArgs& a, SeqGeo* g, long long* v0, long long* v1, int* e0,
                                        int* e1) {
@@ -401,16 +424,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     // ------------------------------------------------------------ TMA warp
     // Lane i looks up the i-th of 32 groups of 16 keys (eight tiles, across
     // items of a sequence): its page, then its scales. The next eight tiles'
-    // two dependent loads are under way while the present ones are issued.
-    const int box_rows = min(a.batch.page_size, kTile);
-    const int boxes = kTile / box_rows, groups_per_box = box_rows / kGroup;
+    // two dependent loads are under way while the present ones are issued. The
+    // lane of a box's first group issues its copies.
+    const int box_rows = min(a.batch.page_size, kTile), per_box = box_rows / kGroup;
+    const uint32_t box_bytes = 2u * box_rows * D;  // of K and V
     while (more) {
       const int seq = walk.b - 1;
       long long left = v1 - v0;  // tiles not looked up yet
-      int item = sg.nt > 0 ? static_cast<int>(v0 / sg.nt) : 0;
-      int tile = sg.nt > 0 ? static_cast<int>(v0 % sg.nt) : 0;
-      int page = -1, head = 0, key = 0, count = 0;
-      float sk = -1.f, sv = 1.f;
+      int item = 0, tile = 0;
+      if (sg.nt > 0) split_by(v0, sg.nt, &item, &tile);
       int n_page = -1, n_head = 0, n_key = 0, n_count = 0;
       auto look = [&]() {  // the next (up to) eight tiles' pages
         n_count = static_cast<int>(min(left, 8LL));
@@ -421,12 +443,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
         }
         n_page = -1;
         if ((lane >> 2) < n_count) {
-          const RowTile g = row_tile<R>(a, sg, ii % sg.rts);
-          n_head = ii / sg.rts;
-          n_key = (sg.t0 + ti) * kTile;
-          const int j0 = n_key + (lane & 3) * kGroup;
-          if (j0 < g.hi && j0 + kGroup > g.lo)
-            n_page = paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status);
+          n_head = sg.rts == 1 ? ii : ii / sg.rts;
+          const RowTile g = row_tile<R>(a, sg, ii - n_head * sg.rts);
+          n_key = (sg.t0 + ti) * kTile + (lane & 3) * kGroup;
+          if (n_key < g.hi && n_key + kGroup > g.lo)
+            n_page = paged_page(a.batch, seq, n_key >> a.batch.page_shift, a.status);
         }
         left -= n_count;
         tile += n_count;
@@ -447,41 +468,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       look();
       scales();
       while (n_count > 0) {
-        page = n_page;
-        head = n_head;
-        key = n_key;
-        count = n_count;
-        sk = n_sk;
-        sv = n_sv;
+        int box_page = n_page;  // of this lane's box: its groups share a page, or have none to read
+        const int head = n_head, key = n_key, count = n_count;
+        const float sk = n_sk, sv = n_sv;
         look();
+        if (per_box > 1) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 1));
+        if (per_box > 2) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 2));
+        const bool issues = (lane & 3) % per_box == 0 && box_page >= 0;
+        const uint32_t issuers = __ballot_sync(0xffffffffu, issues);
+        const int slot = key & (a.batch.page_size - 1), blk = box_page * a.Hkv + head;
+        const uint32_t off = (lane & 3) * kGroup * D;
         for (int i = 0; i < count && !*abort_flag; ++i) {
           const int st = it % kS;
-          int pg[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) pg[q] = __shfl_sync(0xffffffffu, page, 4 * i + q);
-          const int hd = __shfl_sync(0xffffffffu, head, 4 * i), tok = __shfl_sync(0xffffffffu, key, 4 * i);
           if (it >= kS && !mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag)) break;
-          // the copies need the pages only: they go out before the scales are waited for
-          uint32_t bytes = 0;
-          if (lane == 0) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              if (b >= boxes) break;
-              int bp = -1;
-              for (int q = 0; q < groups_per_box; ++q) {
-                const int x = b * groups_per_box + q;
-                bp = max(bp, x == 0 ? pg[0] : x == 1 ? pg[1] : x == 2 ? pg[2] : pg[3]);
-              }
-              if (bp < 0) continue;
-              const int slot = (tok + b * box_rows) & (a.batch.page_size - 1);
-              const int blk = bp * a.Hkv + hd;
-              const uint32_t off = st * C::kTileBytes + b * box_rows * D;
-              tma_load_3d(sb + C::kKOff + off, &tmK, full + 8 * st, 0, slot, blk);
-              tma_load_3d(sb + C::kVOff + off, &tmV, full + 8 * st, 0, slot, blk);
-              bytes += 2u * box_rows * D;
+          if ((lane >> 2) == i) {
+            // the copies need the pages only: they go out before the scales are waited for
+            if (issues) {
+              tma_load_3d(sb + C::kKOff + st * C::kTileBytes + off, &tmK, full + 8 * st, 0, slot, blk);
+              tma_load_3d(sb + C::kVOff + st * C::kTileBytes + off, &tmV, full + 8 * st, 0, slot, blk);
             }
-          }
-          if (lane / 4 == i) {
             const uint32_t bits = __float_as_uint(sv);
             // exact for the powers of two that the append writes
             const float ev = (bits & 0x7fffffu) ? log2f(sv)
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
           }
           __syncwarp();
           // (bytes that have landed already count as well: the phase cannot end before this arrival)
-          if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+          if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, __popc(issuers & (0xfu << (4 * i))) * box_bytes);
           if (i == min(3, count - 1)) scales();
           ++it;
         }
@@ -529,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       const float x[kCols] = {};
       if (r < sg.rows) store_row<D>(a, sg, e / sg.rts, r, c0, x, -INFINITY);
     }
-    int item = sg.nt > 0 ? static_cast<int>(v0 / sg.nt) : 0;
-    int tile = sg.nt > 0 ? static_cast<int>(v0 % sg.nt) : 0;
+    int item = 0, tile = 0;
+    if (sg.nt > 0) split_by(v0, sg.nt, &item, &tile);
     for (long long left = v1 - v0; left > 0;) {
       // the piece [tile, tile_end) of this item
       const int tile_end = static_cast<int>(min(static_cast<long long>(sg.nt), tile + left));
-      const int h = item / sg.rts;
-      const RowTile g = row_tile<R>(a, sg, item % sg.rts);
+      const int h = sg.rts == 1 ? item : item / sg.rts;
+      const RowTile g = row_tile<R>(a, sg, item - h * sg.rts);
       uint32_t qb[NB][D / 8];   // B operand of S^T: row n of each block, D/4 channels
       float qf[NB][2];          // per column of the accumulators (rows 2t, 2t + 1 of a block)
       int p_row[NB][2];
@@ -851,21 +856,32 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
   constexpr int R = 8 * NB, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
   __shared__ float s_x[R][kShare][D];
   __shared__ float s_m[R][kShare], s_sum[R][kShare];
-  grid_dep_wait();
-  grid_dep_launch();
+  // The geometry comes from the batch's lengths alone, which the kernel before
+  // does not write: it started only when they were settled. So that is worked
+  // out while that kernel ends.
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wrow = warp / kShare, share = warp % kShare;
-  const long long units = all_units<R>(a);
+  Units<R> all;
+  all.start(a);
+  const long long units = all.total;
   const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
-  if (u0 >= u1) return;
-  long long base;
-  const int seq = find_seq<R>(a, u1 - 1, &base);
-  const SeqGeo sg = seq_geo<R>(a, seq);
-  const int per = sg.nt + kItemUnits;
-  const int item = static_cast<int>((u1 - 1 - base) / per);
-  const long long first = base + static_cast<long long>(item) * per + kItemUnits;  // unit of the item's tile 0
-  const long long end = u1 - first;                                                  // tiles up to here
-  if (u0 > first || end <= 0 || end >= sg.nt) return;
+  bool work = u0 < u1;
+  SeqGeo sg{};
+  int item = 0;
+  long long first = 0;
+  if (work) {
+    long long base;
+    const int seq = all.find(a, u1 - 1, &base);
+    sg = seq_geo<R>(a, seq);
+    const int per = sg.nt + kItemUnits;
+    item = static_cast<int>(div_pos(u1 - 1 - base, per));
+    first = base + static_cast<long long>(item) * per + kItemUnits;  // unit of the item's tile 0
+    const long long end = u1 - first;                                // tiles up to here
+    work = u0 <= first && end > 0 && end < sg.nt;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (!work) return;
   const int r = item % sg.rts * R + wrow;
   const bool live = r < sg.rows;
   // part k > c holds tiles of the item when it starts before the item's end; it continues it (piece 0)

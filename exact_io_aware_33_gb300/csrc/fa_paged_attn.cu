@@ -21,8 +21,8 @@
 // What bounds it: at one token per sequence every cached byte is read once
 // for G = Hq / Hkv rows of arithmetic, far below the tensor core's rate, so
 // the kernel is a copy from HBM. It therefore is organised as one: a TMA warp
-// keeps a ring of tiles (64 tokens of K and V) full and four warps take 16
-// tokens of each tile, each with an online softmax of its own, so that no two
+// keeps a ring of tiles (64 keys, or 128 at d = 64) full and four warps take a
+// quarter of each tile, each with an online softmax of its own, so that no two
 // warps wait for one another until the end of an item. Codes go from shared
 // memory to registers and are widened there (mma.sync takes its operands from
 // registers; tcgen05 would want them widened in shared memory first, which
@@ -46,8 +46,7 @@
 namespace fa {
 namespace {
 
-constexpr int kTile = 64;        // tokens per stage
-constexpr int kGroup = 16;       // tokens per warp of a stage
+constexpr int kGroup = 16;       // keys of one mma tile; a page is one or more groups
 constexpr int kThreads = 160;    // four warps and the TMA warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -59,8 +58,16 @@ constexpr float kSlack = 8.f;    // log2 units that a weight may pass its refere
 constexpr int kItemUnits = 2;
 
 // NB: blocks of eight query rows per CTA.
+// Keys per stage. At d = 64 a tile of 64 would be 8 KiB for the same waiting,
+// voting and reference keeping, and those, not the bytes, would set the pace.
+template <int D>
+constexpr int kTileOf = D == 64 ? 128 : 64;
+
 template <int D, int NB>
 struct Cfg {
+  static constexpr int kTile = kTileOf<D>;
+  static constexpr int kGpt = kTile / kGroup;  // groups per tile
+  static constexpr int kGpw = kGpt / 4;        // and per warp
   static constexpr int kRows = 8 * NB;
   static constexpr int kCtasPerSm = NB == 1 ? 3 : 2;
   static constexpr int kTileBytes = kTile * D;
@@ -68,13 +75,13 @@ struct Cfg {
   static constexpr int kPitch = D + 4;
   static constexpr int kStateBytes = 4 * kRows * (kPitch + 4) * 4;
   // as many stages as leave room for the other CTAs of the SM
-  static constexpr int kRoom = 233472 / kCtasPerSm - 1024 - 1024 - 512 - kStateBytes;
+  static constexpr int kRoom = 233472 / kCtasPerSm - 1024 - 1024 - 768 - kStateBytes;
   static constexpr int kStages = kRoom / (2 * kTileBytes) < 10 ? kRoom / (2 * kTileBytes) : 10;
   static constexpr int kKOff = 0;
   static constexpr int kVOff = kStages * kTileBytes;
   static constexpr int kStateOff = 2 * kStages * kTileBytes;
-  static constexpr int kScaleOff = kStateOff + kStateBytes;  // [stage][4] {sk, log2 sv}
-  static constexpr int kBarOff = kScaleOff + kStages * 4 * 8;
+  static constexpr int kScaleOff = kStateOff + kStateBytes;  // [stage][group] {sk, log2 sv}
+  static constexpr int kBarOff = kScaleOff + kStages * kGpt * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + slack to align the base
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "the CTAs of an SM must fit");
@@ -99,8 +106,8 @@ struct AttnArgs {
   float scale_log2;
 };
 
-// One sequence's items: its tiles of R rows, and the tiles of 64 keys that any of
-// its queries sees.
+// One sequence's items: its tiles of R rows, and the tiles of kTile keys that any
+// of its queries sees.
 struct SeqGeo {
   PagedSeq s;
   int rows, rts;  // packed (query, head of the group) rows of a key head, and tiles of R of them
@@ -108,7 +115,7 @@ struct SeqGeo {
   int t0, nt;
 };
 
-template <int R>
+template <int R, int kTile>
 __device__ __forceinline__ SeqGeo seq_geo(const AttnArgs& a, int seq) {
   SeqGeo g;
   g.s = paged_seq(a.batch, seq, a.status);
@@ -166,14 +173,14 @@ __device__ __forceinline__ long long part_start(long long units, int parts, int 
 // The units of the sequences, by one warp: their total, and, kept from that
 // pass, the first 32 sequences' (what a batch of up to 32 needs no second
 // pass over the lengths for).
-template <int R>
+template <int R, int kTile>
 struct Units {
   long long total;
   long long own, end;  // of sequence lane_id(): its units, and the units up to its end
 
   __device__ __forceinline__ void scan(const AttnArgs& a, int b0, long long before) {
     const int b = b0 + static_cast<int>(lane_id());
-    own = b < a.batch.B ? seq_units(a, seq_geo<R>(a, b)) : 0;
+    own = b < a.batch.B ? seq_units(a, seq_geo<R, kTile>(a, b)) : 0;
     end = own;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -187,7 +194,7 @@ struct Units {
     total = __shfl_sync(0xffffffffu, end, 31);
     if (a.batch.B > 32) {
       long long sum = 0;
-      for (int b = 32 + static_cast<int>(lane_id()); b < a.batch.B; b += 32) sum += seq_units(a, seq_geo<R>(a, b));
+      for (int b = 32 + static_cast<int>(lane_id()); b < a.batch.B; b += 32) sum += seq_units(a, seq_geo<R, kTile>(a, b));
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       total += sum;
@@ -213,14 +220,14 @@ struct Units {
 // [v0, v1) of the sequence's tiles laid end to end, item after item (key head
 // by key head, row tile by row tile). A sequence whose rows see no key has
 // items [e0, e1) to be filled with zeros instead. Every warp walks alike.
-template <int R>
+template <int R, int kTile>
 struct Walk {
   long long u0, u1;  // this CTA's units
   long long base;    // first unit of sequence b
   int b;
 
   __device__ __forceinline__ void start(const AttnArgs& a, int part, int parts) {
-    Units<R> units;
+    Units<R, kTile> units;
     units.start(a);
     u0 = part_start(units.total, parts, part);
     u1 = part_start(units.total, parts, part + 1);
@@ -237,7 +244,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const AttnArgs& a, SeqGeo* g, long long* v0, long long* v1, int* e0,
                                        int* e1) {
     while (b < a.batch.B && base < u1) {
-      *g = seq_geo<R>(a, b);
+      *g = seq_geo<R, kTile>(a, b);
       const long long own = seq_units(a, *g);
       const long long lo = max(u0 - base, 0LL), hi = min(u1 - base, own);
       base += own;
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const AttnArgs a) {
   using C = Cfg<D, NB>;
-  constexpr int kS = C::kStages, R = C::kRows;
+  constexpr int kS = C::kStages, R = C::kRows, kTile = C::kTile, kGpt = C::kGpt, kGpw = C::kGpw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
 
   // What this CTA does: a walk over its part (streaming), or its piece of one
   // item (cluster; `rank` of `pieces` that have any tile).
-  Walk<R> walk;
+  Walk<R, kTile> walk;
   SeqGeo sg;
   long long v0 = 0, v1 = 0;
   int e0 = 0, e1 = 0, rank = 0, pieces = 1;
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     const int rt = static_cast<int>(item % a.row_tiles);
     const long long bh = item / a.row_tiles;
     const int h = static_cast<int>(bh % a.Hkv);
-    sg = seq_geo<R>(a, static_cast<int>(bh / a.Hkv));
+    sg = seq_geo<R, kTile>(a, static_cast<int>(bh / a.Hkv));
     if (rt >= sg.rts) return;  // the whole cluster alike
     walk.b = static_cast<int>(bh / a.Hkv) + 1;
     const int own = h * sg.rts + rt;
@@ -422,10 +429,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
 
   if (warp == 4) {
     // ------------------------------------------------------------ TMA warp
-    // Lane i looks up the i-th of 32 groups of 16 keys (eight tiles, across
-    // items of a sequence): its page, then its scales. The next eight tiles'
+    // Lane i looks up the i-th of 32 groups of 16 keys (four or eight tiles,
+    // across items of a sequence): its page, then its scales. The next tiles'
     // two dependent loads are under way while the present ones are issued. The
     // lane of a box's first group issues its copies.
+    constexpr int kBatch = 32 / kGpt;  // tiles looked up at once
+    const int tile_in = lane / kGpt, grp = lane % kGpt;
     const int box_rows = min(a.batch.page_size, kTile), per_box = box_rows / kGroup;
     const uint32_t box_bytes = 2u * box_rows * D;  // of K and V
     while (more) {
@@ -434,18 +443,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       int item = 0, tile = 0;
       if (sg.nt > 0) split_by(v0, sg.nt, &item, &tile);
       int n_page = -1, n_head = 0, n_key = 0, n_count = 0;
-      auto look = [&]() {  // the next (up to) eight tiles' pages
-        n_count = static_cast<int>(min(left, 8LL));
-        int ti = tile + (lane >> 2), ii = item;
+      auto look = [&]() {  // the next (up to) kBatch tiles' pages
+        n_count = static_cast<int>(min(left, static_cast<long long>(kBatch)));
+        int ti = tile + tile_in, ii = item;
         while (ti >= sg.nt && sg.nt > 0) {
           ti -= sg.nt;
           ++ii;
         }
         n_page = -1;
-        if ((lane >> 2) < n_count) {
+        if (tile_in < n_count) {
           n_head = sg.rts == 1 ? ii : ii / sg.rts;
           const RowTile g = row_tile<R>(a, sg, ii - n_head * sg.rts);
-          n_key = (sg.t0 + ti) * kTile + (lane & 3) * kGroup;
+          n_key = (sg.t0 + ti) * kTile + grp * kGroup;
           if (n_key < g.hi && n_key + kGroup > g.lo)
             n_page = paged_page(a.batch, seq, n_key >> a.batch.page_shift, a.status);
         }
@@ -474,14 +483,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
         look();
         if (per_box > 1) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 1));
         if (per_box > 2) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 2));
-        const bool issues = (lane & 3) % per_box == 0 && box_page >= 0;
+        if (per_box > 4) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 4));
+        const bool issues = grp % per_box == 0 && box_page >= 0;
         const uint32_t issuers = __ballot_sync(0xffffffffu, issues);
         const int slot = key & (a.batch.page_size - 1), blk = box_page * a.Hkv + head;
-        const uint32_t off = (lane & 3) * kGroup * D;
+        const uint32_t off = grp * kGroup * D;
         for (int i = 0; i < count && !*abort_flag; ++i) {
           const int st = it % kS;
           if (it >= kS && !mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag)) break;
-          if ((lane >> 2) == i) {
+          if (tile_in == i) {
             // the copies need the pages only: they go out before the scales are waited for
             if (issues) {
               tma_load_3d(sb + C::kKOff + st * C::kTileBytes + off, &tmK, full + 8 * st, 0, slot, blk);
@@ -492,12 +502,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
             const float ev = (bits & 0x7fffffu) ? log2f(sv)
                              : bits == 0       ? -INFINITY
                                                : static_cast<float>(static_cast<int>(bits >> 23) - 127);
-            *reinterpret_cast<float2*>(smem + C::kScaleOff + (st * 4 + (lane & 3)) * 8) = make_float2(sk, ev);
+            *reinterpret_cast<float2*>(smem + C::kScaleOff + (st * kGpt + grp) * 8) = make_float2(sk, ev);
           }
           __syncwarp();
           // (bytes that have landed already count as well: the phase cannot end before this arrival)
-          if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, __popc(issuers & (0xfu << (4 * i))) * box_bytes);
-          if (i == min(3, count - 1)) scales();
+          if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, __popc(issuers & (((1u << kGpt) - 1) << (kGpt * i))) * box_bytes);
+          if (i == min(kBatch / 2 - 1, count - 1)) scales();
           ++it;
         }
         __syncwarp();
@@ -573,61 +583,78 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
         const int st = it % kS;
         ok = ok && mbar_wait_w(full + 8 * st, (it / kS) & 1, abort_flag);
         if (!ok) continue;
-        const float2 sc = *reinterpret_cast<const float2*>(smem + C::kScaleOff + (st * 4 + warp) * 8);
-        if (!(sc.x < 0.f)) {  // below zero: no row sees these keys, or they have no page
-          const int j0 = (sg.t0 + ti) * kTile + warp * kGroup;
-          const bool part = !all_see(g, j0, a.window);
-          const uint8_t* kb = smem + C::kKOff + st * C::kTileBytes;
-          const uint8_t* vb = smem + C::kVOff + st * C::kTileBytes;
+        // this warp's groups of 16 keys
+        float2 sc[kGpw];
+        bool any = false;
+#pragma unroll
+        for (int q = 0; q < kGpw; ++q) {
+          sc[q] = *reinterpret_cast<const float2*>(smem + C::kScaleOff + (st * kGpt + warp * kGpw + q) * 8);
+          any = any || !(sc[q].x < 0.f);  // below zero: no row sees these keys, or they have no page
+        }
+        if (any) {
+          const int j0 = (sg.t0 + ti) * kTile + warp * kGpw * kGroup;
+          bool part = false;
+#pragma unroll
+          for (int q = 0; q < kGpw; ++q) part = part || !all_see(g, j0 + q * kGroup, a.window) || sc[q].x < 0.f;
+          const uint8_t* kb = smem + C::kKOff + st * C::kTileBytes + warp * kGpw * kGroup * D;
+          const uint8_t* vb = smem + C::kVOff + st * C::kTileBytes + warp * kGpw * kGroup * D;
           // S^T = K Q^T: 16 keys x 8 NB rows. A lane holds D/4 consecutive
           // channels of keys n and n + 8, four per mma step, in the order
-          // that its queries have.
-          constexpr int kChains = NB == 1 ? 2 : 1;  // of dependent products: with two blocks they alternate
-          float acc[NB][kChains][4] = {};
-          uint4 kw[2][D / 64];
+          // that its queries have. (kb lies on a multiple of eight rows, so a
+          // row's swizzle is that of its number here.)
+          constexpr int kChains = NB * kGpw == 1 ? 2 : 1;  // of dependent products, where there is only one
+          float acc[kGpw][NB][kChains][4] = {};
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int row = warp * kGroup + hh * 8 + n;
-            if constexpr (D == 128) {
-              kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t) ^ (row & 7)) << 4));
-              kw[hh][1] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t + 1) ^ (row & 7)) << 4));
-            } else {
-              kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
-            }
-          }
+          for (int q = 0; q < kGpw; ++q) {
+            uint4 kw[2][D / 64];
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t ka[4];
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t w = e == 0 ? kw[hh][c].x : e == 1 ? kw[hh][c].y : e == 2 ? kw[hh][c].z : kw[hh][c].w;
-                ka[hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w));
-                ka[2 + hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+            for (int hh = 0; hh < 2; ++hh) {
+              const int row = q * kGroup + hh * 8 + n;
+              if constexpr (D == 128) {
+                kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t) ^ (row & 7)) << 4));
+                kw[hh][1] = *reinterpret_cast<const uint4*>(kb + row * 128 + (((2 * t + 1) ^ (row & 7)) << 4));
+              } else {
+                kw[hh][0] = *reinterpret_cast<const uint4*>(kb + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
               }
+            }
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816(acc[nb][e % kChains], ka, qb[nb][2 * (4 * c + e)], qb[nb][2 * (4 * c + e) + 1]);
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t ka[4];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t w = e == 0 ? kw[hh][c].x : e == 1 ? kw[hh][c].y : e == 2 ? kw[hh][c].z : kw[hh][c].w;
+                  ka[hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w));
+                  ka[2 + hh] = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816(acc[q][nb][e % kChains], ka, qb[nb][2 * (4 * c + e)], qb[nb][2 * (4 * c + e) + 1]);
+              }
             }
           }
-          // x[nb][2 hh + e]: key n + 8 hh, row 2t + e, in log2 units
-          float x[NB][4];
+          // x[q][nb][2 hh + e]: key n + 8 hh of group q, row 2t + e, in log2 units
+          float x[kGpw][NB][4];
           bool over = false;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float f = qf[nb][e] * sc.x;
-              const float bar = fminf(ms[nb][e], mt[nb][e] - sc.y) + kSlack;
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                float v = acc[nb][0][2 * hh + e];
-                if constexpr (kChains == 2) v += acc[nb][1][2 * hh + e];
-                v *= f;
-                if (part && !sees(p_row[nb][e], j0 + n + 8 * hh, a.window)) v = -INFINITY;
-                x[nb][2 * hh + e] = v;
-                over = over || v > bar;
+              for (int q = 0; q < kGpw; ++q) {
+                const float f = qf[nb][e] * sc[q].x;
+                const float bar = fminf(ms[nb][e], mt[nb][e] - sc[q].y) + kSlack;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  float v = acc[q][nb][0][2 * hh + e];
+                  if constexpr (kChains == 2) v += acc[q][nb][1][2 * hh + e];
+                  v *= f;
+                  if (part && (sc[q].x < 0.f || !sees(p_row[nb][e], j0 + q * kGroup + n + 8 * hh, a.window)))
+                    v = -INFINITY;
+                  x[q][nb][2 * hh + e] = v;
+                  over = over || v > bar;
+                }
               }
             }
           }
@@ -639,8 +666,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
               float alpha[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float mx = column_max(fmaxf(x[nb][e], x[nb][2 + e]));
-                const float ms_new = fmaxf(ms[nb][e], mx), mt_new = fmaxf(mt[nb][e], mx + sc.y);
+                float ms_new = ms[nb][e], mt_new = mt[nb][e];
+#pragma unroll
+                for (int q = 0; q < kGpw; ++q) {
+                  const float mx = column_max(fmaxf(x[q][nb][e], x[q][nb][2 + e]));
+                  ms_new = fmaxf(ms_new, mx);
+                  mt_new = fmaxf(mt_new, mx + sc[q].y);
+                }
                 // a row that has seen nothing yet has both at -infinity
                 l[nb][e] *= ex2(ms[nb][e] - (ms_new == -INFINITY ? 0.f : ms_new));
                 alpha[e] = ex2(mt[nb][e] - (mt_new == -INFINITY ? 0.f : mt_new));
@@ -656,66 +688,76 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
               }
             }
           }
-          uint32_t pb[NB][2];
+          uint32_t pb[kGpw][NB][2];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            float w[4];
+            float w[kGpw][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float su = ms[nb][e] == -INFINITY ? 0.f : ms[nb][e];
               const float tu = mt[nb][e] == -INFINITY ? 0.f : mt[nb][e];
-              const float f2 = ex2(fminf(su + sc.y - tu + kPShift, 126.f));
-              const float p0 = ex2(x[nb][e] - su), p1 = ex2(x[nb][2 + e] - su);
-              l[nb][e] += p0 + p1;
-              w[e] = p0 * f2;
-              w[2 + e] = p1 * f2;
+#pragma unroll
+              for (int q = 0; q < kGpw; ++q) {
+                const float f2 = ex2(fminf(su + sc[q].y - tu + kPShift, 126.f));
+                const float p0 = ex2(x[q][nb][e] - su), p1 = ex2(x[q][nb][2 + e] - su);
+                l[nb][e] += p0 + p1;
+                w[q][e] = p0 * f2;
+                w[q][2 + e] = p1 * f2;
+              }
             }
-            pb[nb][0] = transpose8x8(pack_f16(w[0], w[1]));
-            pb[nb][1] = transpose8x8(pack_f16(w[2], w[3]));
+#pragma unroll
+            for (int q = 0; q < kGpw; ++q) {
+              pb[q][nb][0] = transpose8x8(pack_f16(w[q][0], w[q][1]));
+              pb[q][nb][1] = transpose8x8(pack_f16(w[q][2], w[q][3]));
+            }
           }
           // O^T += V^T P^T: lane (n, t) takes channels [n D/8, (n + 1) D/8) of
           // keys 2t, 2t+1, 2t+8, 2t+9; an mma tile's rows n and n + 8 are two
           // neighbouring channels
-          uint32_t vw[4][D / 32];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = warp * kGroup + 2 * t + (e & 1) + 8 * (e >> 1);
-            if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(vb + row * 128 + ((n ^ (row & 7)) << 4));
-              vw[e][0] = w.x; vw[e][1] = w.y; vw[e][2] = w.z; vw[e][3] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(
-                  vb + row * 64 + (((n >> 1) ^ ((row >> 1) & 3)) << 4) + ((n & 1) << 3));
-              vw[e][0] = w.x; vw[e][1] = w.y;
-            }
-          }
-          if (part) {
-            // keys that a row does not see have weight 0, and 0 x NaN is NaN: here
-            // NaN codes are taken out, and rows that do see one are mended at the end
+          for (int q = 0; q < kGpw; ++q) {
+            uint32_t vw[4][D / 32];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                const uint32_t z = nan_bytes(vw[e][i]);
-                saw_nan = saw_nan || z != 0;
-                vw[e][i] &= ~z;
+              const int row = q * kGroup + 2 * t + (e & 1) + 8 * (e >> 1);
+              if constexpr (D == 128) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vb + row * 128 + ((n ^ (row & 7)) << 4));
+                vw[e][0] = w.x; vw[e][1] = w.y; vw[e][2] = w.z; vw[e][3] = w.w;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(
+                    vb + row * 64 + (((n >> 1) ^ ((row >> 1) & 3)) << 4) + ((n & 1) << 3));
+                vw[e][0] = w.x; vw[e][1] = w.y;
               }
             }
-          }
+            const bool absent = sc[q].x < 0.f;  // (nothing was loaded)
+            if (part && (absent || !all_see(g, j0 + q * kGroup, a.window))) {
+              // keys that a row does not see have weight 0, and 0 x NaN is NaN: here
+              // NaN codes are taken out, and rows that do see one are mended at the end
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            // byte pairs of two neighbouring keys, channel by channel
-            const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
-            const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
-            const uint32_t va[2][4] = {
-                {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
-                 e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))},
-                {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
-                 e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))}};
+              for (int e = 0; e < 4; ++e) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816(o[nb][2 * i], va[0], pb[nb][0], pb[nb][1]);
-              mma16816(o[nb][2 * i + 1], va[1], pb[nb][0], pb[nb][1]);
+                for (int i = 0; i < D / 32; ++i) {
+                  const uint32_t z = nan_bytes(vw[e][i]);
+                  saw_nan = saw_nan || (z != 0 && !absent);
+                  vw[e][i] = absent ? 0u : vw[e][i] & ~z;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              // byte pairs of two neighbouring keys, channel by channel
+              const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[0][i], vw[1][i], 0x7362);
+              const uint32_t b01 = __byte_perm(vw[2][i], vw[3][i], 0x5140), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+              const uint32_t va[2][4] = {
+                  {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
+                   e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))},
+                  {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
+                   e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))}};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma16816(o[nb][2 * i], va[0], pb[q][nb][0], pb[q][nb][1]);
+                mma16816(o[nb][2 * i + 1], va[1], pb[q][nb][0], pb[q][nb][1]);
+              }
             }
           }
         }
@@ -853,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
 // 16 for few items of many parts.
 template <int D, int NB, int kShare>
 __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const AttnArgs a, int parts) {
-  constexpr int R = 8 * NB, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
+  constexpr int R = 8 * NB, kTile = kTileOf<D>, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
   __shared__ float s_x[R][kShare][D];
   __shared__ float s_m[R][kShare], s_sum[R][kShare];
   // The geometry comes from the batch's lengths alone, which the kernel before
@@ -861,7 +903,7 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
   // out while that kernel ends.
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wrow = warp / kShare, share = warp % kShare;
-  Units<R> all;
+  Units<R, kTile> all;
   all.start(a);
   const long long units = all.total;
   const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
@@ -872,7 +914,7 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
   if (work) {
     long long base;
     const int seq = all.find(a, u1 - 1, &base);
-    sg = seq_geo<R>(a, seq);
+    sg = seq_geo<R, kTile>(a, seq);
     const int per = sg.nt + kItemUnits;
     item = static_cast<int>(div_pos(u1 - 1 - base, per));
     first = base + static_cast<long long>(item) * per + kItemUnits;  // unit of the item's tile 0
@@ -960,7 +1002,7 @@ template <int D, int NB, bool kCluster>
 int launch_rows(const PagedPool& pool, const AttnArgs& a, const PagedPlan& plan, cudaStream_t stream) {
   using C = Cfg<D, NB>;
   CUtensorMap mk, mv;
-  const int box = pool.page_size < kTile ? pool.page_size : kTile;
+  const int box = pool.page_size < C::kTile ? pool.page_size : C::kTile;
   const int blocks = pool.num_pages * pool.num_heads;
   if (!make_map_pages(&mk, pool.k_pages, blocks, pool.page_size, D, box, true) ||
       !make_map_pages(&mv, pool.v_pages, blocks, pool.page_size, D, box, true))
@@ -1012,7 +1054,8 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   r.row_tiles = static_cast<int>((rows + r.rows - 1) / r.rows);
   const long long items = static_cast<long long>(batch.B) * pool.num_heads * r.row_tiles;
   r.items = items;
-  const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + kTile - 1) / kTile : 1;
+  const int tile = pool.d == 64 ? kTileOf<64> : kTileOf<128>;
+  const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + tile - 1) / tile : 1;
   const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
   // The cluster form while every CTA of a cluster of up to eight has a slot and
   // at most eight tiles.

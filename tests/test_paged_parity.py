@@ -216,7 +216,9 @@ def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, max_pages):
     n = 200
     w = World([n], 1, 16, 64, seed=7, max_pages=max_pages).fill()
     rows = news[0]
-    for j, c in ((n - 1, 5), (n - rows // 2 - 1, 60)):   # the last key, and one that half of the rows see
+    # the last key, one that half of the rows see, and one that all rows see, next to keys that they do not
+    spots = ((n - 1, 5), (n - rows // 2 - 1, 60), ((n - rows) // 16 * 16 - 1, 17))
+    for j, c in spots:
         w.oracle.codes["v"][w.table[0, j // 16], 0, j % 16, c] = 0x7F if c == 5 else 0xFF
     cu, batch = w.batch(news)
     q = bf16(w.rng, rows, 4, 64)
@@ -226,7 +228,7 @@ def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, max_pages):
     o = o.float().cpu().numpy()
     for i in range(rows):
         p = n - rows + i
-        want = {c for j, c in ((n - 1, 5), (n - rows // 2 - 1, 60)) if j <= p}
+        want = {c for j, c in spots if j <= p}
         got = set(np.nonzero(np.isnan(o[i]).any(0))[0])
         assert got == want, (i, got, want)
 

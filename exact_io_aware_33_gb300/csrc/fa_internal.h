@@ -184,7 +184,7 @@ struct PagedPlan {
   int row_tiles;           // tiles of that many rows of the longest packed sequence and a key head
   long long items;         // sequences x key heads x row tiles
   int cluster;             // CTAs per item in the cluster form; 0: the streaming form
-  bool chunk;              // many rows: the kernel of fa_paged_chunk.cu, nothing below
+  bool chunk;              // many rows: the kernel of fa_paged_chunk.cu
   long long ctas;
   size_t workspace_bytes;  // the pieces' states of the streaming form
 };
@@ -193,7 +193,9 @@ int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const P
                       const PagedPlan& plan, void* workspace, cudaStream_t stream);
 
 // Attention for many query rows (fa_paged_chunk.cu).
-int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, cudaStream_t stream);
+int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, int ctas,
+                       void* workspace, cudaStream_t stream);
+size_t paged_chunk_workspace_bytes(int d, int ctas);
 
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 

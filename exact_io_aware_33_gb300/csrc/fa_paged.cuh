@@ -56,6 +56,22 @@ __device__ __forceinline__ int paged_page(const PagedBatchDev& b, int seq, int i
   return -1;
 }
 
+// r / G for a packed row 0 <= r < 2^31 without a division: with m = floor(2^32
+// / G), r m / 2^32 is less than r / 2^32 < 1 below r / G, so its floor is the
+// quotient or one less, and the remainder tells which.
+struct GroupDiv {
+  int G;
+  uint32_t magic;
+  __host__ static GroupDiv of(int g) {
+    return GroupDiv{g, g == 1 ? 0xffffffffu : static_cast<uint32_t>((1ull << 32) / static_cast<unsigned>(g))};
+  }
+  __device__ __forceinline__ int div(int r) const {
+    int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), magic));
+    if (r - q * G >= G) ++q;
+    return q;
+  }
+};
+
 // Two e4m3 codes (low byte first) to an f16 pair; exact, and a NaN code gives NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
   uint32_t r;

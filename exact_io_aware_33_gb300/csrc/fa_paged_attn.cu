@@ -99,12 +99,19 @@ struct AttnArgs {
   const float* k_scales;
   const float* v_scales;
   int* status;
-  int Hq, Hkv, G;
+  int Hq, Hkv;
+  GroupDiv g;  // G = Hq / Hkv
   int window;
   int row_tiles;   // cluster form: row tiles of the longest packed sequence
   int cluster;     // CTAs per item (cluster form)
   float scale_log2;
 };
+
+// Where row r of a key head stands in o and lse: (token, query head).
+__device__ __forceinline__ long long row_at(const AttnArgs& a, int row0, int h, int r) {
+  const int i = a.g.div(r);
+  return static_cast<long long>(row0 + i) * a.Hq + h * a.g.G + (r - i * a.g.G);
+}
 
 // One sequence's items: its tiles of R rows, and the tiles of kTile keys that any
 // of its queries sees.
@@ -119,7 +126,7 @@ template <int R, int kTile>
 __device__ __forceinline__ SeqGeo seq_geo(const AttnArgs& a, int seq) {
   SeqGeo g;
   g.s = paged_seq(a.batch, seq, a.status);
-  g.rows = g.s.n * a.G;
+  g.rows = g.s.n * a.g.G;
   g.rts = (g.rows + R - 1) / R;
   g.p0 = g.s.len - g.s.n;
   const int hi = g.s.n > 0 ? g.s.len : 0;
@@ -147,8 +154,8 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqGeo& s, 
   g.rows = s.rows;
   g.r0 = rt * R;
   g.p0 = s.p0;
-  g.p_lo = g.p0 + g.r0 / a.G;
-  g.p_hi = g.p0 + (min(g.r0 + R, g.rows) - 1) / a.G;
+  g.p_lo = g.p0 + a.g.div(g.r0);
+  g.p_hi = g.p0 + a.g.div(min(g.r0 + R, g.rows) - 1);
   g.hi = max(g.p_hi + 1, 0);
   g.lo = a.window > 0 ? max(g.p_lo - a.window + 1, 0) : 0;
   return g;
@@ -352,7 +359,7 @@ __device__ __forceinline__ void cluster_sync() {
 template <int D, int kCols>
 __device__ __forceinline__ void store_row(const AttnArgs& a, const SeqGeo& sg, int h, int r, int c0,
                                           const float (&x)[kCols], float lse2) {
-  const long long at = static_cast<long long>(sg.s.row0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const long long at = row_at(a, sg.s.row0, h, r);
   __nv_bfloat16* dst = a.o + at * D + c0;
 #pragma unroll
   for (int i = 0; i < kCols; i += 4)
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       for (int nb = 0; nb < NB; ++nb) {
         const int row = g.r0 + nb * 8 + n;
         const bool on = row < g.rows;
-        const int i = on ? row / a.G : 0, hd = h * a.G + (on ? row % a.G : 0);
+        const int i = on ? a.g.div(row) : 0, hd = h * a.g.G + (on ? row - i * a.g.G : 0);
         const float f = load_query<D>(
             a.q + static_cast<long long>(sg.s.row0 + i) * a.q_stride + hd * D + t * (D / 4), on, a.scale_log2, qb[nb]);
         const int p = on ? g.p0 + i : g.p_hi;
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < kCols; ++i) x[i] *= f;
         if (nan_flag[turn]) {
-          const int p = g.p0 + (g.r0 + wrow) / a.G;
+          const int p = g.p0 + a.g.div(g.r0 + wrow);
           for (int j = max((sg.t0 + tile) * kTile, g.lo); j < min((sg.t0 + tile_end) * kTile, g.hi); ++j) {
             if (all_see(g, j & ~(kGroup - 1), a.window) || !sees(p, j, a.window)) continue;
             const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
@@ -991,7 +998,7 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
     for (int c2 = 0; c2 < kCols; ++c2) x[c2] = fmaf(s_x[wrow][i][lane * kCols + c2], w, x[c2]);
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
-  const long long at = static_cast<long long>(sg.s.row0 + r / a.G) * a.Hq + item / sg.rts * a.G + r % a.G;
+  const long long at = row_at(a, sg.s.row0, item / sg.rts, r);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + at * D + lane * kCols);
 #pragma unroll
   for (int i = 0; i < kCols; i += 2) dst[i / 2] = pack_bf16(x[i] * f, x[i + 1] * f);
@@ -1048,6 +1055,8 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   const long long rows = static_cast<long long>(batch.max_q) * (Hq / pool.num_heads);
   if (rows > 64) {
     r.chunk = true;
+    r.ctas = sms;
+    r.workspace_bytes = paged_chunk_workspace_bytes(pool.d, sms);
     return r;
   }
   r.rows = rows <= 8 ? 8 : 16;
@@ -1073,7 +1082,7 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
 
 int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p,
                       const PagedPlan& plan, void* workspace, cudaStream_t stream) {
-  if (plan.chunk) return launch_paged_chunk(pool, batch, p, stream);
+  if (plan.chunk) return launch_paged_chunk(pool, batch, p, static_cast<int>(plan.ctas), workspace, stream);
   AttnArgs a{};
   a.batch = batch;
   a.q = static_cast<const __nv_bfloat16*>(p.q);
@@ -1087,7 +1096,7 @@ int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const P
   if (!a.status) return -3;
   a.Hq = p.Hq;
   a.Hkv = pool.num_heads;
-  a.G = p.Hq / pool.num_heads;
+  a.g = GroupDiv::of(p.Hq / pool.num_heads);
   a.window = p.window;
   a.row_tiles = plan.row_tiles;
   a.cluster = plan.cluster;

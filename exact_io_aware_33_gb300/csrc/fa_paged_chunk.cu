@@ -29,11 +29,21 @@
 // Rows are packed: row r of a sequence and key head is query r / G, head r % G
 // of the group, so that a group's heads share the key tiles.
 //
+// Division of the work. An item is one sequence, key head and pair of query
+// tiles (256 rows); its steps are the key tiles that any of its rows sees. As
+// in fa_paged_attn.cu the steps of all items, laid end to end, are cut into
+// equal parts, one per CTA, of which each SM has one for the whole call: items
+// number a few per SM and their lengths differ, so whole items would leave
+// SMs idle at the end (512 items on 152 SMs: four rounds instead of 3.4).
+// Pieces of items go to the workspace, normalised, and a second kernel joins
+// them. The TMA warp walks the part and leaves a record of each piece for the
+// other warps, whose rings run on from piece to piece.
+//
 // CTA organisation (512 threads, one CTA per SM):
 //   warps 0-3, 4-7  softmax of query tiles 0 and 1 (thread = row = TMEM lane)
 //   warps 8-11      widening
 //   warp 12         MMA issue and TMEM allocation
-//   warp 13         TMA producer, page and scale lookup
+//   warp 13         TMA producer, walk, page and scale lookup
 //   warps 14, 15    none (they complete the warpgroup that gives registers up)
 
 #include "fa_paged.cuh"
@@ -47,10 +57,16 @@ constexpr int kThreads = 512;
 constexpr int kWidenWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kGroups = kBN / 16;
 constexpr int kInfos = 8;        // tiles' scale records kept
+constexpr int kPieces = 4;       // pieces' records kept
+constexpr int kItemSteps = 3;    // an item costs about this many steps more than it has
+constexpr int kPartSteps = 8;    // a part has at least this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;    // log2 units that a weight may pass its reference by
 constexpr float kPShift = 6.f;   // P is held as 2^6 P
+// Least factor of S: keeps -infinity, where a key is not seen, from meeting a
+// factor that underflowed to 0. |S| stays below 2^37, so it changes nothing.
+constexpr float kLeast = 1e-37f;
 
 // What the softmax and the widening need to know of a tile.
 struct TileInfo {
@@ -62,6 +78,19 @@ struct TileInfo {
   uint32_t vh[kGroups];
   float kr[kGroups];      // by_group: the keys' scale relative to ek (below 0: group absent)
   float vr[kGroups];      // and log2 of the values' scale
+};
+
+// A piece of an item, left by the TMA warp.
+struct Piece {
+  int end;               // 1: no more pieces (the rest is not set)
+  int h, row0, rows;     // key head; packed rows of the sequence: first token row, and their number
+  int p0, r0;            // position of query 0; first packed row of the item
+  int key0, steps;       // first key, and number of key tiles
+  int a0, b0, a1, b1;    // steps that query tiles 0 and 1 take part in
+  int full_lo, full_hi;  // keys that every row of the item sees
+  int whole;             // 1: all of the item
+  int slot;              // workspace slot of a piece that is not
+  int seq;
 };
 
 template <int D>
@@ -77,10 +106,11 @@ struct Cfg {
   static constexpr int kRawKOff = kVOff + kStages * kTileBytes;
   static constexpr int kRawVOff = kRawKOff + kRawBytes;
   static constexpr int kInfoOff = kRawVOff + kRawBytes;
-  static constexpr int kBarOff = kInfoOff + kInfos * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kPieceOff = kInfoOff + kInfos * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kBarOff = kPieceOff + (kPieces * static_cast<int>(sizeof(Piece)) + 7) / 8 * 8;
   enum : int {
-    kBarQFull = 0,
-    kBarRawKFull, kBarRawKEmpty, kBarRawVFull, kBarRawVEmpty,
+    kBarQFull = 0,                      // two
+    kBarRawKFull = kBarQFull + 2, kBarRawKEmpty, kBarRawVFull, kBarRawVEmpty,
     kBarKFull,                          // two of each from here
     kBarKEmpty = kBarKFull + kStages,
     kBarVFull = kBarKEmpty + kStages,
@@ -88,7 +118,9 @@ struct Cfg {
     kBarSFull = kBarVEmpty + kStages,
     kBarPFull = kBarSFull + 2,
     kBarOFinal = kBarPFull + 2,
-    kBarDrain = kBarOFinal + 2,
+    kBarPieceFull = kBarOFinal + 2,
+    kBarPieceEmpty = kBarPieceFull + kPieces,
+    kBarDrain = kBarPieceEmpty + kPieces,
     kNumBars
   };
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -109,14 +141,146 @@ struct ChunkArgs {
   const float* k_scales;
   const float* v_scales;
   int* status;
-  int Hq, Hkv, G;
+  int Hq, Hkv;
+  GroupDiv g;  // G = Hq / Hkv
   int window;
-  int pairs;         // of 256 rows: those of the longest packed sequence and a key head
   float scale_log2;
+  float* part_o;     // [part][2][256][d], normalised
+  float* part_lse;   // [part][2][256], log2 units
+};
+
+// Where row r of a key head stands in o and lse: (token, query head).
+__device__ __forceinline__ long long row_at(const ChunkArgs& a, int row0, int h, int r) {
+  const int i = a.g.div(r);
+  return static_cast<long long>(row0 + i) * a.Hq + h * a.g.G + (r - i * a.g.G);
+}
+
+// The key tiles of an item's two query tiles.
+struct PairGeo {
+  int lo[2], n[2];   // first key tile and number of them, per query tile
+  int first, steps;  // of both together
+};
+
+__device__ __forceinline__ PairGeo pair_geo(const ChunkArgs& a, int rows, int p0, int pair) {
+  PairGeo g;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int r0 = (2 * pair + t) * kBM;
+    const int p_last = p0 + a.g.div(min(r0 + kBM, rows) - 1);
+    const int hi = r0 < rows && p_last >= 0 ? p_last / kBN + 1 : 0;
+    g.lo[t] = a.window > 0 ? max(p0 + a.g.div(r0) - a.window + 1, 0) / kBN : 0;
+    g.n[t] = max(hi - g.lo[t], 0);
+  }
+  g.first = g.n[0] == 0 ? g.lo[1] : g.n[1] == 0 ? g.lo[0] : min(g.lo[0], g.lo[1]);
+  g.steps = max(max(g.n[0] > 0 ? g.lo[0] + g.n[0] : 0, g.n[1] > 0 ? g.lo[1] + g.n[1] : 0) - g.first, 0);
+  return g;
+}
+
+__device__ __forceinline__ int pairs_of(int rows) { return (rows + 2 * kBM - 1) / (2 * kBM); }
+
+// The units (steps, and kItemSteps per item) of a sequence, by one lane. Its
+// items come pair by pair, key head by key head.
+__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const PagedSeq& s) {
+  const int rows = s.n * a.g.G, pairs = pairs_of(rows);
+  long long sum = 0;
+  for (int i = 0; i < pairs; ++i) sum += pair_geo(a, rows, s.len - s.n, i).steps + kItemSteps;
+  return sum * a.Hkv;
+}
+
+__device__ __forceinline__ long long scan_sum(long long own) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, own, m);
+    if (lane_id() >= static_cast<uint32_t>(m)) own += x;
+  }
+  return own;
+}
+
+__device__ __forceinline__ long long batch_units(const ChunkArgs& a) {
+  long long sum = 0;
+  for (int b = static_cast<int>(lane_id()); b < a.batch.B; b += 32) sum += seq_units(a, paged_seq(a.batch, b, a.status));
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  return sum;
+}
+
+// Parts that the units are cut into, and the first unit of part c.
+__device__ __forceinline__ int parts_of(long long units, int ctas) {
+  return static_cast<int>(min(static_cast<long long>(ctas), max(units / kPartSteps, 1LL)));
+}
+__device__ __forceinline__ long long part_start(long long units, int parts, int c) {
+  return units * min(c, parts) / parts;
+}
+
+// An item, found from one of its units (all by one warp).
+struct Item {
+  int seq, pair, h;
+  PagedSeq s;
+  PairGeo g;
+  long long first;  // its first unit
+
+  __device__ __forceinline__ long long units() const { return g.steps + kItemSteps; }
+  __device__ __forceinline__ void find(const ChunkArgs& a, long long u) {
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
+      const int b = b0 + static_cast<int>(lane_id());
+      const long long own = b < a.batch.B ? seq_units(a, paged_seq(a.batch, b, a.status)) : 0;
+      const long long end = before + scan_sum(own);
+      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        seq = b0 + i;
+        before = __shfl_sync(0xffffffffu, end - own, i);
+        break;
+      }
+      before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    s = paged_seq(a.batch, seq, a.status);
+    const int rows = s.n * a.g.G, pairs = pairs_of(rows);
+    for (int i0 = 0; i0 < pairs; i0 += 32) {
+      const int i = i0 + static_cast<int>(lane_id());
+      const long long own =
+          i < pairs ? static_cast<long long>(a.Hkv) * (pair_geo(a, rows, s.len - s.n, i).steps + kItemSteps) : 0;
+      const long long end = before + scan_sum(own);
+      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        pair = i0 + k;
+        before = __shfl_sync(0xffffffffu, end - own, k);
+        break;
+      }
+      before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    g = pair_geo(a, rows, s.len - s.n, pair);
+    h = static_cast<int>((u - before) / units());
+    first = before + h * units();
+  }
+  // The next item; false past the last.
+  __device__ __forceinline__ bool next(const ChunkArgs& a) {
+    first += units();
+    if (++h < a.Hkv) return true;
+    h = 0;
+    if (++pair < pairs_of(s.n * a.g.G)) {
+      g = pair_geo(a, s.n * a.g.G, s.len - s.n, pair);
+      return true;
+    }
+    pair = 0;
+    do {
+      if (++seq >= a.batch.B) return false;
+      s = paged_seq(a.batch, seq, a.status);
+    } while (s.n == 0);
+    g = pair_geo(a, s.n * a.g.G, s.len - s.n, 0);
+    return true;
+  }
 };
 
 __device__ __forceinline__ int exponent_of(float x) {
   return static_cast<int>(__float_as_uint(x) >> 23) - 127;  // of a positive normal number
+}
+
+// The lowest n bits (none below 0, all above 31).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -142,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kBarQFull), 8);
     mbar_init(bar(C::kBarRawKFull), 1);
     mbar_init(bar(C::kBarRawKEmpty), 4);
     mbar_init(bar(C::kBarRawVFull), 1);
@@ -154,11 +317,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kBarVEmpty + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(C::kBarQFull + t), 4);
       // the MMAs' completion, and the MMA warp itself, which passes on that
       // the tile's records (and, at the end, the NaN flag) have been written
       mbar_init(bar(C::kBarSFull + t), 2);
       mbar_init(bar(C::kBarPFull + t), 4);
       mbar_init(bar(C::kBarOFinal + t), 2);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar(C::kBarPieceFull + i), 1);
+      mbar_init(bar(C::kBarPieceEmpty + i), 13);  // the softmax, widening and MMA warps
     }
     mbar_init(bar(C::kBarDrain), 1);
     *abort_flag = 0;
@@ -176,36 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  // The item: heaviest (last) pairs of rows first.
-  const int per_pair = a.batch.B * a.Hkv;
-  const int pair = a.pairs - 1 - static_cast<int>(blockIdx.x / per_pair);
-  const int h = static_cast<int>(blockIdx.x % per_pair) % a.Hkv;
-  const int seq = static_cast<int>(blockIdx.x % per_pair) / a.Hkv;
-  const PagedSeq s = paged_seq(a.batch, seq, a.status);
-  const int rows = s.n * a.G, p0 = s.len - s.n;
-  int r0[2], lo_t[2], n_t[2], p_first[2], p_last[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    r0[t] = pair * 2 * kBM + t * kBM;
-    p_first[t] = p0 + r0[t] / a.G;
-    p_last[t] = p0 + (min(r0[t] + kBM, rows) - 1) / a.G;
-    const int hi = r0[t] < rows && p_last[t] >= 0 ? p_last[t] / kBN + 1 : 0;
-    lo_t[t] = a.window > 0 ? max(p_first[t] - a.window + 1, 0) / kBN : 0;
-    n_t[t] = max(hi - lo_t[t], 0);
-  }
-  const int j_first = n_t[0] == 0 ? lo_t[1] : n_t[1] == 0 ? lo_t[0] : min(lo_t[0], lo_t[1]);
-  const int j_end = max(n_t[0] > 0 ? lo_t[0] + n_t[0] : 0, n_t[1] > 0 ? lo_t[1] + n_t[1] : 0);
-  const int n_stream = max(j_end - j_first, 0);
-  const int a0 = lo_t[0] - j_first, b0 = a0 + n_t[0], a1 = lo_t[1] - j_first, b1 = a1 + n_t[1];
-  // keys that every row of the CTA sees lie in [full_lo, full_hi]
-  const int full_hi = p_first[0];
-  const int full_lo = a.window > 0 ? (r0[1] < rows ? p_last[1] : p_last[0]) - a.window + 1 : 0;
-  // keys that any row sees lie in [key_lo, key_end)
-  const int key_lo = a.window > 0 ? max(p_first[0] - a.window + 1, 0) : 0;
-  const int key_end = max(max(p_last[0], r0[1] < rows ? p_last[1] : 0) + 1, 0);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieceOff);
+  // Hands piece number i to a consuming warp; false when the CTA gave up.
+  auto get_piece = [&](int i, Piece* p) -> bool {
+    if (!mbar_wait_w(bar(C::kBarPieceFull + i % kPieces), (i / kPieces) & 1, abort_flag)) return false;
+    *p = pieces[i % kPieces];
+    mbar_arrive_warp(bar(C::kBarPieceEmpty + i % kPieces));
+    return true;
+  };
 
   if (warp >= kMmaWarp) {
-    regs_decrease<56>();
+    regs_decrease<80>();
     if (warp == kLoadWarp) {
       // ---------------------------------------------------------- TMA warp
       tma_prefetch_map(&tmK);
@@ -213,94 +362,154 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Lane i looks up the i-th of 32 groups of 16 keys (four tiles): its
       // page, then its scales. The next four tiles' loads are under way while
       // the present ones are issued.
-      const int box_rows = min(a.batch.page_size, kBN), boxes = kBN / box_rows, per_box = box_rows / 16;
-      int n_page = -1;
-      float n_sk = 1.f, n_sv = 1.f;
-      bool n_want = false;
-      auto look = [&](int step) {
-        const int j0 = (j_first + step) * kBN + lane * 16;
-        n_want = step + (lane >> 3) < n_stream && j0 < key_end && j0 + 16 > key_lo;
-        n_page = n_want ? paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status) : -1;
-      };
-      auto scales = [&]() {
-        n_sk = n_sv = 1.f;
-        if (n_page >= 0) {
-          const long long at = static_cast<long long>(n_page) * a.Hkv + h;
-          n_sk = a.k_scales[at];
-          n_sv = a.v_scales[at];
-        }
-      };
+      const int box_rows = min(a.batch.page_size, kBN), per_box = box_rows / 16;
+      const uint32_t box_bytes = static_cast<uint32_t>(box_rows * D);
+      const long long units = batch_units(a);
+      const int parts = parts_of(units, gridDim.x);
+      long long u = part_start(units, parts, blockIdx.x);
+      const long long u1 = part_start(units, parts, blockIdx.x + 1);
       bool ok = true;
+      int gs = 0;   // steps so far: the rings run on
+      int np = 0;   // pieces so far
       int k_copies = 0, v_copies = 0;
-      look(0);
-      scales();
-      for (int base4 = 0; base4 < n_stream && ok; base4 += 4) {
-        const int page = n_page;
-        const float sk = n_sk, sv = n_sv;
-        const bool on = page >= 0, missing = n_want && !on;
-        look(base4 + 4);
-        // the four tiles' scales, eight lanes each
-        const bool pow2 = (__float_as_uint(sk) & 0x7fffffu) == 0 && (__float_as_uint(sv) & 0x7fffffu) == 0 &&
-                          sk > 0.f && sv > 0.f && sk < INFINITY && sv < INFINITY;
-        const int ke = on ? exponent_of(sk) : -1000, ve = on ? exponent_of(sv) : -1000;
-        int kmax = ke, vmax = ve, kmin = on ? ke : 1000, vmin = on ? ve : 1000;
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
-          kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, d));
-          vmax = max(vmax, __shfl_xor_sync(0xffffffffu, vmax, d));
-          kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, d));
-          vmin = min(vmin, __shfl_xor_sync(0xffffffffu, vmin, d));
+      auto put_piece = [&](const Piece& p) {
+        if (np >= kPieces)
+          ok = mbar_wait_w(bar(C::kBarPieceEmpty + np % kPieces), (np / kPieces - 1) & 1, abort_flag);
+        if (!ok) return;
+        if (lane == 0) {
+          pieces[np % kPieces] = p;
+          mbar_arrive(bar(C::kBarPieceFull + np % kPieces));
         }
-        const uint32_t mine = 0xffu << (lane & 24);
-        const bool by_group = (__ballot_sync(0xffffffffu, (on && !pow2) || missing) & mine) != 0 ||
-                              kmax - kmin > 8 || vmax - vmin > 8;
-        const bool absent = (__ballot_sync(0xffffffffu, !on) & mine) != 0;
-        kmax = min(max(kmax, -126), 126);
-        vmax = min(max(vmax, -126), 126);
-        const float ek = pow2i(kmax);
-        const float kh = by_group ? 1.f : on ? pow2i(ke - kmax) : 0.f, vh = by_group ? 1.f : on ? pow2i(ve - vmax) : 0.f;
-        const float kr = !on ? -1.f : sk / ek, vr = log2f(sv);
-        for (int i = 0; i < 4 && base4 + i < n_stream; ++i) {
-          const int jj = base4 + i;
-          if (i == 2) scales();
-          // lane b: the page of box b of the tile
-          int bp = __shfl_sync(0xffffffffu, page, 8 * i + (lane & 7) * per_box % 8);
-          for (int q = 1; q < per_box; ++q) bp = max(bp, __shfl_sync(0xffffffffu, page, 8 * i + ((lane & 7) * per_box + q) % 8));
-          const bool box = lane < boxes && bp >= 0;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * static_cast<uint32_t>(box_rows * D);
-          const int slot = (lane * box_rows) & (a.batch.page_size - 1), blk = bp * a.Hkv + h;
-          if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawKEmpty), (jj - 1) & 1, abort_flag);
-          if (!ok) break;
-          if (box)
-            tma_load_3d(base + C::kRawKOff + lane * box_rows * D, &tmK, bar(C::kBarRawKFull), 0, slot, blk);
-          if ((lane >> 3) == i) {
-            TileInfo& ti = infos[jj % kInfos];
-            const int g = lane & 7;
-            ti.kh[g] = pack_f16(kh, kh);
-            ti.vh[g] = pack_f16(vh, vh);
-            ti.kr[g] = kr;
-            ti.vr[g] = vr;
-            if (g == 0) {
-              ti.ek = ek;
-              ti.ev = static_cast<float>(vmax);
-              ti.by_group = by_group ? 1 : 0;
-              ti.absent = absent ? 1 : 0;
-            }
+        __syncwarp();
+        ++np;
+      };
+      Item it;
+      bool more = u < u1;
+      if (more) it.find(a, u);
+      for (; more && ok && it.first < u1; more = it.next(a)) {
+        // steps [s0, s1) of the item; one without steps belongs to the part of its first unit
+        const int n = it.g.steps;
+        const int s0 = static_cast<int>(max(u - it.first - kItemSteps, 0LL));
+        const int s1 = static_cast<int>(min(max(u1 - it.first - kItemSteps, 0LL), static_cast<long long>(n)));
+        if (n > 0 ? s1 <= s0 : it.first < u) continue;
+        const int rows = it.s.n * a.g.G, p0 = it.s.len - it.s.n, h = it.h, seq = it.seq;
+        const int r0 = it.pair * 2 * kBM;
+        const int p_first = p0 + a.g.div(r0), p_last = p0 + a.g.div(min(r0 + 2 * kBM, rows) - 1);
+        const int first_tile = it.g.first + s0, steps = s1 - s0;
+        Piece pc;
+        pc.end = 0;
+        pc.seq = seq;
+        pc.h = h;
+        pc.row0 = it.s.row0;
+        pc.rows = rows;
+        pc.p0 = p0;
+        pc.r0 = r0;
+        pc.key0 = first_tile * kBN;
+        pc.steps = steps;
+        pc.a0 = min(max(it.g.lo[0] - first_tile, 0), steps);
+        pc.b0 = max(min(it.g.lo[0] + it.g.n[0] - first_tile, steps), pc.a0);
+        pc.a1 = min(max(it.g.lo[1] - first_tile, 0), steps);
+        pc.b1 = max(min(it.g.lo[1] + it.g.n[1] - first_tile, steps), pc.a1);
+        pc.full_hi = p_first;
+        pc.full_lo = a.window > 0 ? p_last - a.window + 1 : 0;
+        pc.whole = s0 == 0 && s1 == n;
+        pc.slot = static_cast<int>(blockIdx.x) * 2 + (s0 == 0 ? 1 : 0);  // 0: continues an item, 1: begins one
+        put_piece(pc);
+        if (!ok) break;
+        // keys that any row sees lie in [key_lo, key_end)
+        const int key_lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0, key_end = max(p_last + 1, 0);
+        int n_page = -1;
+        float n_sk = 1.f, n_sv = 1.f;
+        bool n_want = false;
+        auto look = [&](int step) {
+          const int j0 = (first_tile + step) * kBN + lane * 16;
+          n_want = step + (lane >> 3) < steps && j0 < key_end && j0 + 16 > key_lo;
+          n_page = n_want ? paged_page(a.batch, seq, j0 >> a.batch.page_shift, a.status) : -1;
+        };
+        auto scales = [&]() {
+          n_sk = n_sv = 1.f;
+          if (n_page >= 0) {
+            const long long at = static_cast<long long>(n_page) * a.Hkv + h;
+            n_sk = a.k_scales[at];
+            n_sv = a.v_scales[at];
           }
-          __syncwarp();
-          // (bytes that have landed already count as well: the phase cannot end before this arrival)
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull), bytes);
-          ++k_copies;
-          if (jj >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (jj - 1) & 1, abort_flag);
-          if (!ok) break;
-          if (box)
-            tma_load_3d(base + C::kRawVOff + lane * box_rows * D, &tmV, bar(C::kBarRawVFull), 0, slot, blk);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawVFull), bytes);
-          ++v_copies;
+        };
+        look(0);
+        scales();
+        for (int base4 = 0; base4 < steps && ok; base4 += 4) {
+          const int page = n_page;
+          const float sk = n_sk, sv = n_sv;
+          const bool on = page >= 0, missing = n_want && !on;
+          look(base4 + 4);
+          // this lane's box: its groups share a page, or have none to read
+          int box_page = page;
+          if (per_box > 1) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 1));
+          if (per_box > 2) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 2));
+          if (per_box > 4) box_page = max(box_page, __shfl_xor_sync(0xffffffffu, box_page, 4));
+          const int grp = lane & 7;
+          const bool issues = grp % per_box == 0 && box_page >= 0;
+          const uint32_t issuers = __ballot_sync(0xffffffffu, issues);
+          const int slot = (grp * 16) & (a.batch.page_size - 1), blk = box_page * a.Hkv + h;
+          // the four tiles' scales, eight lanes each
+          const bool pow2 = (__float_as_uint(sk) & 0x7fffffu) == 0 && (__float_as_uint(sv) & 0x7fffffu) == 0 &&
+                            sk > 0.f && sv > 0.f && sk < INFINITY && sv < INFINITY;
+          const int ke = on ? exponent_of(sk) : -1000, ve = on ? exponent_of(sv) : -1000;
+          int kmax = ke, vmax = ve, kmin = on ? ke : 1000, vmin = on ? ve : 1000;
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) {
+            kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, d));
+            vmax = max(vmax, __shfl_xor_sync(0xffffffffu, vmax, d));
+            kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, d));
+            vmin = min(vmin, __shfl_xor_sync(0xffffffffu, vmin, d));
+          }
+          const uint32_t mine = 0xffu << (lane & 24);
+          const bool by_group = (__ballot_sync(0xffffffffu, (on && !pow2) || missing) & mine) != 0 ||
+                                kmax - kmin > 8 || vmax - vmin > 8;
+          const bool absent = (__ballot_sync(0xffffffffu, !on) & mine) != 0;
+          kmax = min(max(kmax, -126), 126);
+          vmax = min(max(vmax, -126), 126);
+          const float ek = pow2i(kmax);
+          const float kh = by_group ? 1.f : on ? pow2i(ke - kmax) : 0.f;
+          const float vh = by_group ? 1.f : on ? pow2i(ve - vmax) : 0.f;
+          const float kr = !on ? -1.f : sk / ek, vr = log2f(sv);
+          for (int i = 0; i < 4 && base4 + i < steps; ++i, ++gs) {
+            if (i == 2) scales();
+            const uint32_t bytes = __popc(issuers & (0xffu << (8 * i))) * box_bytes;
+            const bool own = (lane >> 3) == i;
+            if (gs >= 1) ok = mbar_wait_w(bar(C::kBarRawKEmpty), (gs - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (own) {
+              if (issues) tma_load_3d(base + C::kRawKOff + grp * 16 * D, &tmK, bar(C::kBarRawKFull), 0, slot, blk);
+              TileInfo& ti = infos[gs % kInfos];
+              ti.kh[grp] = pack_f16(kh, kh);
+              ti.vh[grp] = pack_f16(vh, vh);
+              ti.kr[grp] = kr;
+              ti.vr[grp] = vr;
+              if (grp == 0) {
+                ti.ek = ek;
+                ti.ev = static_cast<float>(vmax);
+                ti.by_group = by_group ? 1 : 0;
+                ti.absent = absent ? 1 : 0;
+              }
+            }
+            __syncwarp();
+            // (bytes that have landed already count as well: the phase cannot end before this arrival)
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull), bytes);
+            ++k_copies;
+            if (gs >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (gs - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (own && issues)
+              tma_load_3d(base + C::kRawVOff + grp * 16 * D, &tmV, bar(C::kBarRawVFull), 0, slot, blk);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawVFull), bytes);
+            ++v_copies;
+          }
         }
-        if (base4 + 2 >= n_stream) break;  // (fewer than three tiles in this batch: none follows)
+        u = max(u, it.first);  // from the next item on
       }
+      Piece last{};
+      last.end = 1;
+      if (ok) put_piece(last);
       // Let the copies in flight land before the CTA can end, whoever gives up:
       // each buffer's last phase (over already unless someone did).
       if (k_copies > 0) mbar_wait(bar(C::kBarRawKFull), (k_copies - 1) & 1, nullptr);
@@ -309,22 +518,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issue
       constexpr uint32_t kIdS = idesc_f16_f32(kBM, kBN, false, false);
       constexpr uint32_t kIdO = idesc_f16_f32(kBM, D, false, true);
-      bool ok = n_stream > 0 ? mbar_wait_w(bar(C::kBarQFull), 0, abort_flag) : false;
-      tc_fence_after();
+      bool ok = true;
+      int gs0 = 0;         // ring position of the piece's first step
       int k_ready = -1;
-      auto ensure_k = [&](int jj) {
-        if (ok && jj > k_ready) {
-          ok = mbar_wait_w(bar(C::kBarKFull + jj % C::kStages), (jj / C::kStages) & 1, abort_flag);
+      auto ensure_k = [&](int g) {
+        if (ok && g > k_ready) {
+          ok = mbar_wait_w(bar(C::kBarKFull + g % C::kStages), (g / C::kStages) & 1, abort_flag);
           tc_fence_after();
-          k_ready = jj;
+          k_ready = g;
         }
       };
       const uint64_t dQ0 = sdesc_sw128(base + C::kQOff, 16, 1024);
       const uint64_t dK0 = sdesc_sw128(base + C::kKOff, 16, 1024);
       const uint64_t dV0 = sdesc_sw128(base + C::kVOff, C::kChunkBytes, 1024);
-      auto issue_s = [&](int t, int jj) {
+      auto issue_s = [&](int t, int g) {
         const uint64_t q = dQ0 + static_cast<uint64_t>(t * C::kTileBytes >> 4);
-        const uint64_t k = dK0 + static_cast<uint64_t>((jj % C::kStages) * (C::kTileBytes >> 4));
+        const uint64_t k = dK0 + static_cast<uint64_t>((g % C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4);
@@ -333,56 +542,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_w(bar(C::kBarSFull + t));
         mbar_arrive_warp(bar(C::kBarSFull + t));
       };
-      auto issue_pv = [&](int t, int jj, bool first) {
-        const uint64_t v = dV0 + static_cast<uint64_t>((jj % C::kStages) * (C::kTileBytes >> 4));
+      auto issue_pv = [&](int t, int g, bool first) {
+        const uint64_t v = dV0 + static_cast<uint64_t>((g % C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           mma_ts_w(tmem + C::kColO + t * D, tmem + t * kBN + kk * 8, v + 128 * kk, kIdO,
                    (!first || kk > 0) ? 1u : 0u);
       };
-      auto step_of = [&](int t, int jj) -> int {  // tile-local step, or -1
-        const int x = t == 0 ? a0 : a1, y = t == 0 ? b0 : b1;
-        return (jj >= x && jj < y) ? jj - x : -1;
-      };
       // P overwrites S: each tile's next QK^T is issued after its P.V. Step
       // jj: per tile, the P.V of key tile jj, then the QK^T of jj + 1 (the
       // first step, -1, has none of the former). One copy of the code for
       // both tiles: the loops of the four roles share the instruction cache.
+      int done0 = 0, done1 = 0;  // steps of each query tile before this piece
+      int with0 = 0, with1 = 0;  // pieces that each had steps in before this one
+      for (int np = 0; ok; ++np) {
+        Piece pc;
+        ok = get_piece(np, &pc);
+        if (!ok || pc.end) break;
+        const int n = pc.steps;
+        if (n == 0) continue;
+        const int a0 = pc.a0, b0 = pc.b0, a1 = pc.a1, b1 = pc.b1;
+        auto step_of = [&](int t, int jj) -> int {  // tile-local step, or -1
+          const int x = t == 0 ? a0 : a1, y = t == 0 ? b0 : b1;
+          return (jj >= x && jj < y) ? jj - x : -1;
+        };
 #pragma unroll 1
-      for (int jj = -1; jj < n_stream && ok; ++jj) {
-        if (jj >= 0) {
-          ok = mbar_wait_w(bar(C::kBarVFull + jj % C::kStages), (jj / C::kStages) & 1, abort_flag);
-          tc_fence_after();
-        }
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          const int u = step_of(t, jj);
-          if (ok && u >= 0) {
-            ok = mbar_wait_w(bar(C::kBarPFull + t), u & 1, abort_flag);
-            if (!ok) break;
+        for (int jj = -1; jj < n && ok; ++jj) {
+          const int g = gs0 + jj;
+          if (jj >= 0) {
+            ok = mbar_wait_w(bar(C::kBarVFull + g % C::kStages), (g / C::kStages) & 1, abort_flag);
             tc_fence_after();
-            issue_pv(t, jj, u == 0);
-            if (jj + 1 >= (t == 0 ? b0 : b1)) {
-              mma_commit_w(bar(C::kBarOFinal + t));
-              mbar_arrive_warp(bar(C::kBarOFinal + t));
+          }
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int u = step_of(t, jj);
+            if (ok && u >= 0) {
+              ok = mbar_wait_w(bar(C::kBarPFull + t), ((t == 0 ? done0 : done1) + u) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(t, g, u == 0);
+              if (jj + 1 >= (t == 0 ? b0 : b1)) {
+                mma_commit_w(bar(C::kBarOFinal + t));
+                mbar_arrive_warp(bar(C::kBarOFinal + t));
+              }
+            }
+            if (ok && step_of(t, jj + 1) >= 0) {
+              ensure_k(g + 1);
+              if (ok && u < 0) {  // the tile's first step: its queries
+                ok = mbar_wait_w(bar(C::kBarQFull + t), (t == 0 ? with0 : with1) & 1, abort_flag);
+                tc_fence_after();
+              }
+              if (!ok) break;
+              issue_s(t, g + 1);
             }
           }
-          if (ok && step_of(t, jj + 1) >= 0) {
-            ensure_k(jj + 1);
-            if (!ok) break;
-            issue_s(t, jj + 1);
+          if (!ok) break;
+          if (jj >= 0) mma_commit_w(bar(C::kBarVEmpty + g % C::kStages));
+          if (jj + 1 < n) {
+            ensure_k(g + 1);  // (a step that no tile takes part in)
+            if (ok) mma_commit_w(bar(C::kBarKEmpty + (g + 1) % C::kStages));
           }
         }
-        if (!ok) break;
-        if (jj >= 0) mma_commit_w(bar(C::kBarVEmpty + jj % C::kStages));
-        if (jj + 1 < n_stream) mma_commit_w(bar(C::kBarKEmpty + (jj + 1) % C::kStages));
+        gs0 += n;
+        done0 += b0 - a0;
+        done1 += b1 - a1;
+        with0 += b0 > a0;
+        with1 += b1 > a1;
       }
       // let every MMA this warp issued finish before TMEM is released
       mma_commit_w(bar(C::kBarDrain));
       mbar_wait_w(bar(C::kBarDrain), 0, nullptr);
     }
   } else if (warp >= kWidenWarp) {
-    regs_decrease<88>();
+    regs_decrease<80>();
     // ------------------------------------------------------------ widening
     // Eight codes per thread and step become one 16-byte unit of the widened
     // row. The eight lanes of a store phase hold the eight units of one row,
@@ -395,297 +627,387 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t dst0 = static_cast<uint32_t>(row0 * 128 + ((unit ^ (row0 & 7)) << 4));
     bool ok = true;
     bool saw_nan = false;
+    int gs0 = 0;
+    for (int np = 0; ok; ++np) {
+      Piece pc;
+      ok = get_piece(np, &pc);
+      if (!ok || pc.end) break;
+      const int full_lo = pc.full_lo, full_hi = pc.full_hi;
 #pragma unroll 1
-    for (int w2 = 0; w2 < 2 * n_stream && ok; ++w2) {  // keys and values in turn
-      const int jj = w2 >> 1, st = jj % C::kStages;
-      const bool values = w2 & 1;
-      const TileInfo& ti = infos[jj % kInfos];
-      const int key0 = (j_first + jj) * kBN;
-      const uint8_t* raw = smem + (values ? C::kRawVOff : C::kRawKOff) + src0;
-      uint8_t* out = smem + (values ? C::kVOff : C::kKOff) + st * C::kTileBytes + dst0;
-      ok = mbar_wait_w(bar(values ? C::kBarRawVFull : C::kBarRawKFull), jj & 1, abort_flag);
-      if (ok && jj >= C::kStages)
-        ok = mbar_wait_w(bar((values ? C::kBarVEmpty : C::kBarKEmpty) + st), ((jj / C::kStages) + 1) & 1, abort_flag);
-      if (!ok) break;
-      const uint32_t* ratios = values ? ti.vh : ti.kh;
-      // Values of keys that some row does not see: 0 x NaN is NaN, so no code
-      // of theirs may be one. Groups without a page: nothing was loaded.
-      const bool check = ti.absent || (values && (key0 + kBN - 1 > full_hi || key0 < full_lo));
-      // Codes are fetched eight units ahead of the stores: the compiler cannot
-      // move a shared load above a shared store itself, and one unit at a time
-      // is all latency (115 cycles each, against about 12 instructions).
-      constexpr int kUnits = kSteps * C::kChunks, kBatch = 8;
-      uint2 w[kUnits];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
-#pragma unroll
-      for (int b = 0; b < kUnits; b += kBatch) {
-        if (b + kBatch < kUnits) {
-#pragma unroll
-          for (int i = b + kBatch; i < b + 2 * kBatch; ++i)
-            w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
-        }
-        uint32_t ratio[kBatch / C::kChunks];
-#pragma unroll
-        for (int i = 0; i < kBatch / C::kChunks; ++i) ratio[i] = ratios[b / C::kChunks + i];
-        if (check) {
-#pragma unroll
-          for (int i = b; i < b + kBatch; ++i) {
-            const int g = i / C::kChunks;
-            if (ti.kr[g] < 0.f) w[i] = make_uint2(0, 0);
-            if (values && (key0 + g * 16 + 15 > full_hi || key0 + g * 16 < full_lo)) {
-              const uint2 z = make_uint2(nan_bytes(w[i].x), nan_bytes(w[i].y));
-              saw_nan = saw_nan || (z.x | z.y) != 0;
-              w[i] = make_uint2(w[i].x & ~z.x, w[i].y & ~z.y);
-            }
+      for (int w2 = 0; w2 < 2 * pc.steps && ok; ++w2) {  // keys and values in turn
+        const int g = gs0 + (w2 >> 1), st = g % C::kStages;
+        const bool values = w2 & 1;
+        const TileInfo& ti = infos[g % kInfos];
+        const int key0 = pc.key0 + (w2 >> 1) * kBN;
+        uint8_t* raw = smem + (values ? C::kRawVOff : C::kRawKOff) + src0;
+        uint8_t* out = smem + (values ? C::kVOff : C::kKOff) + st * C::kTileBytes + dst0;
+        ok = mbar_wait_w(bar(values ? C::kBarRawVFull : C::kBarRawKFull), g & 1, abort_flag);
+        if (ok && g >= C::kStages)
+          ok = mbar_wait_w(bar((values ? C::kBarVEmpty : C::kBarKEmpty) + st), ((g / C::kStages) + 1) & 1, abort_flag);
+        if (!ok) break;
+        const uint32_t* ratios = values ? ti.vh : ti.kh;
+        if (ti.absent) {  // groups without a page: nothing was loaded
+#pragma unroll 1
+          for (int q = 0; q < kSteps; ++q) {
+            if (ti.kr[q] >= 0.f) continue;
+            for (int cb = 0; cb < C::kChunks; ++cb)
+              *reinterpret_cast<uint2*>(raw + q * 16 * D + cb * 64) = make_uint2(0, 0);
           }
         }
+        // Values of keys that some row does not see: 0 x NaN is NaN, so no code
+        // of theirs may be one.
+        bool check = values && (key0 + kBN - 1 > full_hi || key0 < full_lo);
+        // Codes are fetched eight units ahead of the stores: the compiler cannot
+        // move a shared load above a shared store itself, and one unit at a time
+        // is all latency (115 cycles each, against about 12 instructions).
+        constexpr int kUnits = kSteps * C::kChunks, kBatch = 8;
+        uint2 w[kUnits];
+      again:
 #pragma unroll
-        for (int i = b; i < b + kBatch; ++i) {
-          const uint32_t r = ratio[(i - b) / C::kChunks];
-          *reinterpret_cast<uint4*>(out + i / C::kChunks * 2048 + i % C::kChunks * C::kChunkBytes) =
-              make_uint4(hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x)), r),
-                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x >> 16)), r),
-                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y)), r),
-                         hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y >> 16)), r));
+        for (int i = 0; i < kBatch; ++i)
+          w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
+#pragma unroll
+        for (int b = 0; b < kUnits; b += kBatch) {
+          if (b + kBatch < kUnits) {
+#pragma unroll
+            for (int i = b + kBatch; i < b + 2 * kBatch; ++i)
+              w[i] = *reinterpret_cast<const uint2*>(raw + i / C::kChunks * 16 * D + i % C::kChunks * 64);
+          }
+          if (check) {
+            uint32_t z = 0;  // the top bit of a byte that holds a NaN code
+#pragma unroll
+            for (int i = b; i < b + kBatch; ++i)
+              z |= ((w[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[i].y & 0x7f7f7f7fu) + 0x01010101u);
+            if (z & 0x80808080u) {
+              // rare: put this thread's codes right where they lie, and begin again
+              check = false;
+#pragma unroll 1
+              for (int q = 0; q < kSteps; ++q) {
+                if (key0 + q * 16 + 15 <= full_hi && key0 + q * 16 >= full_lo) continue;
+#pragma unroll 1
+                for (int cb = 0; cb < C::kChunks; ++cb) {
+                  uint2* at = reinterpret_cast<uint2*>(raw + q * 16 * D + cb * 64);
+                  const uint2 v = *at, n = make_uint2(nan_bytes(v.x), nan_bytes(v.y));
+                  saw_nan = saw_nan || (n.x | n.y) != 0;
+                  *at = make_uint2(v.x & ~n.x, v.y & ~n.y);
+                }
+              }
+              goto again;
+            }
+          }
+          uint32_t ratio[kBatch / C::kChunks];
+#pragma unroll
+          for (int i = 0; i < kBatch / C::kChunks; ++i) ratio[i] = ratios[b / C::kChunks + i];
+#pragma unroll
+          for (int i = b; i < b + kBatch; ++i) {
+            const uint32_t r = ratio[(i - b) / C::kChunks];
+            *reinterpret_cast<uint4*>(out + i / C::kChunks * 2048 + i % C::kChunks * C::kChunkBytes) =
+                make_uint4(hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x)), r),
+                           hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x >> 16)), r),
+                           hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y)), r),
+                           hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y >> 16)), r));
+          }
         }
+        if (saw_nan) *nan_flag = 1;
+        fence_async_smem();
+        mbar_arrive_warp(bar((values ? C::kBarVFull : C::kBarKFull) + st));
+        mbar_arrive_warp(bar(values ? C::kBarRawVEmpty : C::kBarRawKEmpty));
       }
-      if (saw_nan) *nan_flag = 1;
-      fence_async_smem();
-      mbar_arrive_warp(bar((values ? C::kBarVFull : C::kBarKFull) + st));
-      mbar_arrive_warp(bar(values ? C::kBarRawVEmpty : C::kBarRawKEmpty));
+      gs0 += pc.steps;
     }
   } else {
-    regs_increase<184>();
+    regs_increase<176>();
     // ------------------------------------------------------------ softmax
     const int t = warp / 4;
-    const int n_mine = n_t[t], row0_tile = r0[t];
-    const int step0 = t == 0 ? a0 : a1;
-    const int r = row0_tile + (threadIdx.x & 127);  // packed row
-    const bool live = r < rows;
-    const int i = live ? r / a.G : 0, hd = h * a.G + (live ? r % a.G : 0);
-    const int p = live ? p0 + i : p_last[t];
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + t * kBN;
     const uint32_t tO = tmem + lane_base + C::kColO + t * D;
     uint8_t* q_tile = smem + C::kQOff + t * C::kTileBytes;
-    float qf = 0.f;
-    if (n_stream > 0) {
-      // this row's query, scaled into f16 by a power of two (exact within 2^27 of its largest value)
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(s.row0 + i) * a.q_stride + hd * D);
-      uint4 w[D / 8];
-      float m = 0.f;
+    // ring position, and this tile's steps and pieces with steps, before this piece
+    int gs0 = 0, done = 0, finals = 0;
+    Piece pc;
+    bool ok = get_piece(0, &pc);
+    // This thread's query of a piece, fetched while the piece before it is written back.
+    uint4 qw[D / 8];
+    auto fetch_query = [&](const Piece& x) {
+      const int r = x.r0 + t * kBM + (threadIdx.x & 127), i = a.g.div(r);
+      const bool on = !x.end && r < x.rows && (t == 0 ? x.b0 > x.a0 : x.b1 > x.a1);
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(x.row0 + i) * a.q_stride +
+                                                        (x.h * a.g.G + (r - i * a.g.G)) * D);
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        w[u] = live ? src[u] : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      for (int u = 0; u < D / 8; ++u) qw[u] = on ? src[u] : make_uint4(0, 0, 0, 0);
+    };
+    if (ok) fetch_query(pc);
+    for (int np = 0; ok && !pc.end; ++np) {
+      const int rows = pc.rows, row0_tile = pc.r0 + t * kBM, h = pc.h, seq = pc.seq;
+      const int step0 = t == 0 ? pc.a0 : pc.a1, n_mine = (t == 0 ? pc.b0 : pc.b1) - step0;
+      const int r = row0_tile + (threadIdx.x & 127);  // packed row
+      const bool live = r < rows;
+      const int i = live ? a.g.div(r) : 0, hd = h * a.g.G + (live ? r - i * a.g.G : 0);
+      const int p_first = pc.p0 + a.g.div(row0_tile), p_last = pc.p0 + a.g.div(min(row0_tile + kBM, rows) - 1);
+      const int p = live ? pc.p0 + i : p_last;
+      const int full_lo = pc.full_lo, full_hi = pc.full_hi;
+      float qf = 0.f;
+      if (n_mine > 0) {
+        // scaled into f16 by a power of two (exact within 2^27 of the row's largest value)
+        float m = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          m = max3(m, fabsf(__uint_as_float(x[q] << 16)), fabsf(__uint_as_float(x[q] & 0xffff0000u)));
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t x[4] = {qw[u].x, qw[u].y, qw[u].z, qw[u].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            m = max3(m, fabsf(__uint_as_float(x[q] << 16)), fabsf(__uint_as_float(x[q] & 0xffff0000u)));
+        }
+        int k = 13 - exponent_of(m);
+        k = m == 0.f ? 0 : min(max(k, -126), 126);
+        const float up = pow2i(k);
+        qf = a.scale_log2 * pow2i(-k);
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t x[4] = {qw[u].x, qw[u].y, qw[u].z, qw[u].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            f[q] = pack_f16(__uint_as_float(x[q] << 16) * up, __uint_as_float(x[q] & 0xffff0000u) * up);
+          const int tr = threadIdx.x & 127;
+          *reinterpret_cast<uint4*>(q_tile + (u >> 3) * C::kChunkBytes + tr * 128 + (((u & 7) ^ (tr & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        fence_async_smem();
+        mbar_arrive_warp(bar(C::kBarQFull + t));
       }
-      int k = 13 - exponent_of(m);
-      k = m == 0.f ? 0 : min(max(k, -126), 126);
-      const float up = pow2i(k);
-      qf = a.scale_log2 * pow2i(-k);
-#pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        uint32_t f[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          f[q] = pack_f16(__uint_as_float(x[q] << 16) * up, __uint_as_float(x[q] & 0xffff0000u) * up);
-        const int tr = threadIdx.x & 127;
-        *reinterpret_cast<uint4*>(q_tile + (u >> 3) * C::kChunkBytes + tr * 128 + (((u & 7) ^ (tr & 7)) << 4)) =
-            make_uint4(f[0], f[1], f[2], f[3]);
-      }
-      fence_async_smem();
-      mbar_arrive_warp(bar(C::kBarQFull));
-    }
 
-    float ms = -INFINITY, mt = -INFINITY, l = 0.f;  // references (log2 units) and denominator
-    bool ok = true;
-    for (int u = 0; u < n_mine; ++u) {
-      const int key0 = (j_first + step0 + u) * kBN;
-      ok = mbar_wait_w(bar(C::kBarSFull + t), u & 1, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const TileInfo& ti = infos[(step0 + u) % kInfos];
-      uint32_t sr[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
-      const float sl2 = qf * ti.ek, ev = ti.ev;
-      const bool by_group = ti.by_group != 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
-      float x[128];
-#pragma unroll
-      for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c >> 5][c & 31]);
-      if (key0 + kBN - 1 > p_first[t] || (a.window > 0 && key0 <= p_last[t] - a.window)) {
-        const int lim_hi = p + 1 - key0, lim_lo = a.window > 0 ? p - a.window + 1 - key0 : 0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= lim_hi || c < lim_lo) x[c] = -INFINITY;
-      }
-      const float m_tile = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96)) * sl2;
-      const float ms_old = ms, mt_old = mt;
-      bool moved = m_tile > fminf(ms, mt - ev) + kSlack;
-      if (moved && !by_group) {
-        ms = fmaxf(ms, m_tile);
-        mt = fmaxf(mt, m_tile + ev);
-      }
-      float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
-      // P = 2^(x sl2 + ev - m_t + 6); the denominator's terms are P 2^(m_t - ev - 6 - m_s),
-      // unless the two references lie too far apart for P not to underflow
-      if (!by_group && !__any_sync(0xffffffffu, su + ev - tu < -60.f)) {
-        const float add = ev - tu + kPShift;
-        const float2 sl2x2 = make_float2(sl2, sl2), add2 = make_float2(add, add);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float2 e2 = __ffma2_rn(make_float2(x[64 * hf + 2 * c], x[64 * hf + 2 * c + 1]), sl2x2, add2);
-            const float2 pr = make_float2(ex2(e2.x), ex2(e2.y));
-            if (c & 1) acc1 = __fadd2_rn(acc1, pr);
-            else acc0 = __fadd2_rn(acc0, pr);
-            pk[c] = pack_f16(pr.x, pr.y);
-          }
-          tmem_st32(tS + 32 * hf, pk);
-        }
-        const float als = moved ? ex2(ms_old - su) : 1.f;
-        l = fmaf(l, als, ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * ex2(tu - ev - kPShift - su));
-      } else {
-        // Group by group from tensor memory again, with the group's scales,
-        // numerators and denominators apart. P of group g takes columns
-        // 8 g .. 8 g + 7, which no later group's S lies in.
-        auto group = [&](int g, float (&y)[16], float* vlog) {
-          uint32_t w[16];
-          tmem_ld16(tS + 16 * g, w);
-          tmem_ld_wait(w);
-          const float kr = by_group ? ti.kr[g] : 1.f;
-          *vlog = by_group ? ti.vr[g] : ev;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int j = key0 + 16 * g + c;
-            // (no page: no key of the group takes part)
-            y[c] = kr >= 0.f && sees(p, j, a.window) ? __uint_as_float(w[c]) * (sl2 * kr) : -INFINITY;
-          }
-        };
-        float vlog;
-#pragma unroll 1
-        for (int g = 0; g < kGroups; ++g) {
-          float y[16], m = -INFINITY;
-          group(g, y, &vlog);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) m = fmaxf(m, y[c]);
-          ms = fmaxf(ms, m);
-          mt = fmaxf(mt, m + vlog);
-        }
-        moved = true;
-        su = ms == -INFINITY ? 0.f : ms;
-        tu = mt == -INFINITY ? 0.f : mt;
-        l *= ex2(ms_old - su);
-#pragma unroll 1
-        for (int g = 0; g < kGroups; ++g) {
-          float y[16];
-          uint32_t pk[8];
-          group(g, y, &vlog);
-          const float add = vlog - tu + kPShift;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            l += ex2(y[2 * c] - su) + ex2(y[2 * c + 1] - su);
-            pk[c] = pack_f16(ex2(y[2 * c] + add), ex2(y[2 * c + 1] + add));
-          }
-          tmem_st8(tS + 8 * g, pk);
-        }
-      }
-      const float alpha = moved ? ex2(mt_old - tu) : 1.f;  // of the accumulator
-      // O is settled: this tile's S was committed after the previous P.V
-      if (u > 0 && __any_sync(0xffffffffu, moved)) {
-        const float2 al2 = make_float2(alpha, alpha);
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_ld_wait(o);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2);
-            o[e] = __float_as_uint(v.x);
-            o[e + 1] = __float_as_uint(v.y);
-          }
-          tmem_st32(tO + c * 32, o);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive_warp(bar(C::kBarPFull + t));
-    }
-    if (ok && row0_tile < rows) {
-      const long long at = static_cast<long long>(s.row0 + i) * a.Hq + hd;
-      if (n_mine > 0) ok = mbar_wait_w(bar(C::kBarOFinal + t), 0, abort_flag);
-      if (ok && n_mine == 0) {
-        if (live) {  // no row of the tile sees a key
-          uint4* dst = reinterpret_cast<uint4*>(a.o + at * D);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-          a.lse[at] = -INFINITY;
-        }
-      } else if (ok) {
+      float ms = -INFINITY, mt = -INFINITY, l = 0.f;  // references (log2 units) and denominator
+      for (int u = 0; u < n_mine; ++u) {
+        const int key0 = pc.key0 + (step0 + u) * kBN;
+        ok = mbar_wait_w(bar(C::kBarSFull + t), (done + u) & 1, abort_flag);
+        if (!ok) break;
         tc_fence_after();
-        const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
-        const float f = l == 0.f ? 0.f : ex2(tu - su - kPShift) / l;
-        // as in the forward: 32 rows x 64 columns at a time through this
-        // warp's part of the Q tile (free by now), so that rows leave as whole lines
-        uint8_t* blk = q_tile + (warp & 3) * 4096;
-        uint8_t* mine = blk + lane * 128;
+        const TileInfo& ti = infos[(gs0 + step0 + u) % kInfos];
+        if (key0 + kBN - 1 > p_first || (a.window > 0 && key0 <= p_last - a.window)) {
+          // Some row does not see some key: columns outside [lo, hi) of S
+          // become -infinity in tensor memory. A rolled loop of its own: with
+          // the selects inside the unrolled code below, that code no longer
+          // fits the instruction cache next to the other roles' (2048 queries
+          // over 8192 keys, hardly any of whose tiles are cut: 430 us, not 403).
+          const int hi = p + 1 - key0, lo = a.window > 0 ? p - a.window + 1 - key0 : 0;
 #pragma unroll 1
-        for (int hh = 0; hh < D / 64; ++hh) {
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w);
+            uint32_t y[32];
+            tmem_ld32(tS + 32 * w, y);
+            tmem_ld_wait(y);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((bits >> c) & 1u)) y[c] = 0xff800000u;
+            tmem_st32(tS + 32 * w, y);
+          }
+          tmem_st_wait();
+        }
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+        const float sl2 = fmaxf(qf * ti.ek, kLeast), ev = ti.ev;
+        const bool by_group = ti.by_group != 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c >> 5][c & 31]);
+        const float m_tile = max3(fmaxf(max32(x), max32(x + 32)), max32(x + 64), max32(x + 96)) * sl2;
+        const float ms_old = ms, mt_old = mt;
+        bool moved = m_tile > fminf(ms, mt - ev) + kSlack;
+        if (moved && !by_group) {
+          ms = fmaxf(ms, m_tile);
+          mt = fmaxf(mt, m_tile + ev);
+        }
+        float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
+        // P = 2^(x sl2 + ev - m_t + 6); the denominator's terms are P 2^(m_t - ev - 6 - m_s),
+        // unless the two references lie too far apart for P not to underflow
+        if (!by_group && !__any_sync(0xffffffffu, su + ev - tu < -60.f)) {
+          const float add = ev - tu + kPShift;
+          const float2 sl2x2 = make_float2(sl2, sl2), add2 = make_float2(add, add);
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 e2 = __ffma2_rn(make_float2(x[64 * hf + 2 * c], x[64 * hf + 2 * c + 1]), sl2x2, add2);
+              const float2 pr = make_float2(ex2(e2.x), ex2(e2.y));
+              if (c & 1) acc1 = __fadd2_rn(acc1, pr);
+              else acc0 = __fadd2_rn(acc0, pr);
+              pk[c] = pack_f16(pr.x, pr.y);
+            }
+            tmem_st32(tS + 32 * hf, pk);
+          }
+          const float als = moved ? ex2(ms_old - su) : 1.f;
+          l = fmaf(l, als, ((acc0.x + acc0.y) + (acc1.x + acc1.y)) * ex2(tu - ev - kPShift - su));
+        } else {
+          // Group by group from tensor memory again, with the group's scales,
+          // numerators and denominators apart. P of group g takes columns
+          // 8 g .. 8 g + 7, which no later group's S lies in.
+          auto group = [&](int g, float (&y)[16], float* vlog) {
+            uint32_t w[16];
+            tmem_ld16(tS + 16 * g, w);
+            tmem_ld_wait(w);
+            const float kr = by_group ? ti.kr[g] : 1.f;
+            *vlog = by_group ? ti.vr[g] : ev;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              // (no page: no key of the group takes part)
+              y[c] = kr >= 0.f ? __uint_as_float(w[c]) * fmaxf(sl2 * kr, kLeast) : -INFINITY;
+            }
+          };
+          float vlog;
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int g = 0; g < kGroups; ++g) {
+            float y[16], m = -INFINITY;
+            group(g, y, &vlog);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) m = fmaxf(m, y[c]);
+            ms = fmaxf(ms, m);
+            mt = fmaxf(mt, m + vlog);
+          }
+          moved = true;
+          su = ms == -INFINITY ? 0.f : ms;
+          tu = mt == -INFINITY ? 0.f : mt;
+          l *= ex2(ms_old - su);
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g) {
+            float y[16];
+            uint32_t pk[8];
+            group(g, y, &vlog);
+            const float add = vlog - tu + kPShift;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              l += ex2(y[2 * c] - su) + ex2(y[2 * c + 1] - su);
+              pk[c] = pack_f16(ex2(y[2 * c] + add), ex2(y[2 * c + 1] + add));
+            }
+            tmem_st8(tS + 8 * g, pk);
+          }
+        }
+        const float alpha = moved ? ex2(mt_old - tu) : 1.f;  // of the accumulator
+        // O is settled: this tile's S was committed after the previous P.V
+        if (u > 0 && __any_sync(0xffffffffu, moved)) {
+          const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(tO + hh * 64 + c * 32, o);
+            tmem_ld32(tO + c * 32, o);
             tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                w[q] = pack_bf16(__uint_as_float(o[8 * e + 2 * q]) * f, __uint_as_float(o[8 * e + 2 * q + 1]) * f);
-              *reinterpret_cast<uint4*>(mine + (((4 * c + e) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2);
+              o[e] = __float_as_uint(v.x);
+              o[e + 1] = __float_as_uint(v.y);
             }
+            tmem_st32(tO + c * 32, o);
           }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int rr = 4 * j + (lane >> 3), v = lane & 7;
-            const uint4 val = *reinterpret_cast<const uint4*>(blk + rr * 128 + ((v ^ (rr & 7)) * 16));
-            const int pr = row0_tile + (warp & 3) * 32 + rr;
-            if (pr < rows)
-              *reinterpret_cast<uint4*>(a.o + (static_cast<long long>(s.row0 + pr / a.G) * a.Hq + h * a.G + pr % a.G) * D +
-                                        hh * 64 + v * 8) = val;
-          }
-          __syncwarp();
         }
-        if (live) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (su + log2f(l));
-        if (*nan_flag && live) {
-          // a NaN code was taken out of a tile that not every row sees: put it into the rows that do
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(bar(C::kBarPFull + t));
+      }
+      if (!ok) break;
+      Piece nx;
+      ok = get_piece(np + 1, &nx);
+      if (!ok) break;
+      fetch_query(nx);
+      if (n_mine > 0) ok = mbar_wait_w(bar(C::kBarOFinal + t), finals & 1, abort_flag);
+      if (!ok) break;
+      if (n_mine > 0) ++finals;
+      done += n_mine;
+      gs0 += pc.steps;
+      if (row0_tile >= rows) {
+        pc = nx;
+        continue;
+      }
+      tc_fence_after();
+      const long long at = static_cast<long long>(pc.row0 + i) * a.Hq + hd;
+      const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
+      const float f = l == 0.f ? 0.f : ex2(tu - su - kPShift) / l;
+      const float lse2 = l == 0.f ? -INFINITY : su + log2f(l);
+      const long long part = static_cast<long long>(pc.slot) * 2 * kBM + t * kBM;  // the tile's first row there
+      if (pc.whole) {
+        if (live) a.lse[at] = kLn2 * lse2;
+      } else {
+        a.part_lse[part + (threadIdx.x & 127)] = lse2;
+      }
+      if (n_mine == 0) {  // no row of the tile sees a key of the piece
+        if (pc.whole && live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o + at * D);
 #pragma unroll 1
-          for (int j = max(a.window > 0 ? p - a.window + 1 : 0, 0); j <= p; ++j) {
-            const int j0 = j & ~15;
-            if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
-            const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
-            if (page < 0) continue;
-            const uint8_t* code = a.v_pages + ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
-                                               (j & (a.batch.page_size - 1))) * D;
+          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+        }
+        pc = nx;
+        continue;
+      }
+      // As in the forward: 32 rows x 128 bytes at a time through this warp's
+      // part of the Q tile (free by now), so that rows leave as whole lines: 64
+      // channels of bf16, or 32 of a piece's fp32.
+      uint8_t* blk = q_tile + (warp & 3) * 4096;
+      uint8_t* mine = blk + lane * 128;
+      const int wr = (warp & 3) * 32;  // first row of the warp in the tile
 #pragma unroll 1
-            for (int c = 0; c < D; ++c)
-              if ((code[c] & 0x7f) == 0x7f) a.o[at * D + c] = __float2bfloat16(__int_as_float(0x7fffffff));
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait(o);
+        if (pc.whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = pack_bf16(__uint_as_float(o[8 * e + 2 * q]) * f, __uint_as_float(o[8 * e + 2 * q + 1]) * f);
+            *reinterpret_cast<uint4*>(mine + (((4 * (c & 1) + e) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if ((c & 1) == 0) continue;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) * 16)) =
+                make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                            __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rr = 4 * j + (lane >> 3), v = lane & 7;
+          const uint4 val = *reinterpret_cast<const uint4*>(blk + rr * 128 + ((v ^ (rr & 7)) * 16));
+          const int pr = row0_tile + wr + rr;
+          if (pr < rows) {
+            if (pc.whole)
+              *reinterpret_cast<uint4*>(a.o + row_at(a, pc.row0, h, pr) * D +
+                                        (c >> 1) * 64 + v * 8) = val;
+            else
+              *reinterpret_cast<uint4*>(a.part_o + (part + wr + rr) * D + c * 32 + v * 4) = val;
+          }
+        }
+        __syncwarp();
+      }
+      if (*nan_flag && live) {
+        // a NaN code was taken out of a tile that not every row sees: put it into the rows that do
+#pragma unroll 1
+        for (int j = max(pc.key0, a.window > 0 ? p - a.window + 1 : 0); j <= min(p, pc.key0 + pc.steps * kBN - 1); ++j) {
+          const int j0 = j & ~15;
+          if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
+          const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
+          if (page < 0) continue;
+          const uint8_t* code = a.v_pages + ((static_cast<long long>(page) * a.Hkv + h) * a.batch.page_size +
+                                             (j & (a.batch.page_size - 1))) * D;
+#pragma unroll 1
+          for (int c = 0; c < D; ++c) {
+            if ((code[c] & 0x7f) != 0x7f) continue;
+            if (pc.whole)
+              a.o[at * D + c] = __float2bfloat16(__int_as_float(0x7fffffff));
+            else
+              a.part_o[(part + (threadIdx.x & 127)) * D + c] = __int_as_float(0x7fffffff);
           }
         }
       }
+      pc = nx;
     }
   }
 
@@ -699,8 +1021,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && *abort_flag) *a.status = kStatusTimeout;
 }
 
+// Joins the pieces of an item that parts c, c + 1, ... share, by the rule of
+// fa_paged_attn.cu's join. Blocks 8 c .. 8 c + 7 take 32 rows each of the item
+// that part c begins and does not end, if there is one. Eight threads per row.
 template <int D>
-int launch_chunk_d(const PagedPool& pool, const ChunkArgs& a, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a, int ctas) {
+  constexpr int kCols = D / 8;
+  // (from the batch's lengths alone, while the kernel before ends, as in fa_paged_attn.cu)
+  const int c = blockIdx.x / 8;
+  const long long units = batch_units(a);
+  const int parts = parts_of(units, ctas);
+  const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
+  Item it;
+  bool work = c + 1 < parts && u0 < u1;
+  long long first = 0;
+  if (work) {
+    it.find(a, u1 - 1);
+    first = it.first + kItemSteps;  // unit of the item's step 0
+    const long long end = u1 - first;
+    work = u0 <= first && end > 0 && end < it.g.steps;
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (!work) return;
+  const int row = blockIdx.x % 8 * 32 + static_cast<int>(threadIdx.x >> 3), c0 = (threadIdx.x & 7) * kCols;
+  const int r = it.pair * 2 * kBM + row;
+  if (r >= it.s.n * a.g.G) return;
+  float m = -INFINITY, sum = 0.f, x[kCols] = {};
+  for (int k = c; k < parts && part_start(units, parts, k) - first < it.g.steps; ++k) {
+    const long long at = (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * 2 * kBM + row;
+    const float ls = a.part_lse[at];
+    if (ls == -INFINITY) continue;  // (nothing of the row: its channels were not written)
+    const float mx = fmaxf(m, ls), alpha = ex2(m - mx), w = ex2(ls - mx);
+    sum = fmaf(sum, alpha, w);
+    const float* src = a.part_o + at * D + c0;
+#pragma unroll
+    for (int i = 0; i < kCols; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src + i);
+      x[i] = fmaf(x[i], alpha, w * v.x);
+      x[i + 1] = fmaf(x[i + 1], alpha, w * v.y);
+      x[i + 2] = fmaf(x[i + 2], alpha, w * v.z);
+      x[i + 3] = fmaf(x[i + 3], alpha, w * v.w);
+    }
+    m = mx;
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const long long at = row_at(a, it.s.row0, it.h, r);
+  uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c0);
+#pragma unroll
+  for (int i = 0; i < kCols; i += 8)
+    dst[i / 8] = make_uint4(pack_bf16(x[i] * f, x[i + 1] * f), pack_bf16(x[i + 2] * f, x[i + 3] * f),
+                            pack_bf16(x[i + 4] * f, x[i + 5] * f), pack_bf16(x[i + 6] * f, x[i + 7] * f));
+  if (c0 == 0) a.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (m + log2f(sum));
+}
+
+template <int D>
+int launch_chunk_d(const PagedPool& pool, const ChunkArgs& a, int ctas, cudaStream_t stream) {
   using C = Cfg<D>;
   CUtensorMap mk, mv;
   const int blocks = pool.num_pages * pool.num_heads;
@@ -710,16 +1086,21 @@ int launch_chunk_d(const PagedPool& pool, const ChunkArgs& a, cudaStream_t strea
   auto kern = paged_chunk_kernel<D>;
   // attribute slots 28, 29
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, D == 64 ? 28 : 29)) return -3;
-  const long long grid = static_cast<long long>(a.pairs) * a.batch.B * a.Hkv;
-  if (grid > 0x7fffffffLL) return -1;
-  const cudaError_t e = launch_overlapped(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), C::kSmemBytes,
-                                          stream, mk, mv, a);
+  // (not overlapped with the kernel before: see launch_rows in fa_paged_attn.cu)
+  cudaError_t e = launch_with(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, false, 1, stream, mk, mv, a);
+  if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
+  e = launch_overlapped(paged_chunk_join_kernel<D>, dim3(8 * (ctas - 1)), dim3(256), 0, stream, a, ctas);
   return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace
 
-int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, cudaStream_t stream) {
+size_t paged_chunk_workspace_bytes(int d, int ctas) {
+  return static_cast<size_t>(ctas) * 2 * 2 * kBM * (d + 1) * sizeof(float);
+}
+
+int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, int ctas,
+                       void* workspace, cudaStream_t stream) {
   ChunkArgs a{};
   a.batch = batch;
   a.q = static_cast<const __nv_bfloat16*>(p.q);
@@ -733,13 +1114,14 @@ int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const 
   if (!a.status) return -3;
   a.Hq = p.Hq;
   a.Hkv = pool.num_heads;
-  a.G = p.Hq / pool.num_heads;
+  a.g = GroupDiv::of(p.Hq / pool.num_heads);
   a.window = p.window;
-  a.pairs = static_cast<int>((static_cast<long long>(batch.max_q) * a.G + 2 * kBM - 1) / (2 * kBM));
   // scale 0 (uniform weights) runs as a tiny positive scale, as in the forward
   const float sl2 = p.scale * kLog2e;
   a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
-  return pool.d == 64 ? launch_chunk_d<64>(pool, a, stream) : launch_chunk_d<128>(pool, a, stream);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o + static_cast<size_t>(ctas) * 2 * 2 * kBM * pool.d;
+  return pool.d == 64 ? launch_chunk_d<64>(pool, a, ctas, stream) : launch_chunk_d<128>(pool, a, ctas, stream);
 }
 
 }  // namespace fa

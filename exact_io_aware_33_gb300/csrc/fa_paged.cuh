@@ -72,6 +72,23 @@ struct GroupDiv {
   }
 };
 
+// Left in the workspace by each part of a divided launch, for the kernel that
+// joins the pieces of items: the item that the part begins and does not end.
+struct JoinRecord {
+  int parts;      // that hold a piece of it, this one first; 0: there is no such item
+  int row0;       // first token row of its sequence
+  int h;          // key head
+  int r0, rows;   // its first packed row, and the sequence's packed rows
+  int pad[3];
+};
+
+// Parts that hold units before `end` from part c on, of `parts` equal parts of
+// `units`: part k starts at floor(k units / parts), which is below `end` for k
+// < end parts / units.
+__device__ __forceinline__ int parts_until(long long end, long long units, int parts, int c) {
+  return static_cast<int>((end * parts + units - 1) / units) - c;
+}
+
 // Two e4m3 codes (low byte first) to an f16 pair; exact, and a NaN code gives NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
   uint32_t r;

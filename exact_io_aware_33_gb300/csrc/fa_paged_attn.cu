@@ -56,6 +56,7 @@ constexpr float kSlack = 8.f;    // log2 units that a weight may pass its refere
 // Each item costs about this many tiles more than it has (its queries, the
 // joining of its four warps, the write-back).
 constexpr int kItemUnits = 2;
+constexpr int kPartUnits = 4;  // a part has at least this many units, and so a tile of an item that it continues
 
 // NB: blocks of eight query rows per CTA.
 // Keys per stage. At d = 64 a tile of 64 would be 8 KiB for the same waiting,
@@ -95,6 +96,7 @@ struct AttnArgs {
   float* lse;
   float* part_o;    // [part][2][16][d], normalised
   float* part_lse;  // [part][2][16], log2 units
+  JoinRecord* records;  // [part]
   const uint8_t* v_pages;  // the rare path that looks for NaN codes again
   const float* k_scales;
   const float* v_scales;
@@ -230,17 +232,22 @@ struct Units {
 template <int R, int kTile>
 struct Walk {
   long long u0, u1;  // this CTA's units
+  long long units;   // of the whole batch, in `parts` parts
+  int parts;
   long long base;    // first unit of sequence b
+  long long seq0;    // and of the sequence that next() gave
   int b;
 
-  __device__ __forceinline__ void start(const AttnArgs& a, int part, int parts) {
-    Units<R, kTile> units;
-    units.start(a);
-    u0 = part_start(units.total, parts, part);
-    u1 = part_start(units.total, parts, part + 1);
+  __device__ __forceinline__ void start(const AttnArgs& a, int part, int ctas) {
+    Units<R, kTile> all;
+    all.start(a);
+    units = all.total;
+    parts = static_cast<int>(min(static_cast<long long>(ctas), max(units / kPartUnits, 1LL)));
+    u0 = part_start(units, parts, min(part, parts));
+    u1 = part_start(units, parts, min(part + 1, parts));
     b = a.batch.B;
     base = 0;
-    if (u0 < u1) b = units.find(a, u0, &base);
+    if (u0 < u1) b = all.find(a, u0, &base);
   }
   // unit -> tile index in the sequence: the first kItemUnits of an item are not tiles
   static __device__ __forceinline__ long long tile_of(long long u, int nt) {
@@ -254,6 +261,7 @@ struct Walk {
       *g = seq_geo<R, kTile>(a, b);
       const long long own = seq_units(a, *g);
       const long long lo = max(u0 - base, 0LL), hi = min(u1 - base, own);
+      seq0 = base;
       base += own;
       ++b;
       if (hi <= lo) continue;
@@ -444,8 +452,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     const int tile_in = lane / kGpt, grp = lane % kGpt;
     const int box_rows = min(a.batch.page_size, kTile), per_box = box_rows / kGroup;
     const uint32_t box_bytes = 2u * box_rows * D;  // of K and V
+    JoinRecord record{};
     while (more) {
       const int seq = walk.b - 1;
+      if (!kCluster && sg.nt > 0) {
+        int item, end;  // of the last tile here
+        split_by(v1 - 1, sg.nt, &item, &end);
+        if (end + 1 < sg.nt && v0 <= static_cast<long long>(item) * sg.nt) {  // begun and not ended
+          const int h = item / sg.rts;
+          record = JoinRecord{parts_until(walk.seq0 + (item + 1LL) * (sg.nt + kItemUnits), walk.units, walk.parts, blockIdx.x),
+                              sg.s.row0, h, (item - h * sg.rts) * R, sg.rows, {}};
+        }
+      }
       long long left = v1 - v0;  // tiles not looked up yet
       int item = 0, tile = 0;
       if (sg.nt > 0) split_by(v0, sg.nt, &item, &tile);
@@ -523,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       if (*abort_flag) break;
       more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
     }
+    if (!kCluster && lane == 0) a.records[blockIdx.x] = record;
     // let every copy in flight land before the CTA can end
     for (uint32_t i = it > kS ? it - kS : 0; i < it; ++i) mbar_wait(full + 8 * (i % kS), (i / kS) & 1, nullptr);
     if (lane == 0 && *abort_flag) *a.status = kStatusTimeout;
@@ -901,52 +920,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
 // parts each and want small blocks, many to an SM; up to four warps and runs of
 // 16 for few items of many parts.
 template <int D, int NB, int kShare>
-__global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const AttnArgs a, int parts) {
-  constexpr int R = 8 * NB, kTile = kTileOf<D>, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
+__global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const AttnArgs a) {
+  constexpr int R = 8 * NB, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
   __shared__ float s_x[R][kShare][D];
   __shared__ float s_m[R][kShare], s_sum[R][kShare];
-  // The geometry comes from the batch's lengths alone, which the kernel before
-  // does not write: it started only when they were settled. So that is worked
-  // out while that kernel ends.
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wrow = warp / kShare, share = warp % kShare;
-  Units<R, kTile> all;
-  all.start(a);
-  const long long units = all.total;
-  const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
-  bool work = u0 < u1;
-  SeqGeo sg{};
-  int item = 0;
-  long long first = 0;
-  if (work) {
-    long long base;
-    const int seq = all.find(a, u1 - 1, &base);
-    sg = seq_geo<R, kTile>(a, seq);
-    const int per = sg.nt + kItemUnits;
-    item = static_cast<int>(div_pos(u1 - 1 - base, per));
-    first = base + static_cast<long long>(item) * per + kItemUnits;  // unit of the item's tile 0
-    const long long end = u1 - first;                                // tiles up to here
-    work = u0 <= first && end > 0 && end < sg.nt;
-  }
   grid_dep_wait();
   grid_dep_launch();
-  if (!work) return;
-  const int r = item % sg.rts * R + wrow;
-  const bool live = r < sg.rows;
-  // part k > c holds tiles of the item when it starts before the item's end; it continues it (piece 0)
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wrow = warp / kShare, share = warp % kShare;
+  const JoinRecord rec = a.records[c];
+  if (rec.parts == 0) return;
+  const int r = rec.r0 + wrow, last = c + rec.parts - 1;
+  const bool live = r < rec.rows;
   float m = -INFINITY, sum = 0.f, x[kCols] = {};
-  for (int k0 = c + share * kRun; live && k0 < parts; k0 += kShare * kRun) {
+  for (int k0 = c + share * kRun; live && k0 <= last; k0 += kShare * kRun) {
     const int k = k0 + lane;
-    const long long s0 = lane < kRun && k < parts ? part_start(units, parts, k) : units;
-    const bool in = lane < kRun && k < parts && s0 - first < sg.nt;
-    if (!__any_sync(0xffffffffu, in)) break;
-    const bool on = in && s0 < part_start(units, parts, k + 1);  // (with fewer units than parts some are empty)
+    const bool on = lane < kRun && k <= last;
+    // part c begins the item (piece 1), the others continue it (piece 0)
     const long long at = (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * R + wrow;
     const float ls = on ? a.part_lse[at] : -INFINITY;
     float v[kRun][kCols];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      // a part without a state: part c's stands in, with weight 0
+      // past the last: part c's state stands in, with weight 0
       const int kj = __shfl_sync(0xffffffffu, on ? k : c, j);
       const float* src = a.part_o + ((static_cast<long long>(kj) * 2 + (kj == c ? 1 : 0)) * R + wrow) * D + lane * kCols;
       if constexpr (kCols == 4) {
@@ -998,7 +994,7 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
     for (int c2 = 0; c2 < kCols; ++c2) x[c2] = fmaf(s_x[wrow][i][lane * kCols + c2], w, x[c2]);
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
-  const long long at = row_at(a, sg.s.row0, item / sg.rts, r);
+  const long long at = row_at(a, rec.row0, rec.h, r);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + at * D + lane * kCols);
 #pragma unroll
   for (int i = 0; i < kCols; i += 2) dst[i / 2] = pack_bf16(x[i] * f, x[i + 1] * f);
@@ -1034,8 +1030,7 @@ int launch_rows(const PagedPool& pool, const AttnArgs& a, const PagedPlan& plan,
     constexpr int kShare = 4 / NB;
     auto join = plan.items < plan.ctas / C::kCtasPerSm ? paged_join_kernel<D, NB, kShare> : paged_join_kernel<D, NB, 1>;
     const int threads = 256 * NB * (plan.items < plan.ctas / C::kCtasPerSm ? kShare : 1);
-    e = launch_overlapped(join, dim3(static_cast<unsigned>(plan.ctas - 1)), dim3(threads), 0, stream, a,
-                          static_cast<int>(plan.ctas));
+    e = launch_overlapped(join, dim3(static_cast<unsigned>(plan.ctas - 1)), dim3(threads), 0, stream, a);
     if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
   }
   return 0;
@@ -1076,7 +1071,7 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
     return r;
   }
   r.ctas = slots;
-  r.workspace_bytes = static_cast<size_t>(slots) * 2 * r.rows * (pool.d + 1) * sizeof(float);
+  r.workspace_bytes = static_cast<size_t>(slots) * (2 * r.rows * (pool.d + 1) * sizeof(float) + sizeof(JoinRecord));
   return r;
 }
 
@@ -1104,7 +1099,10 @@ int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const P
   const float sl2 = p.scale * kLog2e;
   a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
   a.part_o = static_cast<float*>(workspace);
-  a.part_lse = a.part_o + (plan.workspace_bytes > 0 ? plan.ctas * 2 * plan.rows * pool.d : 0);
+  if (plan.workspace_bytes > 0) {
+    a.part_lse = a.part_o + plan.ctas * 2 * plan.rows * pool.d;
+    a.records = reinterpret_cast<JoinRecord*>(a.part_lse + plan.ctas * 2 * plan.rows);
+  }
   return pool.d == 64 ? launch_rows_d<64>(pool, a, plan, stream) : launch_rows_d<128>(pool, a, plan, stream);
 }
 

@@ -147,6 +147,7 @@ struct ChunkArgs {
   float scale_log2;
   float* part_o;     // [part][2][256][d], normalised
   float* part_lse;   // [part][2][256], log2 units
+  JoinRecord* records;  // [part]
 };
 
 // Where row r of a key head stands in o and lse: (token, query head).
@@ -178,13 +179,12 @@ __device__ __forceinline__ PairGeo pair_geo(const ChunkArgs& a, int rows, int p0
 
 __device__ __forceinline__ int pairs_of(int rows) { return (rows + 2 * kBM - 1) / (2 * kBM); }
 
-// The units (steps, and kItemSteps per item) of a sequence, by one lane. Its
-// items come pair by pair, key head by key head.
-__device__ __forceinline__ long long seq_units(const ChunkArgs& a, const PagedSeq& s) {
-  const int rows = s.n * a.g.G, pairs = pairs_of(rows);
-  long long sum = 0;
-  for (int i = 0; i < pairs; ++i) sum += pair_geo(a, rows, s.len - s.n, i).steps + kItemSteps;
-  return sum * a.Hkv;
+// Steps of a pair alone: its two tiles' ranges overlap or adjoin.
+__device__ __forceinline__ int pair_steps(const ChunkArgs& a, int rows, int p0, int pair) {
+  const int r0 = pair * 2 * kBM, p_last = p0 + a.g.div(min(r0 + 2 * kBM, rows) - 1);
+  const int hi = p_last >= 0 ? p_last / kBN + 1 : 0;
+  const int lo = a.window > 0 ? max(p0 + a.g.div(r0) - a.window + 1, 0) / kBN : 0;
+  return max(hi - lo, 0);
 }
 
 __device__ __forceinline__ long long scan_sum(long long own) {
@@ -196,13 +196,54 @@ __device__ __forceinline__ long long scan_sum(long long own) {
   return own;
 }
 
-__device__ __forceinline__ long long batch_units(const ChunkArgs& a) {
-  long long sum = 0;
-  for (int b = static_cast<int>(lane_id()); b < a.batch.B; b += 32) sum += seq_units(a, paged_seq(a.batch, b, a.status));
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  return sum;
-}
+// The units (steps, and kItemSteps per item) of the sequences, by one warp.
+// `lanes` lanes (a power of two) share a sequence's pairs, so that a batch of
+// few sequences with many pairs does not take long.
+struct Units {
+  int lanes;
+  long long total;
+  long long own, end;  // of sequence b0 + lane / lanes: its units, and the units up to its end
+
+  __device__ __forceinline__ void scan(const ChunkArgs& a, int b0, long long before) {
+    const int lane = static_cast<int>(lane_id()), b = b0 + lane / lanes;
+    long long sum = 0;
+    if (b < a.batch.B) {
+      const PagedSeq s = paged_seq(a.batch, b, a.status);
+      const int rows = s.n * a.g.G, pairs = pairs_of(rows);
+      for (int i = lane % lanes; i < pairs; i += lanes) sum += pair_steps(a, rows, s.len - s.n, i) + kItemSteps;
+    }
+    end = scan_sum(sum * a.Hkv);
+    for (int m = 1; m < lanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    own = sum * a.Hkv;
+    end = before + __shfl_sync(0xffffffffu, end, lane | (lanes - 1));
+  }
+  __device__ __forceinline__ void start(const ChunkArgs& a) {
+    lanes = 1;
+    while (lanes < 32 && lanes * 2 * a.batch.B <= 32) lanes *= 2;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch.B; b0 += 32 / lanes) {
+      scan(a, b0, before);
+      before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    total = before;
+  }
+  // The sequence that holds unit u (below the total), and its first unit.
+  __device__ __forceinline__ int find(const ChunkArgs& a, long long u, long long* first) {
+    const int per = 32 / lanes;
+    if (a.batch.B > per) scan(a, 0, 0);  // (otherwise as start() left it)
+    for (int b0 = 0; b0 < a.batch.B; b0 += per) {
+      if (b0 > 0) scan(a, b0, __shfl_sync(0xffffffffu, end, 31));
+      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        *first = __shfl_sync(0xffffffffu, end - own, i);
+        return b0 + i / lanes;
+      }
+    }
+    *first = 0;  // not reached for u below the total
+    return a.batch.B;
+  }
+};
 
 // Parts that the units are cut into, and the first unit of part c.
 __device__ __forceinline__ int parts_of(long long units, int ctas) {
@@ -220,27 +261,15 @@ struct Item {
   long long first;  // its first unit
 
   __device__ __forceinline__ long long units() const { return g.steps + kItemSteps; }
-  __device__ __forceinline__ void find(const ChunkArgs& a, long long u) {
-    long long before = 0;
-    for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
-      const int b = b0 + static_cast<int>(lane_id());
-      const long long own = b < a.batch.B ? seq_units(a, paged_seq(a.batch, b, a.status)) : 0;
-      const long long end = before + scan_sum(own);
-      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
-      if (past) {
-        const int i = __ffs(past) - 1;
-        seq = b0 + i;
-        before = __shfl_sync(0xffffffffu, end - own, i);
-        break;
-      }
-      before = __shfl_sync(0xffffffffu, end, 31);
-    }
+  __device__ __forceinline__ void find(const ChunkArgs& a, Units& all, long long u) {
+    long long before;
+    seq = all.find(a, u, &before);
     s = paged_seq(a.batch, seq, a.status);
     const int rows = s.n * a.g.G, pairs = pairs_of(rows);
     for (int i0 = 0; i0 < pairs; i0 += 32) {
       const int i = i0 + static_cast<int>(lane_id());
       const long long own =
-          i < pairs ? static_cast<long long>(a.Hkv) * (pair_geo(a, rows, s.len - s.n, i).steps + kItemSteps) : 0;
+          i < pairs ? static_cast<long long>(a.Hkv) * (pair_steps(a, rows, s.len - s.n, i) + kItemSteps) : 0;
       const long long end = before + scan_sum(own);
       const uint32_t past = __ballot_sync(0xffffffffu, end > u);
       if (past) {
@@ -364,7 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the present ones are issued.
       const int box_rows = min(a.batch.page_size, kBN), per_box = box_rows / 16;
       const uint32_t box_bytes = static_cast<uint32_t>(box_rows * D);
-      const long long units = batch_units(a);
+      Units all;
+      all.start(a);
+      const long long units = all.total;
       const int parts = parts_of(units, gridDim.x);
       long long u = part_start(units, parts, blockIdx.x);
       const long long u1 = part_start(units, parts, blockIdx.x + 1);
@@ -385,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Item it;
       bool more = u < u1;
-      if (more) it.find(a, u);
+      if (more) it.find(a, all, u);
+      JoinRecord record{};
       for (; more && ok && it.first < u1; more = it.next(a)) {
         // steps [s0, s1) of the item; one without steps belongs to the part of its first unit
         const int n = it.g.steps;
@@ -414,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pc.full_lo = a.window > 0 ? p_last - a.window + 1 : 0;
         pc.whole = s0 == 0 && s1 == n;
         pc.slot = static_cast<int>(blockIdx.x) * 2 + (s0 == 0 ? 1 : 0);  // 0: continues an item, 1: begins one
+        if (!pc.whole && s0 == 0)
+          record = JoinRecord{parts_until(it.first + it.units(), units, parts, blockIdx.x), it.s.row0, h, r0, rows, {}};
         put_piece(pc);
         if (!ok) break;
         // keys that any row sees lie in [key_lo, key_end)
@@ -507,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         u = max(u, it.first);  // from the next item on
       }
+      if (lane == 0) a.records[blockIdx.x] = record;
       Piece last{};
       last.end = 1;
       if (ok) put_piece(last);
@@ -1025,30 +1060,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // fa_paged_attn.cu's join. Blocks 8 c .. 8 c + 7 take 32 rows each of the item
 // that part c begins and does not end, if there is one. Eight threads per row.
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a, int ctas) {
+__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a) {
   constexpr int kCols = D / 8;
-  // (from the batch's lengths alone, while the kernel before ends, as in fa_paged_attn.cu)
-  const int c = blockIdx.x / 8;
-  const long long units = batch_units(a);
-  const int parts = parts_of(units, ctas);
-  const long long u0 = part_start(units, parts, c), u1 = part_start(units, parts, c + 1);
-  Item it;
-  bool work = c + 1 < parts && u0 < u1;
-  long long first = 0;
-  if (work) {
-    it.find(a, u1 - 1);
-    first = it.first + kItemSteps;  // unit of the item's step 0
-    const long long end = u1 - first;
-    work = u0 <= first && end > 0 && end < it.g.steps;
-  }
   grid_dep_wait();
   grid_dep_launch();
-  if (!work) return;
+  const int c = blockIdx.x / 8;
+  const JoinRecord rec = a.records[c];
+  if (rec.parts == 0) return;
   const int row = blockIdx.x % 8 * 32 + static_cast<int>(threadIdx.x >> 3), c0 = (threadIdx.x & 7) * kCols;
-  const int r = it.pair * 2 * kBM + row;
-  if (r >= it.s.n * a.g.G) return;
+  const int r = rec.r0 + row;
+  if (r >= rec.rows) return;
   float m = -INFINITY, sum = 0.f, x[kCols] = {};
-  for (int k = c; k < parts && part_start(units, parts, k) - first < it.g.steps; ++k) {
+  for (int k = c; k < c + rec.parts; ++k) {
     const long long at = (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * 2 * kBM + row;
     const float ls = a.part_lse[at];
     if (ls == -INFINITY) continue;  // (nothing of the row: its channels were not written)
@@ -1066,7 +1089,7 @@ __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a
     m = mx;
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
-  const long long at = row_at(a, it.s.row0, it.h, r);
+  const long long at = row_at(a, rec.row0, rec.h, r);
   uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c0);
 #pragma unroll
   for (int i = 0; i < kCols; i += 8)
@@ -1089,14 +1112,14 @@ int launch_chunk_d(const PagedPool& pool, const ChunkArgs& a, int ctas, cudaStre
   // (not overlapped with the kernel before: see launch_rows in fa_paged_attn.cu)
   cudaError_t e = launch_with(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, false, 1, stream, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
-  e = launch_overlapped(paged_chunk_join_kernel<D>, dim3(8 * (ctas - 1)), dim3(256), 0, stream, a, ctas);
+  e = launch_overlapped(paged_chunk_join_kernel<D>, dim3(8 * (ctas - 1)), dim3(256), 0, stream, a);
   return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;
 }
 
 }  // namespace
 
 size_t paged_chunk_workspace_bytes(int d, int ctas) {
-  return static_cast<size_t>(ctas) * 2 * 2 * kBM * (d + 1) * sizeof(float);
+  return static_cast<size_t>(ctas) * (2 * 2 * kBM * (d + 1) * sizeof(float) + sizeof(JoinRecord));
 }
 
 int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const PagedAttn& p, int ctas,
@@ -1121,6 +1144,7 @@ int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const 
   a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + static_cast<size_t>(ctas) * 2 * 2 * kBM * pool.d;
+  a.records = reinterpret_cast<JoinRecord*>(a.part_lse + static_cast<size_t>(ctas) * 2 * 2 * kBM);
   return pool.d == 64 ? launch_chunk_d<64>(pool, a, ctas, stream) : launch_chunk_d<128>(pool, a, ctas, stream);
 }
 

@@ -182,7 +182,7 @@ int launch_paged_append(const PagedPool& pool, const PagedBatchDev& batch, const
 struct PagedPlan {
   int rows;                // (query, head) rows per CTA: 8 or 16
   int row_tiles;           // tiles of that many rows of the longest packed sequence and a key head
-  long long items;         // sequences x key heads x row tiles
+  long long items;         // streaming form: row tiles of all sequences and key heads, about
   int cluster;             // CTAs per item in the cluster form; 0: the streaming form
   bool chunk;              // many rows: the kernel of fa_paged_chunk.cu
   long long ctas;

@@ -1047,22 +1047,17 @@ int launch_rows_d(const PagedPool& pool, const AttnArgs& a, const PagedPlan& pla
 
 PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, const int Hq, int max_kv, int sms) {
   PagedPlan r{};
-  const long long rows = static_cast<long long>(batch.max_q) * (Hq / pool.num_heads);
-  if (rows > 64) {
-    r.chunk = true;
-    r.ctas = sms;
-    r.workspace_bytes = paged_chunk_workspace_bytes(pool.d, sms);
-    return r;
-  }
+  const long long G = Hq / pool.num_heads;
+  const long long rows = batch.max_q * G;
   r.rows = rows <= 8 ? 8 : 16;
   r.row_tiles = static_cast<int>((rows + r.rows - 1) / r.rows);
   const long long items = static_cast<long long>(batch.B) * pool.num_heads * r.row_tiles;
-  r.items = items;
   const int tile = pool.d == 64 ? kTileOf<64> : kTileOf<128>;
   const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + tile - 1) / tile : 1;
   const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
   // The cluster form while every CTA of a cluster of up to eight has a slot and
-  // at most eight tiles.
+  // at most eight tiles. One sequence of 300 keys (32 query heads, 8 key heads,
+  // d = 128): 6.3 us, against 14 us for the streaming form and its join.
   long long want = 1;
   while (want < 8 && 2 * want < tiles) want *= 2;
   if (items * want <= slots && tiles <= 8 * want) {
@@ -1070,8 +1065,26 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
     r.ctas = items * want;
     return r;
   }
-  r.ctas = slots;
-  r.workspace_bytes = static_cast<size_t>(slots) * (2 * r.rows * (pool.d + 1) * sizeof(float) + sizeof(JoinRecord));
+  // Rows (16 a tile, the cached tiles read once for each) or chunks (256 rows
+  // on the tensor memory)? What each costs was measured: about 12 us and 1.07
+  // us per tile and CTA slot (two per SM), against 22 us and 1.6 us (d = 64:
+  // 0.95 us) per step of 128 keys and SM, on 152 SMs. At 16 sequences of 2048
+  // keys, d = 128: 32 rows 43 against 45 us, 64 rows 70 against 46; at 24 of
+  // 4096 keys, d = 64: 15 rows 19 against 43, 48 rows 46 against 43 us.
+  // A ragged batch has at most its packed rows' tiles and one more per sequence.
+  const double seqs = batch.B, heads = pool.num_heads, packed = static_cast<double>(batch.T) * G;
+  const double row_items = heads * fmin(seqs * r.row_tiles, seqs + packed / r.rows);
+  const double pair_items = heads * fmin(seqs * ((rows + 255) / 256), seqs + packed / 256);
+  const double steps = max_kv / 128 + 1;
+  const double row_cost = 12 + 1.07 / 304 * row_items * (tiles + kItemUnits);
+  const double chunk_cost = 22 + (pool.d == 64 ? 0.95 : 1.6) / 152 * pair_items * (steps + 3);
+  r.chunk = rows > 8 && chunk_cost < row_cost;
+  r.ctas = r.chunk ? sms : slots;
+  r.items = static_cast<long long>(row_items);
+  // The choice depends on the packed rows, what a caller has to provide does not.
+  const size_t row_bytes = static_cast<size_t>(slots) * (2 * r.rows * (pool.d + 1) * sizeof(float) + sizeof(JoinRecord));
+  const size_t chunk_bytes = rows > 8 ? paged_chunk_workspace_bytes(pool.d, sms) : 0;
+  r.workspace_bytes = row_bytes > chunk_bytes ? row_bytes : chunk_bytes;
   return r;
 }
 

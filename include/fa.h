@@ -371,8 +371,9 @@ int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, co
  *   o        : out, bf16 [T, Hq, d] contiguous
  *   lse      : out, fp32 [T, Hq], natural-log log-sum-exp
  *   workspace: at least fa_paged_attn_workspace_bytes(cache, batch, Hq)
- *              bytes (0: may be NULL), 256-byte aligned; nothing in it
- *              outlives the call. Two calls in flight at once need two.
+ *              bytes (0: may be NULL; it does not depend on T), 256-byte
+ *              aligned; nothing in it outlives the call. Two calls in flight
+ *              at once need two, also as replays of two captured graphs.
  * Long key ranges are divided among the SMs and the parts' states joined with
  * the rule of fa_decode_splitkv; how depends on the lengths, so the same
  * inputs give the same bits.

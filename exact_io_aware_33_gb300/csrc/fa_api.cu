@@ -469,7 +469,7 @@ int check_paged(const fa_paged_cache* c, const fa_paged_batch* b, fa::PagedPool*
   if (c->num_pages == 0 || b->max_pages == 0) return FA_ERR_INVALID;
   // tensor-map coordinates and positions are 32-bit
   if (static_cast<long long>(c->num_pages) * c->num_heads > 0x7fffffffLL) return FA_ERR_INVALID;
-  if (static_cast<long long>(b->max_pages) * ps > 0x7fffffffLL - 256) return FA_ERR_INVALID;
+  if (static_cast<long long>(b->max_pages) * ps > 0x7fffffffLL - 4096) return FA_ERR_INVALID;  // (and tiles ahead)
   if (!fa::aligned16(c->k_pages) || !fa::aligned16(c->v_pages) || !aligned4(c->k_scales) ||
       !aligned4(c->v_scales) || !aligned4(b->block_table) || !aligned4(b->kv_lens) ||
       (b->cu_q != nullptr && !aligned4(b->cu_q)))
@@ -552,7 +552,7 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   if (!fa::aligned16(q) || !fa::aligned16(o) || !aligned4(lse) || !row_stride_ok(q_stride, Hq, cache->d))
     return FA_ERR_INVALID;
   // packed (query, head) rows of a key head are counted in 32 bits
-  if (static_cast<long long>(batch->max_q) * Hq > 0x7fffffffLL) return FA_ERR_INVALID;
+  if (static_cast<long long>(batch->max_q) * Hq > 0x7fffffffLL - 4096) return FA_ERR_INVALID;
   const fa::PagedPlan plan = fa::paged_attn_plan(pool, dev, Hq, paged_max_kv(cache, batch), paged_sms());
   if (plan.workspace_bytes > 0 &&
       (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||

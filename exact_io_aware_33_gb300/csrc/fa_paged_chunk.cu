@@ -261,9 +261,11 @@ struct Item {
   long long first;  // its first unit
 
   __device__ __forceinline__ long long units() const { return g.steps + kItemSteps; }
-  __device__ __forceinline__ void find(const ChunkArgs& a, Units& all, long long u) {
+  __device__ __forceinline__ bool find(const ChunkArgs& a, Units& all, long long u) {
     long long before;
     seq = all.find(a, u, &before);
+    if (seq >= a.batch.B) return false;
+    pair = 0;
     s = paged_seq(a.batch, seq, a.status);
     const int rows = s.n * a.g.G, pairs = pairs_of(rows);
     for (int i0 = 0; i0 < pairs; i0 += 32) {
@@ -283,6 +285,7 @@ struct Item {
     g = pair_geo(a, rows, s.len - s.n, pair);
     h = static_cast<int>((u - before) / units());
     first = before + h * units();
+    return true;
   }
   // The next item; false past the last.
   __device__ __forceinline__ bool next(const ChunkArgs& a) {
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Item it;
       bool more = u < u1;
-      if (more) it.find(a, all, u);
+      if (more) more = it.find(a, all, u);
       JoinRecord record{};
       for (; more && ok && it.first < u1; more = it.next(a)) {
         // steps [s0, s1) of the item; one without steps belongs to the part of its first unit
@@ -530,6 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (bytes that have landed already count as well: the phase cannot end before this arrival)
             if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull), bytes);
             ++k_copies;
+#ifdef FA_TEST_SKIP_ARRIVE
+            // Test-only build (never in libfa.so): a piece's last values are
+            // never loaded, so the widening warps' bounded wait for them runs
+            // out and the CTA winds down through the abort path.
+            if (base4 + i == steps - 1) {
+              ok = false;
+              break;
+            }
+#endif
             if (gs >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (gs - 1) & 1, abort_flag);
             if (!ok) break;
             if (own && issues)

@@ -87,16 +87,17 @@ def check_attn(w, cu, o, lse, q, scale, window=0):
     o, lse = o.float().cpu().double().numpy(), lse.cpu().double().numpy()
     G = q.shape[1] // w.H
     for b, n in enumerate(w.lens):
-        v = w.oracle.read("v", w.table[b], n)
-        top = np.abs(v).max(axis=(1, 2)) if n else np.zeros(w.H)
-        top = np.repeat(np.nan_to_num(top), G)[None, :, None]
-        r = slice(cu[b], cu[b + 1])
-        assert np.array_equal(np.isnan(o[r]), np.isnan(want[r]))
-        err = np.nan_to_num(np.abs(o[r] - want[r]) - 2.0 ** -8 * np.abs(want[r]))
-        assert (err <= 2.0 ** -10 * top).all(), (b, (err / np.maximum(top, 1e-30)).max())
-        none = np.isneginf(want_lse[r])
-        assert np.array_equal(none, np.isneginf(lse[r]))
-        assert (np.abs(lse[r][~none] - want_lse[r][~none]) <= 5e-4).all()
+        size = np.nan_to_num(np.abs(w.oracle.read("v", w.table[b], n))).max(-1) if n else None  # [H, n]
+        for r in range(cu[b], cu[b + 1]):
+            p = n - cu[b + 1] + r
+            lo = max(p - window + 1, 0) if window else 0
+            top = np.repeat(size[:, lo:p + 1].max(-1), G)[:, None] if p >= lo else 0.0  # max |v| that the row sees
+            assert np.array_equal(np.isnan(o[r]), np.isnan(want[r])), (b, r)
+            err = np.nan_to_num(np.abs(o[r] - want[r]) - 2.0 ** -8 * np.abs(want[r]))
+            assert (err <= 2.0 ** -10 * top).all(), (b, r, (err / np.maximum(top, 1e-300)).max())
+            none = np.isneginf(want_lse[r])
+            assert np.array_equal(none, np.isneginf(lse[r])), (b, r)
+            assert (np.abs(lse[r][~none] - want_lse[r][~none]) <= 5e-4).all(), (b, r)
 
 
 # ------------------------------------------------------------------ attention
@@ -158,12 +159,13 @@ def test_several_tokens_per_sequence(lens, news, Hq, Hkv, d, page, window, max_k
     check_attn(w, cu, o, lse, q, 1 / math.sqrt(d), window)
 
 
+@pytest.mark.parametrize("max_kv", [0, STREAM])
 @pytest.mark.parametrize("news", [[1, 1], [40, 33]])
-def test_scales_of_very_different_sizes(news):
+def test_scales_of_very_different_sizes(news, max_kv):
     # pages whose scales lie up to 2^24 apart: the largest values decide the output, but every row that
     # sees only small ones keeps its relative precision (the bound is relative to the row's largest value)
     for seed in range(4):
-        w = World([120, 75], 2, 16, 64, seed=seed).fill()
+        w = World([120, 75], 2, 16, 64, seed=seed, max_pages=STREAM // 16 if max_kv else None).fill()
         big = 2.0 ** w.rng.integers(-12, 12, w.oracle.scales["v"].shape)
         w.oracle.scales["v"] *= big
         w.oracle.scales["k"] *= 2.0 ** w.rng.integers(-3, 2, big.shape)
@@ -174,8 +176,25 @@ def test_scales_of_very_different_sizes(news):
         check_attn(w, cu, o, lse, q, 0.125)
 
 
-def test_a_scale_need_not_be_a_power_of_two():
-    w = World([90, 31], 2, 32, 128, seed=4).fill()
+@pytest.mark.parametrize("max_kv", [0, STREAM])
+@pytest.mark.parametrize("news", [[1], [150]])
+def test_values_near_the_ends_of_the_float_range(news, max_kv):
+    # one page's values some 2^180 above the others': the weights' references for numerators and
+    # denominators lie as far apart, and a row that does not see that page must not notice it
+    for where in (0, 3, 9):
+        w = World([150], 1, 16, 64, seed=where, max_pages=STREAM // 16 if max_kv else None).fill()
+        w.oracle.scales["v"][:] = 2.0 ** -90
+        w.oracle.scales["v"][w.table[0, where]] = 2.0 ** 90
+        cu, batch = w.batch(news)
+        q = bf16(w.rng, news[0], 4, 64)
+        o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+        done()
+        check_attn(w, cu, o, lse, q, 0.125)
+
+
+@pytest.mark.parametrize("max_pages", [3, STREAM // 32])
+def test_a_scale_need_not_be_a_power_of_two(max_pages):
+    w = World([90, 31], 2, 32, 128, seed=4, max_pages=max_pages).fill()
     for name in ("k", "v"):
         w.oracle.scales[name] = (w.oracle.scales[name] * w.rng.uniform(1, 2, w.oracle.scales[name].shape)
                                  ).astype(np.float32).astype(np.float64)
@@ -233,24 +252,28 @@ def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, max_pages):
         assert got == want, (i, got, want)
 
 
-def test_a_key_with_nan_gives_nan_to_the_rows_that_see_it():
-    w = World([40], 1, 16, 64, seed=8).fill()
+@pytest.mark.parametrize("max_pages", [3, STREAM // 16])
+@pytest.mark.parametrize("heads", [2, 8])
+def test_a_key_with_nan_gives_nan_to_the_rows_that_see_it(heads, max_pages):
+    w = World([40], 1, 16, 64, seed=8, max_pages=max_pages).fill()
     w.oracle.codes["k"][w.table[0, 36 // 16], 0, 36 % 16, 3] = 0x7F
     cu, batch = w.batch([8])
-    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, bf16(w.rng, 8, 2, 64).cuda())
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, bf16(w.rng, 8, heads, 64).cuda())
     done()
     seen = torch.arange(32, 40) >= 36
     assert torch.isnan(o.cpu()).all(-1).all(-1).equal(seen) and torch.isnan(lse.cpu()).all(-1).equal(seen)
     assert torch.isfinite(o[:4]).all()
 
 
-def test_rows_outside_every_sequence_stay_as_they_were():
-    w = World([50, 20], 2, 16, 64, seed=9).fill()
+@pytest.mark.parametrize("max_pages", [4, STREAM // 16])
+@pytest.mark.parametrize("Hq", [4, 32])
+def test_rows_outside_every_sequence_stay_as_they_were(Hq, max_pages):
+    w = World([50, 20], 2, 16, 64, seed=9, max_pages=max_pages).fill()
     cu, batch = w.batch([3, 2])
     T = 9
-    q = bf16(w.rng, T, 4, 64)
-    out = torch.full((T, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
-    lse = torch.full((T, 4), 7.0, device="cuda")
+    q = bf16(w.rng, T, Hq, 64)
+    out = torch.full((T, Hq, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), 7.0, device="cuda")
     fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), out=out, lse=lse)
     done()
     assert (out[5:] == 7).all() and (lse[5:] == 7).all()
@@ -288,6 +311,96 @@ def test_shared_pages_may_be_read_by_several_sequences():
     o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
     done()
     check_attn(w, cu, o, lse, q, 0.125)
+
+
+@pytest.mark.parametrize("rows,heads", [(1, 4), (4, 4), (64, 4)])
+def test_a_long_sequence_is_cut_into_many_parts(rows, heads):
+    # a few items over all SMs: up to one part per CTA of each item to join
+    n = 20011
+    w = World([n, 130], 1, 128, 128, seed=51 + rows).fill()
+    cu, batch = w.batch([rows, 1])
+    q = bf16(w.rng, int(cu[-1]), heads, 128)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+    done()
+    check_attn(w, cu, o, lse, q, 1 / math.sqrt(128))
+
+
+def test_a_prompt_among_single_tokens():
+    lens = [300, 1, 77, 513, 40, 1000, 2]
+    news = [1, 1, 1, 300, 40, 1, 2]
+    w = World(lens, 2, 64, 64, seed=52, max_pages=STREAM // 64).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, int(cu[-1]), 8, 64)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+    done()
+    check_attn(w, cu, o, lse, q, 0.125)
+
+
+@pytest.mark.parametrize("news_of,Hq", [(lambda b: 1, 2), (lambda b: b % 4, 2), (lambda b: b % 3, 24)])
+def test_many_sequences(news_of, Hq):
+    B = 700
+    news = [news_of(b) for b in range(B)]
+    lens = [1 + (b * 37) % 90 for b in range(B)]
+    w = World(lens, 1, 16, 64, seed=53).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, int(cu[-1]), Hq, 64)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+    done()
+    check_attn(w, cu, o, lse, q, 0.125)
+
+
+@pytest.mark.parametrize("rows,Hq", [(1, 2), (9, 2), (40, 8)])
+def test_pages_before_the_window_may_be_gone(rows, Hq):
+    n, window = 700, 100
+    for max_pages in (None, STREAM // 16):
+        w = World([n], 1, 16, 64, seed=54, max_pages=max_pages).fill()
+        keep = w.table.copy()
+        w.table[0, :(n - rows - window + 1) // 16] = -1     # handed back to the pool
+        cu, batch = w.batch([rows])
+        q = bf16(w.rng, rows, Hq, 64)
+        o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), window=window)
+        done()
+        w.table = keep
+        check_attn(w, cu, o, lse, q, 0.125, window)
+
+
+def test_a_chunk_captured_once_and_replayed():
+    w = World([900, 350], 2, 32, 128, seed=55).fill()
+    q = bf16(w.rng, 240, 8, 128)
+    cache, gpu = w.to_gpu(), q.cuda()
+    cu, batch = w.batch([200, 40])
+    whole = list(w.lens)
+    ws = torch.empty(fa.fa_paged_attn_workspace_bytes(cache, batch, 8), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fa.fa_paged_attn(cache, batch, gpu, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = fa.fa_paged_attn(cache, batch, gpu, workspace=ws)
+    for lens in (whole, [640, 41], [200, 350]):
+        batch.kv_lens.copy_(torch.tensor(lens))
+        graph.replay()
+        done()
+        w.lens = lens
+        check_attn(w, cu, o, lse, q, 1 / math.sqrt(128))
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    worlds = [World([5000, 1200], 2, 64, 128, seed=56 + i).fill() for i in range(2)]
+    calls = []
+    for i, w in enumerate(worlds):
+        news = [1, 1] if i == 0 else [100, 60]
+        cu, batch = w.batch(news)
+        q = bf16(w.rng, int(cu[-1]), 8, 128)
+        calls.append((w, cu, batch, q, w.to_gpu(), q.cuda(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        outs = [fa.fa_paged_attn(c[4], c[2], c[5], stream=c[6]) for c in calls]
+    done()
+    for c, (o, lse) in zip(calls, outs):
+        check_attn(c[0], c[1], o, lse, c[3], 1 / math.sqrt(128))
 
 
 # ------------------------------------------------------------------ append
@@ -565,6 +678,22 @@ def test_indices_out_of_range_are_reported_and_touch_nothing():
         assert fa.fa_get_last_device_status() == fa.FA_ERR_INDEX
         changed = (cache.k_pages.view(torch.uint8) != before).flatten(1).any(1).nonzero().flatten().tolist()
         assert changed == [int(w.table[0, 2])]
+    # a chunk: 20 rows of each sequence, the second sequence's last page bad
+    long_table = torch.full((2, STREAM // 16), -1, dtype=torch.int32)
+    long_table[:, :3] = torch.from_numpy(w.table)
+    long_table[1, 2] = w.P
+    batch = fa.PagedBatch(long_table.cuda(), torch.tensor([40, 40], dtype=torch.int32, device="cuda"),
+                          torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda"), max_q=20)
+    many = bf16(w.rng, 40, 4, 64)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, many.cuda())
+    torch.cuda.synchronize()
+    assert fa.fa_get_last_device_status() == fa.FA_ERR_INDEX
+    check_attn(whole, [0, 20], o[:20], lse[:20], many[:20], 0.125)
+    # absent keys take no part: the rows of sequence 1 see its first 32 keys, up to their own position
+    part = World.__new__(World)
+    part.__dict__.update(w.__dict__, lens=[32], table=w.table[1:])
+    check_attn(part, [0, 12], o[20:32], lse[20:32], many[20:32], 0.125)
+    check_attn(part, [0, 1], o[39:], lse[39:], many[39:], 0.125)
     for lens in ([40, -5], [40, 10 ** 6]):
         batch = fa.PagedBatch(torch.from_numpy(w.table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
         fa.fa_paged_attn(w.to_gpu(), batch, q)

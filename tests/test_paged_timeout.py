@@ -1,0 +1,57 @@
+"""The bounded waits of the paged attention kernels, on the GPU, without a fault.
+
+The test-only variant of the library (see test_timeout_path.py; never part of libfa.so) never loads the
+last tile of a sequence, so the warps that wait for it give up after the variant's 20 ms, raise the
+CTA's abort flag, and every role winds down. Each form is run once: clusters, streaming, chunks. The
+status says FA_ERR_TIMEOUT once, and the product library's results in the same process are right.
+"""
+
+import ctypes
+import time
+
+import pytest
+
+torch = pytest.importorskip("torch")
+fa = pytest.importorskip("exact_io_aware_33_gb300")
+
+from test_paged_parity import STREAM, World, bf16, check_attn, done  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def timeout_lib():
+    from exact_io_aware_33_gb300 import build as b
+    return fa.load_library(b.build_timeout_test_variant())
+
+
+@pytest.mark.parametrize("rows,heads,max_kv", [(1, 4, 0), (1, 4, STREAM), (9, 2, STREAM), (300, 4, STREAM)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_wait_runs_out_and_the_context_survives(timeout_lib, d, rows, heads, max_kv):
+    w = World([500], 2, 64, d, seed=d + rows, max_pages=STREAM // 64 if max_kv else None).fill()
+    cu, batch = w.batch([rows])
+    q = bf16(w.rng, rows, heads, d)
+    cache, gpu = w.to_gpu(), q.cuda()
+    o = torch.empty_like(gpu)
+    lse = torch.empty(rows, heads, device="cuda")
+    struct = batch._for_rows(rows)[2]
+    need = timeout_lib.fa_paged_attn_workspace_bytes(cache._address, struct, heads)
+    ws = torch.zeros(max(need, 1), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert fa.fa_get_last_device_status() == fa.FA_OK
+
+    t0 = time.perf_counter()
+    rc = timeout_lib.fa_paged_attn(cache._address, struct, gpu.data_ptr(), heads * d, o.data_ptr(), lse.data_ptr(),
+                                   heads, 0, d ** -0.5, ws.data_ptr(), need,
+                                   ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == fa.FA_OK  # launched; the failure shows in the status word
+    status = timeout_lib.fa_get_last_device_status()  # synchronises the device
+    elapsed = time.perf_counter() - t0
+    assert status == fa.FA_ERR_TIMEOUT
+    assert elapsed < 10.0, f"the wind-down took {elapsed:.2f} s"
+    assert timeout_lib.fa_get_last_device_status() == fa.FA_OK  # read once, then cleared
+    assert fa.fa_get_last_device_status() == fa.FA_OK           # the product library's word is its own
+
+    o, lse = fa.fa_paged_attn(cache, batch, gpu)
+    done()
+    check_attn(w, cu, o, lse, q, d ** -0.5)

@@ -1,8 +1,9 @@
-"""Builds libfa.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libfa.so in-tree with nvcc for sm_103a (GB300), and the paged cache's
+Python binding with the host compiler.
 
 Each translation unit under ``csrc/`` is compiled in parallel into
-``_build/`` at the repository root and linked into ``libfa.so`` next to this
-file. A unit is recompiled only when it, or a header it may include, is
+``_build/`` at the repository root and linked into ``libfa.so`` (and
+``_paged_native.so``, which links against it and PyTorch) next to this file. A unit is recompiled only when it, or a header it may include, is
 newer than its object file.
 """
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
+BINDING = os.path.join(PKG, "_paged_native.so")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_noalloc.cu", "fa_paged_append.cu",
            "fa_paged_attn.cu", "fa_paged_chunk.cu"]
@@ -37,6 +39,13 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is needed to build libfa.so")
 
 
+def cxx() -> str:
+    path = shutil.which("g++") or shutil.which("c++")
+    if path:
+        return path
+    raise RuntimeError("g++ not found: the paged cache's binding is built with it")
+
+
 def _headers():
     out = []
     for d in (CSRC, INCLUDE):
@@ -44,6 +53,21 @@ def _headers():
             if f.endswith((".h", ".cuh")):
                 out.append(os.path.join(d, f))
     return out
+
+
+def _binding_flags():
+    """(compile, link) flags of the binding: Python's and PyTorch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    link = ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG,
+            "-l:libfa.so", "-Wl,-rpath,$ORIGIN"]
+    return flags + ["-I" + i for i in include], link
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir: str | None = None,
@@ -72,6 +96,14 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
             cmd.append("-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding = None
+    if lib == LIB:
+        src = "paged_binding.cpp"
+        path, binding = os.path.join(CSRC, src), os.path.join(build_dir, src.replace(".cpp", ".o"))
+        if (force or not os.path.exists(binding)
+                or os.path.getmtime(binding) < max(os.path.getmtime(path), newest_header)):
+            procs.append((src, subprocess.Popen([cxx(), "-c", path, "-o", binding] + _binding_flags()[0],
+                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -91,6 +123,14 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
         os.replace(tmp, lib)
+    if binding and (force or not os.path.exists(BINDING)
+                    or os.path.getmtime(BINDING) < max(os.path.getmtime(binding), os.path.getmtime(lib))):
+        tmp = BINDING + ".tmp"
+        r = subprocess.run([cxx(), "-shared", "-o", tmp, binding] + _binding_flags()[1], stdout=subprocess.PIPE,
+                           stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+        os.replace(tmp, BINDING)
     return lib
 
 

@@ -13,6 +13,8 @@ and updates ``kv_lens`` and ``block_table`` in place between steps; the calls ca
 CUDA graph and replayed that way. All tensors of a call must be on one device, which need not be the
 current one. With ``stream`` the work is queued there and outputs and workspaces belong to that stream;
 tensors of other streams must be ready, and kept, by the caller.
+
+The calls' own checks and allocations are in csrc/paged_binding.cpp.
 """
 
 from __future__ import annotations
@@ -22,19 +24,24 @@ import math
 
 _PAGE_SIZES = (16, 32, 64, 128)
 
-# Set with the first object: the package loads neither torch nor libfa.so by itself. The functions are
-# bound here once because a step's small calls are bound by what the host does per call.
-torch = _lib = _fail = _empty = _bf16 = _raw_stream = _current = None
+# Set with the first object: the package loads neither torch nor the libraries by itself.
+torch = _lib = _native = _current = None
 
 
 def _load():
-    global torch, _lib, _fail, _empty, _bf16, _raw_stream, _current
+    global torch, _lib, _native, _current
     if torch is None:
         import torch as t
 
         from . import _check, load_library
-        _lib, _fail, _empty, _bf16 = load_library(), _check, t.empty, t.bfloat16
-        _raw_stream, _current = t._C._cuda_getCurrentRawStream, t._C._cuda_getDevice
+        lib = load_library()
+        try:
+            from . import _paged_native as native
+        except ImportError as e:
+            raise ImportError(f"the paged cache's binding is not built ({e}); run "
+                              "`python -m exact_io_aware_33_gb300.build` or __graft_entry__.build() first") from e
+        native.set_fail(_check)
+        _lib, _native, _current = lib, native, t._C._cuda_getDevice
         torch = t
 
 
@@ -136,37 +143,10 @@ class PagedBatch:
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
         self.device = dev
         self._index = dev.index
-        self._made = (-1, None, 0)
-
-    def _for_rows(self, T: int):
-        """(T, C struct, its address) for tensors of T rows."""
-        made = self._made
-        if made[0] != T:
-            if self.cu_q is None and T != self.B:
-                raise ValueError(f"{T} rows for {self.B} sequences of one token each")
-            s = _BatchStruct(self.block_table.data_ptr(), self.kv_lens.data_ptr(),
-                             0 if self.cu_q is None else self.cu_q.data_ptr(), self.B, T, self.max_q,
-                             self.max_pages, self.max_kv)
-            made = (T, s, ctypes.addressof(s))
-            self._made = made  # one assignment: another thread sees the old tuple or this one
-        return made
-
-
-def _stride(t, name, rows, heads, d, device):
-    """Checks a packed [rows, heads, d] tensor whose rows may lie apart (0: any number of them); the row stride."""
-    shape, st = t.shape, t.stride()
-    if (t.dtype is not _bf16 or t.device != device or len(shape) != 3 or shape[2] != d or st[2] != 1
-            or (st[1] != d and shape[1] != 1) or (rows and shape[0] != rows) or (heads and shape[1] != heads)):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-        if t.dtype is not _bf16:
-            raise TypeError(f"{name} must be {_bf16}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if len(shape) == 3 and shape[2] == d and (not rows or shape[0] == rows) and (not heads or shape[1] == heads):
-            raise ValueError(f"the heads and channels of {name} must lie side by side")
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows or 'T'}, {heads or 'heads'}, {d}]")
-    return st[0] if shape[0] > 1 else shape[1] * d  # (one row: whatever its stride says)
+        # (the rows of a call's tensors take the place of T there)
+        self._struct = _BatchStruct(block_table.data_ptr(), kv_lens.data_ptr(),
+                                    0 if cu_q is None else cu_q.data_ptr(), B, B, self.max_q, max_pages, self.max_kv)
+        self._address = ctypes.addressof(self._struct)
 
 
 def _elsewhere(device, stream):
@@ -188,43 +168,10 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
     if stream is not None or _current() != index:
         with _elsewhere(cache.device, stream):
             return fa_paged_append(cache, batch, k, v, q, rope, interleaved, q_out)
-    dev, d, H = cache.device, cache.d, cache.num_heads
     if batch._index != index:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    ks = _stride(k, "k", 0, H, d, dev)
-    T = k.shape[0]
-    vs = _stride(v, "v", T, H, d, dev) if T else 0
-    made = batch._made
-    if made[0] != T:
-        made = batch._for_rows(T)
-    cos = sin = max_pos = rot = Hq = qp = qs = op = os_ = 0
-    if rope is not None:
-        c, s = rope
-        _require(c, "cos", torch.float32, 2, dev)
-        _require(s, "sin", torch.float32, 2, dev)
-        max_pos, rot = shape = c.shape
-        if shape != s.shape or not c.is_contiguous() or not s.is_contiguous():
-            raise ValueError("cos and sin must be contiguous and of one shape")
-        if rot:
-            rot *= 2
-            cos, sin = c.data_ptr(), s.data_ptr()
-    if q is not None:
-        Hq = q.shape[1]
-        qs = _stride(q, "q", T, Hq, d, dev) if T else 0
-        if q_out is None:
-            q_out = _empty((T, Hq, d), dtype=_bf16, device=dev)
-            os_ = Hq * d
-        else:
-            os_ = _stride(q_out, "q_out", T, Hq, d, dev) if T else 0
-        if Hq:
-            qp, op = q.data_ptr(), q_out.data_ptr()
-    else:
-        q_out = None
-    rc = _lib.fa_paged_append(cache._address, made[2], k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, op, os_, Hq, cos,
-                              sin, max_pos, rot, 1 if interleaved else 0, _raw_stream(index))
-    if rc:
-        _fail(rc, "fa_paged_append")
-    return q_out
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    cos, sin = (None, None) if rope is None else rope
+    return _native.append(cache._address, batch._address, index, k, v, q, cos, sin, interleaved, q_out)
 
 
 def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int) -> int:
@@ -232,7 +179,7 @@ def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int)
     if _current() != cache._index:
         with _elsewhere(cache.device, None):
             return fa_paged_attn_workspace_bytes(cache, batch, Hq)
-    return _lib.fa_paged_attn_workspace_bytes(cache._address, batch._for_rows(batch.B)[2], Hq)
+    return _lib.fa_paged_attn_workspace_bytes(cache._address, batch._address, Hq)
 
 
 def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scale: float | None = None,
@@ -245,37 +192,7 @@ def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scal
     if stream is not None or _current() != index:
         with _elsewhere(cache.device, stream):
             return fa_paged_attn(cache, batch, q, window, scale, out, lse, workspace)
-    dev, d = cache.device, cache.d
     if batch._index != index:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {dev}")
-    qs = _stride(q, "q", 0, 0, d, dev)
-    T, Hq, _ = q.shape
-    made = batch._made
-    if made[0] != T:
-        made = batch._for_rows(T)
-    if out is None:
-        out = _empty((T, Hq, d), dtype=_bf16, device=dev)
-    elif T and (_stride(out, "out", T, Hq, d, dev) < 0 or not out.is_contiguous()):
-        raise ValueError(f"out must be contiguous [{T}, {Hq}, {d}]")
-    if lse is None:
-        lse = _empty((T, Hq), dtype=torch.float32, device=dev)
-    else:
-        _require(lse, "lse", torch.float32, 2, dev)
-        if tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous [{T}, {Hq}]")
-    ws = need = 0
-    if workspace is None:
-        need = _lib.fa_paged_attn_workspace_bytes(cache._address, made[2], Hq)
-        if need:
-            workspace = _empty(need, dtype=torch.uint8, device=dev)
-            ws = workspace.data_ptr()
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
-    else:
-        need = workspace.nbytes
-        ws = workspace.data_ptr() if need else 0
-    rc = _lib.fa_paged_attn(cache._address, made[2], q.data_ptr(), qs, out.data_ptr(), lse.data_ptr(), Hq, window,
-                            cache._scale if scale is None else scale, ws, need, _raw_stream(index))
-    if rc:
-        _fail(rc, "fa_paged_attn")
-    return out, lse
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    return _native.attn(cache._address, batch._address, index, q, window, cache._scale if scale is None else scale,
+                        out, lse, workspace)

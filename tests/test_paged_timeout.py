@@ -34,7 +34,9 @@ def test_wait_runs_out_and_the_context_survives(timeout_lib, d, rows, heads, max
     cache, gpu = w.to_gpu(), q.cuda()
     o = torch.empty_like(gpu)
     lse = torch.empty(rows, heads, device="cuda")
-    struct = batch._for_rows(rows)[2]
+    c_batch = type(batch._struct).from_buffer_copy(batch._struct)
+    c_batch.T = rows
+    struct = ctypes.addressof(c_batch)
     need = timeout_lib.fa_paged_attn_workspace_bytes(cache._address, struct, heads)
     ws = torch.zeros(max(need, 1), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()

@@ -10,6 +10,15 @@
 // checked against the sizes the host gave before it is used; what fails the
 // check is treated as absent and kStatusIndex is raised, so a bad table never
 // becomes a bad address.
+//
+// Launch overlap. The attention's streaming and chunk kernels need every SM
+// for themselves: one that starts while its predecessor's blocks are still
+// there places fewer of its CTAs on some SMs and keeps them so for the whole
+// run (8 sequences of 8192 keys, 32 heads, one call after another: 119 us,
+// 87 us otherwise). So the kernels that come before it in a step, the append
+// and the joins, do not call grid_dep_launch: the next kernel is launched
+// ahead and starts when their last block ends, which is still some 3 us
+// sooner than without programmatic serialization.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -195,8 +195,7 @@ template <int D>
 __global__ void __launch_bounds__(128) append_one_kernel(const AppendArgs a) {
   constexpr int kUnits = D / 16;
   constexpr int kHeadsPerWarp = 32 / kUnits;  // of queries
-  grid_dep_wait();
-  grid_dep_launch();
+  grid_dep_wait();  // (no early launch of the next kernel: see fa_paged.cuh)
   const int per_seq = a.Hkv + (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp;
   const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int seq = static_cast<int>(w / per_seq);
@@ -288,8 +287,7 @@ template <int D>
 __global__ void __launch_bounds__(1024) append_pages_kernel(const AppendArgs a) {
   constexpr int kUnits = D / 16;
   __shared__ float red[2][2][32];  // [parity of the head][key or value][warp]
-  grid_dep_wait();
-  grid_dep_launch();
+  grid_dep_wait();  // (no early launch of the next kernel: see fa_paged.cuh)
   const int parts = a.kv_parts + a.q_parts;
   const long long item = blockIdx.x / parts;
   const int part = static_cast<int>(blockIdx.x % parts);

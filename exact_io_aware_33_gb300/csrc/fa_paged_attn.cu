@@ -930,8 +930,7 @@ __global__ void __launch_bounds__(256 * NB * kShare) paged_join_kernel(const Att
   constexpr int R = 8 * NB, kCols = D / 32, kRun = kShare == 1 ? 4 : 16;
   __shared__ float s_x[R][kShare][D];
   __shared__ float s_m[R][kShare], s_sum[R][kShare];
-  grid_dep_wait();
-  grid_dep_launch();
+  grid_dep_wait();  // (no early launch of the next kernel: see fa_paged.cuh)
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wrow = warp / kShare, share = warp % kShare;
   const JoinRecord rec = a.records[c];
@@ -1022,14 +1021,7 @@ int launch_rows(const PagedPool& pool, const AttnArgs& a, const PagedPlan& plan,
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, kSlot)) return -3;
   const dim3 grid(static_cast<unsigned>(plan.ctas)), block(kThreads);
   cudaError_t e;
-  // The streaming form fills every SM's shared memory and does not start under
-  // the kernel before it: on SMs whose shared memory that kernel had set up
-  // smaller, fewer of its CTAs would fit for the whole run (B = 8, 32 heads,
-  // 8192 keys, one call after another: 119 us overlapped, 92 us not).
-  if (kCluster)
-    e = launch_with(kern, grid, block, C::kSmemBytes, true, plan.cluster, stream, mk, mv, a);
-  else
-    e = launch_with(kern, grid, block, C::kSmemBytes, false, 1, stream, mk, mv, a);
+  e = launch_clusters(kern, grid, block, C::kSmemBytes, kCluster ? plan.cluster : 1, stream, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
   if (!kCluster && plan.ctas > 1) {
     // fewer items than SMs: several parts to most of them

@@ -1077,8 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkArgs a) {
   constexpr int kCols = D / 8;
-  grid_dep_wait();
-  grid_dep_launch();
+  grid_dep_wait();  // (no early launch of the next kernel: see fa_paged.cuh)
   const int c = blockIdx.x / 8;
   const JoinRecord rec = a.records[c];
   if (rec.parts == 0) return;
@@ -1124,8 +1123,7 @@ int launch_chunk_d(const PagedPool& pool, const ChunkArgs& a, int ctas, cudaStre
   auto kern = paged_chunk_kernel<D>;
   // attribute slots 28, 29
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, D == 64 ? 28 : 29)) return -3;
-  // (not overlapped with the kernel before: see launch_rows in fa_paged_attn.cu)
-  cudaError_t e = launch_with(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, false, 1, stream, mk, mv, a);
+  cudaError_t e = launch_overlapped(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) return -3;
   e = launch_overlapped(paged_chunk_join_kernel<D>, dim3(8 * (ctas - 1)), dim3(256), 0, stream, a);
   return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;

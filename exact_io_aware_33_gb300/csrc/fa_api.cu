@@ -488,6 +488,17 @@ bool row_stride_ok(long long stride, int heads, int d) {
   return stride >= static_cast<long long>(heads) * d && stride % 8 == 0 && stride <= (1LL << 40);
 }
 
+// Whether two packed bf16 tensors of T rows share memory: rows of `aw` and `bw`
+// elements, `as` and `bs` elements apart. Exact where the strides are equal
+// (slices of one fused projection interleave without meeting).
+bool rows_meet(const void* a, long long as, long long aw, const void* b, long long bs, long long bw, int T) {
+  const long long a0 = static_cast<long long>(reinterpret_cast<uintptr_t>(a)), b0 = static_cast<long long>(reinterpret_cast<uintptr_t>(b));
+  if (a0 + 2 * ((T - 1) * as + aw) <= b0 || b0 + 2 * ((T - 1) * bs + bw) <= a0) return false;
+  if (T == 1 || as != bs) return true;
+  const long long off = (b0 - a0) % (2 * as), ahead = off < 0 ? off + 2 * as : off;  // of a's nearest row before it
+  return ahead < 2 * aw || ahead + 2 * bw > 2 * as;
+}
+
 // SMs of the current device, looked up once; a GB300's where there is none.
 int paged_sms() {
   const int sms = fa::device_sm_count();
@@ -520,6 +531,14 @@ int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, co
   if (Hq > 0 && (!fa::aligned16(q) || !fa::aligned16(q_out) || !row_stride_ok(q_stride, Hq, d) ||
                  !row_stride_ok(q_out_stride, Hq, d)))
     return FA_ERR_INVALID;
+  if (Hq > 0) {
+    const long long qw = static_cast<long long>(Hq) * d, kw = static_cast<long long>(pool.num_heads) * d;
+    const bool in_place = q_out == q && (q_out_stride == q_stride || dev.T == 1);
+    if ((!in_place && rows_meet(q_out, q_out_stride, qw, q, q_stride, qw, dev.T)) ||
+        rows_meet(q_out, q_out_stride, qw, k, k_stride, kw, dev.T) ||
+        rows_meet(q_out, q_out_stride, qw, v, v_stride, kw, dev.T))
+      return FA_ERR_INVALID;
+  }
   if (rot > 0 && (!fa::aligned16(cos) || !fa::aligned16(sin) || max_pos == 0)) return FA_ERR_INVALID;
   fa::DeviceState* st = nullptr;
   rc = fa::current_device(&st);
@@ -550,6 +569,10 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID;
   if (empty) return FA_OK;
   if (!fa::aligned16(q) || !fa::aligned16(o) || !aligned4(lse) || !row_stride_ok(q_stride, Hq, cache->d))
+    return FA_ERR_INVALID;
+  // o may be q itself: a row is read before it is written, by the CTA that writes it or by a kernel before
+  const long long width = static_cast<long long>(Hq) * cache->d;
+  if (!(o == q && (q_stride == width || dev.T == 1)) && rows_meet(o, width, width, q, q_stride, width, dev.T))
     return FA_ERR_INVALID;
   // packed (query, head) rows of a key head are counted in 32 bits
   if (static_cast<long long>(batch->max_q) * Hq > 0x7fffffffLL - 4096) return FA_ERR_INVALID;

@@ -134,8 +134,8 @@ class PagedBatch:
                 raise ValueError(f"cu_q has {cu_q.shape[0]} entries, expected {B + 1}")
         elif max_q != 1:
             raise ValueError("max_q must be 1 without cu_q")
-        if max_q < 1 or max_kv < 0:
-            raise ValueError("max_q must be at least 1 and max_kv at least 0")
+        if not (1 <= max_q < 2 ** 31 and 0 <= max_kv < 2 ** 31 and max_pages < 2 ** 31):
+            raise ValueError("max_q must be at least 1 and max_kv at least 0, all sizes below 2^31")
         for name, t in (("block_table", block_table), ("kv_lens", kv_lens), ("cu_q", cu_q)):
             if t is not None and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
@@ -170,6 +170,8 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
             return fa_paged_append(cache, batch, k, v, q, rope, interleaved, q_out)
     if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
     cos, sin = (None, None) if rope is None else rope
     return _native.append(cache._address, batch._address, index, k, v, q, cos, sin, interleaved, q_out)
 

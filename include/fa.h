@@ -339,7 +339,8 @@ typedef struct fa_paged_batch {
  *   q       : in,  bf16 [T, Hq, d], rows q_stride elements apart; NULL with
  *             Hq = 0. Hq need not be related to num_heads here.
  *   q_out   : out, bf16 [T, Hq, d], rows q_out_stride apart: the rotated
- *             queries; may be q itself (with the same stride)
+ *             queries; may be q itself (with the same stride), and must not
+ *             overlap q otherwise, nor k or v (FA_ERR_INVALID)
  *   cos, sin: in,  fp32 [max_pos, rot / 2]: the angles of each position;
  *             NULL with rot = 0 (no rotation)
  *   rot     : channels that turn, a multiple of 16 up to d; pairs are
@@ -368,7 +369,8 @@ int fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, co
  * p - window < j <= p; 0 = none), grouped heads (query head h reads key head
  * h / (Hq / num_heads); Hq must be a multiple of num_heads).
  *   q        : in,  bf16 [T, Hq, d], rows q_stride elements apart (a multiple of 8)
- *   o        : out, bf16 [T, Hq, d] contiguous
+ *   o        : out, bf16 [T, Hq, d] contiguous; may be q itself (when that is
+ *              contiguous), and must not overlap it otherwise (FA_ERR_INVALID)
  *   lse      : out, fp32 [T, Hq], natural-log log-sum-exp
  *   workspace: at least fa_paged_attn_workspace_bytes(cache, batch, Hq)
  *              bytes (0: may be NULL; it does not depend on T), 256-byte

@@ -101,12 +101,12 @@ def _batch(**kw):
     return _BatchStruct(**f)
 
 
-def _attn(lib, c, b, q=P, stride=4 * 64, o=P, lse=P, Hq=4, window=0, scale=0.125, ws=0, bytes_=0):
+def _attn(lib, c, b, q=P, stride=4 * 64, o=P + 0x10000, lse=P, Hq=4, window=0, scale=0.125, ws=0, bytes_=0):
     return lib.fa_paged_attn(ctypes.addressof(c) if c else 0, ctypes.addressof(b) if b else 0, q, stride, o, lse, Hq,
                              window, scale, ws, bytes_, 0)
 
 
-def _append(lib, c, b, k=P, ks=2 * 64, v=P, vs=2 * 64, q=P, qs=4 * 64, qo=P, qos=4 * 64, Hq=4, cos=P, sin=P,
+def _append(lib, c, b, k=P, ks=2 * 64, v=P, vs=2 * 64, q=P, qs=4 * 64, qo=P + 0x10000, qos=4 * 64, Hq=4, cos=P, sin=P,
             max_pos=9, rot=64):
     return lib.fa_paged_append(ctypes.addressof(c) if c else 0, ctypes.addressof(b) if b else 0, k, ks, v, vs, q, qs,
                                qo, qos, Hq, cos, sin, max_pos, rot, 0, 0)
@@ -170,6 +170,29 @@ def test_attention_arguments_are_checked_on_the_host(lib, kw, code):
     (dict(cos=0), fa.FA_ERR_INVALID), (dict(sin=P + 4), fa.FA_ERR_INVALID), (dict(max_pos=0), fa.FA_ERR_INVALID)])
 def test_append_arguments_are_checked_on_the_host(lib, kw, code):
     assert _append(lib, _cache(), _batch(), **kw) == code
+
+
+ROW = 4 * 64 * 2  # bytes of a query row; nine rows
+
+
+@pytest.mark.parametrize("o,stride,code", [
+    (P, 256, fa.FA_ERR_WORKSPACE),                 # in place: past this check
+    (P, 512, fa.FA_ERR_INVALID),                   # ... but the rows lie apart
+    (P + ROW, 256, fa.FA_ERR_INVALID), (P - 8 * ROW, 256, fa.FA_ERR_INVALID), (P + 8 * ROW, 256, fa.FA_ERR_INVALID),
+    (P + 9 * ROW, 256, fa.FA_ERR_WORKSPACE), (P - 9 * ROW, 256, fa.FA_ERR_WORKSPACE)])
+def test_attention_output_may_be_the_queries_or_apart_from_them(lib, o, stride, code):
+    assert _attn(lib, _cache(), _batch(max_pages=100000), o=o, stride=stride) == code
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=P + ROW), dict(qo=P - ROW), dict(qo=P, qos=512), dict(qo=P, qs=512),
+    # slices of a fused projection of 8 heads: queries 0..3, keys 4..5, values 6..7
+    dict(qs=512, qos=512, ks=512, vs=512, k=P + ROW, v=P + ROW + ROW // 2, qo=P + 16),
+    dict(qs=512, qos=512, ks=512, vs=512, k=P + ROW, v=P + ROW + ROW // 2, qo=P + ROW),
+    dict(qs=512, qos=512, ks=512, vs=512, k=P + ROW, v=P + ROW + ROW // 2, qo=P - 16),
+    dict(qo=P + 0x10000, k=P + 0x10000 + 8 * ROW), dict(qo=P + 0x10000, v=P + 0x10000 - 8 * 256)])
+def test_rotated_queries_may_not_overlap_the_inputs(lib, kw):
+    assert _append(lib, _cache(), _batch(), **kw) == fa.FA_ERR_INVALID
 
 
 def test_workspace(lib):

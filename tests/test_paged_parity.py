@@ -303,6 +303,20 @@ def test_the_length_bound_only_divides_the_work(max_kv):
     check_attn(w, cu, o, lse, q, 0.125)
 
 
+@pytest.mark.parametrize("lens,news,max_pages", [([300, 70], [1, 1], None), ([300, 2000], [2, 3], 5000),
+                                                 ([900, 2500], [300, 200], 5000)])
+def test_the_output_may_take_the_queries_place(lens, news, max_pages):
+    # the cluster, streaming and chunk forms
+    w = World(lens, 2, 16, 128, seed=61, max_pages=max_pages).fill()
+    cu, batch = w.batch(news)
+    cache = w.to_gpu()
+    q = bf16(w.rng, sum(news), 16, 128).cuda()
+    want, want_lse = fa.fa_paged_attn(cache, batch, q)
+    o, lse = fa.fa_paged_attn(cache, batch, q, out=q)
+    done()
+    assert o is q and torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_shared_pages_may_be_read_by_several_sequences():
     w = World([64, 64], 2, 16, 64, seed=12).fill()
     w.table[1, :3] = w.table[0, :3]  # a common beginning
@@ -741,6 +755,14 @@ def test_arguments_that_the_binding_refuses():
         fa.PagedBatch(batch.block_table, batch.kv_lens[:1])
     with pytest.raises(ValueError):
         fa.PagedBatch(batch.block_table, batch.kv_lens, max_q=2)
+    with pytest.raises(ValueError):
+        fa.PagedBatch(batch.block_table, batch.kv_lens, batch.cu_q, max_q=2 ** 32 + 1)
+    with pytest.raises(ValueError):
+        fa.fa_paged_append(cache, batch, k, k, q_out=q)
+    with pytest.raises(fa.FAError):
+        fa.fa_paged_attn(cache, batch, q[:2], out=q[1:])      # outputs over another row's queries
+    with pytest.raises(fa.FAError):
+        fa.fa_paged_append(cache, batch, k, k.clone(), q=k.clone(), q_out=k)  # rotated queries over the keys
     with pytest.raises(TypeError):
         fa.PagedBatch(batch.block_table.long(), batch.kv_lens)
     with pytest.raises(ValueError):

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // kernel has completed and its writes are visible (at once when there is no
 // such kernel). grid_dep_launch() then lets the next kernel's CTAs start;
 // because it follows the wait, a kernel never overlaps the one two places
-// before it.
+// before it. (A kernel that leaves it out lets them start when it ends.)
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

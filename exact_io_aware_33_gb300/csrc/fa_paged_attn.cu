@@ -1041,6 +1041,27 @@ int launch_rows_d(const PagedPool& pool, const AttnArgs& a, const PagedPlan& pla
   return plan.rows == 8 ? launch_rows<D, 1, false>(pool, a, plan, stream) : launch_rows<D, 2, false>(pool, a, plan, stream);
 }
 
+// What the cluster and the streaming form cost, in microseconds, fitted to the
+// times of 350 batch shapes on 152 SMs, of even and of ragged lengths (1 to 64
+// sequences of up to 256 to 8192 keys, 2 to 32 key heads, one or a few tokens
+// each): the form chosen is within 2 % of the best one on average. A cluster CTA's tiles follow one another, the
+// slower the more CTAs share an SM (`more`: CTAs per SM, less one); clusters of
+// eight double up on an SM sooner. A streaming CTA has at least kPartUnits
+// units, and a second launch joins its pieces. Measured, cluster / streaming:
+// 32 query and 8 key heads, d = 128: 1 x 256 keys 5.5 / 9.7 us, 1 x 4096 10.5 /
+// 11.4, 8 x 1024 10.6 / 13.8, 16 x 4096 29 / 34, but 1 x 8192 15.6 / 14.1 and
+// 32 x 2048 32 / 31; 24 x 5 tokens over 4096 keys, 12 and 4 heads, d = 64: 21 /
+// 25 us.
+struct RowCosts {
+  double start, join, more;    // cluster form: one CTA per item, several, and per further CTA of an SM
+  double tile, tile_more;      // a tile, and per further CTA of an SM
+  double eights;               // SMs that clusters of eight fill before they double up, of all
+  double stream, stream_tile;  // streaming form: a launch and its join, and a unit
+};
+constexpr RowCosts kRowCosts[2][2] = {  // d = 64, 128; 8, 16 rows
+    {{2.5, 2, 1.5, 0.80, 0.20, 1.0, 12, 0.90}, {4.0, 2, 3.0, 1.00, 0.40, 1.0, 13, 1.00}},
+    {{2.5, 2, 1.6, 0.60, 0.28, 0.6, 10, 0.95}, {4.4, 5, 4.4, 0.72, 0.30, 0.6, 9, 1.00}}};
+
 }  // namespace
 
 PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, const int Hq, int max_kv, int sms) {
@@ -1053,15 +1074,34 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   const int tile = pool.d == 64 ? kTileOf<64> : kTileOf<128>;
   const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + tile - 1) / tile : 1;
   const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
-  // The cluster form while every CTA of a cluster of up to eight has a slot and
-  // at most eight tiles. One sequence of 300 keys (32 query heads, 8 key heads,
-  // d = 128): 6.3 us, against 14 us for the streaming form and its join.
-  long long want = 1;
-  while (want < 8 && 2 * want < tiles) want *= 2;
-  if (items * want <= slots && tiles <= 8 * want) {
-    r.cluster = static_cast<int>(want);
-    r.ctas = items * want;
-    return r;
+  const auto chunk_cost = [&](double pair_items) {
+    return 22 + (pool.d == 64 ? 0.95 : 1.6) / 152 * pair_items * (max_kv / 128 + 4);
+  };
+  const double seqs = batch.B, heads = pool.num_heads;
+
+  // The cluster form, of how many CTAs, or one that needs a workspace? None of
+  // what this depends on is the number of packed rows, so that the workspace
+  // does not depend on it either.
+  const RowCosts& w = kRowCosts[pool.d == 128][r.rows == 16];
+  double least = 0;
+  for (int c = 1; c <= 8 && items * c <= slots; ++c) {
+    const long long per = (tiles + c - 1) / c;
+    if (c > 1 && per == (tiles + c - 2) / (c - 1)) continue;  // no fewer tiles per CTA than with one CTA less
+    const double more = fmax(static_cast<double>(items * c) / (c > 6 ? w.eights * sms : sms) - 1, 0.0);
+    const double cost = w.start + w.more * more + per * (w.tile + w.tile_more * more) + (c > 1 ? w.join : 0);
+    if (r.cluster == 0 || cost < least) {
+      r.cluster = c;
+      least = cost;
+    }
+  }
+  if (r.cluster > 0) {
+    const double units = static_cast<double>(items) * (tiles + kItemUnits) / slots;
+    if (least < w.stream + w.stream_tile * fmax(units, kPartUnits) &&
+        (rows <= 8 || least < chunk_cost(heads * seqs * ((rows + 255) / 256)))) {
+      r.ctas = items * r.cluster;
+      return r;
+    }
+    r.cluster = 0;
   }
   // Rows (16 a tile, the cached tiles read once for each) or chunks (256 rows
   // on the tensor memory)? What each costs was measured: about 12 us and 1.07
@@ -1070,13 +1110,11 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   // keys, d = 128: 32 rows 43 against 45 us, 64 rows 70 against 46; at 24 of
   // 4096 keys, d = 64: 15 rows 19 against 43, 48 rows 46 against 43 us.
   // A ragged batch has at most its packed rows' tiles and one more per sequence.
-  const double seqs = batch.B, heads = pool.num_heads, packed = static_cast<double>(batch.T) * G;
+  const double packed = static_cast<double>(batch.T) * G;
   const double row_items = heads * fmin(seqs * r.row_tiles, seqs + packed / r.rows);
   const double pair_items = heads * fmin(seqs * ((rows + 255) / 256), seqs + packed / 256);
-  const double steps = max_kv / 128 + 1;
   const double row_cost = 12 + 1.07 / 304 * row_items * (tiles + kItemUnits);
-  const double chunk_cost = 22 + (pool.d == 64 ? 0.95 : 1.6) / 152 * pair_items * (steps + 3);
-  r.chunk = rows > 8 && chunk_cost < row_cost;
+  r.chunk = rows > 8 && chunk_cost(pair_items) < row_cost;
   r.ctas = r.chunk ? sms : slots;
   r.items = static_cast<long long>(row_items);
   // The choice depends on the packed rows, what a caller has to provide does not.

@@ -303,6 +303,24 @@ def test_the_length_bound_only_divides_the_work(max_kv):
     check_attn(w, cu, o, lse, q, 0.125)
 
 
+@pytest.mark.parametrize("lens,news,Hq,Hkv,d", [
+    ([381, 130], [1, 1], 25, 25, 128),             # clusters of three, five, six and seven
+    ([320], [1], 30, 30, 128),
+    ([765], [1], 25, 25, 128),
+    ([430], [1], 13, 13, 128),
+    ([1500, 1490, 3, 700, 1], [1] * 5, 32, 32, 128),   # more tiles per CTA than its ring holds
+    ([2000, 1100], [5, 3], 60, 30, 64),
+    ([3000, 1], [2, 1], 48, 6, 128),
+    ([2100] * 3, [1] * 3, 24, 24, 64)])
+def test_clusters_of_any_size(lens, news, Hq, Hkv, d):
+    w = World(lens, Hkv, 64, d, seed=62).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, sum(news), Hq, d)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+    done()
+    check_attn(w, cu, o, lse, q, d ** -0.5)
+
+
 @pytest.mark.parametrize("lens,news,max_pages", [([300, 70], [1, 1], None), ([300, 2000], [2, 3], 5000),
                                                  ([900, 2500], [300, 200], 5000)])
 def test_the_output_may_take_the_queries_place(lens, news, max_pages):

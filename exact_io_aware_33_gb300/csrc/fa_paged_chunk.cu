@@ -16,7 +16,7 @@
 // about 200 instructions per thread for a tile of K or of V, next to the 256
 // rows that share it; doing it once per pair of 128-row tiles is why a CTA
 // holds two of them. Measured: 2 x 2048 queries over 8192 keys, 32 query and 8
-// key heads, d = 128, in 382 us: 1.26 PFLOP/s, 65 % of the measured matrix
+// key heads, d = 128, in 380 us: 1.26 PFLOP/s, 65 % of the measured matrix
 // product's rate. Per step and tile the MMAs take 0.76 us and the softmax 0.85
 // us, two tiles in turn.
 //
@@ -61,7 +61,11 @@ constexpr int kWidenWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 constexpr int kGroups = kBN / 16;
 constexpr int kInfos = 8;        // tiles' scale records kept
 constexpr int kPieces = 4;       // pieces' records kept
-constexpr int kItemSteps = 3;    // an item costs about this many steps more than it has
+// An item costs about this many steps more than it has: its queries, the start
+// of its chain, its write-back. Four prompts of 2048 tokens, 32 query and 8 key
+// heads, d = 128: 180 us with 5, 192 with 3; 16 heads, d = 64: 85 and 82 us.
+template <int D>
+constexpr int kItemSteps = D == 64 ? 3 : 5;
 constexpr int kPartSteps = 8;    // a part has at least this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -103,18 +107,22 @@ struct Cfg {
   static constexpr int kTileBytes = kChunks * kChunkBytes;   // widened
   static constexpr int kRawBytes = kBN * D;                  // codes
   static constexpr int kStages = 2;
+  static constexpr int kRaw = D == 64 ? 4 : 1;  // tiles of codes ahead of the widening: as many as there is room for
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kRawKOff = kVOff + kStages * kTileBytes;
-  static constexpr int kRawVOff = kRawKOff + kRawBytes;
-  static constexpr int kInfoOff = kRawVOff + kRawBytes;
+  static constexpr int kRawVOff = kRawKOff + kRaw * kRawBytes;
+  static constexpr int kInfoOff = kRawVOff + kRaw * kRawBytes;
   static constexpr int kPieceOff = kInfoOff + kInfos * static_cast<int>(sizeof(TileInfo));
   static constexpr int kBarOff = kPieceOff + (kPieces * static_cast<int>(sizeof(Piece)) + 7) / 8 * 8;
   enum : int {
     kBarQFull = 0,                      // two
-    kBarRawKFull = kBarQFull + 2, kBarRawKEmpty, kBarRawVFull, kBarRawVEmpty,
-    kBarKFull,                          // two of each from here
+    kBarRawKFull = kBarQFull + 2,       // kRaw of each
+    kBarRawKEmpty = kBarRawKFull + kRaw,
+    kBarRawVFull = kBarRawKEmpty + kRaw,
+    kBarRawVEmpty = kBarRawVFull + kRaw,
+    kBarKFull = kBarRawVEmpty + kRaw,   // two of each from here
     kBarKEmpty = kBarKFull + kStages,
     kBarVFull = kBarKEmpty + kStages,
     kBarVEmpty = kBarVFull + kStages,
@@ -199,9 +207,10 @@ __device__ __forceinline__ long long scan_sum(long long own) {
   return own;
 }
 
-// The units (steps, and kItemSteps per item) of the sequences, by one warp.
+// The units (steps, and kExtra per item) of the sequences, by one warp.
 // `lanes` lanes (a power of two) share a sequence's pairs, so that a batch of
 // few sequences with many pairs does not take long.
+template <int kExtra>
 struct Units {
   int lanes;
   long long total;
@@ -213,7 +222,7 @@ struct Units {
     if (b < a.batch.B) {
       const PagedSeq s = paged_seq(a.batch, b, a.status);
       const int rows = s.n * a.g.G, pairs = pairs_of(rows);
-      for (int i = lane % lanes; i < pairs; i += lanes) sum += pair_steps(a, rows, s.len - s.n, i) + kItemSteps;
+      for (int i = lane % lanes; i < pairs; i += lanes) sum += pair_steps(a, rows, s.len - s.n, i) + kExtra;
     }
     end = scan_sum(sum * a.Hkv);
     for (int m = 1; m < lanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -257,14 +266,15 @@ __device__ __forceinline__ long long part_start(long long units, int parts, int 
 }
 
 // An item, found from one of its units (all by one warp).
+template <int kExtra>
 struct Item {
   int seq, pair, h;
   PagedSeq s;
   PairGeo g;
   long long first;  // its first unit
 
-  __device__ __forceinline__ long long units() const { return g.steps + kItemSteps; }
-  __device__ __forceinline__ bool find(const ChunkArgs& a, Units& all, long long u) {
+  __device__ __forceinline__ long long units() const { return g.steps + kExtra; }
+  __device__ __forceinline__ bool find(const ChunkArgs& a, Units<kExtra>& all, long long u) {
     long long before;
     seq = all.find(a, u, &before);
     if (seq >= a.batch.B) return false;
@@ -274,7 +284,7 @@ struct Item {
     for (int i0 = 0; i0 < pairs; i0 += 32) {
       const int i = i0 + static_cast<int>(lane_id());
       const long long own =
-          i < pairs ? static_cast<long long>(a.Hkv) * (pair_steps(a, rows, s.len - s.n, i) + kItemSteps) : 0;
+          i < pairs ? static_cast<long long>(a.Hkv) * (pair_steps(a, rows, s.len - s.n, i) + kExtra) : 0;
       const long long end = before + scan_sum(own);
       const uint32_t past = __ballot_sync(0xffffffffu, end > u);
       if (past) {
@@ -341,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(C::kBarRawKFull), 1);
-    mbar_init(bar(C::kBarRawKEmpty), 4);
-    mbar_init(bar(C::kBarRawVFull), 1);
-    mbar_init(bar(C::kBarRawVEmpty), 4);
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(bar(C::kBarRawKFull + s), 1);
+      mbar_init(bar(C::kBarRawKEmpty + s), 4);
+      mbar_init(bar(C::kBarRawVFull + s), 1);
+      mbar_init(bar(C::kBarRawVEmpty + s), 4);
+    }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar(C::kBarKFull + s), 4);
       mbar_init(bar(C::kBarKEmpty + s), 1);
@@ -399,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the present ones are issued.
       const int box_rows = min(a.batch.page_size, kBN), per_box = box_rows / 16;
       const uint32_t box_bytes = static_cast<uint32_t>(box_rows * D);
-      Units all;
+      constexpr int kExtra = kItemSteps<D>;
+      Units<kExtra> all;
       all.start(a);
       const long long units = all.total;
       const int parts = parts_of(units, gridDim.x);
@@ -420,15 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++np;
       };
-      Item it;
+      Item<kExtra> it;
       bool more = u < u1;
       if (more) more = it.find(a, all, u);
       JoinRecord record{};
       for (; more && ok && it.first < u1; more = it.next(a)) {
         // steps [s0, s1) of the item; one without steps belongs to the part of its first unit
         const int n = it.g.steps;
-        const int s0 = static_cast<int>(max(u - it.first - kItemSteps, 0LL));
-        const int s1 = static_cast<int>(min(max(u1 - it.first - kItemSteps, 0LL), static_cast<long long>(n)));
+        const int s0 = static_cast<int>(max(u - it.first - kExtra, 0LL));
+        const int s1 = static_cast<int>(min(max(u1 - it.first - kExtra, 0LL), static_cast<long long>(n)));
         if (n > 0 ? s1 <= s0 : it.first < u) continue;
         const int rows = it.s.n * a.g.G, p0 = it.s.len - it.s.n, h = it.h, seq = it.seq;
         const int r0 = it.pair * 2 * kBM;
@@ -516,10 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == 2) scales();
             const uint32_t bytes = __popc(issuers & (0xffu << (8 * i))) * box_bytes;
             const bool own = (lane >> 3) == i;
-            if (gs >= 1) ok = mbar_wait_w(bar(C::kBarRawKEmpty), (gs - 1) & 1, abort_flag);
+            const int rs = gs % C::kRaw;
+            if (gs >= C::kRaw) ok = mbar_wait_w(bar(C::kBarRawKEmpty + rs), (gs / C::kRaw - 1) & 1, abort_flag);
             if (!ok) break;
             if (own) {
-              if (issues) tma_load_3d(base + C::kRawKOff + grp * 16 * D, &tmK, bar(C::kBarRawKFull), 0, slot, blk);
+              if (issues) tma_load_3d(base + C::kRawKOff + rs * C::kRawBytes + grp * 16 * D, &tmK, bar(C::kBarRawKFull + rs), 0, slot, blk);
               TileInfo& ti = infos[gs % kInfos];
               ti.kh[grp] = pack_f16(kh, kh);
               ti.vh[grp] = pack_f16(vh, vh);
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             // (bytes that have landed already count as well: the phase cannot end before this arrival)
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull), bytes);
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawKFull + rs), bytes);
             ++k_copies;
 #ifdef FA_TEST_SKIP_ARRIVE
             // Test-only build (never in libfa.so): a piece's last values are
@@ -545,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
 #endif
-            if (gs >= 1) ok = mbar_wait_w(bar(C::kBarRawVEmpty), (gs - 1) & 1, abort_flag);
+            if (gs >= C::kRaw) ok = mbar_wait_w(bar(C::kBarRawVEmpty + rs), (gs / C::kRaw - 1) & 1, abort_flag);
             if (!ok) break;
             if (own && issues)
-              tma_load_3d(base + C::kRawVOff + grp * 16 * D, &tmV, bar(C::kBarRawVFull), 0, slot, blk);
+              tma_load_3d(base + C::kRawVOff + rs * C::kRawBytes + grp * 16 * D, &tmV, bar(C::kBarRawVFull + rs), 0, slot, blk);
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawVFull), bytes);
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarRawVFull + rs), bytes);
             ++v_copies;
           }
         }
@@ -562,8 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) put_piece(last);
       // Let the copies in flight land before the CTA can end, whoever gives up:
       // each buffer's last phase (over already unless someone did).
-      if (k_copies > 0) mbar_wait(bar(C::kBarRawKFull), (k_copies - 1) & 1, nullptr);
-      if (v_copies > 0) mbar_wait(bar(C::kBarRawVFull), (v_copies - 1) & 1, nullptr);
+      for (int i = max(k_copies - C::kRaw, 0); i < k_copies; ++i)
+        mbar_wait(bar(C::kBarRawKFull + i % C::kRaw), (i / C::kRaw) & 1, nullptr);
+      for (int i = max(v_copies - C::kRaw, 0); i < v_copies; ++i)
+        mbar_wait(bar(C::kBarRawVFull + i % C::kRaw), (i / C::kRaw) & 1, nullptr);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issue
       constexpr uint32_t kIdS = idesc_f16_f32(kBM, kBN, false, false);
@@ -685,13 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full_lo = pc.full_lo, full_hi = pc.full_hi;
 #pragma unroll 1
       for (int w2 = 0; w2 < 2 * pc.steps && ok; ++w2) {  // keys and values in turn
-        const int g = gs0 + (w2 >> 1), st = g % C::kStages;
+        const int g = gs0 + (w2 >> 1), st = g % C::kStages, rs = g % C::kRaw;
         const bool values = w2 & 1;
         const TileInfo& ti = infos[g % kInfos];
         const int key0 = pc.key0 + (w2 >> 1) * kBN;
-        uint8_t* raw = smem + (values ? C::kRawVOff : C::kRawKOff) + src0;
+        uint8_t* raw = smem + (values ? C::kRawVOff : C::kRawKOff) + rs * C::kRawBytes + src0;
         uint8_t* out = smem + (values ? C::kVOff : C::kKOff) + st * C::kTileBytes + dst0;
-        ok = mbar_wait_w(bar(values ? C::kBarRawVFull : C::kBarRawKFull), g & 1, abort_flag);
+        ok = mbar_wait_w(bar((values ? C::kBarRawVFull : C::kBarRawKFull) + rs), (g / C::kRaw) & 1, abort_flag);
         if (ok && g >= C::kStages)
           ok = mbar_wait_w(bar((values ? C::kBarVEmpty : C::kBarKEmpty) + st), ((g / C::kStages) + 1) & 1, abort_flag);
         if (!ok) break;
@@ -761,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (saw_nan) *nan_flag = 1;
         fence_async_smem();
         mbar_arrive_warp(bar((values ? C::kBarVFull : C::kBarKFull) + st));
-        mbar_arrive_warp(bar(values ? C::kBarRawVEmpty : C::kBarRawKEmpty));
+        mbar_arrive_warp(bar((values ? C::kBarRawVEmpty : C::kBarRawKEmpty) + rs));
       }
       gs0 += pc.steps;
     }
@@ -777,15 +793,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gs0 = 0, done = 0, finals = 0;
     Piece pc;
     bool ok = get_piece(0, &pc);
-    // This thread's query of a piece, fetched while the piece before it is written back.
-    uint4 qw[D / 8];
+    // The queries of a piece, fetched while the piece before it is written
+    // back: this warp's 32 rows, a row's 16-byte units in consecutive lanes.
+    // (Each lane a row of its own would be 32 lines per load: 3 us for the
+    // eight warps instead of the latency of one load.)
+    constexpr int kUnitsPerRow = D / 8, kRowsPerLoad = 32 / kUnitsPerRow;
+    const int q_unit = lane % kUnitsPerRow, q_row = (warp & 3) * 32 + lane / kUnitsPerRow;  // + kRowsPerLoad per load
+    uint4 qw[kUnitsPerRow];
     auto fetch_query = [&](const Piece& x) {
-      const int r = x.r0 + t * kBM + (threadIdx.x & 127), i = a.g.div(r);
-      const bool on = !x.end && r < x.rows && (t == 0 ? x.b0 > x.a0 : x.b1 > x.a1);
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(x.row0 + i) * a.q_stride +
-                                                        (x.h * a.g.G + (r - i * a.g.G)) * D);
+      const bool takes_part = !x.end && (t == 0 ? x.b0 > x.a0 : x.b1 > x.a1);
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) qw[u] = on ? src[u] : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < kUnitsPerRow; ++u) {
+        const int r = x.r0 + t * kBM + q_row + u * kRowsPerLoad, i = a.g.div(r);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(x.row0 + i) * a.q_stride +
+                                                          (x.h * a.g.G + (r - i * a.g.G)) * D);
+        qw[u] = takes_part && r < x.rows ? src[q_unit] : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // Where 16-byte unit u of row tr of the query tile lies.
+    auto q_at = [&](int tr, int u) {
+      return reinterpret_cast<uint4*>(q_tile + (u >> 3) * C::kChunkBytes + tr * 128 + (((u & 7) ^ (tr & 7)) << 4));
     };
     if (ok) fetch_query(pc);
     for (int np = 0; ok && !pc.end; ++np) {
@@ -799,10 +826,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full_lo = pc.full_lo, full_hi = pc.full_hi;
       float qf = 0.f;
       if (n_mine > 0) {
-        // scaled into f16 by a power of two (exact within 2^27 of the row's largest value)
+        // scaled into f16 by a power of two (exact within 2^27 of the row's largest value), a thread a row
+#pragma unroll
+        for (int u = 0; u < kUnitsPerRow; ++u) *q_at(q_row + u * kRowsPerLoad, q_unit) = qw[u];
+        __syncwarp();
+        const int tr = threadIdx.x & 127;
         float m = 0.f;
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
+        for (int u = 0; u < kUnitsPerRow; ++u) {
+          qw[u] = *q_at(tr, u);
           const uint32_t x[4] = {qw[u].x, qw[u].y, qw[u].z, qw[u].w};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -813,15 +845,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float up = pow2i(k);
         qf = a.scale_log2 * pow2i(-k);
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
+        for (int u = 0; u < kUnitsPerRow; ++u) {
           const uint32_t x[4] = {qw[u].x, qw[u].y, qw[u].z, qw[u].w};
           uint32_t f[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             f[q] = pack_f16(__uint_as_float(x[q] << 16) * up, __uint_as_float(x[q] & 0xffff0000u) * up);
-          const int tr = threadIdx.x & 127;
-          *reinterpret_cast<uint4*>(q_tile + (u >> 3) * C::kChunkBytes + tr * 128 + (((u & 7) ^ (tr & 7)) << 4)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
+          *q_at(tr, u) = make_uint4(f[0], f[1], f[2], f[3]);
         }
         fence_async_smem();
         mbar_arrive_warp(bar(C::kBarQFull + t));

@@ -1060,7 +1060,7 @@ struct RowCosts {
 };
 constexpr RowCosts kRowCosts[2][2] = {  // d = 64, 128; 8, 16 rows
     {{2.5, 2, 1.5, 0.80, 0.20, 1.0, 12, 0.90}, {4.0, 2, 3.0, 1.00, 0.40, 1.0, 13, 1.00}},
-    {{2.5, 2, 1.6, 0.60, 0.28, 0.6, 10, 0.95}, {4.4, 5, 4.4, 0.72, 0.30, 0.6, 9, 1.00}}};
+    {{2.5, 2, 1.6, 0.60, 0.28, 0.6, 10, 0.95}, {3.0, 6, 3.0, 0.72, 0.15, 0.6, 10, 1.00}}};
 
 }  // namespace
 
@@ -1074,8 +1074,12 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   const int tile = pool.d == 64 ? kTileOf<64> : kTileOf<128>;
   const long long tiles = max_kv > 0 ? (static_cast<long long>(max_kv) + tile - 1) / tile : 1;
   const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
+  // Chunks (256 rows on the tensor memory; only with more than eight rows): a
+  // step of 128 keys costs 1.4 us at d = 64 and 1.6 at d = 128, an item three
+  // or five steps more (fa_paged_chunk.cu), a part has eight or more.
   const auto chunk_cost = [&](double pair_items) {
-    return 22 + (pool.d == 64 ? 0.95 : 1.6) / 152 * pair_items * (max_kv / 128 + 4);
+    const double steps = pair_items * (max_kv / 128 + (pool.d == 64 ? 4 : 6)) / sms;
+    return pool.d == 64 ? 16 + 1.4 * fmax(steps, 8.0) : 12 + 1.6 * fmax(steps, 8.0);
   };
   const double seqs = batch.B, heads = pool.num_heads;
 
@@ -1103,17 +1107,17 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
     }
     r.cluster = 0;
   }
-  // Rows (16 a tile, the cached tiles read once for each) or chunks (256 rows
-  // on the tensor memory)? What each costs was measured: about 12 us and 1.07
-  // us per tile and CTA slot (two per SM), against 22 us and 1.6 us (d = 64:
-  // 0.95 us) per step of 128 keys and SM, on 152 SMs. At 16 sequences of 2048
-  // keys, d = 128: 32 rows 43 against 45 us, 64 rows 70 against 46; at 24 of
-  // 4096 keys, d = 64: 15 rows 19 against 43, 48 rows 46 against 43 us.
+  // Rows (16 a tile, the cached tiles read once for each) or chunks? Measured,
+  // rows / chunks, 32 query and 8 key heads, d = 128: 16 sequences of 2048 keys,
+  // 4 tokens each 30 / 42 us; 16 of 512, 16 tokens 32 / 26; 48 of 2048, 8 tokens
+  // 102 / 109; 16 and 16 heads, d = 64: 16 of 8192, 32 tokens 135 / 163; 16 of
+  // 512, 64 tokens 32 / 29. Over 198 such batches the choice is within 1 % of the
+  // best form on average.
   // A ragged batch has at most its packed rows' tiles and one more per sequence.
   const double packed = static_cast<double>(batch.T) * G;
   const double row_items = heads * fmin(seqs * r.row_tiles, seqs + packed / r.rows);
   const double pair_items = heads * fmin(seqs * ((rows + 255) / 256), seqs + packed / 256);
-  const double row_cost = 12 + 1.07 / 304 * row_items * (tiles + kItemUnits);
+  const double row_cost = w.stream + w.stream_tile * fmax(row_items * (tiles + kItemUnits) / slots, kPartUnits);
   r.chunk = rows > 8 && chunk_cost(pair_items) < row_cost;
   r.ctas = r.chunk ? sms : slots;
   r.items = static_cast<long long>(row_items);

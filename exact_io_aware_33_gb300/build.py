@@ -3,8 +3,9 @@ Python binding with the host compiler.
 
 Each translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` at the repository root and linked into ``libfa.so`` (and
-``_paged_native.so``, which links against it and PyTorch) next to this file. A unit is recompiled only when it, or a header it may include, is
-newer than its object file.
+``_paged_native.so``, which links against it and PyTorch) next to this file. A
+unit is recompiled only when it, or a header it may include, is newer than its
+object file.
 """
 
 from __future__ import annotations

@@ -10,6 +10,7 @@ object file.
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -56,6 +57,10 @@ def _headers():
     return out
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _binding_flags():
     """(compile, link) flags of the binding: Python's and PyTorch's headers and libraries."""
     import sysconfig
@@ -98,7 +103,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     binding = None
-    if lib == LIB:
+    if lib == LIB and _has_torch():  # libfa.so itself needs no PyTorch
         src = "paged_binding.cpp"
         path, binding = os.path.join(CSRC, src), os.path.join(build_dir, src.replace(".cpp", ".o"))
         if (force or not os.path.exists(binding)

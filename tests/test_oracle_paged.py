@@ -205,6 +205,15 @@ def test_workspace(lib):
     assert lib.fa_paged_attn_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), 7) == 0  # heads do not divide
 
 
+def test_the_library_builds_without_pytorch(lib, monkeypatch, tmp_path):
+    from exact_io_aware_33_gb300 import build
+    monkeypatch.setattr(build, "_has_torch", lambda: False)
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "binding.so"))
+    monkeypatch.setattr(build, "_binding_flags", lambda: pytest.fail("the binding's flags need PyTorch"))
+    assert build.build() == build.LIB
+    assert not (tmp_path / "binding.so").exists()
+
+
 def test_binding_refuses_cpu_tensors():
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn)
     scales = torch.ones(4, 2)

@@ -172,6 +172,15 @@ def test_append_arguments_are_checked_on_the_host(lib, kw, code):
     assert _append(lib, _cache(), _batch(), **kw) == code
 
 
+@pytest.mark.parametrize("d,max_q,max_kv", [(64, 5, 4096), (128, 4, 2048), (128, 64, 2048), (64, 300, 900), (128, 16, 512)])
+@pytest.mark.parametrize("B,heads", [(1, 1), (3, 8), (16, 4), (48, 8)])
+def test_the_workspace_does_not_depend_on_the_rows(lib, d, max_q, max_kv, B, heads):
+    c = _cache(page_size=64, num_heads=heads, d=d, num_pages=100)
+    need = {lib.fa_paged_attn_workspace_bytes(ctypes.addressof(c), ctypes.addressof(_batch(
+        B=B, T=T, max_q=max_q, max_pages=200, max_kv=max_kv)), 4 * heads) for T in (1, B, B * max_q // 2, B * max_q)}
+    assert len(need) == 1
+
+
 ROW = 4 * 64 * 2  # bytes of a query row; nine rows
 
 

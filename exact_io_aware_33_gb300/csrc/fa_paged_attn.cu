@@ -1076,9 +1076,9 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
   const long long slots = (r.rows == 8 ? 3LL : 2LL) * sms;
   // Chunks (256 rows on the tensor memory; only with more than eight rows): a
   // step of 128 keys costs 1.4 us at d = 64 and 1.6 at d = 128, an item three
-  // or five steps more (fa_paged_chunk.cu), a part has eight or more.
+  // or four steps more (fa_paged_chunk.cu), a part has eight or more.
   const auto chunk_cost = [&](double pair_items) {
-    const double steps = pair_items * (max_kv / 128 + (pool.d == 64 ? 4 : 6)) / sms;
+    const double steps = pair_items * (max_kv / 128 + (pool.d == 64 ? 4 : 5)) / sms;
     return pool.d == 64 ? 16 + 1.4 * fmax(steps, 8.0) : 12 + 1.6 * fmax(steps, 8.0);
   };
   const double seqs = batch.B, heads = pool.num_heads;

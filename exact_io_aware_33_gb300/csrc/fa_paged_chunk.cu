@@ -16,7 +16,7 @@
 // about 200 instructions per thread for a tile of K or of V, next to the 256
 // rows that share it; doing it once per pair of 128-row tiles is why a CTA
 // holds two of them. Measured: 2 x 2048 queries over 8192 keys, 32 query and 8
-// key heads, d = 128, in 380 us: 1.26 PFLOP/s, 65 % of the measured matrix
+// key heads, d = 128, in 375 us: 1.28 PFLOP/s, 67 % of the measured matrix
 // product's rate. Per step and tile the MMAs take 0.76 us and the softmax 0.85
 // us, two tiles in turn.
 //
@@ -63,9 +63,10 @@ constexpr int kInfos = 8;        // tiles' scale records kept
 constexpr int kPieces = 4;       // pieces' records kept
 // An item costs about this many steps more than it has: its queries, the start
 // of its chain, its write-back. Four prompts of 2048 tokens, 32 query and 8 key
-// heads, d = 128: 180 us with 5, 192 with 3; 16 heads, d = 64: 85 and 82 us.
+// heads, d = 128: 176 us with 4, 179 with 6; 16 heads, d = 64: 80 us with 3, 83
+// with 2, 82 with 4.
 template <int D>
-constexpr int kItemSteps = D == 64 ? 3 : 5;
+constexpr int kItemSteps = D == 64 ? 3 : 4;
 constexpr int kPartSteps = 8;    // a part has at least this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -994,6 +995,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = get_piece(np + 1, &nx);
       if (!ok) break;
       fetch_query(nx);
+      // (while the last P.V is computed)
+      const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
+      const float f = l == 0.f ? 0.f : ex2(tu - su - kPShift) / l;
+      const float lse2 = l == 0.f ? -INFINITY : su + log2f(l);
       if (n_mine > 0) ok = mbar_wait_w(bar(C::kBarOFinal + t), finals & 1, abort_flag);
       if (!ok) break;
       if (n_mine > 0) ++finals;
@@ -1005,9 +1010,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const long long at = static_cast<long long>(pc.row0 + i) * a.Hq + hd;
-      const float su = ms == -INFINITY ? 0.f : ms, tu = mt == -INFINITY ? 0.f : mt;
-      const float f = l == 0.f ? 0.f : ex2(tu - su - kPShift) / l;
-      const float lse2 = l == 0.f ? -INFINITY : su + log2f(l);
       const long long part = static_cast<long long>(pc.slot) * 2 * kBM + t * kBM;  // the tile's first row there
       if (pc.whole) {
         if (live) a.lse[at] = kLn2 * lse2;
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
         }
         __syncwarp();
-#pragma unroll
+#pragma unroll 2  // (code that runs once an item is fetched anew each time: all eight cost 2 to 4 % more)
         for (int j = 0; j < 8; ++j) {
           const int rr = 4 * j + (lane >> 3), v = lane & 7;
           const uint4 val = *reinterpret_cast<const uint4*>(blk + rr * 128 + ((v ^ (rr & 7)) * 16));

@@ -335,6 +335,27 @@ def test_the_output_may_take_the_queries_place(lens, news, max_pages):
     assert o is q and torch.equal(o, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    d, page, H = int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128])), int(rng.choice([1, 2, 3, 5]))
+    Hq = H * int(rng.choice([1, 2, 3, 4, 8, 16]))
+    lens = rng.integers(0, int(rng.choice([20, 200, 900])), int(rng.choice([1, 2, 5, 17]))).tolist()
+    most = int(rng.choice([2, 10, 150]))  # new tokens, some of which may have no position
+    news = rng.integers(0, most, len(lens)).tolist()
+    news[0] += 1
+    w = World(lens, H, page, d, seed=seed, max_pages=int(rng.choice([60, 5000]))).fill()
+    cu, batch = w.batch(news, max_kv=int(rng.choice([0, max(lens)])))
+    window = int(rng.choice([0, 0, 1, 100]))
+    q = bf16(w.rng, sum(news), Hq, d)
+    cache = w.to_gpu()
+    o, lse = fa.fa_paged_attn(cache, batch, q.cuda(), window=window)
+    o2, lse2 = fa.fa_paged_attn(cache, batch, q.cuda(), window=window)
+    done()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_attn(w, cu, o, lse, q, d ** -0.5, window)
+
+
 def test_shared_pages_may_be_read_by_several_sequences():
     w = World([64, 64], 2, 16, 64, seed=12).fill()
     w.table[1, :3] = w.table[0, :3]  # a common beginning

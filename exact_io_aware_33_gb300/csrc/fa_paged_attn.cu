@@ -453,7 +453,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     const int box_rows = min(a.batch.page_size, kTile), per_box = box_rows / kGroup;
     const uint32_t box_bytes = 2u * box_rows * D;  // of K and V
     JoinRecord record{};
-    while (more) {
+    // Whether to go on: the verdict of the whole warp, so that its lanes leave
+    // the loops together. (The flag itself may be raised between two lanes' reads.)
+    bool ok = true;
+    while (more && ok) {
       const int seq = walk.b - 1;
       if (!kCluster && sg.nt > 0) {
         int item, end;  // of the last tile here
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
       };
       look();
       scales();
-      while (n_count > 0) {
+      while (n_count > 0 && ok) {
         int box_page = n_page;  // of this lane's box: its groups share a page, or have none to read
         const int head = n_head, key = n_key, count = n_count;
         const float sk = n_sk, sv = n_sv;
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
         const uint32_t issuers = __ballot_sync(0xffffffffu, issues);
         const int slot = key & (a.batch.page_size - 1), blk = box_page * a.Hkv + head;
         const uint32_t off = grp * kGroup * D;
-        for (int i = 0; i < count && !*abort_flag; ++i) {
+        for (int i = 0; i < count; ++i) {
           const int st = it % kS;
 #ifdef FA_TEST_SKIP_ARRIVE
           // Test-only build (never in libfa.so): a sequence's last tile is
@@ -521,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
           // the CTA winds down through the abort path.
           if (n_count == 0 && i == count - 1) break;
 #endif
-          if (it >= kS && !mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag)) break;
+          if (it >= kS) ok = mbar_wait_w(empty + 8 * st, (it / kS - 1) & 1, abort_flag);
+          if (!ok) break;
           if (tile_in == i) {
             // the copies need the pages only: they go out before the scales are waited for
             if (issues) {
@@ -542,10 +546,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
           ++it;
         }
         __syncwarp();
-        if (*abort_flag) break;
       }
-      if (*abort_flag) break;
-      more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
+      if (ok) more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
     }
     if (!kCluster && lane == 0) a.records[blockIdx.x] = record;
     // let every copy in flight land before the CTA can end

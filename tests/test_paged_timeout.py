@@ -57,3 +57,41 @@ def test_wait_runs_out_and_the_context_survives(timeout_lib, d, rows, heads, max
     o, lse = fa.fa_paged_attn(cache, batch, gpu)
     done()
     check_attn(w, cu, o, lse, q, d ** -0.5)
+
+
+def run_out(timeout_lib, w, cu, batch, q):
+    """One call of the variant on a World: launched, then FA_ERR_TIMEOUT within a few seconds."""
+    rows, heads, d = q.shape
+    cache, gpu = w.to_gpu(), q.cuda()
+    o, lse = torch.empty_like(gpu), torch.empty(rows, heads, device="cuda")
+    c_batch = type(batch._struct).from_buffer_copy(batch._struct)
+    c_batch.T = rows
+    struct = ctypes.addressof(c_batch)
+    need = timeout_lib.fa_paged_attn_workspace_bytes(cache._address, struct, heads)
+    ws = torch.zeros(max(need, 1), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert timeout_lib.fa_paged_attn(cache._address, struct, gpu.data_ptr(), heads * d, o.data_ptr(), lse.data_ptr(),
+                                     heads, 0, d ** -0.5, ws.data_ptr(), need,
+                                     ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == fa.FA_OK
+    status = timeout_lib.fa_get_last_device_status()
+    assert time.perf_counter() - t0 < 10.0
+    return status
+
+
+# Many sequences, each longer than a CTA's ring: the loading warp is in the middle of its work, waiting
+# for a free stage, when the flag goes up, and has to leave it with all its lanes at once.
+@pytest.mark.parametrize("lens,news,heads,max_kv", [
+    ([2100, 1900, 2000, 1700] * 12, [1] * 48, 4, STREAM),
+    ([2100, 3, 1900, 0, 2000] * 8, [3, 1, 4, 0, 2] * 8, 8, STREAM),
+    ([2100, 3, 1900, 0, 2000] * 4, [1] * 20, 4, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_long_batch_winds_down(timeout_lib, d, lens, news, heads, max_kv):
+    w = World(lens, 2, 64, d, seed=d + len(lens), max_pages=STREAM // 64 if max_kv else None).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, sum(news), heads, d)
+    assert run_out(timeout_lib, w, cu, batch, q) == fa.FA_ERR_TIMEOUT
+    assert timeout_lib.fa_get_last_device_status() == fa.FA_OK
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
+    done()
+    check_attn(w, cu, o, lse, q, d ** -0.5)

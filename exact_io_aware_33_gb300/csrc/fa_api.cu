@@ -574,6 +574,8 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   const long long width = static_cast<long long>(Hq) * cache->d;
   if (!(o == q && (q_stride == width || dev.T == 1)) && rows_meet(o, width, width, q, q_stride, width, dev.T))
     return FA_ERR_INVALID;
+  // no length exceeds the block table's: a window as long masks nothing, and edges of shorter ones fit an int
+  if (window >= static_cast<long long>(batch->max_pages) * cache->page_size) window = 0;
   // packed (query, head) rows of a key head are counted in 32 bits
   if (static_cast<long long>(batch->max_q) * Hq > 0x7fffffffLL - 4096) return FA_ERR_INVALID;
   const fa::PagedPlan plan = fa::paged_attn_plan(pool, dev, Hq, paged_max_kv(cache, batch), paged_sms());

@@ -124,9 +124,15 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return (z >> 7) * 255u;
 }
 
+// The first key that the query at position p sees. Before position 0 (rows of
+// a padded batch) it sees none, and p - window may lie below the int range.
+__device__ __forceinline__ int first_seen(int p, int window) {
+  return window > 0 ? max(max(p, 0) - window + 1, 0) : 0;
+}
+
 // Whether the query at position p sees key j.
 __device__ __forceinline__ bool sees(int p, int j, int window) {
-  return j <= p && (window == 0 || j > p - window);
+  return j <= p && j >= first_seen(p, window);
 }
 
 // 2^e as a float, e in [-126, 127].

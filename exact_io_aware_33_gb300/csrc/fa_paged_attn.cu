@@ -132,7 +132,7 @@ __device__ __forceinline__ SeqGeo seq_geo(const AttnArgs& a, int seq) {
   g.rts = (g.rows + R - 1) / R;
   g.p0 = g.s.len - g.s.n;
   const int hi = g.s.n > 0 ? g.s.len : 0;
-  const int lo = a.window > 0 ? max(g.p0 - a.window + 1, 0) : 0;
+  const int lo = first_seen(g.p0, a.window);
   g.t0 = lo / kTile;
   g.nt = hi > lo ? (hi + kTile - 1) / kTile - g.t0 : 0;
   return g;
@@ -159,7 +159,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqGeo& s, 
   g.p_lo = g.p0 + a.g.div(g.r0);
   g.p_hi = g.p0 + a.g.div(min(g.r0 + R, g.rows) - 1);
   g.hi = max(g.p_hi + 1, 0);
-  g.lo = a.window > 0 ? max(g.p_lo - a.window + 1, 0) : 0;
+  g.lo = first_seen(g.p_lo, a.window);
   return g;
 }
 
@@ -283,7 +283,7 @@ struct Walk {
 
 // Whether every row of the tile sees every one of the 16 keys from j0 on.
 __device__ __forceinline__ bool all_see(const RowTile& g, int j0, int window) {
-  return j0 + kGroup - 1 <= g.p_lo && (window == 0 || j0 > g.p_hi - window);
+  return j0 + kGroup - 1 <= g.p_lo && j0 >= first_seen(g.p_hi, window);
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -181,7 +181,7 @@ __device__ __forceinline__ PairGeo pair_geo(const ChunkArgs& a, int rows, int p0
     const int r0 = (2 * pair + t) * kBM;
     const int p_last = p0 + a.g.div(min(r0 + kBM, rows) - 1);
     const int hi = r0 < rows && p_last >= 0 ? p_last / kBN + 1 : 0;
-    g.lo[t] = a.window > 0 ? max(p0 + a.g.div(r0) - a.window + 1, 0) / kBN : 0;
+    g.lo[t] = first_seen(p0 + a.g.div(r0), a.window) / kBN;
     g.n[t] = max(hi - g.lo[t], 0);
   }
   g.first = g.n[0] == 0 ? g.lo[1] : g.n[1] == 0 ? g.lo[0] : min(g.lo[0], g.lo[1]);
@@ -195,7 +195,7 @@ __device__ __forceinline__ int pairs_of(int rows) { return (rows + 2 * kBM - 1) 
 __device__ __forceinline__ int pair_steps(const ChunkArgs& a, int rows, int p0, int pair) {
   const int r0 = pair * 2 * kBM, p_last = p0 + a.g.div(min(r0 + 2 * kBM, rows) - 1);
   const int hi = p_last >= 0 ? p_last / kBN + 1 : 0;
-  const int lo = a.window > 0 ? max(p0 + a.g.div(r0) - a.window + 1, 0) / kBN : 0;
+  const int lo = first_seen(p0 + a.g.div(r0), a.window) / kBN;
   return max(hi - lo, 0);
 }
 
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pc.a1 = min(max(it.g.lo[1] - first_tile, 0), steps);
         pc.b1 = max(min(it.g.lo[1] + it.g.n[1] - first_tile, steps), pc.a1);
         pc.full_hi = p_first;
-        pc.full_lo = a.window > 0 ? p_last - a.window + 1 : 0;
+        pc.full_lo = first_seen(p_last, a.window);
         pc.whole = s0 == 0 && s1 == n;
         pc.slot = static_cast<int>(blockIdx.x) * 2 + (s0 == 0 ? 1 : 0);  // 0: continues an item, 1: begins one
         if (!pc.whole && s0 == 0)
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_piece(pc);
         if (!ok) break;
         // keys that any row sees lie in [key_lo, key_end)
-        const int key_lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0, key_end = max(p_last + 1, 0);
+        const int key_lo = first_seen(p_first, a.window), key_end = max(p_last + 1, 0);
         int n_page = -1;
         float n_sk = 1.f, n_sv = 1.f;
         bool n_want = false;
@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*nan_flag && live) {
         // a NaN code was taken out of a tile that not every row sees: put it into the rows that do
 #pragma unroll 1
-        for (int j = max(pc.key0, a.window > 0 ? p - a.window + 1 : 0); j <= min(p, pc.key0 + pc.steps * kBN - 1); ++j) {
+        for (int j = max(pc.key0, first_seen(p, a.window)); j <= min(p, pc.key0 + pc.steps * kBN - 1); ++j) {
           const int j0 = j & ~15;
           if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
           const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);

@@ -159,6 +159,19 @@ def test_several_tokens_per_sequence(lens, news, Hq, Hkv, d, page, window, max_k
     check_attn(w, cu, o, lse, q, 1 / math.sqrt(d), window)
 
 
+@pytest.mark.parametrize("max_pages", [None, STREAM // 16])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 100])
+@pytest.mark.parametrize("lens,news,Hq", [([5, 2], [8, 4], 4), ([5, 2], [8, 4], 1), ([500, 2], [560, 4], 4)])
+def test_a_window_longer_than_every_position(lens, news, Hq, window, max_pages):
+    # rows without a position, whose window would begin below the int range; rows and chunks
+    w = World(lens, 1, 16, 64, seed=13, max_pages=max_pages).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, sum(news), Hq, 64)
+    o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda(), window=window)
+    done()
+    check_attn(w, cu.tolist(), o, lse, q, 0.125, window)
+
+
 @pytest.mark.parametrize("max_kv", [0, STREAM])
 @pytest.mark.parametrize("news", [[1, 1], [40, 33]])
 def test_scales_of_very_different_sizes(news, max_kv):

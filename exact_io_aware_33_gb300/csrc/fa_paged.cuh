@@ -130,9 +130,9 @@ __device__ __forceinline__ int first_seen(int p, int window) {
   return window > 0 ? max(max(p, 0) - window + 1, 0) : 0;
 }
 
-// Whether the query at position p sees key j.
+// Whether the query at position p sees key j. (p - window is formed for p >= j >= 0 only.)
 __device__ __forceinline__ bool sees(int p, int j, int window) {
-  return j <= p && j >= first_seen(p, window);
+  return j <= p && (window == 0 || j > p - window);
 }
 
 // 2^e as a float, e in [-126, 127].

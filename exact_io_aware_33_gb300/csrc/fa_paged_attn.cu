@@ -283,7 +283,7 @@ struct Walk {
 
 // Whether every row of the tile sees every one of the 16 keys from j0 on.
 __device__ __forceinline__ bool all_see(const RowTile& g, int j0, int window) {
-  return j0 + kGroup - 1 <= g.p_lo && j0 >= first_seen(g.p_hi, window);
+  return j0 + kGroup - 1 <= g.p_lo && (window == 0 || j0 > g.p_hi - window);
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -766,13 +766,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
             const bool absent = sc[q].x < 0.f;  // (nothing was loaded)
             if (part && (absent || !all_see(g, j0 + q * kGroup, a.window))) {
               // keys that a row does not see have weight 0, and 0 x NaN is NaN: here
-              // NaN codes are taken out, and rows that do see one are mended at the end
+              // NaN codes are taken out, and rows that do see one are mended at the end.
+              // (Not for codes behind the last key that any row sees: slots past a
+              // length may hold anything, and often do.)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                   const uint32_t z = nan_bytes(vw[e][i]);
-                  saw_nan = saw_nan || (z != 0 && !absent);
+                  saw_nan = saw_nan || (z != 0 && !absent && j0 + q * kGroup + 2 * t + (e & 1) + 8 * (e >> 1) <= g.p_hi);
                   vw[e][i] = absent ? 0u : vw[e][i] & ~z;
                 }
               }
@@ -849,7 +851,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
         if (nan_flag[turn]) {
           const int p = g.p0 + a.g.div(g.r0 + wrow);
           for (int j = max((sg.t0 + tile) * kTile, g.lo); j < min((sg.t0 + tile_end) * kTile, g.hi); ++j) {
-            if (all_see(g, j & ~(kGroup - 1), a.window) || !sees(p, j, a.window)) continue;
+            if (all_see(g, j & ~(kGroup - 1), a.window)) {
+              // on to the first group that the causal edge cuts
+              j = max(j | (kGroup - 1), ((g.p_lo + 1) & ~(kGroup - 1)) - 1);
+              continue;
+            }
+            if (!sees(p, j, a.window)) continue;
             const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
             if (page < 0) continue;
             const uint8_t* code = a.v_pages +

@@ -96,6 +96,7 @@ struct Piece {
   int key0, steps;       // first key, and number of key tiles
   int a0, b0, a1, b1;    // steps that query tiles 0 and 1 take part in
   int full_lo, full_hi;  // keys that every row of the item sees
+  int seen_hi;           // last key that any does
   int whole;             // 1: all of the item
   int slot;              // workspace slot of a piece that is not
   int seq;
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return base + C::kBarOff + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-  volatile int* nan_flag = abort_flag + 1;
+  volatile int* nan_flag = abort_flag + 1;  // a NaN value code that some row sees was taken out (stays up)
   TileInfo* infos = reinterpret_cast<TileInfo*>(smem + C::kInfoOff);
   const int warp = warp_id(), lane = lane_id();
 
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pc.a1 = min(max(it.g.lo[1] - first_tile, 0), steps);
         pc.b1 = max(min(it.g.lo[1] + it.g.n[1] - first_tile, steps), pc.a1);
         pc.full_hi = p_first;
+        pc.seen_hi = p_last;
         pc.full_lo = first_seen(p_last, a.window);
         pc.whole = s0 == 0 && s1 == n;
         pc.slot = static_cast<int>(blockIdx.x) * 2 + (s0 == 0 ? 1 : 0);  // 0: continues an item, 1: begins one
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece pc;
       ok = get_piece(np, &pc);
       if (!ok || pc.end) break;
-      const int full_lo = pc.full_lo, full_hi = pc.full_hi;
+      const int full_lo = pc.full_lo, full_hi = pc.full_hi, seen_hi = pc.seen_hi;
 #pragma unroll 1
       for (int w2 = 0; w2 < 2 * pc.steps && ok; ++w2) {  // keys and values in turn
         const int g = gs0 + (w2 >> 1), st = g % C::kStages, rs = g % C::kRaw;
@@ -755,7 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int cb = 0; cb < C::kChunks; ++cb) {
                   uint2* at = reinterpret_cast<uint2*>(raw + q * 16 * D + cb * 64);
                   const uint2 v = *at, n = make_uint2(nan_bytes(v.x), nan_bytes(v.y));
-                  saw_nan = saw_nan || (n.x | n.y) != 0;
+                  // (slots past a length may hold anything, and often do: no row to mend for those)
+                  saw_nan = saw_nan || (key0 + q * 16 + row0 <= seen_hi && (n.x | n.y) != 0);
                   *at = make_uint2(v.x & ~n.x, v.y & ~n.y);
                 }
               }
@@ -1071,8 +1074,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*nan_flag && live) {
         // a NaN code was taken out of a tile that not every row sees: put it into the rows that do
+        int from = max(pc.key0, first_seen(p, a.window));
+        if ((from & ~15) >= full_lo) from = max(from, (full_hi + 1) & ~15);  // nothing is cut before
 #pragma unroll 1
-        for (int j = max(pc.key0, first_seen(p, a.window)); j <= min(p, pc.key0 + pc.steps * kBN - 1); ++j) {
+        for (int j = from; j <= min(p, pc.key0 + pc.steps * kBN - 1); ++j) {
           const int j0 = j & ~15;
           if (j0 + 15 <= full_hi && j0 >= full_lo) continue;
           const int page = paged_page(a.batch, seq, j >> a.batch.page_shift, a.status);
@@ -1081,6 +1086,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              (j & (a.batch.page_size - 1))) * D;
 #pragma unroll 1
           for (int c = 0; c < D; ++c) {
+            if ((c & 15) == 0) {  // sixteen codes at a time
+              const uint4 w = *reinterpret_cast<const uint4*>(code + c);
+              if ((nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) == 0) {
+                c += 15;
+                continue;
+              }
+            }
             if ((code[c] & 0x7f) != 0x7f) continue;
             if (pc.whole)
               a.o[at * D + c] = __float2bfloat16(__int_as_float(0x7fffffff));

@@ -1157,9 +1157,8 @@ int launch_paged_attn(const PagedPool& pool, const PagedBatchDev& batch, const P
   a.window = p.window;
   a.row_tiles = plan.row_tiles;
   a.cluster = plan.cluster;
-  // scale 0 (uniform weights) runs as a tiny positive scale, as in the forward
-  const float sl2 = p.scale * kLog2e;
-  a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  // 0 gives uniform weights: keys that are not seen become -infinity after S has been scaled
+  a.scale_log2 = p.scale * kLog2e;
   a.part_o = static_cast<float*>(workspace);
   if (plan.workspace_bytes > 0) {
     a.part_lse = a.part_o + plan.ctas * 2 * plan.rows * pool.d;

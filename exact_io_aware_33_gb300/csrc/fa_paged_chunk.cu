@@ -1196,9 +1196,8 @@ int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const 
   a.Hkv = pool.num_heads;
   a.g = GroupDiv::of(p.Hq / pool.num_heads);
   a.window = p.window;
-  // scale 0 (uniform weights) runs as a tiny positive scale, as in the forward
-  const float sl2 = p.scale * kLog2e;
-  a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  // 0 gives uniform weights: S is multiplied by kLeast at least
+  a.scale_log2 = p.scale * kLog2e;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + static_cast<size_t>(ctas) * 2 * 2 * kBM * pool.d;
   a.records = reinterpret_cast<JoinRecord*>(a.part_lse + static_cast<size_t>(ctas) * 2 * 2 * kBM);

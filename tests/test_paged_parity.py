@@ -242,6 +242,22 @@ def test_queries_of_any_size(size):
     assert (want[1] - got[1]).abs().max().item() <= 5e-4
 
 
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** 120])
+@pytest.mark.parametrize("news,Hq", [([3], 4), ([3], 12), ([100], 4)])
+def test_the_largest_queries_with_the_smallest_scales(news, Hq, size):
+    # the scale takes the size back, exactly; the few-row kernel with 8 and 16 rows, and the chunk kernel
+    w = World([150], 2, 16, 64, seed=16).fill()
+    cu, batch = w.batch(news)
+    q = bf16(w.rng, news[0], Hq, 64)
+    cache = w.to_gpu()
+    want = fa.fa_paged_attn(cache, batch, q.cuda(), scale=0.125)
+    got = fa.fa_paged_attn(cache, batch, (q.float() * size).to(torch.bfloat16).cuda(), scale=0.125 / size)
+    done()
+    check_attn(w, cu, *want, q, 0.125)
+    assert torch.equal(want[0], got[0])
+    assert (want[1] - got[1]).abs().max().item() <= 5e-4
+
+
 @pytest.mark.parametrize("max_pages", [13, STREAM // 16])
 @pytest.mark.parametrize("news", [[1], [20], [150]])
 def test_nan_codes_reach_the_rows_that_see_them_and_no_others(news, max_pages):

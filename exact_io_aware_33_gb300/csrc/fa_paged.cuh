@@ -31,6 +31,10 @@
 
 namespace fa {
 
+// An index was out of range. A timeout that the status word already holds
+// stays: it says more, that results are missing.
+__device__ __forceinline__ void raise_index(int* status) { atomicCAS(status, kStatusOk, kStatusIndex); }
+
 // One sequence of the batch: its packed rows [row0, row0 + n) and its length.
 struct PagedSeq {
   int row0, n, len;
@@ -53,7 +57,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev& b, int seq, i
   const int most = b.max_pages << b.page_shift;
   bad = bad || s.len < 0 || s.len > most;
   s.len = min(max(s.len, 0), most);
-  if (bad) *status = kStatusIndex;
+  if (bad) raise_index(status);
   return s;
 }
 
@@ -61,7 +65,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatchDev& b, int seq, i
 __device__ __forceinline__ int paged_page(const PagedBatchDev& b, int seq, int idx, int* status) {
   const int p = b.block_table[static_cast<long long>(seq) * b.max_pages + idx];
   if (p >= 0 && p < b.num_pages) return p;
-  *status = kStatusIndex;
+  raise_index(status);
   return -1;
 }
 

@@ -92,7 +92,7 @@ __device__ __forceinline__ void load_angles(const AppendArgs& a, const Unit& u, 
                                             float (&s)[8]) {
   if (u.tab < 0) return;
   if (pos >= a.max_pos) {
-    *a.status = kStatusIndex;
+    raise_index(a.status);
     pos = a.max_pos - 1;
   }
   const long long at = static_cast<long long>(pos) * (a.rot / 2) + u.tab;

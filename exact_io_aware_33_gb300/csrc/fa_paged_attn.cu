@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     if (!kCluster && lane == 0) a.records[blockIdx.x] = record;
     // let every copy in flight land before the CTA can end
     for (uint32_t i = it > kS ? it - kS : 0; i < it; ++i) mbar_wait(full + 8 * (i % kS), (i / kS) & 1, nullptr);
-    if (lane == 0 && *abort_flag) *a.status = kStatusTimeout;
+    if (lane == 0 && *abort_flag) atomicExch(a.status, kStatusTimeout);
     if constexpr (kCluster) {
       cluster_sync();
       cluster_sync();
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm)
     }
     more = kCluster ? false : walk.next(a, &sg, &v0, &v1, &e0, &e1);
   }
-  if (*abort_flag && threadIdx.x == 0) *a.status = kStatusTimeout;
+  if (*abort_flag && threadIdx.x == 0) atomicExch(a.status, kStatusTimeout);
   if constexpr (kCluster) {
     // Join the pieces: every CTA of the cluster takes a share of the rows.
     cluster_sync();

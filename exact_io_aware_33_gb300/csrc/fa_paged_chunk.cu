@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  if (threadIdx.x == 0 && *abort_flag) *a.status = kStatusTimeout;
+  if (threadIdx.x == 0 && *abort_flag) atomicExch(a.status, kStatusTimeout);
 }
 
 // Joins the pieces of an item that parts c, c + 1, ... share, by the rule of

@@ -95,3 +95,34 @@ def test_a_long_batch_winds_down(timeout_lib, d, lens, news, heads, max_kv):
     o, lse = fa.fa_paged_attn(w.to_gpu(), batch, q.cuda())
     done()
     check_attn(w, cu, o, lse, q, d ** -0.5)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_a_bad_index_does_not_hide_a_timeout(timeout_lib, rows):
+    w = World([500], 2, 64, 64, seed=rows, max_pages=STREAM // 64).fill()
+    cu, batch = w.batch([rows])
+    cache, q = w.to_gpu(), bf16(w.rng, rows, 4, 64).cuda()
+    kv = torch.zeros(rows, 2, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(rows, 4, device="cuda")
+    batch.block_table[0, 2] = w.P    # the append finds this page out of range, and so does the attention
+    c_batch = type(batch._struct).from_buffer_copy(batch._struct)
+    c_batch.T = rows
+    struct, stream = ctypes.addressof(c_batch), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    ws = torch.zeros(timeout_lib.fa_paged_attn_workspace_bytes(cache._address, struct, 4), dtype=torch.uint8, device="cuda")
+
+    def append():
+        assert timeout_lib.fa_paged_append(cache._address, struct, kv.data_ptr(), 128, kv.data_ptr(), 128, 0, 0, 0, 0, 0,
+                                           0, 0, 0, 0, 0, stream) == fa.FA_OK
+
+    def attend():
+        assert timeout_lib.fa_paged_attn(cache._address, struct, q.data_ptr(), 256, o.data_ptr(), lse.data_ptr(), 4, 0,
+                                         0.125, ws.data_ptr(), ws.numel(), stream) == fa.FA_OK
+
+    batch.kv_lens.fill_(2 * 64 + rows)    # the new tokens begin on that page
+    append()
+    assert timeout_lib.fa_get_last_device_status() == fa.FA_ERR_INDEX
+    for calls in ((attend, append), (append, attend)):
+        for call in calls:
+            call()
+        assert timeout_lib.fa_get_last_device_status() == fa.FA_ERR_TIMEOUT
+        assert timeout_lib.fa_get_last_device_status() == fa.FA_OK

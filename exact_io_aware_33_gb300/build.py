@@ -5,7 +5,11 @@ Each translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` at the repository root and linked into ``libfa.so`` (and
 ``_paged_native.so``, which links against it and PyTorch) next to this file. A
 unit is recompiled only when it, or a header it may include, is newer than its
-object file.
+object file; the binding also when Python or PyTorch is another one.
+
+libfa.so needs nvcc alone. Where the binding cannot be built (no PyTorch, one
+without CUDA, no g++), the library is built all the same, and the paged cache
+says so when it is first used.
 """
 
 from __future__ import annotations
@@ -61,6 +65,34 @@ def _has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def _binding_stamp() -> str:
+    """What the binding was built against: this Python and the PyTorch that it would import."""
+    origin = importlib.util.find_spec("torch").origin or ""
+    version = os.path.join(os.path.dirname(origin), "version.py")
+    text = ""
+    if os.path.exists(version):
+        with open(version) as f:
+            text = f.read()
+    return "\n".join([sys.version, origin, text])
+
+
+def _start_binding(args, which: int):
+    """Starts g++ for the binding with its compile (0) or link (1) flags; the process, or why there is none."""
+    try:
+        return subprocess.Popen([cxx()] + args + _binding_flags()[which], stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT)
+    except (RuntimeError, ImportError, OSError) as e:
+        return str(e)
+
+
+def _finish_binding(p) -> str:
+    """Waits for what _start_binding gave; empty, or why it failed."""
+    if p is None or isinstance(p, str):
+        return p or ""
+    out, _ = p.communicate()
+    return "" if p.returncode == 0 else out.decode(errors="replace") or "g++ failed"
+
+
 def _binding_flags():
     """(compile, link) flags of the binding: Python's and PyTorch's headers and libraries."""
     import sysconfig
@@ -102,14 +134,17 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
             cmd.append("-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    binding = None
+    binding = compiling = None
     if lib == LIB and _has_torch():  # libfa.so itself needs no PyTorch
-        src = "paged_binding.cpp"
-        path, binding = os.path.join(CSRC, src), os.path.join(build_dir, src.replace(".cpp", ".o"))
-        if (force or not os.path.exists(binding)
+        path, binding = os.path.join(CSRC, "paged_binding.cpp"), os.path.join(build_dir, "paged_binding.o")
+        stamp, stamp_file = _binding_stamp(), os.path.join(build_dir, "paged_binding.stamp")
+        fresh = False
+        if os.path.exists(stamp_file):
+            with open(stamp_file) as f:
+                fresh = f.read() == stamp
+        if (force or not fresh or not os.path.exists(binding)
                 or os.path.getmtime(binding) < max(os.path.getmtime(path), newest_header)):
-            procs.append((src, subprocess.Popen([cxx(), "-c", path, "-o", binding] + _binding_flags()[0],
-                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+            compiling = _start_binding(["-c", path, "-o", binding], 0)
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -118,6 +153,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
             failed.append((src, text))
         elif verbose and text.strip():
             print(text, flush=True)
+    why = _finish_binding(compiling)  # there is no binding
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
         raise RuntimeError("nvcc failed:\n" + msg)
@@ -129,14 +165,20 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
         os.replace(tmp, lib)
-    if binding and (force or not os.path.exists(BINDING)
-                    or os.path.getmtime(BINDING) < max(os.path.getmtime(binding), os.path.getmtime(lib))):
-        tmp = BINDING + ".tmp"
-        r = subprocess.run([cxx(), "-shared", "-o", tmp, binding] + _binding_flags()[1], stdout=subprocess.PIPE,
-                           stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-        os.replace(tmp, BINDING)
+    if binding:
+        if not why and (force or not fresh or not os.path.exists(BINDING)
+                        or os.path.getmtime(BINDING) < max(os.path.getmtime(binding), os.path.getmtime(lib))):
+            tmp = BINDING + ".tmp"
+            why = _finish_binding(_start_binding(["-shared", "-o", tmp, binding], 1))
+            if not why:
+                os.replace(tmp, BINDING)
+                with open(stamp_file, "w") as f:
+                    f.write(stamp)
+        if why:
+            for old in (BINDING, stamp_file):  # one that is there does not fit what was built
+                if os.path.exists(old):
+                    os.remove(old)
+            print(f"{lib} is built, the paged cache's Python binding is not:\n{why}", file=sys.stderr, flush=True)
     return lib
 
 

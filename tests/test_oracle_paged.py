@@ -223,6 +223,73 @@ def test_the_library_builds_without_pytorch(lib, monkeypatch, tmp_path):
     assert not (tmp_path / "binding.so").exists()
 
 
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    """build.py with compilers that only write down what they were asked for; g++ fails on request."""
+    from exact_io_aware_33_gb300 import build
+    tool = tmp_path / "bin" / "tool"
+    tool.parent.mkdir()
+    tool.write_text(f'''#!/bin/sh
+echo "$0 $@" >> {tmp_path}/log
+if [ "${{0##*/}}" = g++ ] && [ -e {tmp_path}/fail ]; then echo no such header; exit 1; fi
+while [ $# -gt 0 ]; do [ "$1" = -o ] && touch "$2"; shift; done
+''')
+    tool.chmod(0o755)
+    for name in ("nvcc", "g++"):
+        (tmp_path / "bin" / name).symlink_to(tool)
+        monkeypatch.setattr(build, {"nvcc": "nvcc", "g++": "cxx"}[name], lambda p=str(tmp_path / "bin" / name): p)
+    for name, value in (("BUILD", "obj"), ("LIB", "libfa.so"), ("BINDING", "binding.so")):
+        monkeypatch.setattr(build, name, str(tmp_path / value))
+
+    def asked(word):  # command lines with the word since the last look
+        log = tmp_path / "log"
+        lines = log.read_text().splitlines() if log.exists() else []
+        log.write_text("")
+        return [x for x in lines if word in x]
+    return build, tmp_path, asked
+
+
+def test_the_library_is_built_where_the_binding_is_not(fake_build, monkeypatch, capsys):
+    build, tmp, asked = fake_build
+    assert build.build() == build.LIB and (tmp / "binding.so").exists()
+    (tmp / "fail").touch()
+    (tmp / "libfa.so").unlink()
+    assert build.build(force=True) == build.LIB
+    assert (tmp / "libfa.so").exists()
+    assert not (tmp / "binding.so").exists()                     # the old one does not fit any more
+    assert "no such header" in capsys.readouterr().err
+    (tmp / "fail").unlink()
+    assert build.build() == build.LIB and (tmp / "binding.so").exists()
+    for name in ("cxx", "_binding_flags"):                       # no g++; a PyTorch that cannot be imported
+        with monkeypatch.context() as m:
+            def missing(*_):
+                raise (RuntimeError if name == "cxx" else ImportError)(f"{name} is missing")
+            m.setattr(build, name, missing)
+            (tmp / "libfa.so").unlink()
+            assert build.build(force=True) == build.LIB and (tmp / "libfa.so").exists()
+            assert not (tmp / "binding.so").exists() and f"{name} is missing" in capsys.readouterr().err
+
+
+def test_the_binding_is_built_again_for_another_pytorch(fake_build, monkeypatch):
+    build, tmp, asked = fake_build
+    build.build()
+    assert len(asked("g++")) == 2    # compiled and linked
+    build.build()
+    assert asked("") == []           # nothing to do
+    monkeypatch.setattr(build, "_binding_stamp", lambda: "another one")
+    build.build()
+    assert len(asked("g++")) == 2
+    build.build()
+    assert asked("") == []
+
+
+def test_a_failing_cuda_source_is_still_an_error(fake_build, monkeypatch):
+    build, tmp, asked = fake_build
+    monkeypatch.setattr(build, "nvcc", lambda: "/bin/false")
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        build.build()
+
+
 def test_binding_refuses_cpu_tensors():
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn)
     scales = torch.ones(4, 2)

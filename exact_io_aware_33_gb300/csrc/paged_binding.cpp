@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstddef>
 #include <string>
 
 #include "fa.h"
@@ -96,41 +97,60 @@ bool failed(int code, const char* what) {
   return true;
 }
 
-// attn(cache, batch, device, q, window, scale, out, lse, workspace) -> (out, lse)
+// The tensors that a struct's first fields were taken from, in that order.
+constexpr const char* kCacheTensors[] = {"k_pages", "v_pages", "k_scales", "v_scales"};
+constexpr const char* kBatchTensors[] = {"block_table", "kv_lens", "cu_q"};
+static_assert(sizeof(void*) * 4 == offsetof(fa_paged_cache, num_pages) && sizeof(void*) * 3 == offsetof(fa_paged_batch, B));
+
+// Refuses tensors that no longer lie where the struct says (their memory was
+// replaced, and what the struct points at may be somebody else's).
+template <typename S, size_t N>
+void check_held(PyObject* held, const S* s, const char* const (&names)[N]) {
+  const void* const* fields = reinterpret_cast<const void* const*>(s);
+  for (size_t i = 0; i < N; ++i) {
+    PyObject* o = PyTuple_GET_ITEM(held, i);
+    if (o != Py_None && tensor(o, names[i]).const_data_ptr() != fields[i])
+      refuse(PyExc_ValueError, std::string("the memory of ") + names[i] + " has moved: make a new object for it");
+  }
+}
+
+// attn(cache, its tensors, batch, its tensors, device, q, window, scale, out, lse, workspace) -> (out, lse)
 PyObject* attn(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 9) refuse(PyExc_TypeError, "attn takes 9 arguments");
+  if (n != 11) refuse(PyExc_TypeError, "attn takes 11 arguments");
   const fa_paged_cache* cache = address<const fa_paged_cache>(args[0]);
-  const int device = static_cast<int>(PyLong_AsLong(args[2]));
-  const at::Tensor& q = tensor(args[3], "q");
+  check_held(args[1], cache, kCacheTensors);
+  check_held(args[3], address<const fa_paged_batch>(args[2]), kBatchTensors);
+  const int device = static_cast<int>(PyLong_AsLong(args[4]));
+  const at::Tensor& q = tensor(args[5], "q");
   const int64_t stride = check_rows(q, "q", -1, -1, cache->d, device), T = q.size(0), Hq = q.size(1);
-  const fa_paged_batch batch = batch_for(args[1], T);
-  const long long window = PyLong_AsLongLong(args[4]);
-  const double scale = PyFloat_AsDouble(args[5]);
+  const fa_paged_batch batch = batch_for(args[2], T);
+  const long long window = PyLong_AsLongLong(args[6]);
+  const double scale = PyFloat_AsDouble(args[7]);
   if (PyErr_Occurred()) return nullptr;
 
   at::Tensor o, l, ws;
-  if (args[6] == Py_None) {
+  if (args[8] == Py_None) {
     o = make({T, Hq, cache->d}, at::kBFloat16, device);
   } else {
-    o = tensor(args[6], "out");
+    o = tensor(args[8], "out");
     check_rows(o, "out", T, Hq, cache->d, device);
     if (!o.is_contiguous()) refuse(PyExc_ValueError, "out must be contiguous");
   }
-  if (args[7] == Py_None) {
+  if (args[9] == Py_None) {
     l = make({T, Hq}, at::kFloat, device);
   } else {
-    l = tensor(args[7], "lse");
+    l = tensor(args[9], "lse");
     check_kind(l, "lse", at::kFloat, device);
     if (l.dim() != 2 || l.size(0) != T || l.size(1) != Hq || !l.is_contiguous())
       refuse(PyExc_ValueError, "lse must be contiguous [" + std::to_string(T) + ", " + std::to_string(Hq) + "]");
   }
   size_t bytes = 0;
-  if (args[8] == Py_None) {
+  if (args[10] == Py_None) {
     bytes = fa_paged_attn_workspace_bytes(cache, &batch, small(Hq, "heads"));
     if (bytes > 0) ws = make({static_cast<int64_t>(bytes)}, at::kByte, device);
   } else {
-    ws = tensor(args[8], "workspace");
+    ws = tensor(args[10], "workspace");
     if (!ws.is_cuda() || ws.get_device() != device || !ws.is_contiguous())
       refuse(PyExc_ValueError, "workspace must be contiguous on cuda:" + std::to_string(device));
     bytes = ws.nbytes();
@@ -146,8 +166,8 @@ PyObject* attn(PyObject*, PyObject* const* args, Py_ssize_t n) {
   code = fa_paged_attn(cache, &batch, qp, stride, op, lp, heads, w, static_cast<float>(scale), wp, bytes, stream);
   Py_END_ALLOW_THREADS;
   if (failed(code, "fa_paged_attn")) return nullptr;
-  PyObject* a = args[6] == Py_None ? THPVariable_Wrap(o) : Py_NewRef(args[6]);
-  PyObject* b = args[7] == Py_None ? THPVariable_Wrap(l) : Py_NewRef(args[7]);
+  PyObject* a = args[8] == Py_None ? THPVariable_Wrap(o) : Py_NewRef(args[8]);
+  PyObject* b = args[9] == Py_None ? THPVariable_Wrap(l) : Py_NewRef(args[9]);
   PyObject* both = PyTuple_Pack(2, a, b);
   Py_XDECREF(a);
   Py_XDECREF(b);
@@ -155,24 +175,26 @@ PyObject* attn(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// append(cache, batch, device, k, v, q, cos, sin, interleaved, q_out) -> q_out or None
+// append(cache, its tensors, batch, its tensors, device, k, v, q, cos, sin, interleaved, q_out) -> q_out or None
 PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 10) refuse(PyExc_TypeError, "append takes 10 arguments");
+  if (n != 12) refuse(PyExc_TypeError, "append takes 12 arguments");
   const fa_paged_cache* cache = address<const fa_paged_cache>(args[0]);
-  const int device = static_cast<int>(PyLong_AsLong(args[2]));
+  check_held(args[1], cache, kCacheTensors);
+  check_held(args[3], address<const fa_paged_batch>(args[2]), kBatchTensors);
+  const int device = static_cast<int>(PyLong_AsLong(args[4]));
   const int64_t d = cache->d;
-  const at::Tensor &k = tensor(args[3], "k"), &v = tensor(args[4], "v");
+  const at::Tensor &k = tensor(args[5], "k"), &v = tensor(args[6], "v");
   const int64_t ks = check_rows(k, "k", -1, cache->num_heads, d, device), T = k.size(0);
   const int64_t vs = check_rows(v, "v", T, cache->num_heads, d, device);
-  const fa_paged_batch batch = batch_for(args[1], T);
-  const int interleaved = PyObject_IsTrue(args[8]);
+  const fa_paged_batch batch = batch_for(args[2], T);
+  const int interleaved = PyObject_IsTrue(args[10]);
   if (PyErr_Occurred()) return nullptr;
 
   const float *cos = nullptr, *sin = nullptr;
   int64_t max_pos = 0, rot = 0;
-  if (args[6] != Py_None) {
-    const at::Tensor &c = tensor(args[6], "cos"), &s = tensor(args[7], "sin");
+  if (args[8] != Py_None) {
+    const at::Tensor &c = tensor(args[8], "cos"), &s = tensor(args[9], "sin");
     check_kind(c, "cos", at::kFloat, device);
     check_kind(s, "sin", at::kFloat, device);
     if (c.dim() != 2 || !c.sizes().equals(s.sizes()) || !c.is_contiguous() || !s.is_contiguous())
@@ -186,15 +208,15 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const void* qp = nullptr;
   void* op = nullptr;
   int64_t qs = 0, os = 0, Hq = 0;
-  if (args[5] != Py_None) {
-    const at::Tensor& q = tensor(args[5], "q");
+  if (args[7] != Py_None) {
+    const at::Tensor& q = tensor(args[7], "q");
     qs = check_rows(q, "q", T, -1, d, device);
     Hq = q.size(1);
-    if (args[9] == Py_None) {
+    if (args[11] == Py_None) {
       out = make({T, Hq, d}, at::kBFloat16, device);
       os = Hq * d;
     } else {
-      out = tensor(args[9], "q_out");
+      out = tensor(args[11], "q_out");
       os = check_rows(out, "q_out", T, Hq, d, device);
     }
     qp = q.data_ptr();
@@ -208,8 +230,8 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   code = fa_paged_append(cache, &batch, kp, ks, vp, vs, qp, qs, op, os, heads, cos, sin, mp, r, interleaved, stream);
   Py_END_ALLOW_THREADS;
   if (failed(code, "fa_paged_append")) return nullptr;
-  if (args[5] == Py_None) Py_RETURN_NONE;
-  return args[9] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(args[9]);
+  if (args[7] == Py_None) Py_RETURN_NONE;
+  return args[11] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(args[11]);
   END_HANDLE_TH_ERRORS
 }
 

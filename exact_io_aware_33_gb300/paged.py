@@ -9,7 +9,9 @@ step is two calls on one ``PagedCache`` and one ``PagedBatch``:
     o, lse = fa.fa_paged_attn(cache, batch, q)
 
 Both objects only hold tensors of the caller and their checked sizes, so a decode loop makes them once
-and updates ``kv_lens`` and ``block_table`` in place between steps; the calls can be captured into a
+and updates ``kv_lens`` and ``block_table`` in place between steps (``copy_``, ``add_``, indexing). Other
+tensors take a new object: attributes cannot be set, and a call refuses a tensor whose memory has moved
+since (``resize_``, ``set_``, ``.data``). The calls can be captured into a
 CUDA graph and replayed that way. All tensors of a call must be on one device, which need not be the
 current one. With ``stream`` the work is queued there and outputs and workspaces belong to that stream;
 tensors of other streams must be ready, and kept, by the caller.
@@ -72,7 +74,23 @@ def _require(t, name, dtype, dim, device=None):
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-class PagedCache:
+class _Fixed:
+    """An object whose attributes stay as they are once ``_address``, of the C struct made from them, is set."""
+
+    def _refuse(self, name):
+        if "_address" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make a new {type(self).__name__}")
+
+    def __setattr__(self, name, value):
+        self._refuse(name)
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        self._refuse(name)
+        super().__delattr__(name)
+
+
+class PagedCache(_Fixed):
     """A pool of e4m3 pages [num_pages, num_heads, page_size, d] with fp32 scales [num_pages, num_heads]."""
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales):
@@ -100,6 +118,7 @@ class PagedCache:
         self.device = dev
         self._index = dev.index
         self._scale = 1.0 / math.sqrt(d)
+        self._held = (k_pages, v_pages, k_scales, v_scales)
         self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
                                     v_scales.data_ptr(), P, H, page, d)
         self._address = ctypes.addressof(self._struct)
@@ -114,7 +133,7 @@ class PagedCache:
         return cls(*pages, *scales)
 
 
-class PagedBatch:
+class PagedBatch(_Fixed):
     """The sequences of a step: their pages, lengths (new tokens included) and packed rows.
 
     ``cu_q`` None: one new token per sequence. ``max_q`` bounds the new tokens of a sequence, ``max_kv``
@@ -143,6 +162,7 @@ class PagedBatch:
         self.B, self.max_pages, self.max_q, self.max_kv = B, max_pages, int(max_q), int(max_kv)
         self.device = dev
         self._index = dev.index
+        self._held = (block_table, kv_lens, cu_q)
         # (the rows of a call's tensors take the place of T there)
         self._struct = _BatchStruct(block_table.data_ptr(), kv_lens.data_ptr(),
                                     0 if cu_q is None else cu_q.data_ptr(), B, B, self.max_q, max_pages, self.max_kv)
@@ -173,7 +193,7 @@ def fa_paged_append(cache: PagedCache, batch: PagedBatch, k, v, q=None, rope=Non
     if q is None and q_out is not None:
         raise ValueError("q_out without q")
     cos, sin = (None, None) if rope is None else rope
-    return _native.append(cache._address, batch._address, index, k, v, q, cos, sin, interleaved, q_out)
+    return _native.append(cache._address, cache._held, batch._address, batch._held, index, k, v, q, cos, sin, interleaved, q_out)
 
 
 def fa_paged_attn_workspace_bytes(cache: PagedCache, batch: PagedBatch, Hq: int) -> int:
@@ -196,5 +216,5 @@ def fa_paged_attn(cache: PagedCache, batch: PagedBatch, q, window: int = 0, scal
             return fa_paged_attn(cache, batch, q, window, scale, out, lse, workspace)
     if batch._index != index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
-    return _native.attn(cache._address, batch._address, index, q, window, cache._scale if scale is None else scale,
-                        out, lse, workspace)
+    return _native.attn(cache._address, cache._held, batch._address, batch._held, index, q, window,
+                        cache._scale if scale is None else scale, out, lse, workspace)

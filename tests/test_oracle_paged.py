@@ -290,6 +290,49 @@ def test_a_failing_cuda_source_is_still_an_error(fake_build, monkeypatch):
         build.build()
 
 
+@pytest.fixture
+def on_the_cpu(lib, monkeypatch):
+    """A PagedCache and a PagedBatch of CPU tensors, for what can be refused before a device is looked at."""
+    monkeypatch.setattr(fa.paged, "_require", lambda *a: None)
+    pages = [torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn) for _ in range(2)]
+    cache = fa.PagedCache(*pages, torch.ones(4, 2), torch.ones(4, 2))
+    ints = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    return cache, fa.PagedBatch(ints(3, 4), ints(3), ints(4), max_q=2)
+
+
+def test_what_a_cache_and_a_batch_hold_cannot_be_exchanged(on_the_cpu):
+    cache, batch = on_the_cpu
+    for obj, names in ((cache, ("k_pages", "v_scales", "page_size", "d", "_address")),
+                       (batch, ("block_table", "kv_lens", "cu_q", "max_kv", "max_q", "B"))):
+        for name in names:
+            before = getattr(obj, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(obj, name, before)
+            with pytest.raises(AttributeError, match=name):
+                delattr(obj, name)
+            assert getattr(obj, name) is before
+
+
+@pytest.mark.parametrize("which,name,n_fields", [(0, n, 4) for n in ("k_pages", "v_pages", "k_scales", "v_scales")]
+                         + [(1, n, 3) for n in ("block_table", "kv_lens", "cu_q")])
+def test_tensors_whose_memory_has_moved_are_refused(on_the_cpu, which, name, n_fields):
+    cache, batch = on_the_cpu
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    def attn():
+        return fa.paged._native.attn(cache._address, cache._held, batch._address, batch._held, 0, q, 0, 0.125, None, None, None)
+    def append():
+        return fa.paged._native.append(cache._address, cache._held, batch._address, batch._held, 0, q, q, None, None, None,
+                                       False, None)
+    for call in (attn, append):   # as they are, the calls get as far as q
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    t = getattr((cache, batch)[which], name)
+    t.data = t.detach().clone()
+    for call in (attn, append):
+        with pytest.raises(ValueError, match=f"{name} has moved"):
+            call()
+
+
 def test_binding_refuses_cpu_tensors():
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn)
     scales = torch.ones(4, 2)

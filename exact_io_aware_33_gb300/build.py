@@ -185,7 +185,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
 # Test-only variant for the bounded-wait (timeout) path: the forward's TMA
 # producer never loads the last V tile of its key stream, and every wait gives
 # up after 20 ms instead of about a second. It lives under _build/ and is
-# never loaded by the package; only tests/test_timeout_path.py uses it.
+# never loaded by the package; only tests/test_timeout_path.py and
+# tests/test_paged_timeout.py use it.
 TIMEOUT_TEST_DIR = os.path.join(BUILD, "timeout_test")
 TIMEOUT_TEST_FLAGS = ["-DFA_TEST_SKIP_ARRIVE", "-DFA_WAIT_BUDGET_NS=20000000ull"]
 

@@ -2,7 +2,7 @@
 // batch, its bounds checks, and e4m3 conversions.
 //
 // Pool layout: k_pages and v_pages are e4m3 [num_pages, heads, page_size, d],
-// so the tokens of one head in one page are one contiguous block (2 to 16
+// so the tokens of one head in one page are one contiguous block (1 to 16
 // KiB) that a tiled copy fetches whole; k_scales and v_scales are fp32
 // [num_pages, heads]. A cached value is code * scale.
 //

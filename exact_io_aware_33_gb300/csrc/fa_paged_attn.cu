@@ -58,12 +58,12 @@ constexpr float kSlack = 8.f;    // log2 units that a weight may pass its refere
 constexpr int kItemUnits = 2;
 constexpr int kPartUnits = 4;  // a part has at least this many units, and so a tile of an item that it continues
 
-// NB: blocks of eight query rows per CTA.
 // Keys per stage. At d = 64 a tile of 64 would be 8 KiB for the same waiting,
 // voting and reference keeping, and those, not the bytes, would set the pace.
 template <int D>
 constexpr int kTileOf = D == 64 ? 128 : 64;
 
+// NB: blocks of eight query rows per CTA.
 template <int D, int NB>
 struct Cfg {
   static constexpr int kTile = kTileOf<D>;
@@ -1053,14 +1053,18 @@ int launch_rows_d(const PagedPool& pool, const AttnArgs& a, const PagedPlan& pla
 // What the cluster and the streaming form cost, in microseconds, fitted to the
 // times of 350 batch shapes on 152 SMs, of even and of ragged lengths (1 to 64
 // sequences of up to 256 to 8192 keys, 2 to 32 key heads, one or a few tokens
-// each): the form chosen is within 2 % of the best one on average. A cluster CTA's tiles follow one another, the
+// each, no windows): the form chosen is within 2 % of the best one on average. A
+// cluster CTA's tiles follow one another, the
 // slower the more CTAs share an SM (`more`: CTAs per SM, less one); clusters of
 // eight double up on an SM sooner. A streaming CTA has at least kPartUnits
-// units, and a second launch joins its pieces. Measured, cluster / streaming:
-// 32 query and 8 key heads, d = 128: 1 x 256 keys 5.5 / 9.7 us, 1 x 4096 10.5 /
-// 11.4, 8 x 1024 10.6 / 13.8, 16 x 4096 29 / 34, but 1 x 8192 15.6 / 14.1 and
-// 32 x 2048 32 / 31; 24 x 5 tokens over 4096 keys, 12 and 4 heads, d = 64: 21 /
-// 25 us.
+// units, and a second launch joins its pieces. Measured, best cluster / streaming:
+// 32 query and 8 key heads, d = 128: 1 x 256 keys 5.4 / 9.3 us, 1 x 4096 9.8 /
+// 10.8, 8 x 1024 9.1 / 12.0, but 1 x 8192 14.4 / 12.2 and 32 x 2048 31.5 / 30.2;
+// 24 x 5 tokens over 4096 keys, 12 and 4 heads, d = 64: 21.9 / 25.6. One of the
+// shapes that the costs misjudge: 16 x 4096, 28.7 / 33.1, streamed.
+// The window is left out: the costs count max_kv keys, of which a window shows
+// the kernels fewer. 8 x 32768 keys, window 1024: streamed in 11.9 us, clusters
+// of two would take 9.2.
 struct RowCosts {
   double start, join, more;    // cluster form: one CTA per item, several, and per further CTA of an SM
   double tile, tile_more;      // a tile, and per further CTA of an SM
@@ -1117,11 +1121,15 @@ PagedPlan paged_attn_plan(const PagedPool& pool, const PagedBatchDev& batch, con
     r.cluster = 0;
   }
   // Rows (16 a tile, the cached tiles read once for each) or chunks? Measured,
-  // rows / chunks, 32 query and 8 key heads, d = 128: 16 sequences of 2048 keys,
-  // 4 tokens each 30 / 42 us; 16 of 512, 16 tokens 32 / 26; 48 of 2048, 8 tokens
-  // 102 / 109; 16 and 16 heads, d = 64: 16 of 8192, 32 tokens 135 / 163; 16 of
-  // 512, 64 tokens 32 / 29. Over 198 such batches the choice is within 1 % of the
-  // best form on average.
+  // rows streamed / chunks, 32 query and 8 key heads, d = 128: 16 sequences of
+  // 2048 keys, 4 tokens each 32 / 44 us; 16 of 512, 16 tokens 32 / 19; 48 of 2048,
+  // 8 tokens 103 / 107; 16 and 16 heads, d = 64: 16 of 8192, 32 tokens 135 / 166;
+  // 16 of 512, 64 tokens 31 / 27 (misjudged: rows). Over 198 such batches, without
+  // windows, the choice is within 1 % of the best form on average. With a window
+  // the costs are too high for every form: 4 sequences of 32768 keys, 16 tokens
+  // each, 8 heads on one, window 256: chunks in 26 us, a CTA per item would take 9.
+  // One form serves the whole call: 63 single tokens over 8192 keys and a chunk
+  // of 512 take 472 us together, 161 and 69 in two calls.
   // A ragged batch has at most its packed rows' tiles and one more per sequence.
   const double packed = static_cast<double>(batch.T) * G;
   const double row_items = heads * fmin(seqs * r.row_tiles, seqs + packed / r.rows);

@@ -353,6 +353,9 @@ typedef struct fa_paged_batch {
  * sequence; when it is larger, the older codes are rounded again to it. Codes
  * round to nearest even. Values that are not finite take no part in the
  * scale: +-inf is stored as +-448 s, NaN as NaN.
+ * Where a step's tokens are taken back and their slots appended again (rejected
+ * drafts), a page with tokens before them keeps the scale that they made grow,
+ * and those tokens the second rounding that came with it.
  * A page that is written must not be any other sequence's in the batch, nor
  * its own twice (pages that are only read may be shared); two calls that
  * write the same page must be ordered.

@@ -590,6 +590,54 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   return fa::launch_paged_attn(pool, dev, p, plan, workspace, static_cast<cudaStream_t>(cuda_stream));
 }
 
+int fa_rope_axes(const void* q, long long q_stride, void* q_out, long long q_out_stride, int Hq, const void* k,
+                 long long k_stride, void* k_out, long long k_out_stride, int Hk, const int* positions,
+                 int num_axes, int T, const unsigned char* axis_of, const float* cos, const float* sin,
+                 int max_pos, int rot, int d, int interleaved, int inverse, void* cuda_stream) {
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (Hq < 0 || Hk < 0 || T < 0 || num_axes < 1 || num_axes > 256 || rot < 0 || rot > d || max_pos < 0)
+    return FA_ERR_INVALID;
+  if (rot % 16 != 0) return FA_ERR_UNSUPPORTED;
+  const long long heads = static_cast<long long>(Hq) + Hk;
+  if (heads > 0x7fffff) return FA_ERR_INVALID;
+  if (T == 0 || heads == 0) return FA_OK;
+  if (rot > 0 && (max_pos == 0 || axis_of == nullptr || !aligned4(positions) || !fa::aligned16(cos) ||
+                  !fa::aligned16(sin)))
+    return FA_ERR_INVALID;
+  if (Hq > 0 && (!fa::aligned16(q) || !fa::aligned16(q_out) || !row_stride_ok(q_stride, Hq, d) ||
+                 !row_stride_ok(q_out_stride, Hq, d)))
+    return FA_ERR_INVALID;
+  if (Hk > 0 && (!fa::aligned16(k) || !fa::aligned16(k_out) || !row_stride_ok(k_stride, Hk, d) ||
+                 !row_stride_ok(k_out_stride, Hk, d)))
+    return FA_ERR_INVALID;
+  const long long qw = static_cast<long long>(Hq) * d, kw = static_cast<long long>(Hk) * d;
+  if (Hq > 0 && !(q_out == q && (q_out_stride == q_stride || T == 1)) &&
+      rows_meet(q_out, q_out_stride, qw, q, q_stride, qw, T))
+    return FA_ERR_INVALID;
+  if (Hk > 0 && !(k_out == k && (k_out_stride == k_stride || T == 1)) &&
+      rows_meet(k_out, k_out_stride, kw, k, k_stride, kw, T))
+    return FA_ERR_INVALID;
+  if (Hq > 0 && Hk > 0 && (rows_meet(q_out, q_out_stride, qw, k, k_stride, kw, T) ||
+                           rows_meet(k_out, k_out_stride, kw, q, q_stride, qw, T) ||
+                           rows_meet(q_out, q_out_stride, qw, k_out, k_out_stride, kw, T)))
+    return FA_ERR_INVALID;
+  fa::RopeProblem p{q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, Hq, Hk, positions, cos, sin,
+                    T, d, rot, max_pos, interleaved ? 1 : 0, inverse ? 1 : 0, {}};
+  for (int i = 0; i < rot / 2; ++i) {
+    if (axis_of[i] >= num_axes) return FA_ERR_INVALID;
+    p.axes.of[i] = axis_of[i];
+  }
+  for (int u = 0; u < rot / 16; ++u) {
+    bool whole = true;
+    for (int i = 1; i < 8; ++i) whole = whole && axis_of[8 * u + i] == axis_of[8 * u];
+    p.axes.whole |= whole ? 1u << u : 0u;
+  }
+  fa::DeviceState* st = nullptr;
+  const int rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  return fa::launch_rope_axes(p, static_cast<cudaStream_t>(cuda_stream));
+}
+
 int fa_get_last_device_status(void) {
   fa::DeviceState* st = nullptr;
   if (fa::current_device(&st) != FA_OK) return FA_ERR_LAUNCH;

@@ -191,6 +191,32 @@ int launch_paged_chunk(const PagedPool& pool, const PagedBatchDev& batch, const 
                        void* workspace, cudaStream_t stream);
 size_t paged_chunk_workspace_bytes(int d, int ctas);
 
+// ---------------------------------------------------------------- rotary positions
+constexpr int kRopePairs = 128;  // of a head: d / 2, d up to 256
+
+// The axis of each channel pair; bit u of `whole`: the pairs 8 u .. 8 u + 7 share one.
+struct RopeAxes {
+  uint32_t whole;
+  unsigned char of[kRopePairs];
+};
+
+struct RopeProblem {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+  int Hq, Hk;
+  const int* positions;  // [axes, T]
+  const float* cos;      // [max_pos, rot / 2]
+  const float* sin;
+  int T, d, rot, max_pos;
+  int interleaved, inverse;
+  RopeAxes axes;
+};
+
+int launch_rope_axes(const RopeProblem& p, cudaStream_t stream);
+
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 
 }  // namespace fa

@@ -391,6 +391,39 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
                   void* workspace, size_t ws_bytes, void* cuda_stream);
 size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq);
 
+/*
+ * Rotary positions with several axes (time, height and width of the patches
+ * of a film, say): turns queries and keys of packed rows. The pages have no
+ * counterpart.
+ *   q, k     : in,  bf16 [T, Hq, d] and [T, Hk, d], rows q_stride / k_stride
+ *              elements apart (at least heads * d, a multiple of 8); either may
+ *              be NULL with no heads
+ *   q_out, k_out : out, the same shapes; each may be its input itself (with the
+ *              same stride) and must not meet an input or the other output
+ *              otherwise (FA_ERR_INVALID)
+ *   positions: in,  int32 [num_axes, T] on the device
+ *   axis_of  : in,  rot / 2 axis numbers, in HOST memory, read during the call
+ *   cos, sin : in,  fp32 [max_pos, rot / 2]: the angles of each position
+ *   rot      : channels that turn, a multiple of 16 up to d; pair i is (i, i +
+ *              rot / 2), or (2i, 2i + 1) when interleaved != 0. With p =
+ *              positions[axis_of[i]][t] it becomes (a cos[p][i] - b sin[p][i],
+ *              b cos[p][i] + a sin[p][i]): each product and sum rounded to
+ *              fp32, then to bf16, as fa_paged_append does. The other channels
+ *              are copied.
+ *   inverse  : != 0 turns by the negative angles, which is the gradient: of the
+ *              outputs' gradients it makes the inputs'.
+ *   d        : 64, 128 or 256 (FA_ERR_UNSUPPORTED otherwise, also for a rot
+ *              that is no multiple of 16)
+ * A position outside [0, max_pos) raises FA_ERR_INDEX in the device status
+ * word and is clamped. With one axis whose positions are those of the
+ * sequence this is the rotation of fa_paged_append, bit for bit; with several,
+ * append with rot = 0 what this call has turned.
+ */
+int fa_rope_axes(const void* q, long long q_stride, void* q_out, long long q_out_stride, int Hq, const void* k,
+                 long long k_stride, void* k_out, long long k_out_stride, int Hk, const int* positions,
+                 int num_axes, int T, const unsigned char* axis_of, const float* cos, const float* sin,
+                 int max_pos, int rot, int d, int interleaved, int inverse, void* cuda_stream);
+
 /* Static description of a return code. Never NULL. */
 const char* fa_strerror(int code);
 

@@ -30,11 +30,14 @@ dropout
 paged
     The paged 8-bit key/value cache: e4m3, appending with the rotation of
     positions and power-of-two scales, attention over the pages.
+packed
+    Packed sequences: attention with grouped heads and its gradients, and
+    rotary positions with several axes.
 
 Pins (what fixes each function other than itself) live in
 ``tests/test_oracle_pins.py``, ``tests/test_oracle_general.py``,
-``tests/test_oracle_dropout.py``, ``tests/test_oracle_philox.py`` and
-``tests/test_oracle_paged.py``; each
+``tests/test_oracle_dropout.py``, ``tests/test_oracle_philox.py``,
+``tests/test_oracle_paged.py`` and ``tests/test_oracle_packed.py``; each
 module's docstring names its pins.
 No function here is "parity unpinned".
 
@@ -44,6 +47,6 @@ Sources cited (title of the page, then its section):
   * "FlashAttention" (Road to Intelligence, Chapter 11)
 """
 
-from . import dense, tiled, finite_diff, general, merge, dropout, paged  # noqa: F401
+from . import dense, tiled, finite_diff, general, merge, dropout, paged, packed  # noqa: F401
 
-__all__ = ["dense", "tiled", "finite_diff", "general", "merge", "dropout", "paged"]
+__all__ = ["dense", "tiled", "finite_diff", "general", "merge", "dropout", "paged", "packed"]

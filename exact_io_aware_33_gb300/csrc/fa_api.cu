@@ -21,7 +21,7 @@ __device__ int g_status_word;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kSmemSlots = 32;
+constexpr int kSmemSlots = 48;
 
 struct DeviceState {
   bool probed = false;
@@ -130,6 +130,24 @@ bool make_map_pages(CUtensorMap* map, const void* ptr, int blocks, int rows, int
           CU_TENSOR_MAP_INTERLEAVE_NONE,
           !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_map_packed(CUtensorMap* map, const void* ptr, int T, int heads, int group, int d, long long row_stride,
+                     int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(group),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(group) * static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -588,6 +606,65 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
   if (rc != FA_OK) return rc;
   const fa::PagedAttn p{q, q_stride, o, lse, Hq, window, scale};
   return fa::launch_paged_attn(pool, dev, p, plan, workspace, static_cast<cudaStream_t>(cuda_stream));
+}
+
+namespace {
+
+// Sizes of a packed call.
+int check_packed(int B, int T, int Hq, int Hkv, int d) {
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (B < 0 || T < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID;
+  if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;  // a tile of 128 rows holds a token's group
+  // rows of a key head, and items, are counted in 32 bits
+  if (static_cast<long long>(T) * Hq > 0x7fffffffLL - 4096 || static_cast<long long>(B) * Hkv > 0x3fffffffLL)
+    return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+// row_stride_ok for rows that a tensor map names (strides below 2^40 bytes).
+bool map_stride_ok(long long stride, int heads, int d) { return row_stride_ok(stride, heads, d) && stride < (1LL << 38); }
+
+fa::PackedShape packed_shape(const int* cu, int B, int T, int Hq, int Hkv, int causal, int window) {
+  // no sequence is longer than T: a window as long masks nothing
+  return fa::PackedShape{cu, B, T, Hq, Hkv, 128 / (Hq / Hkv), causal ? 1 : 0, window >= T ? 0 : window,
+                         fa::GroupDiv::of(Hq / Hkv), fa::GroupDiv::of(Hkv)};
+}
+
+bool workspace_ok(const void* workspace, size_t have, size_t need) {
+  return need == 0 ||
+         (workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && have >= need);
+}
+
+}  // namespace
+
+size_t fa_packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d) {
+  if (check_packed(B, T, Hq, Hkv, d) != FA_OK || B == 0 || T == 0) return 0;
+  return fa::packed_fwd_workspace_bytes(B, T, Hq, Hkv, d, paged_sms());
+}
+
+int fa_packed_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const int* cu, int B, int T, int Hq, int Hkv, int d, int causal, int window,
+                  float scale, void* o, float* lse, void* workspace, size_t ws_bytes, void* cuda_stream) {
+  int rc = check_packed(B, T, Hq, Hkv, d);
+  if (rc != FA_OK) return rc;
+  if (!std::isfinite(scale) || scale < 0.f || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!fa::aligned16(q) || !fa::aligned16(k) || !fa::aligned16(v) || !fa::aligned16(o) || !aligned4(lse) ||
+      !aligned4(cu) || !map_stride_ok(q_stride, Hq, d) || !map_stride_ok(k_stride, Hkv, d) ||
+      !map_stride_ok(v_stride, Hkv, d))
+    return FA_ERR_INVALID;
+  const long long qw = static_cast<long long>(Hq) * d, kw = static_cast<long long>(Hkv) * d;
+  if (rows_meet(o, qw, qw, q, q_stride, qw, T) || rows_meet(o, qw, qw, k, k_stride, kw, T) ||
+      rows_meet(o, qw, qw, v, v_stride, kw, T))
+    return FA_ERR_INVALID;
+  if (!workspace_ok(workspace, ws_bytes, fa::packed_fwd_workspace_bytes(B, T, Hq, Hkv, d, paged_sms())))
+    return FA_ERR_WORKSPACE;
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  const fa::PackedProblem p{q, k, v, q_stride, k_stride, v_stride,
+                            packed_shape(cu, B, T, Hq, Hkv, causal, window), d, scale};
+  return fa::launch_packed_fwd(p, o, lse, workspace, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int fa_rope_axes(const void* q, long long q_stride, void* q_out, long long q_out_stride, int Hq, const void* k,

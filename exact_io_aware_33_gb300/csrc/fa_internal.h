@@ -217,6 +217,68 @@ struct RopeProblem {
 
 int launch_rope_axes(const RopeProblem& p, cudaStream_t stream);
 
+// ---------------------------------------------------------------- packed attention
+// r / G without a division, 0 <= r < 2^31 (see div in fa_paged.cuh).
+struct GroupDiv {
+  int G;
+  uint32_t magic;
+  static GroupDiv of(int g) {
+    return GroupDiv{g, g == 1 ? 0xffffffffu : static_cast<uint32_t>((1ull << 32) / static_cast<unsigned>(g))};
+  }
+#ifdef __CUDACC__
+  // With m = floor(2^32 / G), r m / 2^32 is less than r / 2^32 < 1 below r / G,
+  // so its floor is the quotient or one less, and the remainder tells which.
+  __device__ __forceinline__ int div(int r) const {
+    int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), magic));
+    if (r - q * G >= G) ++q;
+    return q;
+  }
+#endif
+};
+
+// The batch and mask, as the kernels take them.
+struct PackedShape {
+  const int* cu;       // [B + 1]
+  int B, T, Hq, Hkv;
+  int tpt;             // tokens per tile of query rows: floor(128 / G)
+  int causal, window;  // window: 0, or shorter than T
+  GroupDiv by_group;   // G = Hq / Hkv
+  GroupDiv by_head;    // Hkv
+};
+
+// Work in the order in which it is handed out, heaviest first.
+struct PackedHead {
+  int count;  // entries
+  int taken;  // items handed out beyond each CTA's first
+  int pad[2];
+};
+struct PackedList {
+  PackedHead* head;
+  int4* entries;  // row0, n, i0, -; nullptr: every item has a CTA, no list is made
+  int cap;
+  int unit;       // tokens per entry
+  int keys;       // 0: an entry's tokens are queries (its cost: key tiles), 1: keys (tiles of query rows)
+};
+
+struct PackedProblem {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  PackedShape s;
+  int d;
+  float scale;
+};
+
+// Tensor map of packed rows [T, heads, group, d] (row_stride elements between
+// tokens): boxes of `tokens` x 1 x group x 64, 128-byte swizzle.
+bool make_map_packed(CUtensorMap* map, const void* ptr, int T, int heads, int group, int d, long long row_stride,
+                     int tokens);
+// Fills the lists (one block each); nothing is launched when none has entries.
+int launch_packed_plan(const PackedShape& s, const PackedList* lists, int n, cudaStream_t stream);
+size_t packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int sms);
+int launch_packed_fwd(const PackedProblem& p, void* o, float* lse, void* workspace, cudaStream_t stream);
+
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 
 }  // namespace fa

@@ -1,0 +1,155 @@
+// What the kernels of packed attention share: the batch and its bounds checks,
+// the tiles of a sequence, and how work is found.
+//
+// Rows are packed twice. Tokens of all sequences lie one after another (cu
+// marks where each begins), and the G query heads that read a key head share
+// its tiles: a tile of query rows holds `tpt` = floor(128 / G) tokens with
+// their G heads each, token by token, so row r of a tile is token r / G, head r
+// % G of the group. One box of a 4-D tensor map fetches it: extents (64
+// channels, G, 1, tpt) of [T, Hkv, G, d]. Short sequences fill their tiles G
+// times as well as with a head per tile, a causal tile has 128 / G positions'
+// spread, and the gradients of a shared key head are summed in its own
+// accumulator, in a fixed order.
+//
+// Everything the device reads as an index (cu) is checked against the sizes
+// that the host gave before it is used: what fails is clamped and kStatusIndex
+// is raised, so a bad table never becomes a bad address.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int kKeyTile = 128;
+
+// First row of sequence b and its number of rows.
+struct PackedSeq {
+  int row0, n;
+};
+
+__device__ __forceinline__ PackedSeq packed_seq(const PackedShape& s, int b, int* status) {
+  const int c0 = s.cu[b], c1 = s.cu[b + 1];
+  PackedSeq q;
+  q.row0 = min(max(c0, 0), s.T);
+  q.n = min(max(c1, q.row0), s.T) - q.row0;
+  if (c0 < 0 || c1 < c0 || c1 > s.T) raise_index(status);
+  return q;
+}
+
+// Key tiles [lo, lo + n) that the tokens [i0, i1) of a sequence of `len` see (none when i0 >= i1).
+struct TileRange {
+  int lo, n;
+};
+__device__ __forceinline__ TileRange keys_of(const PackedShape& s, int len, int i0, int i1) {
+  const int end = s.causal ? i1 : len;
+  const int lo = s.window > 0 ? max(i0 - s.window + 1, 0) / kKeyTile : 0;
+  return TileRange{lo, i0 < i1 ? (end + kKeyTile - 1) / kKeyTile - lo : 0};
+}
+
+// Tiles of query rows [lo, lo + n) that see some of the keys [k0, k1) of a sequence of `len`.
+__device__ __forceinline__ TileRange rows_of(const PackedShape& s, int len, int k0, int k1) {
+  const int end = s.window > 0 ? min(len, k1 - 1 + s.window) : len;
+  const int lo = s.causal ? k0 / s.tpt : 0;
+  return TileRange{lo, k0 < k1 ? (end + s.tpt - 1) / s.tpt - lo : 0};
+}
+
+// An entry of the work: `unit` tokens of a sequence from token i0 on. With a
+// key head it is an item.
+struct PackedEntry {
+  int row0, n, i0;
+};
+
+// Entry number e when the sequences' entries are laid end to end, found by a
+// whole warp; n = 0 when there are fewer.
+__device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, int unit, int e, int* status) {
+  const int lane = static_cast<int>(lane_id());
+  int before = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 32) {
+    PackedSeq q{0, 0};
+    if (b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
+    const int own = (q.n + unit - 1) / unit;
+    int end = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, m);
+      if (lane >= m) end += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + end > e);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const int first = before + __shfl_sync(0xffffffffu, end - own, src);
+      return PackedEntry{__shfl_sync(0xffffffffu, q.row0, src), __shfl_sync(0xffffffffu, q.n, src), (e - first) * unit};
+    }
+    before += __shfl_sync(0xffffffffu, end, 31);
+  }
+  return PackedEntry{0, 0, 0};
+}
+
+// Hands out items: the CTA's own one where every item has a CTA (no list), or
+// the list's, heaviest first, by a counter. The entry of the item after the
+// present one is on its way, and the number of the one behind it asked for,
+// while an item is worked on.
+struct ItemQueue {
+  const PackedList* list;
+  GroupDiv by_head;
+  int count, ahead;   // entries; number of the item after the next
+  PackedEntry entry;  // of the next item
+  int head;
+  bool have;
+
+  // By the whole warp.
+  __device__ __forceinline__ void start(const PackedShape& s, const PackedList& l, int* status) {
+    list = &l;
+    by_head = s.by_head;
+    const int x = static_cast<int>(blockIdx.x), e = by_head.div(x);
+    if (l.entries == nullptr) {
+      entry = find_entry(s, l.unit, e, status);
+      head = x - e * by_head.G;
+      have = entry.n > 0;
+    } else {
+      count = l.head->count;
+      load(x);
+      ahead = request();
+    }
+  }
+  // The next item, for lane 0; false when there are no more.
+  __device__ __forceinline__ bool take(PackedEntry* e, int* h) {
+    if (!have) return false;
+    *e = entry;
+    *h = head;
+    if (list->entries == nullptr) {
+      have = false;
+    } else {
+      load(ahead);
+      ahead = request();
+    }
+    return true;
+  }
+
+ private:
+  __device__ __forceinline__ int request() {
+    return lane_id() == 0 ? static_cast<int>(gridDim.x) + atomicAdd(&list->head->taken, 1) : 0;
+  }
+  __device__ __forceinline__ void load(int x) {
+    const int e = by_head.div(x);
+    have = e < count;
+    head = x - e * by_head.G;
+    const int4 r = list->entries[min(e, list->cap - 1)];
+    entry = PackedEntry{r.x, r.y, r.z};
+  }
+};
+
+// Zeroes rows [row, rows) of a tile of `chunks` 128-byte-swizzled chunks, thread `tid` of `threads`.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int chunk_bytes, int chunks, int row, int rows, int tid,
+                                          int threads) {
+  const int units = max(rows - row, 0) * 8;
+#pragma unroll 1
+  for (int i = tid; i < units * chunks; i += threads) {
+    const int c = i / units;
+    *reinterpret_cast<uint4*>(tile + c * chunk_bytes + row * 128 + (i - c * units) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+}  // namespace fa

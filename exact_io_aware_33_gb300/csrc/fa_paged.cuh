@@ -69,22 +69,6 @@ __device__ __forceinline__ int paged_page(const PagedBatchDev& b, int seq, int i
   return -1;
 }
 
-// r / G for a packed row 0 <= r < 2^31 without a division: with m = floor(2^32
-// / G), r m / 2^32 is less than r / 2^32 < 1 below r / G, so its floor is the
-// quotient or one less, and the remainder tells which.
-struct GroupDiv {
-  int G;
-  uint32_t magic;
-  __host__ static GroupDiv of(int g) {
-    return GroupDiv{g, g == 1 ? 0xffffffffu : static_cast<uint32_t>((1ull << 32) / static_cast<unsigned>(g))};
-  }
-  __device__ __forceinline__ int div(int r) const {
-    int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), magic));
-    if (r - q * G >= G) ++q;
-    return q;
-  }
-};
-
 // Left in the workspace by each part of a divided launch, for the kernel that
 // joins the pieces of items: the item that the part begins and does not end.
 struct JoinRecord {

@@ -3,6 +3,8 @@
 // belong to.
 #pragma once
 
+#include <cmath>
+
 #include "binding_common.h"
 
 namespace {
@@ -36,6 +38,105 @@ int device_of(PyObject* q, const char* name) {
   const at::Tensor& t = tensor(q, name);
   if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(name) + " must be a CUDA tensor (no CPU path exists)");
   return t.get_device();
+}
+
+// The sequences' borders.
+const int* borders(PyObject* o, int device, int64_t* B) {
+  const at::Tensor& cu = tensor(o, "cu");
+  check_kind(cu, "cu", at::kInt, device);
+  if (cu.dim() != 1 || cu.size(0) < 1 || !cu.is_contiguous())
+    refuse(PyExc_ValueError, "cu has shape " + shape_of(cu) + ", expected contiguous [B + 1]");
+  *B = cu.size(0) - 1;
+  return static_cast<const int*>(cu.data_ptr());
+}
+
+// A row statistic [T, Hq].
+float* statistic(const at::Tensor& t, const char* name, int64_t T, int64_t Hq, int device) {
+  check_kind(t, name, at::kFloat, device);
+  if (t.dim() != 2 || t.size(0) != T || t.size(1) != Hq || !t.is_contiguous())
+    refuse(PyExc_ValueError, std::string(name) + " must be contiguous [" + std::to_string(T) + ", " + std::to_string(Hq) + "]");
+  return static_cast<float*>(t.data_ptr());
+}
+
+// The caller's workspace, or a new one of `need` bytes; its address (null where there is none) and size.
+void* scratch(PyObject* given, size_t need, int device, at::Tensor* made, size_t* bytes) {
+  if (given == Py_None) {
+    *bytes = need;
+    if (need == 0) return nullptr;
+    *made = make({static_cast<int64_t>(need)}, at::kByte, device);
+  } else {
+    *made = tensor(given, "workspace");
+    if (!made->is_cuda() || made->get_device() != device || !made->is_contiguous())
+      refuse(PyExc_ValueError, "workspace must be contiguous on cuda:" + std::to_string(device));
+    *bytes = made->nbytes();
+  }
+  return *bytes > 0 ? made->data_ptr() : nullptr;
+}
+
+// q, k and v of a call.
+struct Packed {
+  int device;
+  const void *q, *k, *v;
+  int64_t qs, ks, vs, T, Hq, Hkv, d, B;
+  const int* cu;
+  int t, hq, hkv, dd, b;
+};
+
+Packed packed_args(PyObject* qo, PyObject* ko, PyObject* vo, PyObject* cuo) {
+  Packed p;
+  p.device = device_of(qo, "q");
+  const at::Tensor &q = tensor(qo, "q"), &k = tensor(ko, "k"), &v = tensor(vo, "v");
+  if (q.dim() != 3) refuse(PyExc_ValueError, "q has shape " + shape_of(q) + ", expected [T, heads, d]");
+  p.T = q.size(0);
+  p.Hq = q.size(1);
+  p.d = q.size(2);
+  p.qs = check_rows(q, "q", p.T, p.Hq, p.d, p.device);
+  p.ks = check_rows(k, "k", p.T, -1, p.d, p.device);
+  p.Hkv = k.size(1);
+  p.vs = check_rows(v, "v", p.T, p.Hkv, p.d, p.device);
+  p.cu = borders(cuo, p.device, &p.B);
+  p.q = q.data_ptr();
+  p.k = k.data_ptr();
+  p.v = v.data_ptr();
+  p.t = small(p.T, "rows");
+  p.hq = small(p.Hq, "heads");
+  p.hkv = small(p.Hkv, "heads");
+  p.dd = small(p.d, "d");
+  p.b = small(p.B, "sequences");
+  return p;
+}
+
+// The scale given, or 1 / sqrt(d).
+double scale_of(PyObject* o, int64_t d) { return o == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : PyFloat_AsDouble(o); }
+
+// packed_fwd(q, k, v, cu, causal, window, scale, out, lse, workspace) -> (out, lse)
+PyObject* packed_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10) refuse(PyExc_TypeError, "packed_fwd takes 10 arguments");
+  const Packed p = packed_args(args[0], args[1], args[2], args[3]);
+  const int causal = PyObject_IsTrue(args[4]);
+  const long long window = PyLong_AsLongLong(args[5]);
+  const double scale = scale_of(args[6], p.d);
+  if (PyErr_Occurred()) return nullptr;
+  int64_t os;
+  at::Tensor o = rows_out(args[7], "out", p.T, p.Hq, p.d, p.device, &os), l, ws;
+  if (!o.is_contiguous()) refuse(PyExc_ValueError, "out must be contiguous");
+  l = args[8] == Py_None ? make({p.T, p.Hq}, at::kFloat, p.device) : tensor(args[8], "lse");
+  float* lp = statistic(l, "lse", p.T, p.Hq, p.device);
+  size_t bytes;
+  void* wp = scratch(args[9], args[9] == Py_None ? fa_packed_fwd_workspace_bytes(p.b, p.t, p.hq, p.hkv, p.dd) : 0,
+                     p.device, &ws, &bytes);
+  void* op = o.data_ptr();
+  void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.device)).stream();
+  const int w = small(window, "window");
+  int code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = fa_packed_fwd(p.q, p.qs, p.k, p.ks, p.v, p.vs, p.cu, p.b, p.t, p.hq, p.hkv, p.dd, causal, w,
+                       static_cast<float>(scale), op, lp, wp, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  if (failed(code, "fa_packed_fwd")) return nullptr;
+  return tuple_of(output(args[7], o), output(args[8], l));
+  END_HANDLE_TH_ERRORS
 }
 
 // rope(q, k or None, positions, cos, sin, axis_of (bytes), interleaved, inverse, q_out, k_out) -> (q_out, k_out or None)

@@ -1,9 +1,11 @@
-"""Packed rows of several sequences: rotary positions with several axes.
+"""Packed sequences: attention with grouped heads, and rotary positions with several axes.
 
-Bindings of the ``fa_rope_axes`` entry point (``include/fa.h`` states the operator). The rows of a call's
-sequences lie one after another in tensors [T, heads, d], which may be slices of a fused projection:
+Bindings of ``fa_rope_axes`` and ``fa_packed_fwd`` (``include/fa.h`` states the operators). The rows of a call's
+sequences lie one after another in tensors [T, heads, d], which may be slices of a fused projection; ``cu``
+(int32 [B + 1], on the device) marks where each sequence begins:
 
     q, k = fa.fa_rope_axes(q, k, positions, (cos, sin), sections=(16, 24, 24))
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True)
 
 All tensors of a call must be on one device, which need not be the current one. With ``stream`` the work
 is queued there and outputs belong to that stream; tensors of other streams must be ready, and kept, by
@@ -65,3 +67,24 @@ def fa_rope_axes(q, k, positions, rope, sections=None, axis_of=None, interleaved
     axes = _axes(None if sections is None else tuple(sections), None if axis_of is None else tuple(axis_of))
     cos, sin = rope
     return native.rope(q, k, positions, cos, sin, axes, interleaved, inverse, q_out, k_out)
+
+
+def fa_packed_fwd_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    """Workspace bytes of fa_packed_fwd for B sequences in T rows."""
+    if _paged._native is None:
+        _paged._load()
+    return _paged._lib.fa_packed_fwd_workspace_bytes(B, T, Hq, Hkv, d)
+
+
+def fa_packed_fwd(q, k, v, cu, causal: bool = False, window: int = 0, scale: float | None = None, out=None,
+                  lse=None, workspace=None, stream=None):
+    """Attention of each sequence's rows over its own; (o bf16 [T, Hq, d], lse fp32 [T, Hq]).
+
+    q [T, Hq, d], k and v [T, Hkv, d], bf16; query head h reads key head h / (Hq / Hkv). Rows of a new
+    ``out`` outside the sequences are not written. Without ``workspace`` one is allocated where the call
+    needs it."""
+    native = _ready(q, stream)
+    if native is None:
+        with _elsewhere(q, stream):
+            return fa_packed_fwd(q, k, v, cu, causal, window, scale, out, lse, workspace)
+    return native.packed_fwd(q, k, v, cu, causal, window, scale, out, lse, workspace)

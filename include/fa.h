@@ -392,6 +392,44 @@ int fa_paged_attn(const fa_paged_cache* cache, const fa_paged_batch* batch, cons
 size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged_batch* batch, int Hq);
 
 /*
+ * Attention over packed sequences: exact attention of sequences of different
+ * lengths whose rows lie one after another, with grouped heads (query head h
+ * reads key head h / (Hq / Hkv)). Sources as fa_fwd; packing and grouping have
+ * no counterpart on the pages.
+ *   q       : in,  bf16 [T, Hq, d], rows q_stride elements apart (at least
+ *             Hq * d, a multiple of 8, below 2^38): a slice of a fused
+ *             projection is fine
+ *   k, v    : in,  bf16 [T, Hkv, d], rows k_stride / v_stride elements apart
+ *   cu      : in,  int32 [B + 1] on the device: sequence b's rows are cu[b] ..
+ *             cu[b + 1] - 1, none allowed. Rows outside [cu[0], cu[B]) are no
+ *             sequence's: what they hold has no influence, and outputs there
+ *             are left as they were.
+ *   causal  : != 0: row i of a sequence sees its rows j <= i
+ *   window  : W >= 1 (causal only): and of those only j > i - W; 0: none
+ *   scale   : finite and >= 0, as in fa_fwd
+ *   o       : out, bf16 [T, Hq, d] contiguous; must not meet q, k or v
+ *             (FA_ERR_INVALID)
+ *   lse     : out, fp32 [T, Hq], natural-log log-sum-exp
+ *   workspace : at least fa_packed_fwd_workspace_bytes(...) bytes (0: may be
+ *             NULL), 256-byte aligned; nothing in it outlives the call. Two
+ *             calls in flight at once need two, also as replays of two
+ *             captured graphs.
+ * d is 64 or 128 and Hq / Hkv at most 128 (FA_ERR_UNSUPPORTED otherwise); T * Hq
+ * is below 2^31 - 4096. The same inputs give the same bits. The device checks cu:
+ * what does not rise or lies outside [0, T] is clamped and raises FA_ERR_INDEX
+ * in the device status word; sequences that overlap leave unspecified outputs
+ * in their rows.
+ * Values that are not finite stay within their sequence. There they follow the
+ * formula as the tensor core evaluates it, tile by tile: an infinity or NaN in
+ * v reaches all rows whose tile of 128 keys holds it, seen or not (0 * inf is
+ * NaN), as in fa_fwd.
+ */
+int fa_packed_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const int* cu, int B, int T, int Hq, int Hkv, int d, int causal, int window,
+                  float scale, void* o, float* lse, void* workspace, size_t ws_bytes, void* cuda_stream);
+size_t fa_packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d);
+
+/*
  * Rotary positions with several axes (time, height and width of the patches
  * of a film, say): turns queries and keys of packed rows. The pages have no
  * counterpart.

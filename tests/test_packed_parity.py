@@ -1,9 +1,16 @@
-"""Packed rows on the GPU: fa_rope_axes against the float64 oracle.
+"""Packed sequences on the GPU: fa_rope_axes and fa_packed_fwd against the float64 oracle.
 
 Tolerances, derived from the arithmetic:
 
 * rope: each product and sum is rounded to float32 by definition and the result to bf16; compared bit for bit.
+* o: one rounding to bf16 (2^-8 of the value), and P rounded to bf16 (2^-8 of each weight: at most 2^-8 A with A =
+  sum_j p_j |v_j|). Float32 sums of S err by at most 128 * 2^-24 sum_c |q_c k_c|, below 2^-11 in the exponent here
+  (sum |q_c k_c| scale <= 64), and exponentials and sums by less than 2^-12: together below 2^-10 A.
+  Bound: 2^-8 |o| + (2^-8 + 2^-10) A.
+* lse: the error of S enters it unchanged: 128 * 2^-24 * 64 = 4.9e-4 at the very most. Bound: 5e-4.
 """
+
+import math
 
 import numpy as np
 import pytest
@@ -147,3 +154,190 @@ def test_rope_captured_on_a_stream_and_off_the_current_one():
     g.replay()
     done()
     assert torch.equal(x, c) and torch.equal(y, e) and not torch.equal(a, c)
+
+
+# ------------------------------------------------------------------ attention
+class Rows:
+    """q, k and v of packed sequences, side by side in one tensor; `lead` rows before the sequences and `trail` behind
+    them are no sequence's and hold NaN."""
+
+    def __init__(self, lens, Hq, Hkv, d, seed, lead=0, trail=0):
+        rng = self.rng = np.random.default_rng(seed)
+        self.Hq, self.Hkv, self.d, self.G = Hq, Hkv, d, Hq // Hkv
+        self.cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32) + lead
+        self.T = int(self.cu[-1]) + trail
+        self.inside = np.zeros(self.T, dtype=bool)
+        self.inside[self.cu[0]:self.cu[-1]] = True
+        self.whole = randn(rng, self.T, (Hq + 2 * Hkv) * d + 8)
+        self.whole[~torch.from_numpy(self.inside)] = float("nan")
+        self.q, self.k, self.v = self.views(self.whole)
+
+    def views(self, whole):
+        a, b = self.Hq * self.d, self.Hkv * self.d
+        return (whole[:, :a].view(self.T, self.Hq, self.d), whole[:, a:a + b].view(self.T, self.Hkv, self.d),
+                whole[:, a + b:a + 2 * b].view(self.T, self.Hkv, self.d))
+
+    def on_gpu(self):
+        return self.views(self.whole.cuda()), torch.from_numpy(self.cu).cuda()
+
+
+def f64(*xs):
+    return [x.float().cpu().double().numpy() for x in xs]
+
+
+def check_fwd(rows, o, lse, causal, scale, window, which=None):
+    """Against the oracle in the sequences `which` (all); rows outside the sequences are not looked at."""
+    cu = rows.cu
+    q, k, v = f64(rows.q, rows.k, rows.v)
+    o, lse = f64(o, lse)
+    for b in range(len(cu) - 1) if which is None else which:
+        at = slice(cu[b], cu[b + 1])
+        n = cu[b + 1] - cu[b]
+        one = np.array([0, n])
+        want, want_lse = packed.forward(q[at], k[at], v[at], one, causal, scale, window)
+        A, _ = packed.forward(q[at], k[at], np.abs(v[at]), one, causal, scale, window)
+        err = np.abs(o[at] - want) - 2.0 ** -8 * np.abs(want)
+        assert n == 0 or (err <= (2.0 ** -8 + 2.0 ** -10) * A).all(), (b, (err / A).max())
+        assert (np.abs(lse[at] - want_lse) <= 5e-4).all(), b
+
+
+FWD = [
+    # lens, Hq, Hkv, d, causal, window
+    ([1], 1, 1, 64, True, 0),
+    ([1], 2, 1, 128, False, 0),
+    ([1, 2, 127, 128, 129], 2, 2, 128, True, 0),
+    ([255, 256, 257, 0, 3], 1, 1, 64, True, 0),
+    ([255, 256, 257, 0, 3], 2, 1, 64, False, 0),
+    ([300, 41], 8, 2, 128, True, 0),              # four heads on one, a tile of 32 tokens
+    ([300, 41], 6, 2, 128, False, 0),             # three: 42 tokens and two rows over
+    ([77, 513], 10, 2, 64, True, 0),
+    ([130, 64], 14, 2, 128, True, 0),             # seven: 18 tokens, two rows over
+    ([45], 71, 1, 64, True, 0),                   # one token's heads fill a tile half
+    ([19, 20], 128, 1, 128, False, 0),
+    ([200, 300], 4, 4, 64, True, 1),              # a window of the row itself
+    ([500, 129, 700], 4, 2, 128, True, 130),
+    ([500, 129, 700], 3, 1, 64, True, 200),
+    ([640], 2, 2, 128, True, 127),
+    ([640], 2, 2, 64, True, 2 ** 31 - 1),         # as long as there is: none
+    ([2100], 8, 1, 128, True, 1000),
+    ([1500, 700], 12, 12, 64, False, 0),
+    ([3, 1, 4, 1, 5, 9, 2, 6] * 60, 2, 2, 64, True, 0),       # more items than CTAs
+    ([33, 0, 100, 7] * 60, 4, 2, 128, True, 0),
+    ([33, 0, 100, 7] * 60, 4, 2, 64, False, 0),
+    ([1500, 1, 2300, 129], 24, 8, 128, True, 0),
+    ([1500, 1, 2300, 129], 24, 12, 64, True, 300),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,causal,window", FWD)
+def test_packed_fwd(lens, Hq, Hkv, d, causal, window):
+    rows = Rows(lens, Hq, Hkv, d, seed=sum(lens) + Hq + d, lead=3 if len(lens) > 2 else 0, trail=5)
+    (q, k, v), cu = rows.on_gpu()
+    out = torch.full((rows.T, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows.T, Hq), 7.0, device="cuda")
+    o, l = fa.fa_packed_fwd(q, k, v, cu, causal=causal, window=window, out=out, lse=lse)
+    done()
+    assert o is out and l is lse
+    check_fwd(rows, o, l, causal, 1 / math.sqrt(d), window)
+    outside = torch.from_numpy(~rows.inside).cuda()
+    assert (o[outside] == 7).all() and (l[outside] == 7).all()
+    again, l2 = fa.fa_packed_fwd(q, k, v, cu, causal=causal, window=window)
+    done()
+    inside = ~outside
+    assert torch.equal(again[inside], o[inside]) and torch.equal(l2[inside], l[inside])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 1.0])
+def test_packed_fwd_scales(d, scale):
+    rows = Rows([150, 40], 4, 2, d, seed=d)
+    rows.whole *= 0.25                            # (scale 1: sums |q_c k_c| stay below 64)
+    (q, k, v), cu = rows.on_gpu()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True, scale=scale)
+    done()
+    check_fwd(rows, o, lse, True, scale, 0)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 1), (128, 3)])
+def test_packed_fwd_what_is_not_finite_stays_in_its_sequence(d, G, causal):
+    rows = Rows([100, 60, 200, 90, 300], 2 * G, 2, d, seed=d + G, lead=2, trail=4)
+    for b, bad in ((1, float("nan")), (3, float("inf"))):
+        rows.whole[rows.cu[b]:rows.cu[b + 1]] = bad
+    (q, k, v), cu = rows.on_gpu()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=causal)
+    done()
+    check_fwd(rows, o, lse, causal, 1 / math.sqrt(d), 0, which=(0, 2, 4))
+    assert o[rows.cu[1]:rows.cu[2]].isnan().all()
+
+
+def test_packed_fwd_large_scores():
+    # one key outweighs the others by far, and rows whose maximum grows from tile to tile
+    rows = Rows([400], 2, 2, 64, seed=3)
+    rows.k[:] = 0
+    rows.q[:] = 0
+    rows.q[..., 0] = 1
+    rows.k[:, :, 0] = torch.arange(400).to(torch.bfloat16)[:, None]
+    (q, k, v), cu = rows.on_gpu()
+    for causal in (False, True):
+        o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=causal, scale=1.0)
+        done()
+        check_fwd(rows, o, lse, causal, 1.0, 0)
+
+
+def test_packed_fwd_borders_out_of_range_are_reported():
+    rows = Rows([50, 60], 2, 2, 64, seed=4)
+    (q, k, v), _ = rows.on_gpu()
+    for bad in ([0, 50, 200], [-4, 50, 110], [0, 60, 50], [0, 110, 0, 110, 0, 110]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        fa.fa_packed_fwd(q, k, v, cu, causal=True)
+        done(fa.FA_ERR_INDEX)
+    good = torch.tensor([0, 50, 110], dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_packed_fwd(q, k, v, torch.tensor([0, 50, 200], dtype=torch.int32, device="cuda"), causal=True)
+    done(fa.FA_ERR_INDEX)
+    want, _ = fa.fa_packed_fwd(q, k, v, good, causal=True)
+    done()
+    assert torch.equal(o, want)                   # clamped to the rows there are
+
+
+def test_packed_fwd_too_many_overlapping_rows_for_the_list():
+    # borders that fall and rise again name more rows than there are: the list holds what fits
+    rows = Rows([700] * 4, 2, 2, 64, seed=5)
+    (q, k, v), _ = rows.on_gpu()
+    cu = torch.tensor([0, 2800] * 300, dtype=torch.int32, device="cuda")
+    fa.fa_packed_fwd(q, k, v, cu, causal=True)
+    done(fa.FA_ERR_INDEX)
+
+
+def test_packed_fwd_of_nothing():
+    for T, B in ((0, 1), (5, 0)):
+        q = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda")
+        o, lse = fa.fa_packed_fwd(q, q, q, torch.zeros(B + 1, dtype=torch.int32, device="cuda"), causal=True)
+        assert o.shape == (T, 2, 64) and lse.shape == (T, 2)
+    q = torch.ones(300, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 3)
+    for B in (3, 700):                            # sequences of nothing, with and without a list
+        fa.fa_packed_fwd(q, q, q, torch.full((B + 1,), 9, dtype=torch.int32, device="cuda"), out=out)
+        done()
+        assert (out == 3).all()
+
+
+@pytest.mark.parametrize("lens", [[200, 130], [200, 3, 0, 130] * 50])
+def test_packed_fwd_captured_with_new_borders_and_on_a_stream(lens):
+    rows = Rows(lens, 4, 2, 64, seed=6)
+    (q, k, v), cu = rows.on_gpu()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    a, _ = fa.fa_packed_fwd(q, k, v, cu, causal=True, stream=s)
+    s.synchronize()
+    check_fwd(rows, a, torch.zeros(0), True, 0.125, 0, which=())
+    b, _ = fa.fa_packed_fwd(q, k, v, cu, causal=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True)
+    rows.cu[1:-1] = np.sort(rows.rng.integers(0, rows.T, len(lens) - 1))
+    cu.copy_(torch.from_numpy(rows.cu))
+    g.replay()
+    done()
+    assert torch.equal(a, b)
+    check_fwd(rows, o, lse, True, 0.125, 0)

@@ -15,10 +15,12 @@ The functions carry the C entry points' names:
     fa_paged_append(cache, batch, k, v, q=None, rope=None) -> rotated q
     fa_paged_attn(cache, batch, q, window=0, scale=None) -> (o, lse)
     fa_packed_fwd(q, k, v, cu, causal=False, window=0, scale=None) -> (o, lse)
+    fa_packed_bwd(q, k, v, o, lse, do, cu, causal=False, window=0, scale=None) -> (dq, dk, dv)
     fa_rope_axes(q, k, positions, rope, sections=None) -> (rotated q, rotated k)
     fa_strerror(code), fa_get_last_device_status(), fa_version()
 
-The paged forms work on a PagedCache (a pool of e4m3 pages) and a PagedBatch
+The packed forms take the rows of several sequences one after another; the
+packed module documents them. The paged forms work on a PagedCache (a pool of e4m3 pages) and a PagedBatch
 (the sequences of a step); the paged module documents them. fa_fwd_ex and fa_decode_splitkv take Nq queries [B, H, Nq, d] over Nk keys
 [B, H, Nk, d] (causal queries are the last Nq positions) and an optional
 sliding window.
@@ -78,6 +80,9 @@ SIGNATURES = {
     "fa_paged_attn_workspace_bytes": (_S, [_P, _P, _I]),
     "fa_packed_fwd": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _S, _P]),
     "fa_packed_fwd_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "fa_packed_bwd": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _L, _P, _L,
+                           _P, _L, _P, _S, _P]),
+    "fa_packed_bwd_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "fa_rope_axes": (_I, [_P, _L, _P, _L, _I, _P, _L, _P, _L, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_get_last_device_status": (_I, []),
@@ -410,4 +415,5 @@ def fa_bwd_dropout(q, k, v, o, lse, do, dropout_p: float, seed: int, offset: int
 
 from .paged import (PagedBatch, PagedCache, fa_paged_append, fa_paged_attn,  # noqa: E402,F401
                     fa_paged_attn_workspace_bytes)
-from .packed import fa_packed_fwd, fa_packed_fwd_workspace_bytes, fa_rope_axes  # noqa: E402,F401
+from .packed import (fa_packed_bwd, fa_packed_bwd_workspace_bytes, fa_packed_fwd,  # noqa: E402,F401
+                     fa_packed_fwd_workspace_bytes, fa_rope_axes)

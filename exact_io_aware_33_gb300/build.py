@@ -30,7 +30,7 @@ BINDING = os.path.join(PKG, "_paged_native.so")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_noalloc.cu", "fa_paged_append.cu",
            "fa_paged_attn.cu", "fa_paged_chunk.cu", "fa_rope.cu",
-           "fa_packed_plan.cu", "fa_packed_fwd.cu"]
+           "fa_packed_plan.cu", "fa_packed_fwd.cu", "fa_packed_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I" + INCLUDE, "-I" + CSRC] + ARCH

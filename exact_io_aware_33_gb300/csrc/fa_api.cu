@@ -667,6 +667,53 @@ int fa_packed_fwd(const void* q, long long q_stride, const void* k, long long k_
   return fa::launch_packed_fwd(p, o, lse, workspace, static_cast<cudaStream_t>(cuda_stream));
 }
 
+size_t fa_packed_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d) {
+  if (check_packed(B, T, Hq, Hkv, d) != FA_OK || B == 0 || T == 0) return 0;
+  return fa::packed_bwd_workspace_bytes(B, T, Hq, Hkv, paged_sms());
+}
+
+int fa_packed_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const void* o, const float* lse, const void* dO, long long do_stride,
+                  const int* cu, int B, int T, int Hq, int Hkv, int d, int causal, int window, float scale,
+                  void* dq, long long dq_stride, void* dk, long long dk_stride, void* dv, long long dv_stride,
+                  void* workspace, size_t ws_bytes, void* cuda_stream) {
+  int rc = check_packed(B, T, Hq, Hkv, d);
+  if (rc != FA_OK) return rc;
+  if (!std::isfinite(scale) || scale < 0.f || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
+  if (B == 0 || T == 0) return FA_OK;
+  struct Rows {
+    const void* at;
+    long long stride;
+    int heads;
+  };
+  const Rows in[5] = {{q, q_stride, Hq}, {k, k_stride, Hkv}, {v, v_stride, Hkv}, {dO, do_stride, Hq},
+                      {o, static_cast<long long>(Hq) * d, Hq}};
+  const Rows out[3] = {{dq, dq_stride, Hq}, {dk, dk_stride, Hkv}, {dv, dv_stride, Hkv}};
+  for (const Rows& r : in)
+    if (!fa::aligned16(r.at) || !map_stride_ok(r.stride, r.heads, d)) return FA_ERR_INVALID;
+  for (const Rows& r : out)
+    if (!fa::aligned16(r.at) || !row_stride_ok(r.stride, r.heads, d)) return FA_ERR_INVALID;
+  if (!aligned4(lse) || !aligned4(cu)) return FA_ERR_INVALID;
+  auto meet = [&](const Rows& a, const Rows& b) {
+    return rows_meet(a.at, a.stride, static_cast<long long>(a.heads) * d, b.at, b.stride,
+                     static_cast<long long>(b.heads) * d, T);
+  };
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& r : in)
+      if (meet(out[i], r)) return FA_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return FA_ERR_INVALID;
+  }
+  if (!workspace_ok(workspace, ws_bytes, fa::packed_bwd_workspace_bytes(B, T, Hq, Hkv, paged_sms())))
+    return FA_ERR_WORKSPACE;
+  fa::DeviceState* st = nullptr;
+  rc = fa::current_device(&st);
+  if (rc != FA_OK) return rc;
+  const fa::PackedBwd b{{q, k, v, q_stride, k_stride, v_stride, packed_shape(cu, B, T, Hq, Hkv, causal, window), d, scale},
+                        o, lse, dO, do_stride, dq, dk, dv, dq_stride, dk_stride, dv_stride};
+  return fa::launch_packed_bwd(b, workspace, static_cast<cudaStream_t>(cuda_stream));
+}
+
 int fa_rope_axes(const void* q, long long q_stride, void* q_out, long long q_out_stride, int Hq, const void* k,
                  long long k_stride, void* k_out, long long k_out_stride, int Hk, const int* positions,
                  int num_axes, int T, const unsigned char* axis_of, const float* cos, const float* sin,

@@ -279,6 +279,20 @@ int launch_packed_plan(const PackedShape& s, const PackedList* lists, int n, cud
 size_t packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int sms);
 int launch_packed_fwd(const PackedProblem& p, void* o, float* lse, void* workspace, cudaStream_t stream);
 
+struct PackedBwd {
+  PackedProblem p;
+  const void* o;     // [T, Hq, d]
+  const float* lse;  // [T, Hq]
+  const void* dO;
+  long long do_stride;
+  void* dq;
+  void* dk;
+  void* dv;
+  long long dq_stride, dk_stride, dv_stride;
+};
+size_t packed_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int sms);
+int launch_packed_bwd(const PackedBwd& b, void* workspace, cudaStream_t stream);
+
 size_t bwd_workspace_bytes(long long B, long long H, long long N, long long d);
 
 }  // namespace fa

@@ -1,0 +1,885 @@
+// Gradients of attention over packed sequences with grouped heads.
+//
+// Mathematics, with the forward's O and LSE and the loss's gradient dO, per
+// query row i (a token's head) and key j that it sees:
+//   D_i = sum_c dO_ic O_ic,  P_ij = e^(scale q_i . k_j - LSE_i),
+//   dS_ij = P_ij (dO_i . v_j - D_i),
+//   dV_j = sum_i P_ij dO_i,  dK_j = scale sum_i dS_ij q_i  (over the group's heads too),
+//   dQ_i = scale sum_j dS_ij k_j.
+// P and dS are rounded to bf16 for the products (2^-9 of a term on average);
+// everything else is fp32.
+//
+// Three kernels: D; dK and dV, with a key tile resident and the tiles of query
+// rows streamed; dQ, with a tile of query rows resident and the key tiles
+// streamed. S and dP are computed in both, 7 products instead of the 5 of a
+// single kernel, which would add its dQ tiles up in memory: with fp32 atomics,
+// in an order that changes from run to run (a workspace of 4 T Hq d bytes, its
+// clearing and its conversion with it). Here every sum has its owner and a
+// fixed order, so the same inputs give the same bits.
+//
+// dK, dV: thread = key row = tensor-memory lane, S^T = K Q^T and dP^T = V dO^T
+// with both operands in shared memory, P^T and dS^T written over them as the
+// tensor-memory operands of dV += P^T dO and dK += dS^T Q: no probability goes
+// through shared memory. Per step the MMA warp issues dV, the next S^T, dK, the
+// next dP^T: the exponentials are formed under dK and dP^T, dS under dV and S^T.
+// dQ: thread = query row, S and dP leave for registers at once, so the next
+// step's are computed while dS of this one is formed; dS has columns of its own.
+//
+// Tiles (fa_packed.cuh) hold a key head's whole group. What a box reaches past
+// its sequence belongs to another one and may hold anything; where it would be
+// multiplied by 0 a helper warp puts zeros in its place, in shared memory,
+// before the tile is handed to the tensor core.
+//
+// What bounds it: 14 d flops per visible pair on the tensor core (10 d of them
+// the algorithm's), which reads up to 128 bytes a clock of operands from shared
+// memory, and two exponentials per pair.
+
+#include "fa_packed.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kKT = kKeyTile;  // keys per tile; also rows per tile of query rows
+constexpr int kItems = 4;      // item records kept
+constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 bf16, 128-byte swizzled
+constexpr int kComputeWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
+constexpr int kThreads = 32 * 11;
+constexpr int kStageOut = 2048;  // staging per compute warp: 32 rows x 32 bf16
+constexpr float kLog2e = 1.4426950408889634f;
+
+// An item, left by the TMA warp.
+struct Item {
+  int end;      // 1: no more items (the rest is not set)
+  int row0, n;  // the sequence's first row, and its length
+  int h;        // key head
+  int x0;       // first token of the resident tile
+  int t0, ns;   // first streamed tile, and how many
+  int pad;
+};
+
+struct BwdArgs {
+  PackedShape s;
+  PackedList list;
+  const float* lse;  // [T, Hq]
+  const float* D;    // [T, Hq]
+  __nv_bfloat16* out[2];   // dK, dV; or dQ
+  long long out_stride[2];
+  int* status;
+  float scale, scale_log2;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kResOff = 0;  // resident pair of tiles: K and V, or Q and dO
+  static constexpr int kRingOff = 2 * kTileBytes;  // stages of a pair: Q and dO, or K and V
+  static constexpr int kOutOff = kRingOff + kStages * 2 * kTileBytes;
+  static constexpr int kStatOff = kOutOff + kComputeWarps * kStageOut;  // per stage: 128 LSE, 128 D (dK, dV)
+  static constexpr int kItemOff = kStatOff + kStages * 1024;
+  static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
+  enum : int {
+    kBarResFull = 0,
+    kBarResFree = 1,
+    kBarLoad = 2,                      // a stage's tiles have landed
+    kBarReady = kBarLoad + kStages,    // the helper is done with the stage
+    kBarEmpty = kBarReady + kStages,
+    kBarS = kBarEmpty + kStages,
+    kBarDp,
+    kBarP,      // dK, dV: P is written; dQ: S and dP are in registers
+    kBarDs,     // dS is written
+    kBarDsFree, // dQ: dS has been read
+    kBarFinal,
+    kBarItemFull,
+    kBarItemEmpty = kBarItemFull + kItems,
+    kBarDrain = kBarItemEmpty + kItems,
+    kNumBars
+  };
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + slack to align the base
+  static constexpr uint32_t kColS = 0, kColDp = 128, kColA = 256;  // then dK and dV; or dQ
+  static constexpr uint32_t kColDs = 448;                          // dQ: 64 columns
+  static_assert(kSmemBytes <= 232448, "tiles exceed shared memory");
+  static_assert(kItemOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
+};
+
+// ---------------------------------------------------------------- D
+// D = rowsum(dO O) for every row and head; d / 8 lanes per row. Bound by memory:
+// 4 d bytes a row.
+template <int D>
+__global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16* __restrict__ o,
+                                                            const __nv_bfloat16* __restrict__ dO, long long do_stride,
+                                                            float* __restrict__ out, long long rows, GroupDiv heads) {
+  constexpr int kLanes = D / 8, kUnroll = 4;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x % kLanes;
+  const long long per = 256 / kLanes, first = static_cast<long long>(blockIdx.x) * per * kUnroll + threadIdx.x / kLanes;
+  uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const long long row = first + i * per;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      const int t = heads.div(static_cast<int>(row)), h = static_cast<int>(row) - t * heads.G;
+      a[i] = *reinterpret_cast<const uint4*>(o + row * D + lane * 8);
+      b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + h * D + lane * 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+      sum = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y[e] & 0xffff0000u), sum);
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    const long long row = first + i * per;
+    if (lane == 0 && row < rows) out[row] = sum;
+  }
+}
+
+// ---------------------------------------------------------------- shared parts
+// Bits c of a word for lo <= c < hi.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xffffffffu : (1u << max(hi, 0)) - 1u;
+  const uint32_t skip = lo >= 32 ? 0xffffffffu : (1u << max(lo, 0)) - 1u;
+  return below & ~skip;
+}
+
+// 32 fp32 accumulator columns of this warp's 32 rows to bf16 rows in memory, by
+// way of the warp's staging block (64-byte rows whose 16-byte units change
+// places with the row, so that neither side meets a bank twice); row_at(r) is
+// where columns 0.. of row r go, or null.
+template <typename RowAt>
+__device__ __forceinline__ void store_columns(uint32_t taddr, float f, uint8_t* stage, int lane, RowAt row_at) {
+  uint32_t x[32];
+  tmem_ld32(taddr, x);
+  tmem_ld_wait(x);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(__uint_as_float(x[8 * v + 2 * e]) * f, __uint_as_float(x[8 * v + 2 * e + 1]) * f);
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 8 * j + (lane >> 2), v = lane & 3;
+    const uint4 val = *reinterpret_cast<const uint4*>(stage + r * 64 + ((v ^ ((r >> 1) & 3)) * 16));
+    __nv_bfloat16* to = row_at(r);
+    if (to != nullptr) *reinterpret_cast<uint4*>(to + v * 8) = val;
+  }
+  __syncwarp();  // the block is read back before it is written again
+}
+
+// The CTA's barriers and tensor memory, the item records, and the TMA warp's
+// loop, which the two kernels share: kKeys: K and V resident, Q and dO streamed.
+template <int D, bool kKeys>
+struct Frame {
+  using C = Cfg<D>;
+  uint8_t* smem;
+  uint32_t base, tmem;
+  volatile int* abort_flag;
+
+  __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBarOff + 8u * i; }
+  __device__ __forceinline__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(smem + C::kMiscOff); }
+  __device__ __forceinline__ Item* items() const { return reinterpret_cast<Item*>(smem + C::kItemOff); }
+  __device__ __forceinline__ uint8_t* ring(int st, int which) const {
+    return smem + C::kRingOff + (2 * st + which) * C::kTileBytes;
+  }
+  __device__ __forceinline__ float* stats(int st) const { return reinterpret_cast<float*>(smem + C::kStatOff + st * 1024); }
+
+  __device__ __forceinline__ void open(uint8_t* raw, const PackedShape& s) {
+    const uint32_t raw_u32 = smem_u32(raw);
+    base = (raw_u32 + 1023u) & ~1023u;
+    smem = raw + (base - raw_u32);
+    abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    if (threadIdx.x == 0) {
+      mbar_init(bar(C::kBarResFull), 1);
+      mbar_init(bar(C::kBarResFree), 1);
+      for (int i = 0; i < C::kStages; ++i) {
+        mbar_init(bar(C::kBarLoad + i), 1);
+        mbar_init(bar(C::kBarReady + i), 1);
+        mbar_init(bar(C::kBarEmpty + i), 1);
+      }
+      mbar_init(bar(C::kBarS), 1);
+      mbar_init(bar(C::kBarDp), 1);
+      mbar_init(bar(C::kBarP), kComputeWarps);
+      mbar_init(bar(C::kBarDs), kComputeWarps);
+      mbar_init(bar(C::kBarDsFree), 1);
+      mbar_init(bar(C::kBarFinal), 1);
+      for (int i = 0; i < kItems; ++i) {
+        mbar_init(bar(C::kBarItemFull + i), 1);
+        mbar_init(bar(C::kBarItemEmpty + i), kComputeWarps + 2);  // and the MMA and helper warps
+      }
+      mbar_init(bar(C::kBarDrain), 1);
+      *abort_flag = 0;
+      mbar_fence_init();
+    }
+    if (warp_id() == kMmaWarp) {
+      tmem_alloc(smem_u32(tmem_slot()), 512);
+      tmem_relinquish();
+    }
+    if (kKeys && s.tpt * s.by_group.G < 128) {
+      // rows that no box of query rows reaches: summed over as the others are
+      for (int i = 0; i < 2 * C::kStages; ++i)
+        zero_rows(smem + C::kRingOff + i * C::kTileBytes, kChunkBytes, C::kChunks, s.tpt * s.by_group.G, 128,
+                  threadIdx.x, kThreads);
+      fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *tmem_slot();
+    grid_dep_wait();
+    grid_dep_launch();
+  }
+
+  // Item number k, for a consuming warp that gives it back with give_item.
+  __device__ __forceinline__ bool get_item(int k) const {
+    return mbar_wait_w(bar(C::kBarItemFull + k % kItems), (k / kItems) & 1, abort_flag);
+  }
+  __device__ __forceinline__ void give_item(int k) const { mbar_arrive_warp(bar(C::kBarItemEmpty + k % kItems)); }
+
+  // Whether stream step t0 + jj of an item is a tile that reaches past the sequence.
+  __device__ __forceinline__ static bool last_tile(const PackedShape& s, const Item& it, int jj) {
+    return (it.t0 + jj + 1) * (kKeys ? s.tpt : kKT) > it.n;
+  }
+
+  // The TMA warp; counts the loads of the resident tiles and of stages that it started.
+  __device__ __forceinline__ void produce(const PackedShape& s, const PackedList& list, const CUtensorMap* res0,
+                                          const CUtensorMap* res1, const CUtensorMap* str0, const CUtensorMap* str1,
+                                          int* status, int* res_loads, int* stage_loads) {
+    ItemQueue queue;
+    queue.start(s, list, status);
+    if (lane_id() != 0) return;
+    tma_prefetch_map(res0);
+    tma_prefetch_map(res1);
+    tma_prefetch_map(str0);
+    tma_prefetch_map(str1);
+    const uint32_t rows_bytes = static_cast<uint32_t>(s.tpt * s.by_group.G * 128 * C::kChunks);
+    const uint32_t res_bytes = 2 * (kKeys ? C::kTileBytes : rows_bytes), str_bytes = 2 * (kKeys ? rows_bytes : C::kTileBytes);
+    bool ok = true;
+    int g = 0, q = 0;
+    PackedEntry e;
+    int h;
+    while (ok && queue.take(&e, &h)) {
+      const int x1 = min(e.i0 + list.unit, e.n);
+      const TileRange r = kKeys ? rows_of(s, e.n, e.i0, x1) : keys_of(s, e.n, e.i0, x1);
+      const Item it{0, e.row0, e.n, h, e.i0, r.lo, r.n, 0};
+      if (q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
+      if (!ok) break;
+      items()[q % kItems] = it;
+      mbar_arrive(bar(C::kBarItemFull + q % kItems));
+      if (q > 0) ok = mbar_wait(bar(C::kBarResFree), (q - 1) & 1, abort_flag);
+      if (!ok) break;
+      mbar_arrive_expect_tx(bar(C::kBarResFull), res_bytes);
+      for (int c = 0; c < C::kChunks; ++c) {
+        tma_load_4d(base + C::kResOff + c * kChunkBytes, res0, bar(C::kBarResFull), c * 64, 0, h, e.row0 + e.i0);
+        tma_load_4d(base + C::kResOff + C::kTileBytes + c * kChunkBytes, res1, bar(C::kBarResFull), c * 64, 0, h,
+                    e.row0 + e.i0);
+      }
+      *res_loads = ++q;
+      for (int jj = 0; jj < it.ns && ok; ++jj, ++g) {
+        const int st = g % C::kStages;
+        if (g >= C::kStages) ok = mbar_wait(bar(C::kBarEmpty + st), (g / C::kStages - 1) & 1, abort_flag);
+        if (!ok) break;
+#ifdef FA_TEST_SKIP_ARRIVE
+        // Test-only build (never in libfa.so): the first item's last tiles are
+        // never loaded and nothing more is, so the bounded waits for them run
+        // out and the CTA winds down through the abort path.
+        if (jj == it.ns - 1) {
+          ok = false;
+          break;
+        }
+#endif
+        const uint32_t full = bar(C::kBarLoad + st);
+        mbar_arrive_expect_tx(full, str_bytes);
+        const int row = e.row0 + (it.t0 + jj) * (kKeys ? s.tpt : kKT);
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_4d(smem_u32(ring(st, 0)) + c * kChunkBytes, str0, full, c * 64, 0, h, row);
+          tma_load_4d(smem_u32(ring(st, 1)) + c * kChunkBytes, str1, full, c * 64, 0, h, row);
+        }
+        *stage_loads = g + 1;
+      }
+    }
+    if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
+    if (ok) {
+      items()[q % kItems].end = 1;
+      mbar_arrive(bar(C::kBarItemFull + q % kItems));
+    }
+  }
+
+  __device__ __forceinline__ void close(int res_loads, int stage_loads, int* status) {
+    tc_fence_before();
+    __syncthreads();
+    if (warp_id() == kLoadWarp && lane_id() == 0 && *abort_flag) {
+      // Every role has stopped, so the flag is final: let every copy this
+      // thread started land before the CTA exits (only the last load of each
+      // buffer can still be pending).
+      if (res_loads > 0) mbar_wait(bar(C::kBarResFull), (res_loads - 1) & 1, nullptr);
+      for (int i = max(stage_loads - C::kStages, 0); i < stage_loads; ++i)
+        mbar_wait(bar(C::kBarLoad + i % C::kStages), (i / C::kStages) & 1, nullptr);
+    }
+    if (warp_id() == kMmaWarp) {
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicExch(status, kStatusTimeout);
+  }
+};
+
+// ---------------------------------------------------------------- dK, dV
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
+                      const __grid_constant__ BwdArgs args) {
+  using C = Cfg<D>;
+  constexpr int kS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const PackedShape& sh = args.s;
+  const int G = sh.by_group.G;
+  Frame<D, true> f;
+  f.open(smem_raw, sh);
+  volatile int* abort_flag = f.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  int res_loads = 0, stage_loads = 0;
+
+  if (warp == kLoadWarp) {
+    f.produce(sh, args.list, &tmK, &tmV, &tmQ, &tmDo, args.status, &res_loads, &stage_loads);
+  } else if (warp == kHelpWarp) {
+    // ------------------------------------------------------------ statistics
+    // Each step's 128 LSE (log2 units) and D; rows that are none get P = 0.
+    bool ok = true;
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const Item it = f.items()[q % kItems];
+      f.give_item(q);
+      for (int jj = 0; jj < it.ns; ++jj, ++g) {
+        const int st = g % kS, i0 = (it.t0 + jj) * sh.tpt, cnt = min(sh.tpt, it.n - i0);
+        const long long first = static_cast<long long>(it.row0 + i0) * sh.Hq + it.h * G;
+        float l[4], d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i, x = sh.by_group.div(r);
+          l[i] = INFINITY;
+          d[i] = 0.f;
+          if (x < cnt) {
+            const long long at = first + static_cast<long long>(x) * sh.Hq + (r - x * G);
+            l[i] = args.lse[at] * kLog2e;
+            d[i] = args.D[at];
+          }
+        }
+        if (g >= kS) ok = mbar_wait_w(f.bar(C::kBarEmpty + st), (g / kS - 1) & 1, abort_flag);
+        if (!ok) break;
+        float* stat = f.stats(st);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          stat[lane + 32 * i] = l[i];
+          stat[128 + lane + 32 * i] = d[i];
+        }
+        if (Frame<D, true>::last_tile(sh, it, jj)) {
+          ok = mbar_wait_w(f.bar(C::kBarLoad + st), (g / kS) & 1, abort_flag);
+          if (!ok) break;
+          zero_rows(f.ring(st, 0), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
+          zero_rows(f.ring(st, 1), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
+          fence_async_smem();
+        }
+        mbar_arrive_warp(f.bar(C::kBarReady + st));
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t kIdS = idesc_bf16_f32(kKT, 128, false, false);
+    constexpr uint32_t kIdA = idesc_bf16_f32(kKT, D, false, true);
+    const uint64_t dK0 = sdesc_sw128(f.base + C::kResOff, 16, 1024);
+    const uint64_t dV0 = sdesc_sw128(f.base + C::kResOff + C::kTileBytes, 16, 1024);
+    const uint64_t dR0 = sdesc_sw128(f.base + C::kRingOff, 16, 1024);            // Q, dO by rows
+    const uint64_t dT0 = sdesc_sw128(f.base + C::kRingOff, kChunkBytes, 1024);   // and by columns
+    const uint32_t tmem = f.tmem;
+    bool ok = true;
+    // S^T = K Q^T (which = 0) or dP^T = V dO^T (1) for stream step g
+    auto issue_s = [&](int which, int g) {
+      const uint64_t a = which ? dV0 : dK0;
+      const uint64_t b = dR0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
+        mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
+    };
+    // dV (+)= P^T dO (which = 1) or dK (+)= dS^T Q (0); the operand's queries
+    // 0..63 lie in the first 32 of its columns, 64..127 from column 64 on
+    auto issue_a = [&](int which, int g, bool first) {
+      const uint64_t b = dT0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
+      const uint32_t col = which ? C::kColS : C::kColDp;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts_w(tmem + C::kColA + which * D, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8, b + 128 * kk, kIdA,
+                 (!first || kk > 0) ? 1u : 0u);
+    };
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const int ns = f.items()[q % kItems].ns;
+      f.give_item(q);
+      ok = mbar_wait_w(f.bar(C::kBarResFull), q & 1, abort_flag);
+      auto tiles_ready = [&](int gs) {
+        if (ok) ok = mbar_wait_w(f.bar(C::kBarLoad + gs % kS), (gs / kS) & 1, abort_flag);
+        if (ok) ok = mbar_wait_w(f.bar(C::kBarReady + gs % kS), (gs / kS) & 1, abort_flag);
+        tc_fence_after();
+      };
+      tiles_ready(g);
+      if (!ok) break;
+      issue_s(0, g);
+      issue_s(1, g);
+      if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
+      for (int jj = 0; jj < ns; ++jj) {
+        const int gs = g + jj;
+        ok = mbar_wait_w(f.bar(C::kBarP), gs & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        issue_a(1, gs, jj == 0);
+        if (jj + 1 < ns) {
+          tiles_ready(gs + 1);
+          if (!ok) break;
+          issue_s(0, gs + 1);
+        }
+        ok = mbar_wait_w(f.bar(C::kBarDs), gs & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        issue_a(0, gs, jj == 0);
+        mma_commit_w(f.bar(C::kBarEmpty + gs % kS));
+        if (jj + 1 < ns) {
+          issue_s(1, gs + 1);
+          // K and V are free once the item's last S^T and dP^T have completed
+          if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+        } else {
+          mma_commit_w(f.bar(C::kBarFinal));
+        }
+      }
+      g += ns;
+    }
+    // Let every MMA this warp issued finish before TMEM is released.
+    mma_commit_w(f.bar(C::kBarDrain));
+    mbar_wait_w(f.bar(C::kBarDrain), 0, nullptr);
+  } else {
+    // ------------------------------------------------------------ P and dS
+    const int wg = warp / 4, row = threadIdx.x & 127;  // the group's queries are 64 wg .. 64 wg + 63
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * 64;
+    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * 64;
+    uint8_t* stage = f.smem + C::kOutOff + warp * kStageOut;
+    const float sl2 = args.scale_log2;
+    bool ok = true;
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const Item& it = f.items()[q % kItems];
+      const int ns = it.ns, k0 = it.x0;
+      int i0 = it.t0 * sh.tpt;
+      for (int jj = 0; jj < ns; ++jj, ++g, i0 += sh.tpt) {
+        const int st = g % kS;
+        const float* stat = f.stats(st) + wg * 64;
+        // queries of this key: [k0 + row, k0 + row + window)
+        const bool cut = (sh.causal && i0 < k0 + kKT - 1) || (sh.window > 0 && i0 + sh.tpt > k0 + sh.window);
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        if (cut) {
+          const int lo = sh.causal ? min(max(k0 + row - i0, 0), 128) * G - wg * 64 : 0;
+          const int hi = sh.window > 0 ? min(max(k0 + row - i0 + sh.window, 0), 128) * G - wg * 64 : 64;
+          seen[0] = bits_between(lo, hi);
+          seen[1] = bits_between(lo - 32, hi - 32);
+        }
+        ok = mbar_wait_w(f.bar(C::kBarReady + st), (g / kS) & 1, abort_flag);
+        if (ok) ok = mbar_wait_w(f.bar(C::kBarS), g & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[2][32];
+        tmem_ld32(tS, sr[0]);
+        tmem_ld32(tS + 32, sr[1]);
+        tmem_ld_wait(sr[0]);
+        tmem_ld_wait(sr[1]);
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(stat + c);
+          p[c] = ex2(fmaf(__uint_as_float(sr[c >> 5][c & 31]), sl2, -l.x));
+          p[c + 1] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 1) & 31]), sl2, -l.y));
+          p[c + 2] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 2) & 31]), sl2, -l.z));
+          p[c + 3] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 3) & 31]), sl2, -l.w));
+        }
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((seen[c >> 5] >> (c & 31)) & 1u)) p[c] = 0.f;
+        }
+        {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+          tmem_st32(tS, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(f.bar(C::kBarP));
+        ok = mbar_wait_w(f.bar(C::kBarDp), g & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[32], pk[16];
+          tmem_ld32(tDp + 32 * h, x);
+          tmem_ld_wait(x);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(stat + 128 + 32 * h + c);
+            const float dd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[32 * h + c + e] *= __uint_as_float(x[c + e]) - dd[e];
+          }
+          if (cut) {  // (where a query is not seen, dP may be anything)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((seen[h] >> c) & 1u)) p[32 * h + c] = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[32 * h + 2 * c], p[32 * h + 2 * c + 1]);
+          tmem_st16(tDp + 16 * h, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(f.bar(C::kBarDs));
+      }
+      if (!ok) break;
+      // the first warpgroup writes dK, the second dV; the next item's first
+      // products into them wait for both groups' next P
+      ok = mbar_wait_w(f.bar(C::kBarFinal), q & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int first = k0 + (warp & 3) * 32, n = it.n;
+      const long long stride = args.out_stride[wg];
+      __nv_bfloat16* out = args.out[wg] + static_cast<long long>(it.row0 + first) * stride + it.h * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32)
+        store_columns(f.tmem + lane_base + C::kColA + wg * D + c, wg == 0 ? args.scale : 1.f, stage, lane,
+                      [&](int r) { return first + r < n ? out + r * stride + c : nullptr; });
+      tc_fence_before();
+      f.give_item(q);
+    }
+  }
+  f.close(res_loads, stage_loads, args.status);
+}
+
+// ---------------------------------------------------------------- dQ
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ BwdArgs args) {
+  using C = Cfg<D>;
+  constexpr int kS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const PackedShape& sh = args.s;
+  const int G = sh.by_group.G;
+  Frame<D, false> f;
+  f.open(smem_raw, sh);
+  volatile int* abort_flag = f.abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  int res_loads = 0, stage_loads = 0;
+
+  if (warp == kLoadWarp) {
+    f.produce(sh, args.list, &tmQ, &tmDo, &tmK, &tmV, args.status, &res_loads, &stage_loads);
+  } else if (warp == kHelpWarp) {
+    // ------------------------------------------------------------ keys past a sequence
+    bool ok = true;
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const Item it = f.items()[q % kItems];
+      f.give_item(q);
+      for (int jj = 0; jj < it.ns; ++jj, ++g) {
+        const int st = g % kS;
+        ok = mbar_wait_w(f.bar(C::kBarLoad + st), (g / kS) & 1, abort_flag);
+        if (!ok) break;
+        if (Frame<D, false>::last_tile(sh, it, jj)) {
+          zero_rows(f.ring(st, 0), kChunkBytes, C::kChunks, it.n - (it.t0 + jj) * kKT, kKT, lane, 32);
+          fence_async_smem();
+        }
+        mbar_arrive_warp(f.bar(C::kBarReady + st));
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, kKT, false, false);
+    constexpr uint32_t kIdA = idesc_bf16_f32(128, D, false, true);
+    const uint64_t dQ0 = sdesc_sw128(f.base + C::kResOff, 16, 1024);
+    const uint64_t dO0 = sdesc_sw128(f.base + C::kResOff + C::kTileBytes, 16, 1024);
+    const uint64_t dR0 = sdesc_sw128(f.base + C::kRingOff, 16, 1024);            // K, V by rows
+    const uint64_t dT0 = sdesc_sw128(f.base + C::kRingOff, kChunkBytes, 1024);   // K by columns
+    const uint32_t tmem = f.tmem;
+    bool ok = true;
+    // S = Q K^T and dP = dO V^T for stream step g
+    auto issue_s = [&](int g) {
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const uint64_t a = which ? dO0 : dQ0;
+        const uint64_t b = dR0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
+          mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
+      }
+    };
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const int ns = f.items()[q % kItems].ns;
+      f.give_item(q);
+      ok = mbar_wait_w(f.bar(C::kBarResFull), q & 1, abort_flag);
+      auto tiles_ready = [&](int gs) {
+        if (ok) ok = mbar_wait_w(f.bar(C::kBarLoad + gs % kS), (gs / kS) & 1, abort_flag);
+        if (ok) ok = mbar_wait_w(f.bar(C::kBarReady + gs % kS), (gs / kS) & 1, abort_flag);
+        tc_fence_after();
+      };
+      tiles_ready(g);
+      // the last step's S and dP are in registers: their columns are free
+      if (ok && g > 0) ok = mbar_wait_w(f.bar(C::kBarP), (g - 1) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(g);
+      if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
+      for (int jj = 0; jj < ns; ++jj) {
+        const int gs = g + jj;
+        if (jj + 1 < ns) {
+          tiles_ready(gs + 1);
+          if (ok) ok = mbar_wait_w(f.bar(C::kBarP), gs & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(gs + 1);
+          if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+        }
+        ok = mbar_wait_w(f.bar(C::kBarDs), gs & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        // dQ (+)= dS K
+        const uint64_t b = dT0 + static_cast<uint64_t>((2 * (gs % kS) * C::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(tmem + C::kColA, tmem + C::kColDs + kk * 8, b + 128 * kk, kIdA, (jj > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(f.bar(C::kBarEmpty + gs % kS));
+        mma_commit_w(f.bar(C::kBarDsFree));
+      }
+      g += ns;
+    }
+    // Let every MMA this warp issued finish before TMEM is released.
+    mma_commit_w(f.bar(C::kBarDrain));
+    mbar_wait_w(f.bar(C::kBarDrain), 0, nullptr);
+  } else {
+    // ------------------------------------------------------------ dS
+    const int wg = warp / 4, r = threadIdx.x & 127, ri = sh.by_group.div(r);  // the group's keys are 64 wg .. 64 wg + 63
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * 64;
+    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * 64;
+    const uint32_t tDs = f.tmem + lane_base + C::kColDs + wg * 32;
+    uint8_t* stage = f.smem + C::kOutOff + warp * kStageOut;
+    const float sl2 = args.scale_log2;
+    bool ok = true;
+    int g = 0;
+    for (int q = 0; ok; ++q) {
+      ok = f.get_item(q);
+      if (!ok || f.items()[q % kItems].end) break;
+      const Item& it = f.items()[q % kItems];
+      const int ns = it.ns, n = it.n, i0 = it.x0, pos = i0 + ri;
+      float l = INFINITY, d = 0.f;
+      if (ri < sh.tpt && pos < n) {
+        const long long at = static_cast<long long>(it.row0 + pos) * sh.Hq + it.h * G + (r - ri * G);
+        l = args.lse[at] * kLog2e;
+        d = args.D[at];
+      }
+      const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive
+      const int key_lo = sh.window > 0 ? pos - sh.window + 1 : 0;
+      const int full_hi = sh.causal ? i0 : n - 1;
+      const int full_lo = sh.window > 0 ? min(i0 + sh.tpt, n) - sh.window : 0;
+      int key0 = it.t0 * kKT;
+      for (int jj = 0; jj < ns; ++jj, ++g, key0 += kKT) {
+        ok = mbar_wait_w(f.bar(C::kBarS), g & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[2][32];
+        tmem_ld32(tS, sr[0]);
+        tmem_ld32(tS + 32, sr[1]);
+        tmem_ld_wait(sr[0]);
+        tmem_ld_wait(sr[1]);
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(sr[c >> 5][c & 31]), sl2, -l));
+        ok = mbar_wait_w(f.bar(C::kBarDp), g & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(tDp, sr[0]);
+        tmem_ld32(tDp + 32, sr[1]);
+        tmem_ld_wait(sr[0]);
+        tmem_ld_wait(sr[1]);
+        tc_fence_before();
+        mbar_arrive_warp(f.bar(C::kBarP));  // S and dP may be overwritten
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(sr[c >> 5][c & 31]) - d;
+        if (key0 + kKT - 1 > full_hi || key0 < full_lo) {
+          const int hi = key_hi - key0 - wg * 64, lo = key_lo - key0 - wg * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t seen = bits_between(lo - 32 * h, hi - 32 * h);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((seen >> c) & 1u)) p[32 * h + c] = 0.f;
+          }
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+        if (g > 0) ok = mbar_wait_w(f.bar(C::kBarDsFree), (g - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st32(tDs, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(f.bar(C::kBarDs));
+      }
+      if (!ok) break;
+      // dQ, once the last product has been added: columns [wg D / 2, (wg + 1) D
+      // / 2). The next item's first product waits for both groups' next dS.
+      ok = mbar_wait_w(f.bar(C::kBarDsFree), (g - 1) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int tile_row = (warp & 3) * 32;
+      const long long stride = args.out_stride[0];
+      __nv_bfloat16* out = args.out[0] + static_cast<long long>(it.row0 + i0) * stride + it.h * G * D;
+#pragma unroll 1
+      for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 32)
+        store_columns(f.tmem + lane_base + C::kColA + c, args.scale, stage, lane, [&](int wr) {
+          const int x = sh.by_group.div(tile_row + wr);
+          return x < sh.tpt && i0 + x < n ? out + x * stride + (tile_row + wr - x * G) * D + c : nullptr;
+        });
+      tc_fence_before();
+      f.give_item(q);
+    }
+  }
+  f.close(res_loads, stage_loads, args.status);
+}
+
+// ---------------------------------------------------------------- launches
+// The workspace: D, then the two lists where they are made.
+struct BwdPlan {
+  int slots;
+  int cap[2], unit[2];  // dK and dV; dQ
+  bool listed[2];
+  size_t head[2];       // offsets
+  size_t bytes;
+};
+
+BwdPlan bwd_plan(int B, int T, int Hq, int Hkv, int sms) {
+  BwdPlan p;
+  p.slots = sms;
+  p.unit[0] = kKT;
+  p.unit[1] = 128 / (Hq / Hkv);
+  p.bytes = (static_cast<size_t>(T) * Hq * 4 + 255) / 256 * 256;
+  for (int i = 0; i < 2; ++i) {
+    p.cap[i] = T / p.unit[i] + B;
+    p.listed[i] = static_cast<long long>(p.cap[i]) * Hkv > p.slots;
+    p.head[i] = p.bytes;
+    if (p.listed[i]) p.bytes += (sizeof(PackedHead) + static_cast<size_t>(p.cap[i]) * sizeof(int4) + 255) / 256 * 256;
+  }
+  return p;
+}
+
+template <int D>
+int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[2], float* rowsum, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const PackedProblem& p = b.p;
+  const PackedShape& s = p.s;
+  const int G = s.by_group.G;
+  int* status = device_status_word();
+  CUtensorMap mq, mk, mv, mo;
+  if (!status || !make_map_packed(&mq, p.q, s.T, s.Hkv, G, D, p.q_stride, s.tpt) ||
+      !make_map_packed(&mk, p.k, s.T, s.Hkv, 1, D, p.k_stride, kKT) ||
+      !make_map_packed(&mv, p.v, s.T, s.Hkv, 1, D, p.v_stride, kKT) ||
+      !make_map_packed(&mo, b.dO, s.T, s.Hkv, G, D, b.do_stride, s.tpt))
+    return -3;
+  const auto dkv = packed_dkv_kernel<D>;
+  const auto dq = packed_dq_kernel<D>;
+  // attribute slots 32 to 35 (the other kernels use 0-31)
+  constexpr int kSlot = D == 64 ? 32 : 34;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(dkv), C::kSmemBytes, kSlot) ||
+      !ensure_smem_attr(reinterpret_cast<const void*>(dq), C::kSmemBytes, kSlot + 1))
+    return -3;
+  const long long rows = static_cast<long long>(s.T) * s.Hq, per = 256 / (D / 8) * 4;
+  cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
+                                    0, stream, static_cast<const __nv_bfloat16*>(b.o),
+                                    static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, rowsum, rows,
+                                    GroupDiv::of(s.Hq));
+  if (e != cudaSuccess) return -3;
+  BwdArgs a{};
+  a.s = s;
+  a.lse = b.lse;
+  a.D = rowsum;
+  a.status = status;
+  a.scale = p.scale;
+  const float sl2 = p.scale * kLog2e;
+  a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  auto grid = [&](int i) { return dim3(plan.listed[i] ? plan.slots : plan.cap[i] * s.Hkv); };
+  a.list = lists[0];
+  a.out[0] = static_cast<__nv_bfloat16*>(b.dk);
+  a.out[1] = static_cast<__nv_bfloat16*>(b.dv);
+  a.out_stride[0] = b.dk_stride;
+  a.out_stride[1] = b.dv_stride;
+  e = launch_overlapped(dkv, grid(0), dim3(kThreads), C::kSmemBytes, stream, mk, mv, mq, mo, a);
+  if (e != cudaSuccess) return -3;
+  a.list = lists[1];
+  a.out[0] = static_cast<__nv_bfloat16*>(b.dq);
+  a.out_stride[0] = b.dq_stride;
+  e = launch_overlapped(dq, grid(1), dim3(kThreads), C::kSmemBytes, stream, mq, mo, mk, mv, a);
+  return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;
+}
+
+}  // namespace
+
+size_t packed_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int sms) { return bwd_plan(B, T, Hq, Hkv, sms).bytes; }
+
+int launch_packed_bwd(const PackedBwd& b, void* workspace, cudaStream_t stream) {
+  const PackedShape& s = b.p.s;
+  const int sms = device_sm_count();
+  if (sms <= 0) return -3;
+  const BwdPlan plan = bwd_plan(s.B, s.T, s.Hq, s.Hkv, sms);
+  PackedList lists[2];
+  for (int i = 0; i < 2; ++i) {
+    lists[i] = PackedList{nullptr, nullptr, plan.cap[i], plan.unit[i], i == 0 ? 1 : 0};
+    if (plan.listed[i]) {
+      lists[i].head = reinterpret_cast<PackedHead*>(static_cast<char*>(workspace) + plan.head[i]);
+      lists[i].entries = reinterpret_cast<int4*>(lists[i].head + 1);
+    }
+  }
+  const int rc = launch_packed_plan(s, lists, 2, stream);
+  if (rc != 0) return rc;
+  float* rowsum = static_cast<float*>(workspace);
+  return b.p.d == 64 ? launch_d<64>(b, plan, lists, rowsum, stream) : launch_d<128>(b, plan, lists, rowsum, stream);
+}
+
+}  // namespace fa

@@ -139,6 +139,41 @@ PyObject* packed_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// packed_bwd(q, k, v, o, lse, do, cu, causal, window, scale, dq, dk, dv, workspace) -> (dq, dk, dv)
+PyObject* packed_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 14) refuse(PyExc_TypeError, "packed_bwd takes 14 arguments");
+  const Packed p = packed_args(args[0], args[1], args[2], args[6]);
+  const at::Tensor &o = tensor(args[3], "o"), &l = tensor(args[4], "lse"), &g = tensor(args[5], "do");
+  check_rows(o, "o", p.T, p.Hq, p.d, p.device);
+  if (!o.is_contiguous()) refuse(PyExc_ValueError, "o must be contiguous");
+  const float* lp = statistic(l, "lse", p.T, p.Hq, p.device);
+  const int64_t gs = check_rows(g, "do", p.T, p.Hq, p.d, p.device);
+  const int causal = PyObject_IsTrue(args[7]);
+  const long long window = PyLong_AsLongLong(args[8]);
+  const double scale = scale_of(args[9], p.d);
+  if (PyErr_Occurred()) return nullptr;
+  int64_t dqs, dks, dvs;
+  at::Tensor dq = rows_out(args[10], "dq", p.T, p.Hq, p.d, p.device, &dqs),
+             dk = rows_out(args[11], "dk", p.T, p.Hkv, p.d, p.device, &dks),
+             dv = rows_out(args[12], "dv", p.T, p.Hkv, p.d, p.device, &dvs), ws;
+  size_t bytes;
+  void* wp = scratch(args[13], args[13] == Py_None ? fa_packed_bwd_workspace_bytes(p.b, p.t, p.hq, p.hkv, p.dd) : 0,
+                     p.device, &ws, &bytes);
+  const void *op = o.data_ptr(), *gp = g.data_ptr();
+  void *dqp = dq.data_ptr(), *dkp = dk.data_ptr(), *dvp = dv.data_ptr();
+  void* stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(p.device)).stream();
+  const int w = small(window, "window");
+  int code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = fa_packed_bwd(p.q, p.qs, p.k, p.ks, p.v, p.vs, op, lp, gp, gs, p.cu, p.b, p.t, p.hq, p.hkv, p.dd, causal, w,
+                       static_cast<float>(scale), dqp, dqs, dkp, dks, dvp, dvs, wp, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  if (failed(code, "fa_packed_bwd")) return nullptr;
+  return tuple_of(output(args[10], dq), output(args[11], dk), output(args[12], dv));
+  END_HANDLE_TH_ERRORS
+}
+
 // rope(q, k or None, positions, cos, sin, axis_of (bytes), interleaved, inverse, q_out, k_out) -> (q_out, k_out or None)
 PyObject* rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS

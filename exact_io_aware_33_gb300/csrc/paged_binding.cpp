@@ -185,6 +185,7 @@ PyMethodDef g_methods[] = {
     {"attn", fast(guarded<attn>), METH_FASTCALL, "fa_paged_attn on checked tensors"},
     {"append", fast(guarded<append>), METH_FASTCALL, "fa_paged_append on checked tensors"},
     {"packed_fwd", fast(guarded<packed_fwd>), METH_FASTCALL, "fa_packed_fwd on checked tensors"},
+    {"packed_bwd", fast(guarded<packed_bwd>), METH_FASTCALL, "fa_packed_bwd on checked tensors"},
     {"rope", fast(guarded<rope>), METH_FASTCALL, "fa_rope_axes on checked tensors"},
     {"set_fail", set_fail, METH_O, "the callable that raises a return code"},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,11 +1,14 @@
-"""Packed sequences: attention with grouped heads, and rotary positions with several axes.
+"""Packed sequences: attention with grouped heads and its gradients, and rotary positions with several axes.
 
-Bindings of ``fa_rope_axes`` and ``fa_packed_fwd`` (``include/fa.h`` states the operators). The rows of a call's
-sequences lie one after another in tensors [T, heads, d], which may be slices of a fused projection; ``cu``
-(int32 [B + 1], on the device) marks where each sequence begins:
+Bindings of ``fa_rope_axes``, ``fa_packed_fwd`` and ``fa_packed_bwd`` (``include/fa.h`` states the operators). The rows
+of a call's sequences lie one after another in tensors [T, heads, d], which may be slices of a fused projection; ``cu``
+(int32 [B + 1], on the device) marks where each sequence begins. A layer's step and its gradients:
 
     q, k = fa.fa_rope_axes(q, k, positions, (cos, sin), sections=(16, 24, 24))
     o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True)
+
+    dq, dk, dv = fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True)
+    dq, dk = fa.fa_rope_axes(dq, dk, positions, (cos, sin), sections=(16, 24, 24), inverse=True)
 
 All tensors of a call must be on one device, which need not be the current one. With ``stream`` the work
 is queued there and outputs belong to that stream; tensors of other streams must be ready, and kept, by
@@ -88,3 +91,23 @@ def fa_packed_fwd(q, k, v, cu, causal: bool = False, window: int = 0, scale: flo
         with _elsewhere(q, stream):
             return fa_packed_fwd(q, k, v, cu, causal, window, scale, out, lse, workspace)
     return native.packed_fwd(q, k, v, cu, causal, window, scale, out, lse, workspace)
+
+
+def fa_packed_bwd_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    """Workspace bytes of fa_packed_bwd for B sequences in T rows."""
+    if _paged._native is None:
+        _paged._load()
+    return _paged._lib.fa_packed_bwd_workspace_bytes(B, T, Hq, Hkv, d)
+
+
+def fa_packed_bwd(q, k, v, o, lse, do, cu, causal: bool = False, window: int = 0, scale: float | None = None,
+                  dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of fa_packed_fwd, given its results ``o`` and ``lse``; (dq, dk, dv), bf16.
+
+    ``dq``, ``dk`` and ``dv`` may be slices of the gradient of a fused projection. Rows of new ones outside
+    the sequences are not written."""
+    native = _ready(q, stream)
+    if native is None:
+        with _elsewhere(q, stream):
+            return fa_packed_bwd(q, k, v, o, lse, do, cu, causal, window, scale, dq, dk, dv, workspace)
+    return native.packed_bwd(q, k, v, o, lse, do, cu, causal, window, scale, dq, dk, dv, workspace)

@@ -430,6 +430,29 @@ int fa_packed_fwd(const void* q, long long q_stride, const void* k, long long k_
 size_t fa_packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d);
 
 /*
+ * Gradients of fa_packed_fwd, by recomputation as in fa_bwd.
+ *   q, k, v, cu, causal, window, scale, sizes : as the forward got them
+ *   o, lse  : in,  the forward's results: bf16 [T, Hq, d] and fp32 [T, Hq], contiguous
+ *   dO      : in,  bf16 [T, Hq, d], rows do_stride elements apart
+ *   dq      : out, bf16 [T, Hq, d], rows dq_stride elements apart (slices of
+ *             the gradient of a fused projection are fine, for dk and dv too)
+ *   dk, dv  : out, bf16 [T, Hkv, d]: sums over the query heads that read the
+ *             key head, added up in fp32
+ *   workspace : at least fa_packed_bwd_workspace_bytes(...) bytes, 256-byte
+ *             aligned, as for the forward
+ * Outputs must not meet an input or each other (FA_ERR_INVALID); rows outside
+ * the sequences are left as they were. No sum's order depends on timing: the
+ * same inputs give the same bits. Otherwise as fa_packed_fwd, the device's
+ * checks included.
+ */
+int fa_packed_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const void* o, const float* lse, const void* dO, long long do_stride,
+                  const int* cu, int B, int T, int Hq, int Hkv, int d, int causal, int window, float scale,
+                  void* dq, long long dq_stride, void* dk, long long dk_stride, void* dv, long long dv_stride,
+                  void* workspace, size_t ws_bytes, void* cuda_stream);
+size_t fa_packed_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d);
+
+/*
  * Rotary positions with several axes (time, height and width of the patches
  * of a film, say): turns queries and keys of packed rows. The pages have no
  * counterpart.

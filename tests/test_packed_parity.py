@@ -1,4 +1,4 @@
-"""Packed sequences on the GPU: fa_rope_axes and fa_packed_fwd against the float64 oracle.
+"""Packed sequences on the GPU: fa_rope_axes, fa_packed_fwd and fa_packed_bwd against the float64 oracle.
 
 Tolerances, derived from the arithmetic:
 
@@ -7,6 +7,11 @@ Tolerances, derived from the arithmetic:
   sum_j p_j |v_j|). Float32 sums of S err by at most 128 * 2^-24 sum_c |q_c k_c|, below 2^-11 in the exponent here
   (sum |q_c k_c| scale <= 64), and exponentials and sums by less than 2^-12: together below 2^-10 A.
   Bound: 2^-8 |o| + (2^-8 + 2^-10) A.
+* gradients, of the same o and lse on both sides: one rounding to bf16 (2^-8 of the value); P and dS rounded to bf16
+  (2^-8 of each) and P's own error from S (below 2^-10 of it, as above): (2^-8 + 2^-10) A with A the sum of the
+  absolute terms, sum P |dO| for dV and scale sum |dS| |k| or |q| for dQ and dK; and dP - D, whose 128-term float32 sums
+  err by at most 2^-17 of the sums of their absolute terms each: 2^-16 B with B = scale sum P (|dO| |v| + |dO| |o|) |k|
+  or |q|.
 * lse: the error of S enters it unchanged: 128 * 2^-24 * 64 = 4.9e-4 at the very most. Bound: 5e-4.
 """
 
@@ -341,3 +346,211 @@ def test_packed_fwd_captured_with_new_borders_and_on_a_stream(lens):
     done()
     assert torch.equal(a, b)
     check_fwd(rows, o, lse, True, 0.125, 0)
+
+
+# ------------------------------------------------------------------ gradients
+def check_bwd(rows, o, lse, do, grads, causal, scale, window, which=None):
+    cu, G = rows.cu, rows.G
+    q, k, v = f64(rows.q, rows.k, rows.v)
+    o, lse, do = f64(o, lse, do)
+    got = dict(zip(("dq", "dk", "dv"), f64(*grads)))
+    for b in range(len(cu) - 1) if which is None else which:
+        at, n = slice(cu[b], cu[b + 1]), cu[b + 1] - cu[b]
+        if n == 0:
+            continue
+        want = dict(zip(("dq", "dk", "dv"), packed.backward(q[at], k[at], v[at], o[at], lse[at], do[at], np.array([0, n]),
+                                                            causal, scale, window)))
+        bound = {x: 2.0 ** -8 * np.abs(want[x]) for x in want}
+        far = np.arange(n)[:, None] - np.arange(n)
+        seen = ((far >= 0) if causal else True) & ((far < window) if window else True)
+        for h in range(rows.Hq):
+            qh, kh, vh, oh, dh = q[at, h], k[at, h // G], v[at, h // G], o[at, h], do[at, h]
+            p = np.where(seen, np.exp(np.where(seen, scale * (qh @ kh.T) - lse[at, h][:, None], 0)), 0)
+            ds = np.abs(p * (dh @ vh.T - (dh * oh).sum(-1)[:, None]))
+            off = p * (np.abs(dh) @ np.abs(vh).T + (np.abs(dh) * np.abs(oh)).sum(-1)[:, None])
+            each = scale * ((2.0 ** -8 + 2.0 ** -10) * ds + 2.0 ** -16 * off)
+            bound["dq"][:, h] += each @ np.abs(kh)
+            bound["dk"][:, h // G] += each.T @ np.abs(qh)
+            bound["dv"][:, h // G] += (2.0 ** -8 + 2.0 ** -10) * (p.T @ np.abs(dh))
+        for x in want:
+            err = np.abs(got[x][at] - want[x])
+            assert (err <= bound[x]).all(), (b, x, (err / np.maximum(bound[x], 1e-300)).max())
+
+
+def forward_for(rows, causal, scale, window):
+    """The forward's results, from the oracle, where there are sequences; NaN elsewhere."""
+    o, lse = packed.forward(*f64(rows.q, rows.k, rows.v), rows.cu, causal, scale, window)
+    return torch.from_numpy(o).to(torch.bfloat16), torch.from_numpy(lse).float()
+
+
+BWD = [
+    # lens, Hq, Hkv, d, causal, window
+    ([1], 1, 1, 64, True, 0),
+    ([1], 2, 1, 128, False, 0),
+    ([1, 2, 127, 128, 129], 2, 2, 128, True, 0),
+    ([255, 256, 257, 0, 3], 1, 1, 64, True, 0),
+    ([255, 256, 257, 0, 3], 2, 1, 64, False, 0),
+    ([300, 41], 8, 2, 128, True, 0),
+    ([300, 41], 6, 2, 128, False, 0),
+    ([77, 513], 10, 2, 64, True, 0),
+    ([130, 64], 14, 2, 128, True, 0),
+    ([45], 71, 1, 64, True, 0),
+    ([19, 20], 128, 1, 128, False, 0),
+    ([200, 300], 4, 4, 64, True, 1),
+    ([500, 129, 700], 4, 2, 128, True, 130),
+    ([500, 129, 700], 3, 1, 64, True, 200),
+    ([640], 2, 2, 128, True, 127),
+    ([640], 2, 2, 64, True, 2 ** 31 - 1),
+    ([1100], 8, 1, 128, True, 400),
+    ([1000, 700], 3, 3, 64, False, 0),
+    ([3, 1, 4, 1, 5, 9, 2, 6] * 60, 2, 2, 64, True, 0),
+    ([33, 0, 100, 7] * 60, 4, 2, 128, True, 0),
+    ([33, 0, 100, 7] * 60, 4, 2, 64, False, 0),
+    ([1200, 1, 900, 129], 12, 4, 128, True, 0),
+    ([1200, 1, 900, 129], 8, 4, 64, True, 300),
+]
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,causal,window", BWD)
+def test_packed_bwd(lens, Hq, Hkv, d, causal, window):
+    rows = Rows(lens, Hq, Hkv, d, seed=sum(lens) + Hq + d, lead=3 if len(lens) > 2 else 0, trail=5)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, causal, scale, window)
+    wide = randn(rows.rng, rows.T, Hq * d + 64)
+    wide[~torch.from_numpy(rows.inside)] = float("nan")
+    do = wide[:, :Hq * d].view(rows.T, Hq, d)
+    (q, k, v), cu = rows.on_gpu()
+    args = (q, k, v, o.cuda(), lse.cuda(), wide.cuda()[:, :Hq * d].view(rows.T, Hq, d), cu)
+    # into one gradient of the projection that q, k and v are slices of
+    whole = torch.full_like(rows.whole, 7).cuda()
+    outs = rows.views(whole)
+    got = fa.fa_packed_bwd(*args, causal=causal, window=window, dq=outs[0], dk=outs[1], dv=outs[2])
+    done()
+    assert all(a is b for a, b in zip(got, outs))
+    check_bwd(rows, o, lse, do, got, causal, scale, window)
+    assert (whole[torch.from_numpy(~rows.inside).cuda()] == 7).all() and (whole[:, -8:] == 7).all()
+    again = fa.fa_packed_bwd(*args, causal=causal, window=window)
+    done()
+    inside = torch.from_numpy(rows.inside).cuda()
+    for a, b in zip(again, got):
+        assert torch.equal(a[inside], b[inside])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 4), (128, 1), (128, 3)])
+def test_packed_bwd_what_is_not_finite_stays_in_its_sequence(d, G, causal):
+    rows = Rows([100, 60, 200, 90, 300], 2 * G, 2, d, seed=d + G, lead=2, trail=4)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, causal, scale, 0)
+    do = randn(rows.rng, rows.T, 2 * G, d)
+    for b, bad in ((1, float("nan")), (3, float("inf"))):
+        at = slice(int(rows.cu[b]), int(rows.cu[b + 1]))
+        for x in (rows.whole, o, lse, do):
+            x[at] = bad
+    (q, k, v), cu = rows.on_gpu()
+    got = fa.fa_packed_bwd(q, k, v, o.cuda(), lse.cuda(), do.cuda(), cu, causal=causal)
+    done()
+    check_bwd(rows, o, lse, do, got, causal, scale, 0, which=(0, 2, 4))
+    assert all(x[rows.cu[1]:rows.cu[2]].isnan().all() for x in got)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_packed_bwd_against_differences(d):
+    """The loss sum(o dO) of the GPU's own forward, along a direction, against the GPU's gradients.
+
+    Both ends of a difference carry o's rounding and P's (2^-8 of o at most each, so of o's size a deviation of 2^-8 /
+    sqrt(3) each, independent over the elements): the difference deviates by 2 * 2^-8 / sqrt(3) norm(o dO). Six of these;
+    and 2^-6 of the norm of the gradient's terms for their own roundings (2^-7) and the third derivative: a step of h in
+    each channel moves a score by about h, and h^2 / 6 < 2^-10."""
+    rows = Rows([90, 200], 4, 2, d, seed=d)
+    do = randn(rows.rng, rows.T, 4, d).cuda()
+    (q, k, v), cu = rows.on_gpu()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True)
+    grads = fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True)
+    done()
+    h = 1 / 16
+    for i, x in enumerate((q, k, v)):
+        step = randn(rows.rng, *x.shape).cuda().sign() * h
+        ends = [(x.float() + s * step.float()).to(torch.bfloat16) for s in (1, -1)]
+        moved = (ends[0].double() - ends[1].double())
+        loss = []
+        for e in ends:
+            args = [q, k, v]
+            args[i] = e
+            loss.append(float((fa.fa_packed_fwd(*args, cu, causal=True)[0].double() * do.double()).sum()))
+        got, want = loss[0] - loss[1], float((grads[i].double() * moved).sum())
+        noise = 2 * 2.0 ** -8 / math.sqrt(3) * float((o.double() * do.double()).norm())
+        size = float((grads[i].double() * moved).norm())
+        assert abs(got - want) <= 6 * noise + 2.0 ** -6 * size, (i, got, want, noise, size)
+
+
+def test_packed_bwd_borders_out_of_range_are_reported():
+    rows = Rows([50, 60], 2, 2, 64, seed=4)
+    (q, k, v), _ = rows.on_gpu()
+    o, lse = (x.cuda() for x in forward_for(rows, True, 0.125, 0))
+    for bad in ([0, 50, 200], [-4, 50, 110], [0, 60, 50], [0, 110] * 200):
+        fa.fa_packed_bwd(q, k, v, o, lse, o, torch.tensor(bad, dtype=torch.int32, device="cuda"), causal=True)
+        done(fa.FA_ERR_INDEX)
+
+
+def test_packed_bwd_of_nothing():
+    q = torch.ones(300, 2, 64, dtype=torch.bfloat16, device="cuda")
+    lse, out = torch.zeros(300, 2, device="cuda"), [torch.full_like(q, 3) for _ in range(3)]
+    for B in (3, 700):
+        cu = torch.full((B + 1,), 9, dtype=torch.int32, device="cuda")
+        fa.fa_packed_bwd(q, q, q, q, lse, q, cu, dq=out[0], dk=out[1], dv=out[2])
+        done()
+        assert all((x == 3).all() for x in out)
+    e = q[:0]
+    assert all(x.shape == (0, 2, 64) for x in fa.fa_packed_bwd(e, e, e, e, lse[:0], e, cu))
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,Hq,Hkv,window", [(64, 6, 2, 0), (128, 8, 2, 50)])
+def test_a_layer_and_its_gradients_in_one_graph(d, Hq, Hkv, window):
+    """Rotation, attention and both backwards on slices of one projection, eagerly, then captured and replayed with
+    other lengths and inputs."""
+    lens = [70, 1, 0, 190, 33]
+    rows = Rows(lens, Hq, Hkv, d, seed=d)
+    half = d // 2
+    cos, sin = tables(64, half)
+    sections = (half // 4, half // 4, half // 2)
+    axis_of = [a for a, m in enumerate(sections) for _ in range(m)]
+    pos = rows.rng.integers(0, 64, (3, rows.T)).astype(np.int32)
+    whole, posg, cu = rows.whole.cuda(), torch.from_numpy(pos).cuda(), torch.from_numpy(rows.cu).cuda()
+    rope = (torch.from_numpy(cos).cuda(), torch.from_numpy(sin).cuda())
+    do = randn(rows.rng, rows.T, Hq, d).cuda()
+    back = torch.zeros_like(whole)
+    q, k, v = rows.views(whole)
+    dq, dk, dv = rows.views(back)
+
+    def layer():
+        a, b = fa.fa_rope_axes(q, k, posg, rope, sections=sections)
+        o, lse = fa.fa_packed_fwd(a, b, v, cu, causal=True, window=window)
+        fa.fa_packed_bwd(a, b, v, o, lse, do, cu, causal=True, window=window, dq=dq, dk=dk, dv=dv)
+        fa.fa_rope_axes(dq, dk, posg, rope, sections=sections, inverse=True, q_out=dq, k_out=dk)
+        return a, b, o, lse
+
+    def check(a, b, o, lse):
+        done()
+        now = Rows.__new__(Rows)
+        now.__dict__.update(rows.__dict__)
+        now.q, now.k, now.v = (x.cpu() for x in (a, b, v))
+        check_fwd(now, o, lse, True, 1 / math.sqrt(d), window)
+        turned = [want_rope(x.cpu(), pos, axis_of, cos, sin, False, False) for x in (q, k)]
+        assert torch.equal(a.cpu(), turned[0]) and torch.equal(b.cpu(), turned[1])
+        grads = fa.fa_packed_bwd(a, b, v, o, lse, do, cu, causal=True, window=window)
+        check_bwd(now, o, lse, do, grads, True, 1 / math.sqrt(d), window)
+        assert torch.equal(dq.cpu(), want_rope(grads[0].cpu(), pos, axis_of, cos, sin, False, True))
+        assert torch.equal(dk.cpu(), want_rope(grads[1].cpu(), pos, axis_of, cos, sin, False, True))
+        assert torch.equal(dv, grads[2])
+
+    check(*layer())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = layer()
+    rows.cu[1:-1] = np.sort(rows.rng.integers(0, rows.T, len(lens) - 1))
+    cu.copy_(torch.from_numpy(rows.cu))
+    whole.copy_(randn(rows.rng, *whole.shape))
+    g.replay()
+    check(*outs)

@@ -35,6 +35,21 @@
 // memory, and two exponentials per pair.
 
 #include "fa_packed.cuh"
+#ifndef FA_WAIT
+#define FA_WAIT mbar_wait_w
+#endif
+#ifndef FA_WAITH
+#define FA_WAITH mbar_wait_w
+#endif
+#ifndef FA_ORDER
+#define FA_ORDER 1
+#endif
+#ifndef FA_G_DKV
+#define FA_G_DKV 4
+#endif
+#ifndef FA_G_DQ
+#define FA_G_DQ 4
+#endif
 
 namespace fa {
 namespace {
@@ -42,9 +57,6 @@ namespace {
 constexpr int kKT = kKeyTile;  // keys per tile; also rows per tile of query rows
 constexpr int kItems = 4;      // item records kept
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 bf16, 128-byte swizzled
-constexpr int kComputeWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
-constexpr int kThreads = 32 * 11;
-constexpr int kStageOut = 2048;  // staging per compute warp: 32 rows x 32 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
 // An item, left by the TMA warp.
@@ -68,38 +80,57 @@ struct BwdArgs {
   float scale, scale_log2;
 };
 
-template <int D>
+template <int D, bool kKeys>
 struct Cfg {
+  static constexpr int kGroups = kKeys ? FA_G_DKV : FA_G_DQ;            // compute warpgroups
+  static constexpr int kCols = 128 / kGroups;   // columns of S and dP that each takes
+  static constexpr int kWords = kCols / 32;
+  static constexpr int kComputeWarps = 4 * kGroups;
+  static constexpr int kMmaWarp = kComputeWarps, kSumWarp = kMmaWarp + 1, kLoadWarp = kMmaWarp + 2,
+                       kHelpWarp = kMmaWarp + 3;
+  static constexpr int kThreads = 32 * (kComputeWarps + 4);
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kStages = D == 64 ? 3 : 2;
+  // stages of the streamed pair, Q and dO (dK, dV) or K and V (dQ): what there is room for
+  static constexpr int kStages0 = D == 64 ? 4 : kKeys ? 2 : 3, kStages1 = D == 64 ? 4 : 2;
   static constexpr int kResOff = 0;  // resident pair of tiles: K and V, or Q and dO
-  static constexpr int kRingOff = 2 * kTileBytes;  // stages of a pair: Q and dO, or K and V
-  static constexpr int kOutOff = kRingOff + kStages * 2 * kTileBytes;
-  static constexpr int kStatOff = kOutOff + kComputeWarps * kStageOut;  // per stage: 128 LSE, 128 D (dK, dV)
-  static constexpr int kItemOff = kStatOff + kStages * 1024;
+  static constexpr int kRing0 = 2 * kTileBytes, kRing1 = kRing0 + kStages0 * kTileBytes;
+  static constexpr int kStatOff = kRing1 + kStages1 * kTileBytes;  // dK, dV: per stage 128 -LSE, 128 -D
+  static constexpr int kOutOff = kStatOff + (kKeys ? kStages0 * 1024 : 0);
+  static constexpr bool kStaged = kKeys || D == 64;  // write-back by way of 2 KiB per compute warp (dQ, d = 128: no room)
+  static constexpr int kItemOff = kOutOff + (kStaged ? kComputeWarps * 2048 : 0);
   static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
+  // P and dS have columns of their own, so that S and dP are computed by one
+  // warp's issue and used by another's, neither waiting for the other's order.
+  // (dK, dV at d = 128: no room; one warp issues all products in a fixed order.)
+  static constexpr bool kApart = D == 64 || !kKeys;
+  static constexpr int kIssuers = kApart ? 2 : 1;
   enum : int {
     kBarResFull = 0,
     kBarResFree = 1,
-    kBarLoad = 2,                      // a stage's tiles have landed
-    kBarReady = kBarLoad + kStages,    // the helper is done with the stage
-    kBarEmpty = kBarReady + kStages,
-    kBarS = kBarEmpty + kStages,
+    kBarLoad0 = 2,                        // a stage's tile has landed
+    kBarEmpty0 = kBarLoad0 + kStages0,    // and is not needed any more
+    kBarReady = kBarEmpty0 + kStages0,    // the helper is done with the step
+    kBarLoad1 = kBarReady + kStages0,
+    kBarEmpty1 = kBarLoad1 + kStages1,
+    kBarS = kBarEmpty1 + kStages1,
     kBarDp,
-    kBarP,      // dK, dV: P is written; dQ: S and dP are in registers
-    kBarDs,     // dS is written
-    kBarDsFree, // dQ: dS has been read
+    kBarSFree,   // S is in registers (dQ; dK, dV where P is apart)
+    kBarDpFree,  // dP is
+    kBarP,       // P is written
+    kBarPFree,   // and has been read (P apart)
+    kBarDs,      // dS is written
+    kBarDsFree,  // and has been read (dQ; dS apart)
     kBarFinal,
     kBarItemFull,
     kBarItemEmpty = kBarItemFull + kItems,
-    kBarDrain = kBarItemEmpty + kItems,
-    kNumBars
+    kBarDrain = kBarItemEmpty + kItems,  // two
+    kNumBars = kBarDrain + 2
   };
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;  // + slack to align the base
+  static constexpr int kSmemBytes = kMiscOff + 16;
   static constexpr uint32_t kColS = 0, kColDp = 128, kColA = 256;  // then dK and dV; or dQ
-  static constexpr uint32_t kColDs = 448;                          // dQ: 64 columns
+  [[maybe_unused]] static constexpr uint32_t kColP = 384, kColDs = 448;             // 64 columns each, where they are apart
   static_assert(kSmemBytes <= 232448, "tiles exceed shared memory");
   static_assert(kItemOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
 };
@@ -152,9 +183,11 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
 }
 
 // 32 fp32 accumulator columns of this warp's 32 rows to bf16 rows in memory, by
-// way of the warp's staging block (64-byte rows whose 16-byte units change
-// places with the row, so that neither side meets a bank twice); row_at(r) is
-// where columns 0.. of row r go, or null.
+// way of the warp's staging block: 64-byte rows, whose 16-byte units change
+// places with the row, so that neither side meets a bank twice. Four lanes then
+// write a row's 64 bytes; straight from registers an instruction would touch 32
+// lines (4000 cycles an item at d = 64, dK and dV). row_at(r): where the columns
+// of row r go, or null.
 template <typename RowAt>
 __device__ __forceinline__ void store_columns(uint32_t taddr, float f, uint8_t* stage, int lane, RowAt row_at) {
   uint32_t x[32];
@@ -179,11 +212,38 @@ __device__ __forceinline__ void store_columns(uint32_t taddr, float f, uint8_t* 
   __syncwarp();  // the block is read back before it is written again
 }
 
+// 16 columns of this thread's row straight to memory, or nowhere (to == nullptr). All of a warp together.
+__device__ __forceinline__ void store_direct(uint32_t taddr, float f, __nv_bfloat16* to) {
+  uint32_t x[16];
+  tmem_ld16(taddr, x);
+  tmem_ld_wait(x);
+  if (to == nullptr) return;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(__uint_as_float(x[8 * v + 2 * e]) * f, __uint_as_float(x[8 * v + 2 * e + 1]) * f);
+    *reinterpret_cast<uint4*>(to + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Makes x[c] zero where bit c of `keep` is not set.
+__device__ __forceinline__ void keep_bits(float2* x, uint32_t keep) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    if (!((keep >> (2 * c)) & 1u)) x[c].x = 0.f;
+    if (!((keep >> (2 * c + 1)) & 1u)) x[c].y = 0.f;
+  }
+}
+
+__device__ __forceinline__ float2 pair(const uint32_t* x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); }
+
 // The CTA's barriers and tensor memory, the item records, and the TMA warp's
 // loop, which the two kernels share: kKeys: K and V resident, Q and dO streamed.
 template <int D, bool kKeys>
 struct Frame {
-  using C = Cfg<D>;
+  using C = Cfg<D, kKeys>;
   uint8_t* smem;
   uint32_t base, tmem;
   volatile int* abort_flag;
@@ -191,47 +251,70 @@ struct Frame {
   __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBarOff + 8u * i; }
   __device__ __forceinline__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(smem + C::kMiscOff); }
   __device__ __forceinline__ Item* items() const { return reinterpret_cast<Item*>(smem + C::kItemOff); }
-  __device__ __forceinline__ uint8_t* ring(int st, int which) const {
-    return smem + C::kRingOff + (2 * st + which) * C::kTileBytes;
+  __device__ __forceinline__ uint8_t* ring0(int g) const { return smem + C::kRing0 + g % C::kStages0 * C::kTileBytes; }
+  __device__ __forceinline__ uint8_t* ring1(int g) const { return smem + C::kRing1 + g % C::kStages1 * C::kTileBytes; }
+  // Waits of stream step g on the barriers of its stages.
+  __device__ __forceinline__ bool landed0(int g) const { return at_step(C::kBarLoad0, C::kStages0, g); }
+  __device__ __forceinline__ bool landed1(int g) const { return at_step(C::kBarLoad1, C::kStages1, g); }
+  __device__ __forceinline__ bool ready(int g) const { return at_step(C::kBarReady, C::kStages0, g); }
+  __device__ __forceinline__ bool empty0(int g) const { return g < C::kStages0 || at_step(C::kBarEmpty0, C::kStages0, g - C::kStages0); }
+  __device__ __forceinline__ bool at_step(int b, int stages, int g) const {
+    return FA_WAIT(bar(b + g % stages), (g / stages) & 1, abort_flag);
   }
-  __device__ __forceinline__ float* stats(int st) const { return reinterpret_cast<float*>(smem + C::kStatOff + st * 1024); }
+  __device__ __forceinline__ bool readyc(int g) const {
+    return patient(bar(C::kBarReady + g % C::kStages0), (g / C::kStages0) & 1);
+  }
+  __device__ __forceinline__ bool waitc(int b, int g) const { return patient(bar(b), g & 1); }
+  __device__ __forceinline__ bool patient(uint32_t b, uint32_t parity) const {
+    return D == 64 ? mbar_wait_w(b, parity, abort_flag) : mbar_wait_sleep_w(b, parity, abort_flag);
+  }
+  __device__ __forceinline__ bool landedh0(int g) const {
+    return FA_WAITH(bar(C::kBarLoad0 + g % C::kStages0), (g / C::kStages0) & 1, abort_flag);
+  }
+  __device__ __forceinline__ bool emptyh0(int g) const {
+    return g < C::kStages0 || FA_WAITH(bar(C::kBarEmpty0 + g % C::kStages0), (g / C::kStages0 - 1) & 1, abort_flag);
+  }
+  // The g-th phase of a barrier that has one per step.
+  __device__ __forceinline__ bool wait(int b, int g) const { return FA_WAIT(bar(b), g & 1, abort_flag); }
+  __device__ __forceinline__ float* stats(int g) const {
+    return reinterpret_cast<float*>(smem + C::kStatOff + g % C::kStages0 * 1024);
+  }
 
   __device__ __forceinline__ void open(uint8_t* raw, const PackedShape& s) {
-    const uint32_t raw_u32 = smem_u32(raw);
-    base = (raw_u32 + 1023u) & ~1023u;
-    smem = raw + (base - raw_u32);
+    base = smem_u32(raw);  // 1 KiB aligned, as the array is declared (there is no room to align it here)
+    smem = raw;
     abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     if (threadIdx.x == 0) {
       mbar_init(bar(C::kBarResFull), 1);
       mbar_init(bar(C::kBarResFree), 1);
-      for (int i = 0; i < C::kStages; ++i) {
-        mbar_init(bar(C::kBarLoad + i), 1);
-        mbar_init(bar(C::kBarReady + i), 1);
-        mbar_init(bar(C::kBarEmpty + i), 1);
-      }
+      for (int i = C::kBarLoad0; i < C::kBarS; ++i) mbar_init(bar(i), 1);
       mbar_init(bar(C::kBarS), 1);
       mbar_init(bar(C::kBarDp), 1);
-      mbar_init(bar(C::kBarP), kComputeWarps);
-      mbar_init(bar(C::kBarDs), kComputeWarps);
+      mbar_init(bar(C::kBarSFree), C::kComputeWarps);
+      mbar_init(bar(C::kBarDpFree), C::kComputeWarps);
+      mbar_init(bar(C::kBarP), C::kComputeWarps);
+      mbar_init(bar(C::kBarPFree), 1);
+      mbar_init(bar(C::kBarDs), C::kComputeWarps);
       mbar_init(bar(C::kBarDsFree), 1);
       mbar_init(bar(C::kBarFinal), 1);
       for (int i = 0; i < kItems; ++i) {
         mbar_init(bar(C::kBarItemFull + i), 1);
-        mbar_init(bar(C::kBarItemEmpty + i), kComputeWarps + 2);  // and the MMA and helper warps
+        mbar_init(bar(C::kBarItemEmpty + i), C::kComputeWarps + C::kIssuers + 1);  // and the helper warp
       }
       mbar_init(bar(C::kBarDrain), 1);
+      mbar_init(bar(C::kBarDrain + 1), 1);
       *abort_flag = 0;
       mbar_fence_init();
     }
-    if (warp_id() == kMmaWarp) {
+    if (warp_id() == C::kMmaWarp) {
       tmem_alloc(smem_u32(tmem_slot()), 512);
       tmem_relinquish();
     }
     if (kKeys && s.tpt * s.by_group.G < 128) {
       // rows that no box of query rows reaches: summed over as the others are
-      for (int i = 0; i < 2 * C::kStages; ++i)
-        zero_rows(smem + C::kRingOff + i * C::kTileBytes, kChunkBytes, C::kChunks, s.tpt * s.by_group.G, 128,
-                  threadIdx.x, kThreads);
+      for (int i = 0; i < C::kStages0 + C::kStages1; ++i)
+        zero_rows(smem + C::kRing0 + i * C::kTileBytes, kChunkBytes, C::kChunks, s.tpt * s.by_group.G, 128,
+                  threadIdx.x, C::kThreads);
       fence_async_smem();
     }
     tc_fence_before();
@@ -256,7 +339,7 @@ struct Frame {
   // The TMA warp; counts the loads of the resident tiles and of stages that it started.
   __device__ __forceinline__ void produce(const PackedShape& s, const PackedList& list, const CUtensorMap* res0,
                                           const CUtensorMap* res1, const CUtensorMap* str0, const CUtensorMap* str1,
-                                          int* status, int* res_loads, int* stage_loads) {
+                                          int* status, int* res_loads, int (&stage_loads)[2]) {
     ItemQueue queue;
     queue.start(s, list, status);
     if (lane_id() != 0) return;
@@ -265,7 +348,7 @@ struct Frame {
     tma_prefetch_map(str0);
     tma_prefetch_map(str1);
     const uint32_t rows_bytes = static_cast<uint32_t>(s.tpt * s.by_group.G * 128 * C::kChunks);
-    const uint32_t res_bytes = 2 * (kKeys ? C::kTileBytes : rows_bytes), str_bytes = 2 * (kKeys ? rows_bytes : C::kTileBytes);
+    const uint32_t res_bytes = 2 * (kKeys ? C::kTileBytes : rows_bytes), str_bytes = kKeys ? rows_bytes : C::kTileBytes;
     bool ok = true;
     int g = 0, q = 0;
     PackedEntry e;
@@ -288,26 +371,25 @@ struct Frame {
       }
       *res_loads = ++q;
       for (int jj = 0; jj < it.ns && ok; ++jj, ++g) {
-        const int st = g % C::kStages;
-        if (g >= C::kStages) ok = mbar_wait(bar(C::kBarEmpty + st), (g / C::kStages - 1) & 1, abort_flag);
-        if (!ok) break;
-#ifdef FA_TEST_SKIP_ARRIVE
-        // Test-only build (never in libfa.so): the first item's last tiles are
-        // never loaded and nothing more is, so the bounded waits for them run
-        // out and the CTA winds down through the abort path.
-        if (jj == it.ns - 1) {
-          ok = false;
-          break;
-        }
-#endif
-        const uint32_t full = bar(C::kBarLoad + st);
-        mbar_arrive_expect_tx(full, str_bytes);
         const int row = e.row0 + (it.t0 + jj) * (kKeys ? s.tpt : kKT);
-        for (int c = 0; c < C::kChunks; ++c) {
-          tma_load_4d(smem_u32(ring(st, 0)) + c * kChunkBytes, str0, full, c * 64, 0, h, row);
-          tma_load_4d(smem_u32(ring(st, 1)) + c * kChunkBytes, str1, full, c * 64, 0, h, row);
-        }
-        *stage_loads = g + 1;
+        auto load = [&](int w, int load_bar, int empty_bar, int stages, uint8_t* to) {
+          if (g >= stages) ok = mbar_wait(bar(empty_bar + g % stages), (g / stages - 1) & 1, abort_flag);
+#ifdef FA_TEST_SKIP_ARRIVE
+          // Test-only build (never in libfa.so): the first item's last tile (Q, or
+          // K) is never loaded and nothing more is, so the bounded waits for it
+          // run out and the CTA winds down through the abort path.
+          if (w == 0 && jj == it.ns - 1) ok = false;
+#endif
+          if (!ok) return;
+          const uint32_t full = bar(load_bar + g % stages);
+          mbar_arrive_expect_tx(full, str_bytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_load_4d(smem_u32(to) + c * kChunkBytes, w == 0 ? str0 : str1, full, c * 64, 0, h, row);
+          stage_loads[w] = g + 1;
+        };
+        if (FA_ORDER) load(1, C::kBarLoad1, C::kBarEmpty1, C::kStages1, ring1(g));
+        if (ok) load(0, C::kBarLoad0, C::kBarEmpty0, C::kStages0, ring0(g));
+        if (ok && !FA_ORDER) load(1, C::kBarLoad1, C::kBarEmpty1, C::kStages1, ring1(g));
       }
     }
     if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
@@ -317,18 +399,26 @@ struct Frame {
     }
   }
 
-  __device__ __forceinline__ void close(int res_loads, int stage_loads, int* status) {
+  // Lets every MMA that an issuing warp issued finish, before TMEM is released.
+  __device__ __forceinline__ void drain(int which) const {
+    mma_commit_w(bar(C::kBarDrain + which));
+    mbar_wait_w(bar(C::kBarDrain + which), 0, nullptr);
+  }
+
+  __device__ __forceinline__ void close(int res_loads, const int (&stage_loads)[2], int* status) {
     tc_fence_before();
     __syncthreads();
-    if (warp_id() == kLoadWarp && lane_id() == 0 && *abort_flag) {
+    if (warp_id() == C::kLoadWarp && lane_id() == 0 && *abort_flag) {
       // Every role has stopped, so the flag is final: let every copy this
       // thread started land before the CTA exits (only the last load of each
       // buffer can still be pending).
       if (res_loads > 0) mbar_wait(bar(C::kBarResFull), (res_loads - 1) & 1, nullptr);
-      for (int i = max(stage_loads - C::kStages, 0); i < stage_loads; ++i)
-        mbar_wait(bar(C::kBarLoad + i % C::kStages), (i / C::kStages) & 1, nullptr);
+      for (int i = max(stage_loads[0] - C::kStages0, 0); i < stage_loads[0]; ++i)
+        mbar_wait(bar(C::kBarLoad0 + i % C::kStages0), (i / C::kStages0) & 1, nullptr);
+      for (int i = max(stage_loads[1] - C::kStages1, 0); i < stage_loads[1]; ++i)
+        mbar_wait(bar(C::kBarLoad1 + i % C::kStages1), (i / C::kStages1) & 1, nullptr);
     }
-    if (warp_id() == kMmaWarp) {
+    if (warp_id() == C::kMmaWarp) {
       __syncwarp();
       tc_fence_after();
       tmem_dealloc(tmem, 512);
@@ -339,26 +429,26 @@ struct Frame {
 
 // ---------------------------------------------------------------- dK, dV
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, true>::kThreads, 1)
     packed_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                       const __grid_constant__ BwdArgs args) {
-  using C = Cfg<D>;
-  constexpr int kS = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
+  using F = Frame<D, true>;
+  using C = typename F::C;
+  constexpr int kGroups = C::kGroups, kCols = C::kCols, kWords = C::kWords;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const PackedShape& sh = args.s;
   const int G = sh.by_group.G;
-  Frame<D, true> f;
+  F f;
   f.open(smem_raw, sh);
-  volatile int* abort_flag = f.abort_flag;
   const int warp = warp_id(), lane = lane_id();
-  int res_loads = 0, stage_loads = 0;
+  int res_loads = 0, stage_loads[2] = {0, 0};
 
-  if (warp == kLoadWarp) {
-    f.produce(sh, args.list, &tmK, &tmV, &tmQ, &tmDo, args.status, &res_loads, &stage_loads);
-  } else if (warp == kHelpWarp) {
+  if (warp == C::kLoadWarp) {
+    f.produce(sh, args.list, &tmK, &tmV, &tmQ, &tmDo, args.status, &res_loads, stage_loads);
+  } else if (warp == C::kHelpWarp) {
     // ------------------------------------------------------------ statistics
-    // Each step's 128 LSE (log2 units) and D; rows that are none get P = 0.
+    // Each step's 128 -LSE (log2 units) and -D; rows that are none get P = 0.
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -367,52 +457,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = f.items()[q % kItems];
       f.give_item(q);
       for (int jj = 0; jj < it.ns; ++jj, ++g) {
-        const int st = g % kS, i0 = (it.t0 + jj) * sh.tpt, cnt = min(sh.tpt, it.n - i0);
+        const int i0 = (it.t0 + jj) * sh.tpt, cnt = min(sh.tpt, it.n - i0);
         const long long first = static_cast<long long>(it.row0 + i0) * sh.Hq + it.h * G;
         float l[4], d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = lane + 32 * i, x = sh.by_group.div(r);
-          l[i] = INFINITY;
+          l[i] = -INFINITY;
           d[i] = 0.f;
           if (x < cnt) {
             const long long at = first + static_cast<long long>(x) * sh.Hq + (r - x * G);
-            l[i] = args.lse[at] * kLog2e;
-            d[i] = args.D[at];
+            l[i] = -kLog2e * args.lse[at];
+            d[i] = -args.D[at];
           }
         }
-        if (g >= kS) ok = mbar_wait_w(f.bar(C::kBarEmpty + st), (g / kS - 1) & 1, abort_flag);
+        ok = f.emptyh0(g);
         if (!ok) break;
-        float* stat = f.stats(st);
+        float* stat = f.stats(g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           stat[lane + 32 * i] = l[i];
           stat[128 + lane + 32 * i] = d[i];
         }
-        if (Frame<D, true>::last_tile(sh, it, jj)) {
-          ok = mbar_wait_w(f.bar(C::kBarLoad + st), (g / kS) & 1, abort_flag);
+        if (F::last_tile(sh, it, jj)) {
+          ok = f.landed0(g) && f.landed1(g);
           if (!ok) break;
-          zero_rows(f.ring(st, 0), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
-          zero_rows(f.ring(st, 1), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
+          zero_rows(f.ring0(g), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
+          zero_rows(f.ring1(g), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
           fence_async_smem();
         }
-        mbar_arrive_warp(f.bar(C::kBarReady + st));
+        mbar_arrive_warp(f.bar(C::kBarReady + g % C::kStages0));
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp || (C::kApart && warp == C::kSumWarp)) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kIdS = idesc_bf16_f32(kKT, 128, false, false);
     constexpr uint32_t kIdA = idesc_bf16_f32(kKT, D, false, true);
-    const uint64_t dK0 = sdesc_sw128(f.base + C::kResOff, 16, 1024);
-    const uint64_t dV0 = sdesc_sw128(f.base + C::kResOff + C::kTileBytes, 16, 1024);
-    const uint64_t dR0 = sdesc_sw128(f.base + C::kRingOff, 16, 1024);            // Q, dO by rows
-    const uint64_t dT0 = sdesc_sw128(f.base + C::kRingOff, kChunkBytes, 1024);   // and by columns
+    constexpr uint64_t kTile = C::kTileBytes >> 4;
+    const uint64_t res = sdesc_sw128(f.base + C::kResOff, 16, 1024);
+    const uint64_t rows0 = sdesc_sw128(f.base + C::kRing0, 16, 1024), rows1 = sdesc_sw128(f.base + C::kRing1, 16, 1024);
+    const uint64_t cols0 = sdesc_sw128(f.base + C::kRing0, kChunkBytes, 1024),
+                   cols1 = sdesc_sw128(f.base + C::kRing1, kChunkBytes, 1024);
     const uint32_t tmem = f.tmem;
     bool ok = true;
     // S^T = K Q^T (which = 0) or dP^T = V dO^T (1) for stream step g
     auto issue_s = [&](int which, int g) {
-      const uint64_t a = which ? dV0 : dK0;
-      const uint64_t b = dR0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
+      const uint64_t a = res + (which ? kTile : 0);
+      const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
@@ -420,70 +511,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
     };
-    // dV (+)= P^T dO (which = 1) or dK (+)= dS^T Q (0); the operand's queries
-    // 0..63 lie in the first 32 of its columns, 64..127 from column 64 on
+    // dV (+)= P^T dO (which = 1) or dK (+)= dS^T Q (0); where P and dS are not
+    // apart, each warpgroup's part of them begins where its part of S or dP did
     auto issue_a = [&](int which, int g, bool first) {
-      const uint64_t b = dT0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
-      const uint32_t col = which ? C::kColS : C::kColDp;
+      const uint64_t b = which ? cols1 + g % C::kStages1 * kTile : cols0 + g % C::kStages0 * kTile;
+      const uint32_t col = C::kApart ? (which ? C::kColP : C::kColDs) : which ? C::kColS : C::kColDp;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        mma_ts_w(tmem + C::kColA + which * D, tmem + col + (kk >> 2) * 64 + (kk & 3) * 8, b + 128 * kk, kIdA,
+        mma_ts_w(tmem + C::kColA + which * D,
+                 tmem + col + (C::kApart ? kk * 8 : (kk * 16 / kCols) * kCols + kk * 16 % kCols / 2), b + 128 * kk, kIdA,
                  (!first || kk > 0) ? 1u : 0u);
     };
+    auto ready0 = [&](int g) { return f.landed0(g) && f.ready(g); };
+    auto ready1 = [&](int g) { return f.landed1(g) && f.ready(g); };
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
       if (!ok || f.items()[q % kItems].end) break;
       const int ns = f.items()[q % kItems].ns;
       f.give_item(q);
-      ok = mbar_wait_w(f.bar(C::kBarResFull), q & 1, abort_flag);
-      auto tiles_ready = [&](int gs) {
-        if (ok) ok = mbar_wait_w(f.bar(C::kBarLoad + gs % kS), (gs / kS) & 1, abort_flag);
-        if (ok) ok = mbar_wait_w(f.bar(C::kBarReady + gs % kS), (gs / kS) & 1, abort_flag);
-        tc_fence_after();
-      };
-      tiles_ready(g);
-      if (!ok) break;
-      issue_s(0, g);
-      issue_s(1, g);
-      if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
-      for (int jj = 0; jj < ns; ++jj) {
-        const int gs = g + jj;
-        ok = mbar_wait_w(f.bar(C::kBarP), gs & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        issue_a(1, gs, jj == 0);
-        if (jj + 1 < ns) {
-          tiles_ready(gs + 1);
-          if (!ok) break;
-          issue_s(0, gs + 1);
-        }
-        ok = mbar_wait_w(f.bar(C::kBarDs), gs & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        issue_a(0, gs, jj == 0);
-        mma_commit_w(f.bar(C::kBarEmpty + gs % kS));
-        if (jj + 1 < ns) {
-          issue_s(1, gs + 1);
-          // K and V are free once the item's last S^T and dP^T have completed
-          if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+      if constexpr (C::kApart) {
+        if (warp == C::kMmaWarp) {
+          // S^T and dP^T, each once its predecessor is in registers
+          ok = f.wait(C::kBarResFull, q);
+          for (int jj = 0; jj < ns && ok; ++jj) {
+            const int gs = g + jj;
+            ok = (gs == 0 || f.wait(C::kBarSFree, gs - 1)) && ready0(gs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, gs);
+            ok = (gs == 0 || f.wait(C::kBarDpFree, gs - 1)) && ready1(gs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(1, gs);
+          }
+          if (ok) mma_commit_w(f.bar(C::kBarResFree));
         } else {
-          mma_commit_w(f.bar(C::kBarFinal));
+          // dV and dK; that dS is there says that S^T and dP^T have been computed
+          for (int jj = 0; jj < ns && ok; ++jj) {
+            const int gs = g + jj;
+            ok = ready0(gs) && f.landed1(gs) && f.wait(C::kBarP, gs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_a(1, gs, jj == 0);
+            mma_commit_w(f.bar(C::kBarPFree));
+            ok = f.wait(C::kBarDs, gs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_a(0, gs, jj == 0);
+            mma_commit_w(f.bar(C::kBarDsFree));
+            mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
+            mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
+          }
+          if (ok) mma_commit_w(f.bar(C::kBarFinal));
+        }
+      } else {
+        ok = f.wait(C::kBarResFull, q) && ready0(g);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(0, g);
+        ok = f.landed1(g);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(1, g);
+        if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
+        for (int jj = 0; jj < ns; ++jj) {
+          const int gs = g + jj;
+          ok = f.wait(C::kBarP, gs);
+          if (!ok) break;
+          tc_fence_after();
+          issue_a(1, gs, jj == 0);
+          mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
+          if (jj + 1 < ns) {
+            ok = ready0(gs + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, gs + 1);
+          }
+          ok = f.wait(C::kBarDs, gs);
+          if (!ok) break;
+          tc_fence_after();
+          issue_a(0, gs, jj == 0);
+          mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
+          if (jj + 1 < ns) {
+            ok = f.landed1(gs + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(1, gs + 1);
+            // K and V are free once the item's last S^T and dP^T have completed
+            if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+          } else {
+            mma_commit_w(f.bar(C::kBarFinal));
+          }
         }
       }
       g += ns;
     }
-    // Let every MMA this warp issued finish before TMEM is released.
-    mma_commit_w(f.bar(C::kBarDrain));
-    mbar_wait_w(f.bar(C::kBarDrain), 0, nullptr);
-  } else {
+    f.drain(warp == C::kMmaWarp ? 0 : 1);
+  } else if (warp < C::kComputeWarps) {
     // ------------------------------------------------------------ P and dS
-    const int wg = warp / 4, row = threadIdx.x & 127;  // the group's queries are 64 wg .. 64 wg + 63
+    const int wg = warp / 4, row = threadIdx.x & 127;  // the group's queries are kCols wg .. kCols (wg + 1) - 1
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * 64;
-    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * 64;
-    uint8_t* stage = f.smem + C::kOutOff + warp * kStageOut;
-    const float sl2 = args.scale_log2;
+    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * kCols;
+    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * kCols;
+    const uint32_t tP = C::kApart ? f.tmem + lane_base + C::kColP + wg * kCols / 2 : tS;
+    const uint32_t tDs = C::kApart ? f.tmem + lane_base + C::kColDs + wg * kCols / 2 : tDp;
+    const float2 sl2 = make_float2(args.scale_log2, args.scale_log2);
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -493,89 +626,104 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ns = it.ns, k0 = it.x0;
       int i0 = it.t0 * sh.tpt;
       for (int jj = 0; jj < ns; ++jj, ++g, i0 += sh.tpt) {
-        const int st = g % kS;
-        const float* stat = f.stats(st) + wg * 64;
+        const float* stat = f.stats(g) + wg * kCols;
         // queries of this key: [k0 + row, k0 + row + window)
         const bool cut = (sh.causal && i0 < k0 + kKT - 1) || (sh.window > 0 && i0 + sh.tpt > k0 + sh.window);
-        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+        uint32_t seen[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) seen[w] = 0xffffffffu;
         if (cut) {
-          const int lo = sh.causal ? min(max(k0 + row - i0, 0), 128) * G - wg * 64 : 0;
-          const int hi = sh.window > 0 ? min(max(k0 + row - i0 + sh.window, 0), 128) * G - wg * 64 : 64;
-          seen[0] = bits_between(lo, hi);
-          seen[1] = bits_between(lo - 32, hi - 32);
+          const int lo = sh.causal ? min(max(k0 + row - i0, 0), 128) * G - wg * kCols : 0;
+          const int hi = sh.window > 0 ? min(max(k0 + row - i0 + sh.window, 0), 128) * G - wg * kCols : kCols;
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) seen[w] = bits_between(lo - 32 * w, hi - 32 * w);
         }
-        ok = mbar_wait_w(f.bar(C::kBarReady + st), (g / kS) & 1, abort_flag);
-        if (ok) ok = mbar_wait_w(f.bar(C::kBarS), g & 1, abort_flag);
+        ok = f.readyc(g);
+        if (ok) ok = f.waitc(C::kBarS, g);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[2][32];
-        tmem_ld32(tS, sr[0]);
-        tmem_ld32(tS + 32, sr[1]);
-        tmem_ld_wait(sr[0]);
-        tmem_ld_wait(sr[1]);
-        float p[64];
+        uint32_t x[kWords][32], pk[16];
+        float2 p[kWords][16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(stat + c);
-          p[c] = ex2(fmaf(__uint_as_float(sr[c >> 5][c & 31]), sl2, -l.x));
-          p[c + 1] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 1) & 31]), sl2, -l.y));
-          p[c + 2] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 2) & 31]), sl2, -l.z));
-          p[c + 3] = ex2(fmaf(__uint_as_float(sr[c >> 5][(c + 3) & 31]), sl2, -l.w));
-        }
-        if (cut) {
+        for (int w = 0; w < kWords; ++w) tmem_ld32(tS + 32 * w, x[w]);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((seen[c >> 5] >> (c & 31)) & 1u)) p[c] = 0.f;
+        for (int w = 0; w < kWords; ++w) tmem_ld_wait(x[w]);
+        if constexpr (C::kApart) {
+          tc_fence_before();
+          mbar_arrive_warp(f.bar(C::kBarSFree));
         }
-        {
-          uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
-          tmem_st32(tS, pk);
+        for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(stat + 32 * w + c);
+            const float2 a = __ffma2_rn(pair(x[w] + c), sl2, make_float2(l.x, l.y));
+            const float2 b = __ffma2_rn(pair(x[w] + c + 2), sl2, make_float2(l.z, l.w));
+            p[w][c / 2] = make_float2(ex2(a.x), ex2(a.y));
+            p[w][c / 2 + 1] = make_float2(ex2(b.x), ex2(b.y));
+          }
+          if (cut) keep_bits(p[w], seen[w]);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[w][c].x, p[w][c].y);
+          if constexpr (C::kApart) {
+            if (w == 0 && g > 0) ok = f.waitc(C::kBarPFree, g - 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st16(tP + 16 * w, pk);
         }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(f.bar(C::kBarP));
-        ok = mbar_wait_w(f.bar(C::kBarDp), g & 1, abort_flag);
+        ok = f.waitc(C::kBarDp, g);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[32], pk[16];
-          tmem_ld32(tDp + 32 * h, x);
-          tmem_ld_wait(x);
+        for (int w = 0; w < kWords; ++w) tmem_ld32(tDp + 32 * w, x[w]);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) tmem_ld_wait(x[w]);
+        if constexpr (C::kApart) {
+          tc_fence_before();
+          mbar_arrive_warp(f.bar(C::kBarDpFree));
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(stat + 128 + 32 * h + c);
-            const float dd[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[32 * h + c + e] *= __uint_as_float(x[c + e]) - dd[e];
+            const float4 d = *reinterpret_cast<const float4*>(stat + 128 + 32 * w + c);
+            p[w][c / 2] = __fmul2_rn(p[w][c / 2], __fadd2_rn(pair(x[w] + c), make_float2(d.x, d.y)));
+            p[w][c / 2 + 1] = __fmul2_rn(p[w][c / 2 + 1], __fadd2_rn(pair(x[w] + c + 2), make_float2(d.z, d.w)));
           }
-          if (cut) {  // (where a query is not seen, dP may be anything)
+          if (cut) keep_bits(p[w], seen[w]);  // (where a query is not seen, dP may be anything)
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((seen[h] >> c) & 1u)) p[32 * h + c] = 0.f;
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[w][c].x, p[w][c].y);
+          if constexpr (C::kApart) {
+            if (w == 0 && g > 0) ok = f.waitc(C::kBarDsFree, g - 1);
+            if (!ok) break;
+            tc_fence_after();
           }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[32 * h + 2 * c], p[32 * h + 2 * c + 1]);
-          tmem_st16(tDp + 16 * h, pk);
+          tmem_st16(tDs + 16 * w, pk);
         }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(f.bar(C::kBarDs));
       }
       if (!ok) break;
-      // the first warpgroup writes dK, the second dV; the next item's first
-      // products into them wait for both groups' next P
-      ok = mbar_wait_w(f.bar(C::kBarFinal), q & 1, abort_flag);
+      // the first half of the warpgroups writes dK, the second dV; the next
+      // item's first products into them wait for all groups' next P
+      ok = f.waitc(C::kBarFinal, q);
       if (!ok) break;
       tc_fence_after();
-      const int first = k0 + (warp & 3) * 32, n = it.n;
-      const long long stride = args.out_stride[wg];
-      __nv_bfloat16* out = args.out[wg] + static_cast<long long>(it.row0 + first) * stride + it.h * D;
+      constexpr int kPart = 2 * D / kGroups;  // columns of a group
+      const int first = k0 + (warp & 3) * 32, n = it.n, which = wg / (kGroups / 2), c0 = wg % (kGroups / 2) * kPart;
+      const long long stride = args.out_stride[which];
+      __nv_bfloat16* out = args.out[which] + static_cast<long long>(it.row0 + first) * stride + it.h * D;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32)
-        store_columns(f.tmem + lane_base + C::kColA + wg * D + c, wg == 0 ? args.scale : 1.f, stage, lane,
+      for (int c = c0; c < c0 + kPart; c += 32)
+        store_columns(f.tmem + lane_base + C::kColA + which * D + c, which == 0 ? args.scale : 1.f,
+                      f.smem + C::kOutOff + warp * 2048, lane,
                       [&](int r) { return first + r < n ? out + r * stride + c : nullptr; });
       tc_fence_before();
       f.give_item(q);
@@ -586,25 +734,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- dQ
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, false>::kThreads, 1)
     packed_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ BwdArgs args) {
-  using C = Cfg<D>;
-  constexpr int kS = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
+  using F = Frame<D, false>;
+  using C = typename F::C;
+  constexpr int kGroups = C::kGroups, kCols = C::kCols, kWords = C::kWords;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const PackedShape& sh = args.s;
   const int G = sh.by_group.G;
-  Frame<D, false> f;
+  F f;
   f.open(smem_raw, sh);
-  volatile int* abort_flag = f.abort_flag;
   const int warp = warp_id(), lane = lane_id();
-  int res_loads = 0, stage_loads = 0;
+  int res_loads = 0, stage_loads[2] = {0, 0};
 
-  if (warp == kLoadWarp) {
-    f.produce(sh, args.list, &tmQ, &tmDo, &tmK, &tmV, args.status, &res_loads, &stage_loads);
-  } else if (warp == kHelpWarp) {
+  if (warp == C::kLoadWarp) {
+    f.produce(sh, args.list, &tmQ, &tmDo, &tmK, &tmV, args.status, &res_loads, stage_loads);
+  } else if (warp == C::kHelpWarp) {
     // ------------------------------------------------------------ keys past a sequence
+    // (it takes part in every step: a warp that looked at some phases only could miss one)
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -613,39 +762,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = f.items()[q % kItems];
       f.give_item(q);
       for (int jj = 0; jj < it.ns; ++jj, ++g) {
-        const int st = g % kS;
-        ok = mbar_wait_w(f.bar(C::kBarLoad + st), (g / kS) & 1, abort_flag);
+        ok = f.landedh0(g);
         if (!ok) break;
-        if (Frame<D, false>::last_tile(sh, it, jj)) {
-          zero_rows(f.ring(st, 0), kChunkBytes, C::kChunks, it.n - (it.t0 + jj) * kKT, kKT, lane, 32);
+        if (F::last_tile(sh, it, jj)) {
+          zero_rows(f.ring0(g), kChunkBytes, C::kChunks, it.n - (it.t0 + jj) * kKT, kKT, lane, 32);
           fence_async_smem();
         }
-        mbar_arrive_warp(f.bar(C::kBarReady + st));
+        mbar_arrive_warp(f.bar(C::kBarReady + g % C::kStages0));
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp || warp == C::kSumWarp) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kIdS = idesc_bf16_f32(128, kKT, false, false);
     constexpr uint32_t kIdA = idesc_bf16_f32(128, D, false, true);
-    const uint64_t dQ0 = sdesc_sw128(f.base + C::kResOff, 16, 1024);
-    const uint64_t dO0 = sdesc_sw128(f.base + C::kResOff + C::kTileBytes, 16, 1024);
-    const uint64_t dR0 = sdesc_sw128(f.base + C::kRingOff, 16, 1024);            // K, V by rows
-    const uint64_t dT0 = sdesc_sw128(f.base + C::kRingOff, kChunkBytes, 1024);   // K by columns
+    constexpr uint64_t kTile = C::kTileBytes >> 4;
+    const uint64_t res = sdesc_sw128(f.base + C::kResOff, 16, 1024);
+    const uint64_t rows0 = sdesc_sw128(f.base + C::kRing0, 16, 1024), rows1 = sdesc_sw128(f.base + C::kRing1, 16, 1024);
+    const uint64_t cols0 = sdesc_sw128(f.base + C::kRing0, kChunkBytes, 1024);
     const uint32_t tmem = f.tmem;
     bool ok = true;
-    // S = Q K^T and dP = dO V^T for stream step g
-    auto issue_s = [&](int g) {
+    // S = Q K^T (which = 0) or dP = dO V^T (1) for stream step g
+    auto issue_s = [&](int which, int g) {
+      const uint64_t a = res + (which ? kTile : 0);
+      const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const uint64_t a = which ? dO0 : dQ0;
-        const uint64_t b = dR0 + static_cast<uint64_t>(((2 * (g % kS) + which) * C::kTileBytes) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-          mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
-        }
-        mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
+        mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
       }
+      mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
     };
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -653,54 +798,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || f.items()[q % kItems].end) break;
       const int ns = f.items()[q % kItems].ns;
       f.give_item(q);
-      ok = mbar_wait_w(f.bar(C::kBarResFull), q & 1, abort_flag);
-      auto tiles_ready = [&](int gs) {
-        if (ok) ok = mbar_wait_w(f.bar(C::kBarLoad + gs % kS), (gs / kS) & 1, abort_flag);
-        if (ok) ok = mbar_wait_w(f.bar(C::kBarReady + gs % kS), (gs / kS) & 1, abort_flag);
-        tc_fence_after();
-      };
-      tiles_ready(g);
-      // the last step's S and dP are in registers: their columns are free
-      if (ok && g > 0) ok = mbar_wait_w(f.bar(C::kBarP), (g - 1) & 1, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      issue_s(g);
-      if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
-      for (int jj = 0; jj < ns; ++jj) {
-        const int gs = g + jj;
-        if (jj + 1 < ns) {
-          tiles_ready(gs + 1);
-          if (ok) ok = mbar_wait_w(f.bar(C::kBarP), gs & 1, abort_flag);
+      if (warp == C::kMmaWarp) {
+        // S and dP, each once its predecessor is in registers
+        ok = f.wait(C::kBarResFull, q);
+        for (int jj = 0; jj < ns && ok; ++jj) {
+          const int gs = g + jj;
+          ok = (gs == 0 || f.wait(C::kBarSFree, gs - 1)) && f.landed0(gs) && f.ready(gs);
           if (!ok) break;
           tc_fence_after();
-          issue_s(gs + 1);
-          if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+          issue_s(0, gs);
+          ok = (gs == 0 || f.wait(C::kBarDpFree, gs - 1)) && f.landed1(gs);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(1, gs);
+          mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
         }
-        ok = mbar_wait_w(f.bar(C::kBarDs), gs & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        // dQ (+)= dS K
-        const uint64_t b = dT0 + static_cast<uint64_t>((2 * (gs % kS) * C::kTileBytes) >> 4);
+        if (ok) mma_commit_w(f.bar(C::kBarResFree));
+      } else {
+        // dQ (+)= dS K; that dS is there says that S has been computed
+        for (int jj = 0; jj < ns && ok; ++jj) {
+          const int gs = g + jj;
+          ok = f.landed0(gs) && f.ready(gs) && f.wait(C::kBarDs, gs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b = cols0 + gs % C::kStages0 * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts_w(tmem + C::kColA, tmem + C::kColDs + kk * 8, b + 128 * kk, kIdA, (jj > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_w(f.bar(C::kBarEmpty + gs % kS));
-        mma_commit_w(f.bar(C::kBarDsFree));
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_w(tmem + C::kColA, tmem + C::kColDs + kk * 8, b + 128 * kk, kIdA, (jj > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_w(f.bar(C::kBarDsFree));
+          mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
+        }
       }
       g += ns;
     }
-    // Let every MMA this warp issued finish before TMEM is released.
-    mma_commit_w(f.bar(C::kBarDrain));
-    mbar_wait_w(f.bar(C::kBarDrain), 0, nullptr);
+    f.drain(warp == C::kMmaWarp ? 0 : 1);
   } else {
     // ------------------------------------------------------------ dS
-    const int wg = warp / 4, r = threadIdx.x & 127, ri = sh.by_group.div(r);  // the group's keys are 64 wg .. 64 wg + 63
+    const int wg = warp / 4, r = threadIdx.x & 127, ri = sh.by_group.div(r);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * 64;
-    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * 64;
-    const uint32_t tDs = f.tmem + lane_base + C::kColDs + wg * 32;
-    uint8_t* stage = f.smem + C::kOutOff + warp * kStageOut;
-    const float sl2 = args.scale_log2;
+    const uint32_t tS = f.tmem + lane_base + C::kColS + wg * kCols;  // the group's keys are kCols wg .. kCols (wg + 1) - 1
+    const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * kCols;
+    const uint32_t tDs = f.tmem + lane_base + C::kColDs + wg * kCols / 2;
+    const float2 sl2 = make_float2(args.scale_log2, args.scale_log2);
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -708,76 +847,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || f.items()[q % kItems].end) break;
       const Item& it = f.items()[q % kItems];
       const int ns = it.ns, n = it.n, i0 = it.x0, pos = i0 + ri;
-      float l = INFINITY, d = 0.f;
+      float l = -INFINITY, d = 0.f;
       if (ri < sh.tpt && pos < n) {
         const long long at = static_cast<long long>(it.row0 + pos) * sh.Hq + it.h * G + (r - ri * G);
-        l = args.lse[at] * kLog2e;
-        d = args.D[at];
+        l = -kLog2e * args.lse[at];
+        d = -args.D[at];
       }
+      const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
       const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive
       const int key_lo = sh.window > 0 ? pos - sh.window + 1 : 0;
       const int full_hi = sh.causal ? i0 : n - 1;
       const int full_lo = sh.window > 0 ? min(i0 + sh.tpt, n) - sh.window : 0;
       int key0 = it.t0 * kKT;
       for (int jj = 0; jj < ns; ++jj, ++g, key0 += kKT) {
-        ok = mbar_wait_w(f.bar(C::kBarS), g & 1, abort_flag);
+        ok = f.waitc(C::kBarS, g);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[2][32];
-        tmem_ld32(tS, sr[0]);
-        tmem_ld32(tS + 32, sr[1]);
-        tmem_ld_wait(sr[0]);
-        tmem_ld_wait(sr[1]);
-        float p[64];
+        uint32_t x[kWords][32], pk[16];
+        float2 p[kWords][16];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(sr[c >> 5][c & 31]), sl2, -l));
-        ok = mbar_wait_w(f.bar(C::kBarDp), g & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        tmem_ld32(tDp, sr[0]);
-        tmem_ld32(tDp + 32, sr[1]);
-        tmem_ld_wait(sr[0]);
-        tmem_ld_wait(sr[1]);
+        for (int w = 0; w < kWords; ++w) tmem_ld32(tS + 32 * w, x[w]);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) tmem_ld_wait(x[w]);
         tc_fence_before();
-        mbar_arrive_warp(f.bar(C::kBarP));  // S and dP may be overwritten
+        mbar_arrive_warp(f.bar(C::kBarSFree));
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(sr[c >> 5][c & 31]) - d;
-        if (key0 + kKT - 1 > full_hi || key0 < full_lo) {
-          const int hi = key_hi - key0 - wg * 64, lo = key_lo - key0 - wg * 64;
+        for (int w = 0; w < kWords; ++w) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t seen = bits_between(lo - 32 * h, hi - 32 * h);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((seen >> c) & 1u)) p[32 * h + c] = 0.f;
+          for (int c = 0; c < 16; ++c) {
+            const float2 a = __ffma2_rn(pair(x[w] + 2 * c), sl2, l2);
+            p[w][c] = make_float2(ex2(a.x), ex2(a.y));
           }
         }
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
-        if (g > 0) ok = mbar_wait_w(f.bar(C::kBarDsFree), (g - 1) & 1, abort_flag);
+        ok = f.waitc(C::kBarDp, g);
         if (!ok) break;
         tc_fence_after();
-        tmem_st32(tDs, pk);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) tmem_ld32(tDp + 32 * w, x[w]);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) tmem_ld_wait(x[w]);
+        tc_fence_before();
+        mbar_arrive_warp(f.bar(C::kBarDpFree));
+        const bool cut = key0 + kKT - 1 > full_hi || key0 < full_lo;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) p[w][c] = __fmul2_rn(p[w][c], __fadd2_rn(pair(x[w] + 2 * c), d2));
+          if (cut) {
+            const int at = key0 + wg * kCols + 32 * w;
+            keep_bits(p[w], bits_between(key_lo - at, key_hi - at));
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[w][c].x, p[w][c].y);
+          if (w == 0 && g > 0) ok = f.waitc(C::kBarDsFree, g - 1);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st16(tDs + 16 * w, pk);
+        }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(f.bar(C::kBarDs));
       }
       if (!ok) break;
-      // dQ, once the last product has been added: columns [wg D / 2, (wg + 1) D
-      // / 2). The next item's first product waits for both groups' next dS.
-      ok = mbar_wait_w(f.bar(C::kBarDsFree), (g - 1) & 1, abort_flag);
+      // dQ, once the last product has been added, a group D / kGroups columns of
+      // it. The next item's first product waits for all groups' next dS.
+      ok = f.waitc(C::kBarDsFree, g - 1);
       if (!ok) break;
       tc_fence_after();
-      const int tile_row = (warp & 3) * 32;
       const long long stride = args.out_stride[0];
       __nv_bfloat16* out = args.out[0] + static_cast<long long>(it.row0 + i0) * stride + it.h * G * D;
+      if constexpr (C::kStaged) {
+        const int tile_row = (warp & 3) * 32;
 #pragma unroll 1
-      for (int c = wg * (D / 2); c < (wg + 1) * (D / 2); c += 32)
-        store_columns(f.tmem + lane_base + C::kColA + c, args.scale, stage, lane, [&](int wr) {
-          const int x = sh.by_group.div(tile_row + wr);
-          return x < sh.tpt && i0 + x < n ? out + x * stride + (tile_row + wr - x * G) * D + c : nullptr;
-        });
+        for (int c = wg * 32; c < D; c += kGroups * 32)
+          store_columns(f.tmem + lane_base + C::kColA + c, args.scale, f.smem + C::kOutOff + warp * 2048, lane, [&](int wr) {
+            const int x = sh.by_group.div(tile_row + wr);
+            return x < sh.tpt && i0 + x < n ? out + x * stride + (tile_row + wr - x * G) * D + c : nullptr;
+          });
+      } else {
+        __nv_bfloat16* mine = ri < sh.tpt && pos < n ? out + ri * stride + (r - ri * G) * D : nullptr;
+#pragma unroll 1
+        for (int c = wg * (D / kGroups); c < (wg + 1) * (D / kGroups); c += 16)
+          store_direct(f.tmem + lane_base + C::kColA + c, args.scale, mine != nullptr ? mine + c : nullptr);
+      }
       tc_fence_before();
       f.give_item(q);
     }
@@ -812,7 +965,6 @@ BwdPlan bwd_plan(int B, int T, int Hq, int Hkv, int sms) {
 
 template <int D>
 int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[2], float* rowsum, cudaStream_t stream) {
-  using C = Cfg<D>;
   const PackedProblem& p = b.p;
   const PackedShape& s = p.s;
   const int G = s.by_group.G;
@@ -827,8 +979,9 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   const auto dq = packed_dq_kernel<D>;
   // attribute slots 32 to 35 (the other kernels use 0-31)
   constexpr int kSlot = D == 64 ? 32 : 34;
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(dkv), C::kSmemBytes, kSlot) ||
-      !ensure_smem_attr(reinterpret_cast<const void*>(dq), C::kSmemBytes, kSlot + 1))
+  constexpr int kDkvBytes = Cfg<D, true>::kSmemBytes, kDqBytes = Cfg<D, false>::kSmemBytes;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(dkv), kDkvBytes, kSlot) ||
+      !ensure_smem_attr(reinterpret_cast<const void*>(dq), kDqBytes, kSlot + 1))
     return -3;
   const long long rows = static_cast<long long>(s.T) * s.Hq, per = 256 / (D / 8) * 4;
   cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
@@ -850,12 +1003,12 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   a.out[1] = static_cast<__nv_bfloat16*>(b.dv);
   a.out_stride[0] = b.dk_stride;
   a.out_stride[1] = b.dv_stride;
-  e = launch_overlapped(dkv, grid(0), dim3(kThreads), C::kSmemBytes, stream, mk, mv, mq, mo, a);
+  e = launch_overlapped(dkv, grid(0), dim3(Cfg<D, true>::kThreads), kDkvBytes, stream, mk, mv, mq, mo, a);
   if (e != cudaSuccess) return -3;
   a.list = lists[1];
   a.out[0] = static_cast<__nv_bfloat16*>(b.dq);
   a.out_stride[0] = b.dq_stride;
-  e = launch_overlapped(dq, grid(1), dim3(kThreads), C::kSmemBytes, stream, mq, mo, mk, mv, a);
+  e = launch_overlapped(dq, grid(1), dim3(Cfg<D, false>::kThreads), kDqBytes, stream, mq, mo, mk, mv, a);
   return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;
 }
 

@@ -57,9 +57,6 @@ __device__ __forceinline__ unsigned long long global_ns() {
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 
-#ifndef FA_SPINS
-#define FA_SPINS 32
-#endif
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -472,25 +469,6 @@ __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
 // converged for the elected issue above.
 __device__ __forceinline__ bool mbar_wait_w(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-}
-
-// mbar_wait_w that looks at the clock and the abort flag once in a while only:
-// reading %globaltimer takes hundreds of cycles, which a warp that issues MMAs
-// (or is waited for by one) would otherwise lose whenever it waits at all.
-__device__ __forceinline__ bool mbar_spin_w(uint32_t bar, uint32_t parity, volatile int* abort) {
-  unsigned long long t0 = 0;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < FA_SPINS; ++i)
-      if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, *abort != 0)) return false;
-    const unsigned long long now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (__any_sync(0xffffffffu, now - t0 > kWaitBudgetNs)) {
-      *abort = 1;
-      return false;
-    }
-  }
 }
 
 // mbar_wait_sleep by all 32 lanes of a warp, with one verdict for all.

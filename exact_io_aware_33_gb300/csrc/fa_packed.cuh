@@ -88,56 +88,49 @@ __device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, int unit
 }
 
 // Hands out items: the CTA's own one where every item has a CTA (no list), or
-// the list's, heaviest first, by a counter. The entry of the item after the
-// present one is on its way, and the number of the one behind it asked for,
-// while an item is worked on.
+// the list's, heaviest first, by a counter. The next item's number is asked for
+// kAhead steps before the loads of the present one end, so that the answer is
+// not waited for; sooner would deal items out before it is known who is done
+// first (a whole item sooner: 215 us instead of 190 for 8192 causal rows, 16
+// heads, d = 128).
 struct ItemQueue {
+  static constexpr int kAhead = 4;
   const PackedList* list;
   GroupDiv by_head;
-  int count, ahead;   // entries; number of the item after the next
-  PackedEntry entry;  // of the next item
-  int head;
-  bool have;
+  int count;  // entries
+  int next;   // number of the next item; -1: not asked for
+  PackedEntry own;
 
   // By the whole warp.
   __device__ __forceinline__ void start(const PackedShape& s, const PackedList& l, int* status) {
     list = &l;
     by_head = s.by_head;
-    const int x = static_cast<int>(blockIdx.x), e = by_head.div(x);
-    if (l.entries == nullptr) {
-      entry = find_entry(s, l.unit, e, status);
-      head = x - e * by_head.G;
-      have = entry.n > 0;
-    } else {
+    next = static_cast<int>(blockIdx.x);
+    if (l.entries == nullptr)
+      own = find_entry(s, l.unit, by_head.div(next), status);
+    else
       count = l.head->count;
-      load(x);
-      ahead = request();
-    }
+  }
+  // By lane 0, with `left` steps of the present item still to be loaded, this one included.
+  __device__ __forceinline__ void step(int left) {
+    if (next < 0 && left <= kAhead)
+      next = list->entries == nullptr ? 0x7fffffff
+                                      : static_cast<int>(gridDim.x) + atomicAdd(&list->head->taken, 1);
   }
   // The next item, for lane 0; false when there are no more.
   __device__ __forceinline__ bool take(PackedEntry* e, int* h) {
-    if (!have) return false;
-    *e = entry;
-    *h = head;
+    const int k = by_head.div(next);
     if (list->entries == nullptr) {
-      have = false;
+      if (next == 0x7fffffff || own.n == 0) return false;
+      *e = own;
     } else {
-      load(ahead);
-      ahead = request();
+      if (k >= count) return false;
+      const int4 r = list->entries[k];
+      *e = PackedEntry{r.x, r.y, r.z};
     }
+    *h = next - k * by_head.G;
+    next = -1;
     return true;
-  }
-
- private:
-  __device__ __forceinline__ int request() {
-    return lane_id() == 0 ? static_cast<int>(gridDim.x) + atomicAdd(&list->head->taken, 1) : 0;
-  }
-  __device__ __forceinline__ void load(int x) {
-    const int e = by_head.div(x);
-    have = e < count;
-    head = x - e * by_head.G;
-    const int4 r = list->entries[min(e, list->cap - 1)];
-    entry = PackedEntry{r.x, r.y, r.z};
   }
 };
 

@@ -349,6 +349,7 @@ struct Frame {
       *res_loads = ++q;
       for (int jj = 0; jj < it.ns && ok; ++jj, ++g) {
         const int row = e.row0 + (it.t0 + jj) * (kKeys ? s.tpt : kKT);
+        queue.step(it.ns - jj);
         auto load = [&](int w, int load_bar, int empty_bar, int stages, uint8_t* to) {
           if (g >= stages) ok = mbar_wait(bar(empty_bar + g % stages), (g / stages - 1) & 1, abort_flag);
 #ifdef FA_TEST_SKIP_ARRIVE
@@ -645,6 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * kCols;
     const uint32_t tP = C::kApart ? f.tmem + lane_base + C::kColP + wg * kCols / 2 : tS;
     const uint32_t tDs = C::kApart ? f.tmem + lane_base + C::kColDs + wg * kCols / 2 : tDp;
+    // tokens of the group's first and last columns
+    const int group_i0 = sh.by_group.div(wg * kCols), group_i1 = sh.by_group.div(wg * kCols + kCols - 1);
     const float2 sl2 = make_float2(args.scale_log2, args.scale_log2);
     bool ok = true;
     int g = 0;
@@ -656,8 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int i0 = it.t0 * sh.tpt;
       for (int jj = 0; jj < ns; ++jj, ++g, i0 += sh.tpt) {
         const float* stat = f.stats(g) + wg * kCols;
-        // queries of this key: [k0 + row, k0 + row + window)
-        const bool cut = (sh.causal && i0 < k0 + kKT - 1) || (sh.window > 0 && i0 + sh.tpt > k0 + sh.window);
+        // queries of this key: [k0 + row, k0 + row + window); whether a border cuts the warp's part
+        const bool cut = (sh.causal && i0 + group_i0 < k0 + (warp & 3) * 32 + 31) ||
+                         (sh.window > 0 && i0 + group_i1 >= k0 + (warp & 3) * 32 + sh.window);
         uint32_t seen = 0xffffffffu;
         if (cut) {
           const int lo = sh.causal ? min(max(k0 + row - i0, 0), 128) * G - wg * kCols : 0;
@@ -835,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_increase<kComputeRegs>();
     const int wg = warp / 4, r = threadIdx.x & 127, ri = sh.by_group.div(r);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int warp_i0 = sh.by_group.div(r - lane), warp_i1 = sh.by_group.div(r - lane + 31);  // tokens of the warp's rows
     const uint32_t tS = f.tmem + lane_base + C::kColS + wg * kCols;  // the group's keys are kCols wg .. kCols (wg + 1) - 1
     const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * kCols;
     const uint32_t tDs = f.tmem + lane_base + C::kColDs + wg * kCols / 2;
@@ -855,8 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
       const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive
       const int key_lo = sh.window > 0 ? pos - sh.window + 1 : 0;
-      const int full_hi = sh.causal ? i0 : n - 1;
-      const int full_lo = sh.window > 0 ? min(i0 + sh.tpt, n) - sh.window : 0;
+      // keys that all rows of the warp see: full_lo <= key < full_hi
+      const int full_hi = sh.causal ? min(n, i0 + warp_i0 + 1) : n;
+      const int full_lo = sh.window > 0 ? i0 + warp_i1 - sh.window + 1 : 0;
       int key0 = it.t0 * kKT;
       for (int jj = 0; jj < ns; ++jj, ++g, key0 += kKT) {
         ok = f.wait_calm(C::kBarS, g);
@@ -880,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait(x);
         tc_fence_before();
         mbar_arrive_warp(f.bar(C::kBarDpFree));
-        const bool cut = key0 + kKT - 1 > full_hi || key0 < full_lo;
+        const bool cut = key0 + wg * kCols + kCols > full_hi || key0 + wg * kCols < full_lo;
 #pragma unroll
         for (int c = 0; c < 16; ++c) p[c] = __fmul2_rn(p[c], __fadd2_rn(pair(x + 2 * c), d2));
         if (cut) {

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
           const int st = g % kS;
           const uint32_t ph = ((g / kS) + 1) & 1;
           const int key_row = e.row0 + (it.j0 + jj) * kBN;
+          queue.step(it.ns - jj);
           if (g >= kS) ok = mbar_wait(bar(C::kBarKEmpty + st), ph, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(bar(C::kBarKFull + st), C::kTileBytes);
@@ -397,6 +398,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     const int t = warp / 4;  // query tile
     const int r = threadIdx.x & 127;  // row of the tile
     const int ri = sh.by_group.div(r);  // its token
+    // tokens of the warp's first and last rows
+    const int warp_i0 = sh.by_group.div(r - lane), warp_i1 = sh.by_group.div(r - lane + 31);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + t * kBN;
     const uint32_t tO = tmem + lane_base + C::kColO + t * D;
@@ -419,17 +422,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         mbar_arrive_warp(bar(C::kBarItemEmpty + q % kItems));
         continue;
       }
-      // keys visible to this row: key_lo <= key < key_hi; to all rows of the tile: full_lo <= key <= full_hi
-      int key_hi = n, key_lo = 0, full_hi = n - 1, full_lo = 0;
+      // keys visible to this row: key_lo <= key < key_hi; to all rows of the warp: full_lo <= key < full_hi
+      int key_hi = n, key_lo = 0, full_hi = n, full_lo = 0;
       {
         const int i0 = it.i0 + t * sh.tpt, pos = i0 + ri;
         if (sh.causal) {
           key_hi = min(n, pos + 1);
-          full_hi = i0;
+          full_hi = min(n, i0 + warp_i0 + 1);
         }
         if (sh.window > 0) {
           key_lo = pos - sh.window + 1;
-          full_lo = min(i0 + sh.tpt, n) - sh.window;
+          full_lo = i0 + warp_i1 - sh.window + 1;
         }
       }
       float m_ref = -INFINITY;  // log2-domain reference maximum
@@ -450,11 +453,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         float xs[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) xs[c] = __uint_as_float(sr[c >> 5][c & 31]);
-        if (key0 + kBN - 1 > full_hi || key0 < full_lo) {
+        // masks, in the words of 32 keys that a border of some row of the warp cuts
+        // or leaves out, one border at a time
+        if (key0 + kBN > full_hi || key0 < full_lo) {
           const int hi = key_hi - key0, lo = key_lo - key0;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= hi || c < lo) xs[c] = -INFINITY;
+          for (int w = 0; w < 4; ++w) {
+            if (key0 + 32 * w + 32 > full_hi) {
+#pragma unroll
+              for (int c = 32 * w; c < 32 * w + 32; ++c)
+                if (c >= hi) xs[c] = -INFINITY;
+            }
+            if (key0 + 32 * w < full_lo) {
+#pragma unroll
+              for (int c = 32 * w; c < 32 * w + 32; ++c)
+                if (c < lo) xs[c] = -INFINITY;
+            }
+          }
         }
         const float m_tile = max3(fmaxf(max32(xs), max32(xs + 32)), max32(xs + 64), max32(xs + 96)) * sl2;
         const bool need = m_tile > m_ref + kSlack;

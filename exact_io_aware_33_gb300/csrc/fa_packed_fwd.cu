@@ -62,7 +62,11 @@ struct Cfg {
   static constexpr bool kSepP = D == 64;
   static constexpr int kSoftmaxWarps = 4 * QT;
   static constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+  // d = 128: two warps more, which do nothing, complete the warpgroup that gives
+  // registers up to the softmax (384 x 168 = 256 x 208 + 128 x 88): spilled values
+  // came back from L2, 700 cycles each, at every item's borders.
+  static constexpr bool kSplitRegs = D == 128;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + (kSplitRegs ? 4 : 2));
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kStages = 2;
@@ -178,6 +182,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     return true;
   };
 
+  if (C::kSplitRegs && warp >= C::kSoftmaxWarps) regs_decrease<88>();
   if (warp == C::kLoadWarp) {
     // ------------------------------------------------------------ producer
     ItemQueue queue;
@@ -393,8 +398,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     // Let every MMA this warp issued finish before TMEM is released.
     mma_commit_w(bar(C::kBarDrain));
     mbar_wait_w(bar(C::kBarDrain), 0, nullptr);
-  } else {
+  } else if (warp < C::kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax
+    if constexpr (C::kSplitRegs) regs_increase<208>();
     const int t = warp / 4;  // query tile
     const int r = threadIdx.x & 127;  // row of the tile
     const int ri = sh.by_group.div(r);  // its token
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
       const long long first = static_cast<long long>(it.row0 + i0) * sh.Hq + it.h * G;  // (token, head) of row 0
       uint8_t* stage_blk = smem + (D == 64 ? C::kQOff + (q % C::kQBufs) * C::kQBytes : C::kOStageOff) + warp * 4096;
       uint8_t* stage_row = stage_blk + lane * 128;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -580,14 +586,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         }
         __syncwarp();
         // instruction j: lanes 8r'..8r'+7 write the eight chunks of row 4j + r'
-#pragma unroll 2
+        uint4 val[8];
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int wr = 4 * j + (lane >> 3), v = lane & 7;
-          const uint4 val = *reinterpret_cast<const uint4*>(stage_blk + wr * 128 + ((v ^ (wr & 7)) * 16));
-          const int row = (warp & 3) * 32 + wr, x = sh.by_group.div(row);
+          val[j] = *reinterpret_cast<const uint4*>(stage_blk + wr * 128 + ((v ^ (wr & 7)) * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int row = (warp & 3) * 32 + 4 * j + (lane >> 3), x = sh.by_group.div(row);
           if (x < sh.tpt && i0 + x < n)
             *reinterpret_cast<uint4*>(args.o + (first + static_cast<long long>(x) * sh.Hq + (row - x * G)) * D + h * 64 +
-                                      v * 8) = val;
+                                      (lane & 7) * 8) = val[j];
         }
         __syncwarp();  // the block is read back before it is written again
       }

@@ -114,12 +114,14 @@ struct FwdArgs {
   float* lse;        // [T, Hq]
   int* status;
   float scale_log2;
+  int boxes;         // 1: a warp's 32 rows are whole tokens, which a box of tmO holds
 };
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs args) {
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                      const __grid_constant__ FwdArgs args) {
   using C = Cfg<D>;
   constexpr int kS = C::kStages, QT = C::QT;
   extern __shared__ uint8_t smem_raw[];
@@ -559,47 +561,66 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       const float lse_row = l > 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
       const float2 il2 = make_float2(inv_l, inv_l);
-      // each warp swizzles its 32 rows, 64 columns at a time, into its staging
-      // block and writes them back as four whole lines per instruction
+      // Each warp swizzles its 32 rows, 64 columns at a time, into its staging
+      // block. At d = 128, where they are all the sequence's and whole tokens, one
+      // tensor copy takes them from there while the warp goes on (an SM's own stores
+      // move 32 bytes a clock: 2000 cycles an item; 8 prompts of up to 4096 tokens,
+      // 32 / 8 heads: 189 -> 183 us. At d = 64 the other CTA has the tensor core
+      // meanwhile, and nothing was gained.) Otherwise the warp writes them back as
+      // four whole lines per instruction.
       const int i0 = it.i0 + t * sh.tpt;
       const long long first = static_cast<long long>(it.row0 + i0) * sh.Hq + it.h * G;  // (token, head) of row 0
+      const bool box = D == 128 && args.boxes && i0 + warp_i1 < n;
       uint8_t* stage_blk = smem + (D == 64 ? C::kQOff + (q % C::kQBufs) * C::kQBytes : C::kOStageOff) + warp * 4096;
       uint8_t* stage_row = stage_blk + lane * 128;
 #pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {
+        uint32_t pko[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + h * 64 + c * 32, o);
           tmem_ld_wait(o);
-          uint32_t pko[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), il2);
-            pko[e] = pack_bf16(v.x, v.y);
+            pko[16 * c + e] = pack_bf16(v.x, v.y);
           }
-          // 16-byte chunks 4c..4c+3 of row `lane`, chunk v in slot v ^ (lane & 7)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage_row + (((4 * c + e) ^ (lane & 7)) * 16)) =
-                make_uint4(pko[4 * e], pko[4 * e + 1], pko[4 * e + 2], pko[4 * e + 3]);
         }
-        __syncwarp();
-        // instruction j: lanes 8r'..8r'+7 write the eight chunks of row 4j + r'
-        uint4 val[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int wr = 4 * j + (lane >> 3), v = lane & 7;
-          val[j] = *reinterpret_cast<const uint4*>(stage_blk + wr * 128 + ((v ^ (wr & 7)) * 16));
+        if constexpr (D == 128) {  // the block's last copy has read it
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
         }
+        // 16-byte chunk v of row `lane` in slot v ^ (lane & 7)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = (warp & 3) * 32 + 4 * j + (lane >> 3), x = sh.by_group.div(row);
-          if (x < sh.tpt && i0 + x < n)
-            *reinterpret_cast<uint4*>(args.o + (first + static_cast<long long>(x) * sh.Hq + (row - x * G)) * D + h * 64 +
-                                      (lane & 7) * 8) = val[j];
+        for (int v = 0; v < 8; ++v)
+          *reinterpret_cast<uint4*>(stage_row + ((v ^ (lane & 7)) * 16)) =
+              make_uint4(pko[4 * v], pko[4 * v + 1], pko[4 * v + 2], pko[4 * v + 3]);
+        if (box) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(&tmO, smem_u32(stage_blk), h * 64, 0, it.h, it.row0 + i0 + warp_i0);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+          // instruction j: lanes 8r'..8r'+7 write the eight chunks of row 4j + r'
+          uint4 val[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int wr = 4 * j + (lane >> 3), v = lane & 7;
+            val[j] = *reinterpret_cast<const uint4*>(stage_blk + wr * 128 + ((v ^ (wr & 7)) * 16));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int row = (warp & 3) * 32 + 4 * j + (lane >> 3), x = sh.by_group.div(row);
+            if (x < sh.tpt && i0 + x < n)
+              *reinterpret_cast<uint4*>(args.o + (first + static_cast<long long>(x) * sh.Hq + (row - x * G)) * D + h * 64 +
+                                        (lane & 7) * 8) = val[j];
+          }
+          __syncwarp();  // the block is read back before it is written again
         }
-        __syncwarp();  // the block is read back before it is written again
       }
       if (ri < sh.tpt && i0 + ri < n) args.lse[first + static_cast<long long>(ri) * sh.Hq + (r - ri * G)] = lse_row;
       mbar_arrive_warp(bar(C::kBarItemEmpty + q % kItems));
@@ -609,6 +630,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
       }
       ++qt;
     }
+    if (D == 128 && lane == 0) bulk_wait<0>();  // this warp's copies out of shared memory
   }
 
   tc_fence_before();
@@ -654,16 +676,19 @@ int launch_d(const PackedProblem& p, const FwdArgs& a, const FwdPlan& plan, cuda
   using C = Cfg<D>;
   const PackedShape& s = p.s;
   const int G = s.by_group.G;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
+  FwdArgs args = a;
+  args.boxes = D == 128 && 32 % G == 0;
   if (!make_map_packed(&mq, p.q, s.T, s.Hkv, G, D, p.q_stride, s.tpt) ||
       !make_map_packed(&mk, p.k, s.T, s.Hkv, 1, D, p.k_stride, kBN) ||
-      !make_map_packed(&mv, p.v, s.T, s.Hkv, 1, D, p.v_stride, kBN))
+      !make_map_packed(&mv, p.v, s.T, s.Hkv, 1, D, p.v_stride, kBN) ||
+      !make_map_packed(&mo, a.o, s.T, s.Hkv, G, D, static_cast<long long>(s.Hq) * D, args.boxes ? 32 / G : 1))
     return -3;
   auto kern = packed_fwd_kernel<D>;
   // attribute slots 30 and 31 (the other kernels use 0-29)
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmemBytes, D == 64 ? 30 : 31)) return -3;
   const int grid = plan.listed ? plan.slots : plan.cap * s.Hkv;
-  const cudaError_t e = launch_overlapped(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, mq, mk, mv, a);
+  const cudaError_t e = launch_overlapped(kern, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream, mq, mk, mv, mo, args);
   return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? 0 : -3;
 }
 

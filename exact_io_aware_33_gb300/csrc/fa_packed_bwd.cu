@@ -64,8 +64,8 @@ struct Item {
 struct BwdArgs {
   PackedShape s;
   PackedList list;
-  const float* lse;  // [T, Hq]
-  const float* D;    // [T, Hq]
+  const float* neg_lse;  // [Hkv, T, G], log2 units
+  const float* neg_d;    // [Hkv, T, G]
   __nv_bfloat16* out[2];   // dK, dV; or dQ
   long long out_stride[2];
   int* status;
@@ -121,26 +121,34 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- D
-// D = rowsum(dO O) for every row and head; d / 8 lanes per row. Bound by memory:
+// -D = -rowsum(dO O) and -LSE in log2 units for every row and head, laid out so
+// that the rows of a tile are contiguous; d / 8 lanes per row. Bound by memory:
 // 4 d bytes a row.
 template <int D>
 __global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16* __restrict__ o,
                                                             const __nv_bfloat16* __restrict__ dO, long long do_stride,
-                                                            float* __restrict__ out, long long rows, GroupDiv heads) {
+                                                            const float* __restrict__ lse, float* __restrict__ neg_lse,
+                                                            float* __restrict__ neg_d, int Hq, GroupDiv head_rows,
+                                                            GroupDiv group, long long rows) {
   constexpr int kLanes = D / 8, kUnroll = 4;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % kLanes;
   const long long per = 256 / kLanes, first = static_cast<long long>(blockIdx.x) * per * kUnroll + threadIdx.x / kLanes;
   uint4 a[kUnroll], b[kUnroll];
+  float l[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const long long row = first + i * per;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int t = heads.div(static_cast<int>(row)), h = static_cast<int>(row) - t * heads.G;
-      a[i] = *reinterpret_cast<const uint4*>(o + row * D + lane * 8);
-      b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + h * D + lane * 8);
+    l[i] = 0.f;
+    if (row < rows) {  // key head, then token and head of the group
+      const int h = head_rows.div(static_cast<int>(row)), r = static_cast<int>(row) - h * head_rows.G;
+      const int t = group.div(r), hq = h * group.G + (r - t * group.G);
+      const long long at = static_cast<long long>(t) * Hq + hq;
+      a[i] = *reinterpret_cast<const uint4*>(o + at * D + lane * 8);
+      b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + hq * D + lane * 8);
+      l[i] = lse[at];
     }
   }
 #pragma unroll
@@ -155,7 +163,10 @@ __global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16*
 #pragma unroll
     for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     const long long row = first + i * per;
-    if (lane == 0 && row < rows) out[row] = sum;
+    if (lane == 0 && row < rows) {
+      neg_d[row] = -sum;
+      neg_lse[row] = -kLog2e * l[i];
+    }
   }
 }
 
@@ -263,7 +274,8 @@ struct Frame {
     if (threadIdx.x == 0) {
       mbar_init(bar(C::kBarResFull), 1);
       mbar_init(bar(C::kBarResFree), 1);
-      for (int i = C::kBarLoad0; i < C::kBarS; ++i) mbar_init(bar(i), 1);
+      for (int i = C::kBarLoad0; i < C::kBarS; ++i)
+        mbar_init(bar(i), kKeys && i >= C::kBarReady && i < C::kBarLoad1 ? 32 : 1);  // (dK, dV's helper: each lane's copies)
       mbar_init(bar(C::kBarS), kKeys ? 2 : 1);  // dK, dV: and the MMA warp, which passes on that the statistics are written
       mbar_init(bar(C::kBarDp), 1);
       mbar_init(bar(C::kBarP), kComputeWarps);
@@ -465,7 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     f.produce(sh, args.list, &tmK, &tmV, &tmQ, &tmDo, args.status, &res_loads, stage_loads);
   } else if (warp == kHelpWarp) {
     // ------------------------------------------------------------ statistics
-    // Each step's 128 -LSE (log2 units) and -D; rows that are none get P = 0.
+    // Each step's 128 -LSE and -D are copied without being waited for: they arrive
+    // on the stage's barrier themselves (waited for here, they were what a step
+    // took: 3400 cycles instead of 2100 where they came from memory). Rows that are
+    // none get zeros: their queries and dO are zeros too, so P = 1 adds nothing.
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -474,38 +489,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item it = f.items()[q % kItems];
       f.give_item(q);
       for (int jj = 0; jj < it.ns; ++jj, ++g) {
-        const int i0 = (it.t0 + jj) * sh.tpt, cnt = min(sh.tpt, it.n - i0);
-        const long long first = static_cast<long long>(it.row0 + i0) * sh.Hq + it.h * G;
-        float l[4], d[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = lane + 32 * i, x = sh.by_group.div(r);
-          l[i] = -INFINITY;
-          d[i] = 0.f;
-          if (x < cnt) {
-            const long long at = first + static_cast<long long>(x) * sh.Hq + (r - x * G);
-            l[i] = -kLog2e * args.lse[at];
-            d[i] = -args.D[at];
-          }
-        }
+        const int i0 = (it.t0 + jj) * sh.tpt, rows = min(sh.tpt, it.n - i0) * G;
+        const long long first = (static_cast<long long>(it.h) * sh.T + it.row0 + i0) * G;
         ok = f.stats_free(g);
         if (!ok) break;
-        float* stat = f.stats(g);
+        const uint32_t stat = smem_u32(f.stats(g));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          stat[lane + 32 * i] = l[i];
-          stat[128 + lane + 32 * i] = d[i];
+          const int r = lane + 32 * i;
+          const long long at = first + min(r, rows - 1);
+          cp_async_f32(stat + 4 * r, args.neg_lse + at, r < rows);
+          cp_async_f32(stat + 512 + 4 * r, args.neg_d + at, r < rows);
         }
         if (F::last_tile(sh, it, jj)) {
           ok = f.landed0(g) && f.landed1(g);
           if (!ok) break;
-          zero_rows(f.ring0(g), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
-          zero_rows(f.ring1(g), kChunkBytes, C::kChunks, cnt * G, 128, lane, 32);
+          zero_rows(f.ring0(g), kChunkBytes, C::kChunks, rows, 128, lane, 32);
+          zero_rows(f.ring1(g), kChunkBytes, C::kChunks, rows, 128, lane, 32);
           fence_async_smem();
+          __syncwarp();
         }
-        mbar_arrive_warp(f.bar(C::kBarReady + g % C::kStages0));
+        cp_async_arrive(f.bar(C::kBarReady + g % C::kStages0));
       }
     }
+    cp_async_wait_all();
   } else if (warp == kMmaWarp || (C::kApart && warp == kSumWarp)) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kIdS = idesc_bf16_f32(kKT, 128, false, false);
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             issue_s(0, gs);
-            ok = (gs == 0 || f.wait(C::kBarDs, gs - 1)) && ready1(gs);
+            ok = (gs == 0 || f.wait(C::kBarDpFree, gs - 1)) && ready1(gs);
             if (!ok) break;
             tc_fence_after();
             issue_s(1, gs);
@@ -569,13 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // dV and dK; that dS is there says that S^T and dP^T have been computed
           for (int jj = 0; jj < ns && ok; ++jj) {
             const int gs = g + jj;
-            ok = ready0(gs) && f.landed1(gs) && (jj > 0 || q == 0 || f.wait(C::kBarAccFree, q - 1)) && f.wait(C::kBarP, gs);
+            ok = ready0(gs) && f.landed1(gs) && (jj > 0 || q == 0 || f.wait(C::kBarAccFree, q - 1)) && f.wait(C::kBarDs, gs);
             if (!ok) break;
             tc_fence_after();
             issue_a(1, gs, jj == 0);
-            ok = f.wait(C::kBarDs, gs);
-            if (!ok) break;
-            tc_fence_after();
             issue_a(0, gs, jj == 0);
             mma_commit_w(f.bar(C::kBarDsFree));
             mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
@@ -675,6 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 p[16];
         tmem_ld32(tS, x);
         tmem_ld_wait(x);
+        if constexpr (C::kApart) {
+          tc_fence_before();
+          mbar_arrive_warp(f.bar(C::kBarP));
+        }
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 l = *reinterpret_cast<const float4*>(stat + c);
@@ -692,14 +700,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         tmem_st16(tP, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive_warp(f.bar(C::kBarP));
+        if constexpr (!C::kApart) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(f.bar(C::kBarP));
+        }
         ok = f.wait_calm(C::kBarDp, g);
         if (!ok) break;
         tc_fence_after();
         tmem_ld32(tDp, x);
         tmem_ld_wait(x);
+        if constexpr (C::kApart) {
+          tc_fence_before();
+          mbar_arrive_warp(f.bar(C::kBarDpFree));
+        }
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 d = *reinterpret_cast<const float4*>(stat + 128 + c);
@@ -853,9 +867,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ns = it.ns, n = it.n, i0 = it.x0, pos = i0 + ri;
       float l = -INFINITY, d = 0.f;
       if (ri < sh.tpt && pos < n) {
-        const long long at = static_cast<long long>(it.row0 + pos) * sh.Hq + it.h * G + (r - ri * G);
-        l = -kLog2e * args.lse[at];
-        d = -args.D[at];
+        const long long at = (static_cast<long long>(it.h) * sh.T + it.row0 + i0) * G + r;
+        l = args.neg_lse[at];
+        d = args.neg_d[at];
       }
       const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
       const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive
@@ -912,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- launches
-// The workspace: D, then the two lists where they are made.
+// The workspace: -LSE and -D, then the two lists where they are made.
 struct BwdPlan {
   int slots;
   int cap[2], unit[2];  // dK and dV; dQ
@@ -926,7 +940,7 @@ BwdPlan bwd_plan(int B, int T, int Hq, int Hkv, int sms) {
   p.slots = sms;
   p.unit[0] = kKT;
   p.unit[1] = 128 / (Hq / Hkv);
-  p.bytes = (static_cast<size_t>(T) * Hq * 4 + 255) / 256 * 256;
+  p.bytes = (static_cast<size_t>(T) * Hq * 8 + 255) / 256 * 256;
   for (int i = 0; i < 2; ++i) {
     p.cap[i] = T / p.unit[i] + B;
     p.listed[i] = static_cast<long long>(p.cap[i]) * Hkv > p.slots;
@@ -937,7 +951,7 @@ BwdPlan bwd_plan(int B, int T, int Hq, int Hkv, int sms) {
 }
 
 template <int D>
-int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[2], float* rowsum, cudaStream_t stream) {
+int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[2], float* stats, cudaStream_t stream) {
   const PackedProblem& p = b.p;
   const PackedShape& s = p.s;
   const int G = s.by_group.G;
@@ -959,13 +973,13 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   const long long rows = static_cast<long long>(s.T) * s.Hq, per = 256 / (D / 8) * 4;
   cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
                                     0, stream, static_cast<const __nv_bfloat16*>(b.o),
-                                    static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, rowsum, rows,
-                                    GroupDiv::of(s.Hq));
+                                    static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, b.lse, stats, stats + rows, s.Hq,
+                                    GroupDiv::of(s.T * G), s.by_group, rows);
   if (e != cudaSuccess) return -3;
   BwdArgs a{};
   a.s = s;
-  a.lse = b.lse;
-  a.D = rowsum;
+  a.neg_lse = stats;
+  a.neg_d = stats + rows;
   a.status = status;
   a.scale = p.scale;
   const float sl2 = p.scale * kLog2e;
@@ -1004,8 +1018,8 @@ int launch_packed_bwd(const PackedBwd& b, void* workspace, cudaStream_t stream) 
   }
   const int rc = launch_packed_plan(s, lists, 2, stream);
   if (rc != 0) return rc;
-  float* rowsum = static_cast<float*>(workspace);
-  return b.p.d == 64 ? launch_d<64>(b, plan, lists, rowsum, stream) : launch_d<128>(b, plan, lists, rowsum, stream);
+  float* stats = static_cast<float*>(workspace);
+  return b.p.d == 64 ? launch_d<64>(b, plan, lists, stats, stream) : launch_d<128>(b, plan, lists, stats, stream);
 }
 
 }  // namespace fa

@@ -79,8 +79,9 @@ struct Cfg {
   // stages of the streamed pair, Q and dO (dK, dV) or K and V (dQ): what there is room for
   static constexpr int kStages0 = D == 64 ? 4 : kKeys ? 2 : 3, kStages1 = D == 64 ? 4 : 2;
   static constexpr int kStatStages = D == 64 ? 4 : 2;
-  static constexpr int kResOff = 0;  // resident pair of tiles: K and V, or Q and dO
-  static constexpr int kRing0 = 2 * kTileBytes, kRing1 = kRing0 + kStages0 * kTileBytes;
+  static constexpr int kResOff = 0;  // resident pairs of tiles: K and V, or Q and dO (d = 64: the next item's too)
+  static constexpr int kResBufs = D == 64 ? 2 : 1;
+  static constexpr int kRing0 = kResBufs * 2 * kTileBytes, kRing1 = kRing0 + kStages0 * kTileBytes;
   static constexpr int kStatOff = kRing1 + kStages1 * kTileBytes;  // dK, dV: per stage 128 -LSE, 128 -D
   static constexpr int kOutOff = kStatOff + (kKeys ? kStatStages * 1024 : 0);
   static constexpr bool kStaged = D == 64 || kKeys;  // write-back by way of 2 KiB per warp (dQ, d = 128: no room)
@@ -93,8 +94,8 @@ struct Cfg {
   static constexpr int kIssuers = kApart ? 2 : 1;
   enum : int {
     kBarResFull = 0,
-    kBarResFree = 1,
-    kBarLoad0 = 2,                        // a stage's tile has landed
+    kBarResFree = kBarResFull + kResBufs,
+    kBarLoad0 = kBarResFree + kResBufs,   // a stage's tile has landed
     kBarEmpty0 = kBarLoad0 + kStages0,    // and is not needed any more
     kBarReady = kBarEmpty0 + kStages0,    // the helper is done with the step
     kBarLoad1 = kBarReady + kStages0,
@@ -257,6 +258,7 @@ struct Frame {
   __device__ __forceinline__ bool stats_free(int g) const {
     return g < C::kStatStages || at_step(C::kBarEmpty0, C::kStages0, g - C::kStatStages);
   }
+  __device__ __forceinline__ bool resident(int q) const { return at_step(C::kBarResFull, C::kResBufs, q); }
   // The g-th phase of a barrier that has one per step.
   __device__ __forceinline__ bool wait(int b, int g) const { return mbar_wait_w(bar(b), g & 1, abort_flag); }
   __device__ __forceinline__ float* stats(int g) const {
@@ -272,8 +274,7 @@ struct Frame {
     smem = raw;
     abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     if (threadIdx.x == 0) {
-      mbar_init(bar(C::kBarResFull), 1);
-      mbar_init(bar(C::kBarResFree), 1);
+      for (int i = C::kBarResFull; i < C::kBarLoad0; ++i) mbar_init(bar(i), 1);
       for (int i = C::kBarLoad0; i < C::kBarS; ++i)
         mbar_init(bar(i), kKeys && i >= C::kBarReady && i < C::kBarLoad1 ? 32 : 1);  // (dK, dV's helper: each lane's copies)
       mbar_init(bar(C::kBarS), kKeys ? 2 : 1);  // dK, dV: and the MMA warp, which passes on that the statistics are written
@@ -350,13 +351,14 @@ struct Frame {
       if (!ok) break;
       items()[q % kItems] = it;
       mbar_arrive(bar(C::kBarItemFull + q % kItems));
-      if (q > 0) ok = mbar_wait(bar(C::kBarResFree), (q - 1) & 1, abort_flag);
+      const int rb = q % C::kResBufs;
+      if (q >= C::kResBufs) ok = mbar_wait(bar(C::kBarResFree + rb), (q / C::kResBufs - 1) & 1, abort_flag);
       if (!ok) break;
-      mbar_arrive_expect_tx(bar(C::kBarResFull), res_bytes);
+      const uint32_t res = base + C::kResOff + rb * 2 * C::kTileBytes, res_full = bar(C::kBarResFull + rb);
+      mbar_arrive_expect_tx(res_full, res_bytes);
       for (int c = 0; c < C::kChunks; ++c) {
-        tma_load_4d(base + C::kResOff + c * kChunkBytes, res0, bar(C::kBarResFull), c * 64, 0, h, e.row0 + e.i0);
-        tma_load_4d(base + C::kResOff + C::kTileBytes + c * kChunkBytes, res1, bar(C::kBarResFull), c * 64, 0, h,
-                    e.row0 + e.i0);
+        tma_load_4d(res + c * kChunkBytes, res0, res_full, c * 64, 0, h, e.row0 + e.i0);
+        tma_load_4d(res + C::kTileBytes + c * kChunkBytes, res1, res_full, c * 64, 0, h, e.row0 + e.i0);
       }
       *res_loads = ++q;
       for (int jj = 0; jj < it.ns && ok; ++jj, ++g) {
@@ -437,7 +439,8 @@ struct Frame {
       // Every role has stopped, so the flag is final: let every copy this
       // thread started land before the CTA exits (only the last load of each
       // buffer can still be pending).
-      if (res_loads > 0) mbar_wait(bar(C::kBarResFull), (res_loads - 1) & 1, nullptr);
+      for (int i = max(res_loads - C::kResBufs, 0); i < res_loads; ++i)
+        mbar_wait(bar(C::kBarResFull + i % C::kResBufs), (i / C::kResBufs) & 1, nullptr);
       for (int i = max(stage_loads[0] - C::kStages0, 0); i < stage_loads[0]; ++i)
         mbar_wait(bar(C::kBarLoad0 + i % C::kStages0), (i / C::kStages0) & 1, nullptr);
       for (int i = max(stage_loads[1] - C::kStages1, 0); i < stage_loads[1]; ++i)
@@ -524,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                    cols1 = sdesc_sw128(f.base + C::kRing1, kChunkBytes, 1024);
     const uint32_t tmem = f.tmem;
     bool ok = true;
-    // S^T = K Q^T (which = 0) or dP^T = V dO^T (1) for stream step g
-    auto issue_s = [&](int which, int g) {
-      const uint64_t a = res + (which ? kTile : 0);
+    // S^T = K Q^T (which = 0) or dP^T = V dO^T (1) for stream step g, of item q
+    auto issue_s = [&](int which, int q, int g) {
+      const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
       const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -559,19 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kMmaWarp) {
           // S^T once its predecessor has become P, dP^T once its has become dS:
           // they are not needed before the compute warps are through with the other
-          ok = f.wait(C::kBarResFull, q);
+          ok = f.resident(q);
           for (int jj = 0; jj < ns && ok; ++jj) {
             const int gs = g + jj;
             ok = (gs == 0 || f.wait(C::kBarP, gs - 1)) && ready0(gs);
             if (!ok) break;
             tc_fence_after();
-            issue_s(0, gs);
+            issue_s(0, q, gs);
             ok = (gs == 0 || f.wait(C::kBarDpFree, gs - 1)) && ready1(gs);
             if (!ok) break;
             tc_fence_after();
-            issue_s(1, gs);
+            issue_s(1, q, gs);
           }
-          if (ok) mma_commit_w(f.bar(C::kBarResFree));
+          if (ok) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
         } else {
           // dV and dK; that dS is there says that S^T and dP^T have been computed
           for (int jj = 0; jj < ns && ok; ++jj) {
@@ -588,15 +591,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) mma_commit_w(f.bar(C::kBarFinal));
         }
       } else {
-        ok = f.wait(C::kBarResFull, q) && ready0(g);
+        ok = f.resident(q) && ready0(g);
         if (!ok) break;
         tc_fence_after();
-        issue_s(0, g);
+        issue_s(0, q, g);
         ok = f.landed1(g);
         if (!ok) break;
         tc_fence_after();
-        issue_s(1, g);
-        if (ns == 1) mma_commit_w(f.bar(C::kBarResFree));
+        issue_s(1, q, g);
+        if (ns == 1) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
         for (int jj = 0; jj < ns; ++jj) {
           const int gs = g + jj;
           ok = (jj > 0 || q == 0 || f.wait(C::kBarAccFree, q - 1)) && f.wait(C::kBarP, gs);
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ready0(gs + 1);
             if (!ok) break;
             tc_fence_after();
-            issue_s(0, gs + 1);
+            issue_s(0, q, gs + 1);
           }
           ok = f.wait(C::kBarDs, gs);
           if (!ok) break;
@@ -619,9 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = f.landed1(gs + 1);
             if (!ok) break;
             tc_fence_after();
-            issue_s(1, gs + 1);
+            issue_s(1, q, gs + 1);
             // K and V are free once the item's last S^T and dP^T have completed
-            if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree));
+            if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
           } else {
             mma_commit_w(f.bar(C::kBarFinal));
           }
@@ -784,9 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t cols0 = sdesc_sw128(f.base + C::kRing0, kChunkBytes, 1024);
     const uint32_t tmem = f.tmem;
     bool ok = true;
-    // S = Q K^T (which = 0) or dP = dO V^T (1) for stream step g
-    auto issue_s = [&](int which, int g) {
-      const uint64_t a = res + (which ? kTile : 0);
+    // S = Q K^T (which = 0) or dP = dO V^T (1) for stream step g, of item q
+    auto issue_s = [&](int which, int q, int g) {
+      const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
       const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -804,20 +807,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == kMmaWarp) {
         // S and dP, each once its predecessor is in registers (both once dP is: 345
         // us instead of 295 for 8 x up to 4096 tokens, 32 heads, d = 128)
-        ok = f.wait(C::kBarResFull, q);
+        ok = f.resident(q);
         for (int jj = 0; jj < ns && ok; ++jj) {
           const int gs = g + jj;
           ok = (gs == 0 || f.wait(C::kBarP, gs - 1)) && f.landed0(gs) && f.ready(gs);
           if (!ok) break;
           tc_fence_after();
-          issue_s(0, gs);
+          issue_s(0, q, gs);
           ok = (gs == 0 || f.wait(C::kBarDpFree, gs - 1)) && f.landed1(gs);
           if (!ok) break;
           tc_fence_after();
-          issue_s(1, gs);
+          issue_s(1, q, gs);
           mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
         }
-        if (ok) mma_commit_w(f.bar(C::kBarResFree));
+        if (ok) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
       } else {
         // dQ (+)= dS K; that dS is there says that S has been computed
         for (int jj = 0; jj < ns && ok; ++jj) {

@@ -653,26 +653,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tDp = f.tmem + lane_base + C::kColDp + wg * kCols;
     const uint32_t tP = C::kApart ? f.tmem + lane_base + C::kColP + wg * kCols / 2 : tS;
     const uint32_t tDs = C::kApart ? f.tmem + lane_base + C::kColDs + wg * kCols / 2 : tDp;
-    // tokens of the group's first and last columns
-    const int group_i0 = sh.by_group.div(wg * kCols), group_i1 = sh.by_group.div(wg * kCols + kCols - 1);
     const float2 sl2 = make_float2(args.scale_log2, args.scale_log2);
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
       if (!ok || f.items()[q % kItems].end) break;
-      const Item& it = f.items()[q % kItems];
-      const int ns = it.ns, k0 = it.x0;
+      const Item& it = f.items()[q % kItems];  // (given back at the item's end)
       int i0 = it.t0 * sh.tpt;
-      for (int jj = 0; jj < ns; ++jj, ++g, i0 += sh.tpt) {
+      const int end = g + it.ns;
+      // queries of a key k: [k, k + window); a border cuts the warp's part of a tile
+      // that begins before token cut_lo, or from cut_hi on
+      const int warp_k0 = it.x0 + (warp & 3) * 32;
+      const int cut_lo = sh.causal ? warp_k0 + 31 - sh.by_group.div(wg * kCols) : -0x7fffffff;
+      const int cut_hi = sh.window > 0 ? warp_k0 + sh.window - sh.by_group.div(wg * kCols + kCols - 1) : 0x7fffffff;
+      for (; g < end; ++g, i0 += sh.tpt) {
         const float* stat = f.stats(g) + wg * kCols;
-        // queries of this key: [k0 + row, k0 + row + window); whether a border cuts the warp's part
-        const bool cut = (sh.causal && i0 + group_i0 < k0 + (warp & 3) * 32 + 31) ||
-                         (sh.window > 0 && i0 + group_i1 >= k0 + (warp & 3) * 32 + sh.window);
+        const bool cut = i0 < cut_lo || i0 >= cut_hi;
         uint32_t seen = 0xffffffffu;
         if (cut) {
-          const int lo = sh.causal ? min(max(k0 + row - i0, 0), 128) * G - wg * kCols : 0;
-          const int hi = sh.window > 0 ? min(max(k0 + row - i0 + sh.window, 0), 128) * G - wg * kCols : kCols;
+          const int k = it.x0 + row - i0;
+          const int lo = sh.causal ? min(max(k, 0), 128) * G - wg * kCols : 0;
+          const int hi = sh.window > 0 ? min(max(k + sh.window, 0), 128) * G - wg * kCols : kCols;
           seen = bits_between(lo, hi);
         }
         ok = f.wait_calm(C::kBarS, g);

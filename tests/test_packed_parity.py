@@ -554,3 +554,226 @@ def test_a_layer_and_its_gradients_in_one_graph(d, Hq, Hkv, window):
     whole.copy_(randn(rows.rng, *whole.shape))
     g.replay()
     check(*outs)
+
+
+def test_a_prompt_and_its_answer_with_positions_of_several_axes():
+    """The prompt: rotation, attention over its own rows, its keys and values into the pages. Then token by token:
+    rotation, append, attention over the pages."""
+    from test_paged_parity import World, check_attn, check_cache
+    lens, Hq, Hkv, d, sections = [45, 1, 130], 8, 2, 128, (16, 24, 24)
+    rows = Rows(lens, Hq, Hkv, d, seed=31)
+    w = World([n + 4 for n in lens], Hkv, 16, d, seed=32)
+    cache, cos_sin = w.to_gpu(), tables(200, 64)
+    rope = tuple(torch.from_numpy(x).cuda() for x in cos_sin)
+    axis_of = [a for a, m in enumerate(sections) for _ in range(m)]
+    turned = lambda x, pos: want_rope(x, pos, axis_of, *cos_sin, False, False)  # noqa: E731
+
+    def rotated(q, k, pos):
+        a, b = fa.fa_rope_axes(q, k, torch.from_numpy(pos).cuda(), rope, sections=sections)
+        assert torch.equal(a.cpu(), turned(q.cpu(), pos)) and torch.equal(b.cpu(), turned(k.cpu(), pos))
+        return a, b
+
+    (q, k, v), cu = rows.on_gpu()
+    a, b = rotated(q, k, w.rng.integers(0, 200, (3, rows.T)).astype(np.int32))
+    o, lse = fa.fa_packed_fwd(a, b, v, cu, causal=True)
+    w.lens = lens
+    host, batch = w.batch(lens)
+    fa.fa_paged_append(cache, batch, b, v)
+    done()
+    rows.q, rows.k = a.cpu(), b.cpu()
+    check_fwd(rows, o, lse, True, 1 / math.sqrt(d), 0)
+    w.oracle.append(w.table, lens, host, rows.k.float().numpy(), rows.v.float().numpy())
+    check_cache(w, cache)
+    for step in range(1, 5):
+        w.lens = [n + step for n in lens]
+        host, batch = w.batch([1, 1, 1])
+        q, k, v = (randn(w.rng, 3, h, d).cuda() for h in (Hq, Hkv, Hkv))
+        a, b = rotated(q, k, w.rng.integers(0, 200, (3, 3)).astype(np.int32))
+        fa.fa_paged_append(cache, batch, b, v)
+        o, lse = fa.fa_paged_attn(cache, batch, a)
+        done()
+        w.oracle.append(w.table, w.lens, host, b.cpu().float().numpy(), v.cpu().float().numpy())
+        check_cache(w, cache)
+        check_attn(w, host, o, lse, a.cpu(), 1 / math.sqrt(d))
+
+
+# ------------------------------------------------------------------ layouts, sizes, calls at once
+def backward_of(rows, o, lse, do, causal, window, **kw):
+    (q, k, v), cu = rows.on_gpu()
+    return fa.fa_packed_bwd(q, k, v, o.cuda(), lse.cuda(), do.cuda(), cu, causal=causal, window=window, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 1.0])
+def test_packed_bwd_scales(d, scale):
+    rows = Rows([150, 40], 4, 2, d, seed=d + 1)
+    rows.whole *= 0.25
+    o, lse = forward_for(rows, True, scale, 0)
+    do = randn(rows.rng, rows.T, 4, d)
+    got = backward_of(rows, o, lse, do, True, 0, scale=scale)
+    done()
+    check_bwd(rows, o, lse, do, got, True, scale, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_at_odd_distances_and_bases(d):
+    """Bases that are multiples of 16 bytes and of nothing more, row distances that are odd multiples of 16 bytes."""
+    rows = Rows([90, 3, 200], 6, 2, d, seed=d + 2, trail=2)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, True, scale, 0)
+    do = randn(rows.rng, rows.T, 6, d)
+
+    def apart(x, lead, extra):
+        T, H, _ = x.shape
+        flat = torch.full((lead + T * (H * d + extra),), 7.0, dtype=torch.bfloat16, device="cuda")
+        view = flat[lead:].view(T, H * d + extra)[:, :H * d].view(T, H, d)
+        view.copy_(x)
+        return view, flat
+
+    q, k, v, g = (apart(x, *at)[0] for x, at in ((rows.q, (8, 8)), (rows.k, (24, 40)), (rows.v, (40, 24)), (do, (56, 8))))
+    outs = [apart(torch.full_like(x, 7.0), *at) for x, at in ((rows.q, (8, 24)), (rows.k, (8, 8)), (rows.v, (24, 40)))]
+    cu = torch.from_numpy(rows.cu).cuda()
+    og = torch.full((8 + o.numel(),), 7.0, dtype=torch.bfloat16, device="cuda")[8:].view(o.shape)
+    got, l = fa.fa_packed_fwd(q, k, v, cu, causal=True, out=og)
+    check_fwd(rows, got, l, True, scale, 0)
+    og.copy_(o)
+    before = [flat.clone() for _, flat in outs]
+    grads = fa.fa_packed_bwd(q, k, v, og, lse.cuda(), g, cu, causal=True, dq=outs[0][0], dk=outs[1][0], dv=outs[2][0])
+    done()
+    check_bwd(rows, o, lse, do, grads, True, scale, 0)
+    for (view, flat), was in zip(outs, before):      # and nothing between the rows or behind them
+        view[rows.cu[0]:rows.cu[-1]] = 7.0
+        assert torch.equal(flat, was)
+
+
+class Slice:
+    """Rows [lo, hi) of tensors on the GPU, as `Rows` of one sequence."""
+
+    def __init__(self, q, k, v, lo, hi):
+        self.q, self.k, self.v = (x[lo:hi].cpu() for x in (q, k, v))
+        self.cu, self.T = np.array([0, hi - lo]), hi - lo
+        self.Hq, self.G = q.shape[1], q.shape[1] // k.shape[1]
+
+
+@pytest.mark.parametrize("layout", ["many rows", "far rows"])
+def test_offsets_past_32_bits(layout):
+    """More than 2^31 elements: of many rows of many heads, and of rows that lie far apart."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    d, n = 128, 100
+    if layout == "many rows":
+        Hq, Hkv, B, wide = 128, 2, 1400, 0
+    else:
+        Hq, Hkv, B, wide = 4, 2, 6, 1 << 22
+    T = B * n
+    whole = torch.empty(T, wide or Hq * d, dtype=torch.bfloat16, device="cuda")
+    assert whole.numel() > 2 ** 31
+    q = whole[:, -Hq * d:].view(T, Hq, d)
+    q.normal_(generator=gen)
+    k, v = (torch.empty(T, Hkv, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(2))
+    do = torch.empty(T, Hq, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    cos, sin = tables(50, d // 2)
+    pos = (torch.arange(T, dtype=torch.int32, device="cuda") % 50)[None].contiguous()
+    last = q[-n:].cpu()
+    a, b = fa.fa_rope_axes(q, k, pos, (torch.from_numpy(cos).cuda(), torch.from_numpy(sin).cuda()), sections=(d // 2,),
+                           q_out=q)
+    assert torch.equal(q[-n:].cpu(), want_rope(last, pos[:, -n:].cpu().numpy(), [0] * (d // 2), cos, sin, False, False))
+    o, lse = fa.fa_packed_fwd(q, b, v, cu, causal=True)
+    grad = torch.empty_like(whole)[:, :Hq * d].view(T, Hq, d)
+    grads = fa.fa_packed_bwd(q, b, v, o, lse, do, cu, causal=True, dq=grad)
+    done()
+    for lo in (0, T - n):
+        at = slice(lo, lo + n)
+        one = Slice(q, b, v, lo, lo + n)
+        check_fwd(one, o[at], lse[at], True, 1 / math.sqrt(d), 0)
+        check_bwd(one, o[at].cpu(), lse[at].cpu(), do[at].cpu(), [x[at] for x in grads], True, 1 / math.sqrt(d), 0)
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    both = []
+    for i, (lens, Hq, d) in enumerate((([700, 3, 1200, 40] * 3, 8, 128), ([33, 2000, 500, 0] * 3, 12, 64))):
+        rows = Rows(lens, Hq, 4, d, seed=40 + i)
+        (q, k, v), cu = rows.on_gpu()
+        do = randn(rows.rng, rows.T, Hq, d).cuda()
+        o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True)
+        want = (o, lse, *fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True))
+        both.append((q, k, v, o, lse, do, cu, want, torch.cuda.Stream()))
+    done()
+    outs = []
+    for _ in range(4):
+        for q, k, v, o, lse, do, cu, _, s in both:
+            outs.append((*fa.fa_packed_fwd(q, k, v, cu, causal=True, stream=s),
+                         *fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True, stream=s)))
+    done()
+    for i, got in enumerate(outs):
+        assert all(torch.equal(a, b) for a, b in zip(got, both[i % 2][7]))
+
+
+def test_two_graphs_with_one_workspace_in_turn():
+    rows = [Rows(lens, 4, 2, 64, seed=50 + i) for i, lens in enumerate(([300, 5, 600, 0] * 40, [90] * 160))]
+    ws = torch.empty(max(f(160, r.T, 4, 2, 64) for r in rows for f in (fa.fa_packed_fwd_workspace_bytes,
+                                                                      fa.fa_packed_bwd_workspace_bytes)),
+                     dtype=torch.uint8, device="cuda").fill_(255)
+    made = []
+    for r in rows:
+        (q, k, v), cu = r.on_gpu()
+        do = randn(r.rng, r.T, 4, 64).cuda()
+
+        def step(q=q, k=k, v=v, cu=cu, do=do, **kw):
+            o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True, **kw)
+            return (o, lse, *fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True, **kw))
+
+        want = step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step(workspace=ws)
+        made.append((g, got, want, (q, k, v, cu, do)))
+    for _ in range(3):
+        for g, got, want, _ in made:
+            for x in got:
+                x.zero_()
+            g.replay()
+            done()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_arguments_that_the_binding_refuses():
+    T, Hq, Hkv, d = 40000, 4, 2, 64
+    q, do = (torch.zeros(T, Hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros(T, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(T, Hq, device="cuda")
+    fwd = lambda **kw: fa.fa_packed_fwd(**{**dict(q=q, k=k, v=v, cu=cu, causal=True), **kw})  # noqa: E731
+    bwd = lambda **kw: fa.fa_packed_bwd(**{**dict(q=q, k=k, v=v, o=o, lse=lse, do=do, cu=cu, causal=True), **kw})  # noqa: E731
+    for call in (fwd, bwd):
+        for kw in (dict(q=q.half()), dict(k=k.float()), dict(cu=cu.long())):
+            with pytest.raises(TypeError):
+                call(**kw)
+        for kw in (dict(q=q[0]), dict(k=k[1:]), dict(v=v[:, :1]), dict(v=v[:, :, :32]), dict(cu=cu.cpu()), dict(cu=cu[:0]),
+                   dict(cu=cu[None]), dict(k=k.cpu()), dict(q=q.transpose(0, 1)), dict(window=2 ** 40),
+                   dict(workspace=torch.empty(1 << 24, dtype=torch.uint8))):
+            with pytest.raises(ValueError):
+                call(**kw)
+        for kw in (dict(q=q[:, :3]), dict(window=-1), dict(causal=False, window=3), dict(scale=float("nan")),
+                   dict(scale=-0.5), dict(k=k[:1].expand(T, Hkv, d)),
+                   dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+            with pytest.raises((fa.FAError, ValueError)):     # (three heads: o has not three, says the binding)
+                call(**kw)
+    for kw in (dict(out=q[:, :, :32]), dict(out=torch.empty(T, 2 * Hq, d, dtype=torch.bfloat16, device="cuda")[:, ::2]),
+               dict(lse=lse[:, :2]), dict(out=torch.empty(T, 2 * Hq * d, dtype=torch.bfloat16, device="cuda")[:, :Hq * d].view(T, Hq, d))):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+    for kw in (dict(out=q), dict(out=torch.empty_like(q).flatten()[4:], causal=False)):
+        with pytest.raises((fa.FAError, ValueError)):
+            fwd(**kw)
+    for kw in (dict(o=torch.empty(T, 2 * Hq * d, dtype=torch.bfloat16, device="cuda")[:, :Hq * d].view(T, Hq, d)),
+               dict(lse=lse.double()), dict(lse=lse.t()), dict(do=do[:5]), dict(dq=q[:, :2]), dict(dk=k.float())):
+        with pytest.raises((ValueError, TypeError)):
+            bwd(**kw)
+    for kw in (dict(dq=q), dict(dk=k, dv=torch.empty_like(v)), dict(dq=do), dict(dk=torch.empty_like(k), dv=None, dq=o)):
+        with pytest.raises(fa.FAError):
+            bwd(**kw)
+    same = torch.empty_like(k)
+    with pytest.raises(fa.FAError):
+        bwd(dk=same, dv=same)
+    done()

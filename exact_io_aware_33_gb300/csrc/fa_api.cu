@@ -615,8 +615,8 @@ int check_packed(int B, int T, int Hq, int Hkv, int d) {
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B < 0 || T < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID;
   if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;  // a tile of 128 rows holds a token's group
-  // rows of a key head, and items, are counted in 32 bits
-  if (static_cast<long long>(T) * Hq > 0x7fffffffLL - 4096 || static_cast<long long>(B) * Hkv > 0x3fffffffLL)
+  // rows of a key head, items, and a token with a window behind it are counted in 32 bits
+  if (static_cast<long long>(T) * Hq > 0x7fffffffLL - 4096 || T > 0x3fffffff || static_cast<long long>(B) * Hkv > 0x3fffffffLL)
     return FA_ERR_INVALID;
   return FA_OK;
 }

@@ -24,13 +24,26 @@ namespace fa {
 
 constexpr int kKeyTile = 128;
 
+// What the device reads of the borders and lists it takes from L2: the dQ kernel
+// reads what was written before the kernel ahead of it, which alone has waited.
+
+// Sum of x over this lane and those before it.
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, m);
+    if (lane >= m) x += y;
+  }
+  return x;
+}
+
 // First row of sequence b and its number of rows.
 struct PackedSeq {
   int row0, n;
 };
 
 __device__ __forceinline__ PackedSeq packed_seq(const PackedShape& s, int b, int* status) {
-  const int c0 = s.cu[b], c1 = s.cu[b + 1];
+  const int c0 = __ldcg(s.cu + b), c1 = __ldcg(s.cu + b + 1);
   PackedSeq q;
   q.row0 = min(max(c0, 0), s.T);
   q.n = min(max(c1, q.row0), s.T) - q.row0;
@@ -70,12 +83,7 @@ __device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, int unit
     PackedSeq q{0, 0};
     if (b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
     const int own = (q.n + unit - 1) / unit;
-    int end = own;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, end, m);
-      if (lane >= m) end += x;
-    }
+    const int end = warp_prefix(own, lane);
     const uint32_t past = __ballot_sync(0xffffffffu, before + end > e);
     if (past) {
       const int src = __ffs(past) - 1;
@@ -109,7 +117,7 @@ struct ItemQueue {
     if (l.entries == nullptr)
       own = find_entry(s, l.unit, by_head.div(next), status);
     else
-      count = l.head->count;
+      count = __ldcg(&l.head->count);
   }
   // By lane 0, with `left` steps of the present item still to be loaded, this one included.
   __device__ __forceinline__ void step(int left) {
@@ -125,7 +133,7 @@ struct ItemQueue {
       *e = own;
     } else {
       if (k >= count) return false;
-      const int4 r = list->entries[k];
+      const int4 r = __ldcg(list->entries + k);
       *e = PackedEntry{r.x, r.y, r.z};
     }
     *h = next - k * by_head.G;

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16*
     l[i] = 0.f;
     if (row < rows) {  // key head, then token and head of the group
       const int h = head_rows.div(static_cast<int>(row)), r = static_cast<int>(row) - h * head_rows.G;
-      const int t = group.div(r), hq = h * group.G + (r - t * group.G);
+      const int t = group.div(r);
+      const long long hq = static_cast<long long>(h) * group.G + (r - t * group.G);
       const long long at = static_cast<long long>(t) * Hq + hq;
       a[i] = *reinterpret_cast<const uint4*>(o + at * D + lane * 8);
       b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + hq * D + lane * 8);
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const long long stride = args.out_stride[which];
-        __nv_bfloat16* out = args.out[which] + static_cast<long long>(it.row0 + it.x0 + row) * stride + it.h * D;
+        __nv_bfloat16* out = args.out[which] + static_cast<long long>(it.row0 + it.x0 + row) * stride + static_cast<long long>(it.h) * D;
         put(which, which == 0 ? args.scale : 1.f, [&](int r) { return r < n ? out + r * stride : nullptr; });
       }
     });
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     f.write_back([&](const Item& it, auto&& put) {
       const int row = (warp & 3) * 32;
       const long long stride = args.out_stride[0];
-      __nv_bfloat16* out = args.out[0] + static_cast<long long>(it.row0 + it.x0) * stride + it.h * G * D;
+      __nv_bfloat16* out = args.out[0] + static_cast<long long>(it.row0 + it.x0) * stride + static_cast<long long>(it.h) * (G * D);
       put(0, args.scale, [&](int r) {
         const int x = sh.by_group.div(row + r);
         return x < sh.tpt && it.x0 + x < it.n ? out + x * stride + (row + r - x * G) * D : nullptr;
@@ -873,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = -INFINITY, d = 0.f;
       if (ri < sh.tpt && pos < n) {
         const long long at = (static_cast<long long>(it.h) * sh.T + it.row0 + i0) * G + r;
-        l = args.neg_lse[at];
-        d = args.neg_d[at];
+        l = __ldcg(args.neg_lse + at);
+        d = __ldcg(args.neg_d + at);
       }
       const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
       const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive

@@ -414,8 +414,8 @@ size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged
  *             NULL), 256-byte aligned; nothing in it outlives the call. Two
  *             calls in flight at once need two, also as replays of two
  *             captured graphs.
- * d is 64 or 128 and Hq / Hkv at most 128 (FA_ERR_UNSUPPORTED otherwise); T * Hq
- * is below 2^31 - 4096. The same inputs give the same bits. The device checks cu:
+ * d is 64 or 128 and Hq / Hkv at most 128 (FA_ERR_UNSUPPORTED otherwise); T is
+ * below 2^30 and T * Hq below 2^31 - 4096. The same inputs give the same bits. The device checks cu:
  * what does not rise or lies outside [0, T] is clamped and raises FA_ERR_INDEX
  * in the device status word; sequences that overlap leave unspecified outputs
  * in their rows.

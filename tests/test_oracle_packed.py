@@ -177,7 +177,8 @@ SHARED = [
     (dict(Hq=258, Hkv=2, qs=258 * 128), fa.FA_ERR_UNSUPPORTED),
     (dict(Hq=5), fa.FA_ERR_INVALID), (dict(Hq=0), fa.FA_ERR_INVALID), (dict(Hkv=0), fa.FA_ERR_INVALID),
     (dict(Hkv=-2), fa.FA_ERR_INVALID), (dict(B=-1), fa.FA_ERR_INVALID), (dict(T=-1), fa.FA_ERR_INVALID),
-    (dict(T=2 ** 29 - 1), fa.FA_ERR_INVALID), (dict(B=2 ** 30), fa.FA_ERR_INVALID),
+    (dict(T=2 ** 29 - 1), fa.FA_ERR_INVALID), (dict(T=2 ** 30, Hq=1, Hkv=1), fa.FA_ERR_INVALID),
+    (dict(B=2 ** 30), fa.FA_ERR_INVALID),
     (dict(scale=-1.0), fa.FA_ERR_INVALID), (dict(scale=float("nan")), fa.FA_ERR_INVALID),
     (dict(scale=float("inf")), fa.FA_ERR_INVALID), (dict(window=-1), fa.FA_ERR_INVALID),
     (dict(window=5, causal=0), fa.FA_ERR_INVALID),

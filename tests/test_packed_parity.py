@@ -689,6 +689,23 @@ def test_offsets_past_32_bits(layout):
         check_bwd(one, o[at].cpu(), lse[at].cpu(), do[at].cpu(), [x[at] for x in grads], True, 1 / math.sqrt(d), 0)
 
 
+def test_heads_past_32_bits():
+    """One token with so many heads that a row has more than 2^31 elements."""
+    H, d = (1 << 24) + 8, 128
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, do = (torch.empty(1, H, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(4))
+    assert q.numel() > 2 ** 31
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_packed_fwd(q, k, v, cu)
+    grads = fa.fa_packed_bwd(q, k, v, o, lse, do, cu)
+    done()
+    assert torch.equal(o, v)                     # its own key alone
+    for at in (slice(0, 4), slice(H - 4, H)):
+        one = Slice(q[:, at], k[:, at], v[:, at], 0, 1)
+        check_fwd(one, o[:, at], lse[:, at], False, 1 / math.sqrt(d), 0)
+        check_bwd(one, o[:, at].cpu(), lse[:, at].cpu(), do[:, at].cpu(), [x[:, at] for x in grads], False, 1 / math.sqrt(d), 0)
+
+
 def test_two_streams_with_workspaces_of_their_own():
     both = []
     for i, (lens, Hq, d) in enumerate((([700, 3, 1200, 40] * 3, 8, 128), ([33, 2000, 500, 0] * 3, 12, 64))):

@@ -145,12 +145,11 @@ struct ItemQueue {
 // Zeroes rows [row, rows) of a tile of `chunks` 128-byte-swizzled chunks, thread `tid` of `threads`.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int chunk_bytes, int chunks, int row, int rows, int tid,
                                           int threads) {
-  const int units = max(rows - row, 0) * 8;
-#pragma unroll 1
-  for (int i = tid; i < units * chunks; i += threads) {
-    const int c = i / units;
-    *reinterpret_cast<uint4*>(tile + c * chunk_bytes + row * 128 + (i - c * units) * 16) = make_uint4(0, 0, 0, 0);
-  }
+  uint8_t* at = tile + (tid & 7) * 16;
+#pragma unroll 2
+  for (int r = row + tid / 8; r < rows; r += threads / 8)
+#pragma unroll
+    for (int c = 0; c < chunks; ++c) *reinterpret_cast<uint4*>(at + c * chunk_bytes + r * 128) = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace fa

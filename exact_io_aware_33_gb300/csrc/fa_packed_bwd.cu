@@ -352,16 +352,20 @@ struct Frame {
       if (!ok) break;
       items()[q % kItems] = it;
       mbar_arrive(bar(C::kBarItemFull + q % kItems));
-      const int rb = q % C::kResBufs;
-      if (q >= C::kResBufs) ok = mbar_wait(bar(C::kBarResFree + rb), (q / C::kResBufs - 1) & 1, abort_flag);
-      if (!ok) break;
-      const uint32_t res = base + C::kResOff + rb * 2 * C::kTileBytes, res_full = bar(C::kBarResFull + rb);
-      mbar_arrive_expect_tx(res_full, res_bytes);
-      for (int c = 0; c < C::kChunks; ++c) {
-        tma_load_4d(res + c * kChunkBytes, res0, res_full, c * 64, 0, h, e.row0 + e.i0);
-        tma_load_4d(res + C::kTileBytes + c * kChunkBytes, res1, res_full, c * 64, 0, h, e.row0 + e.i0);
-      }
-      *res_loads = ++q;
+      auto load_resident = [&]() {
+        const int rb = q % C::kResBufs;
+        if (q >= C::kResBufs) ok = mbar_wait(bar(C::kBarResFree + rb), (q / C::kResBufs - 1) & 1, abort_flag);
+        if (!ok) return;
+        const uint32_t res = base + C::kResOff + rb * 2 * C::kTileBytes, res_full = bar(C::kBarResFull + rb);
+        mbar_arrive_expect_tx(res_full, res_bytes);
+        for (int c = 0; c < C::kChunks; ++c) {
+          tma_load_4d(res + c * kChunkBytes, res0, res_full, c * 64, 0, h, e.row0 + e.i0);
+          tma_load_4d(res + C::kTileBytes + c * kChunkBytes, res1, res_full, c * 64, 0, h, e.row0 + e.i0);
+        }
+        *res_loads = q + 1;
+      };
+      // a second buffer is free before the ring's next stage is, the only one after it
+      if (C::kResBufs > 1) load_resident();
       for (int jj = 0; jj < it.ns && ok; ++jj, ++g) {
         const int row = e.row0 + (it.t0 + jj) * (kKeys ? s.tpt : kKT);
         queue.step(it.ns - jj);
@@ -382,7 +386,9 @@ struct Frame {
         };
         load(1, C::kBarLoad1, C::kBarEmpty1, C::kStages1, ring1(g));
         if (ok) load(0, C::kBarLoad0, C::kBarEmpty0, C::kStages0, ring0(g));
+        if (C::kResBufs == 1 && jj == 0 && ok) load_resident();
       }
+      ++q;
     }
     if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
     if (ok) {

@@ -1,5 +1,5 @@
-"""Builds libfa.so in-tree with nvcc for sm_103a (GB300), and the paged cache's
-Python binding with the host compiler.
+"""Builds libfa.so in-tree with nvcc for sm_103a (GB300), and the Python binding of
+the paged cache's and packed sequences' calls with the host compiler.
 
 Each translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` at the repository root and linked into ``libfa.so`` (and
@@ -8,8 +8,8 @@ unit is recompiled only when it, or a header it may include, is newer than its
 object file; the binding also when Python or PyTorch is another one.
 
 libfa.so needs nvcc alone. Where the binding cannot be built (no PyTorch, one
-without CUDA, no g++), the library is built all the same, and the paged cache
-says so when it is first used.
+without CUDA, no g++), the library is built all the same, and those calls say so
+when they are first used.
 """
 
 from __future__ import annotations

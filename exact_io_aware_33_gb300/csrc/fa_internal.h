@@ -274,8 +274,8 @@ struct PackedProblem {
 // tokens): boxes of `tokens` x 1 x group x 64, 128-byte swizzle.
 bool make_map_packed(CUtensorMap* map, const void* ptr, int T, int heads, int group, int d, long long row_stride,
                      int tokens);
-// Fills the lists (one block each); nothing is launched when none has entries.
-int launch_packed_plan(const PackedShape& s, const PackedList* lists, int n, cudaStream_t stream);
+// Fills the forward's list.
+int launch_packed_plan(const PackedShape& s, const PackedList& list, cudaStream_t stream);
 size_t packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int sms);
 int launch_packed_fwd(const PackedProblem& p, void* o, float* lse, void* workspace, cudaStream_t stream);
 

@@ -18,21 +18,31 @@
 // fixed order, so the same inputs give the same bits.
 //
 // dK, dV: thread = key row = tensor-memory lane, S^T = K Q^T and dP^T = V dO^T
-// with both operands in shared memory, P^T and dS^T written over them as the
-// tensor-memory operands of dV += P^T dO and dK += dS^T Q: no probability goes
-// through shared memory. Per step the MMA warp issues dV, the next S^T, dK, the
-// next dP^T: the exponentials are formed under dK and dP^T, dS under dV and S^T.
-// dQ: thread = query row, S and dP leave for registers at once, so the next
-// step's are computed while dS of this one is formed; dS has columns of its own.
+// with both operands in shared memory, P^T and dS^T left in tensor memory as the
+// first operands of dV += P^T dO and dK += dS^T Q: no probability goes through
+// shared memory. At d = 64 P and dS have columns of their own; one warp issues
+// S^T and dP^T, each as soon as its predecessor is in registers, and another dV
+// and dK, neither waiting for the other's order. At d = 128 there are no columns
+// for that: P and dS lie over S and dP, and one warp issues dV, the next S^T, dK,
+// the next dP^T: the exponentials are formed under dK and dP^T, dS under dV and
+// S^T. dQ: thread = query row, S and dP leave for registers at once, dS has
+// columns of its own, and two warps issue.
 //
-// Tiles (fa_packed.cuh) hold a key head's whole group. What a box reaches past
-// its sequence belongs to another one and may hold anything; where it would be
-// multiplied by 0 a helper warp puts zeros in its place, in shared memory,
-// before the tile is handed to the tensor core.
+// Sixteen warps form P and dS (a quarter of a tile's columns per warpgroup), four
+// write the accumulators back while the next item is at work, and a helper brings
+// the row statistics. Tiles (fa_packed.cuh) hold a key head's whole group. What a
+// box reaches past its sequence belongs to another one and may hold anything;
+// where it would be multiplied by 0 the helper puts zeros in its place, in shared
+// memory, before the tile is handed to the tensor core.
 //
 // What bounds it: 14 d flops per visible pair on the tensor core (10 d of them
 // the algorithm's), which reads up to 128 bytes a clock of operands from shared
-// memory, and two exponentials per pair.
+// memory, two exponentials per pair, and the hand-offs between the roles: a step
+// of 128 x 128 takes 2780 (dK, dV) and 2020 (dQ) cycles at d = 128, 2150 and 1600
+// at d = 64, of which the tensor core is at work for 2200, 1600, 1100 and 800.
+// Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 624 us, 964
+// TFLOP/s of the algorithm's; one of 8192, 16 heads: 619, 1111; 24 images of
+// up to 1369 tokens, 16 heads, d = 64, unmasked: 277, 606.
 
 #include "fa_packed.cuh"
 
@@ -122,35 +132,55 @@ struct Cfg {
 };
 
 // ---------------------------------------------------------------- D
-// -D = -rowsum(dO O) and -LSE in log2 units for every row and head, laid out so
-// that the rows of a tile are contiguous; d / 8 lanes per row. Bound by memory:
-// 4 d bytes a row.
+// -D = -rowsum(dO O) and -LSE in log2 units for every row and head, read as they
+// lie and laid out so that the rows of a tile are contiguous; d / 8 lanes per row.
+// Bound by memory: 4 d + 12 bytes a row (37 us for 12400 tokens of 32 heads, d =
+// 128, 207 MB). Many threads with two rows each keep more loads in flight than
+// fewer with four or eight (46 and 67 us). The first blocks make the lists of the two kernels that
+// follow, under the others' loads (before them, it was 4 to 5 us of the call).
+constexpr int kSumThreads = 512;
+
+struct SumArgs {
+  PackedShape s;
+  PackedList lists[2];
+  int n_lists;
+  int* status;
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16* __restrict__ o,
-                                                            const __nv_bfloat16* __restrict__ dO, long long do_stride,
-                                                            const float* __restrict__ lse, float* __restrict__ neg_lse,
-                                                            float* __restrict__ neg_d, int Hq, GroupDiv head_rows,
-                                                            GroupDiv group, long long rows) {
-  constexpr int kLanes = D / 8, kUnroll = 4;
+__global__ void __launch_bounds__(kSumThreads, 4) packed_rowsum_kernel(const __nv_bfloat16* __restrict__ o,
+                                                                    const __nv_bfloat16* __restrict__ dO,
+                                                                    long long do_stride, const float* __restrict__ lse,
+                                                                    float* __restrict__ neg_lse, float* __restrict__ neg_d,
+                                                                    GroupDiv by_token, long long rows,
+                                                                    const __grid_constant__ SumArgs args) {
+  constexpr int kLanes = D / 8, kUnroll = 2;
   grid_dep_wait();
   grid_dep_launch();
+  const int block = static_cast<int>(blockIdx.x) - args.n_lists;
+  if (block < 0) {
+    make_list<kSumThreads>(args.s, args.lists[blockIdx.x], args.status);
+    return;
+  }
+  const GroupDiv group = args.s.by_group;
+  const int Hq = args.s.Hq;
   const int lane = threadIdx.x % kLanes;
-  const long long per = 256 / kLanes, first = static_cast<long long>(blockIdx.x) * per * kUnroll + threadIdx.x / kLanes;
+  const long long per = kSumThreads / kLanes, first = block * per * kUnroll + threadIdx.x / kLanes;
   uint4 a[kUnroll], b[kUnroll];
   float l[kUnroll];
+  long long to[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const long long row = first + i * per;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
     l[i] = 0.f;
-    if (row < rows) {  // key head, then token and head of the group
-      const int h = head_rows.div(static_cast<int>(row)), r = static_cast<int>(row) - h * head_rows.G;
-      const int t = group.div(r);
-      const long long hq = static_cast<long long>(h) * group.G + (r - t * group.G);
-      const long long at = static_cast<long long>(t) * Hq + hq;
-      a[i] = *reinterpret_cast<const uint4*>(o + at * D + lane * 8);
-      b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + hq * D + lane * 8);
-      l[i] = lse[at];
+    if (row < rows) {
+      const int t = by_token.div(static_cast<int>(row)), hq = static_cast<int>(row) - t * Hq;
+      a[i] = *reinterpret_cast<const uint4*>(o + row * D + lane * 8);
+      b[i] = *reinterpret_cast<const uint4*>(dO + t * do_stride + static_cast<long long>(hq) * D + lane * 8);
+      l[i] = lse[row];
+      const int h = group.div(hq);
+      to[i] = (static_cast<long long>(h) * args.s.T + t) * group.G + (hq - h * group.G);
     }
   }
 #pragma unroll
@@ -166,8 +196,8 @@ __global__ void __launch_bounds__(256) packed_rowsum_kernel(const __nv_bfloat16*
     for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     const long long row = first + i * per;
     if (lane == 0 && row < rows) {
-      neg_d[row] = -sum;
-      neg_lse[row] = -kLog2e * l[i];
+      neg_d[to[i]] = -sum;
+      neg_lse[to[i]] = -kLog2e * l[i];
     }
   }
 }
@@ -250,8 +280,9 @@ struct Frame {
   }
   // The same for the compute warps. At d = 128 they wait for the tensor core most
   // of the time, and asleep they take no issue slots and shared-memory cycles from
-  // it (655 us instead of 669, 8 x up to 4096 tokens, 32 / 8 heads); at d = 64 they
-  // are what is waited for (232 instead of 240, 8 x 2048 tokens, 12 heads).
+  // it (655 us instead of 669 when it was put in, 8 documents of up to 4096 tokens,
+  // 32 / 8 heads); at d = 64 they are what is waited for (232 instead of 240, 8 x
+  // 2048 tokens, 12 heads).
   __device__ __forceinline__ bool wait_calm(int b, int g) const {
     return D == 64 ? mbar_wait_w(bar(b), g & 1, abort_flag) : mbar_wait_sleep_w(bar(b), g & 1, abort_flag);
   }
@@ -815,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       f.give_item(q);
       if (warp == kMmaWarp) {
         // S and dP, each once its predecessor is in registers (both once dP is: 345
-        // us instead of 295 for 8 x up to 4096 tokens, 32 heads, d = 128)
+        // us instead of 295 when it was put in, 8 x up to 4096 tokens, 32 heads, d = 128)
         ok = f.resident(q);
         for (int jj = 0; jj < ns && ok; ++jj) {
           const int gs = g + jj;
@@ -982,11 +1013,16 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   if (!ensure_smem_attr(reinterpret_cast<const void*>(dkv), kDkvBytes, kSlot) ||
       !ensure_smem_attr(reinterpret_cast<const void*>(dq), kDqBytes, kSlot + 1))
     return -3;
-  const long long rows = static_cast<long long>(s.T) * s.Hq, per = 256 / (D / 8) * 4;
-  cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
-                                    0, stream, static_cast<const __nv_bfloat16*>(b.o),
-                                    static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, b.lse, stats, stats + rows, s.Hq,
-                                    GroupDiv::of(s.T * G), s.by_group, rows);
+  const long long rows = static_cast<long long>(s.T) * s.Hq, per = kSumThreads / (D / 8) * 2;
+  SumArgs sum{};
+  sum.s = s;
+  sum.status = status;
+  for (const PackedList& l : lists)
+    if (l.entries != nullptr) sum.lists[sum.n_lists++] = l;
+  cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per + sum.n_lists)),
+                                    dim3(kSumThreads), 0, stream, static_cast<const __nv_bfloat16*>(b.o),
+                                    static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, b.lse, stats, stats + rows,
+                                    GroupDiv::of(s.Hq), rows, sum);
   if (e != cudaSuccess) return -3;
   BwdArgs a{};
   a.s = s;
@@ -1028,8 +1064,6 @@ int launch_packed_bwd(const PackedBwd& b, void* workspace, cudaStream_t stream) 
       lists[i].entries = reinterpret_cast<int4*>(lists[i].head + 1);
     }
   }
-  const int rc = launch_packed_plan(s, lists, 2, stream);
-  if (rc != 0) return rc;
   float* stats = static_cast<float*>(workspace);
   return b.p.d == 64 ? launch_d<64>(b, plan, lists, stats, stream) : launch_d<128>(b, plan, lists, stats, stream);
 }

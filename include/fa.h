@@ -491,8 +491,8 @@ const char* fa_strerror(int code);
 /*
  * Device status word of the current device: FA_OK, or FA_ERR_TIMEOUT when a
  * kernel launched since the last read gave up on a bounded wait, or
- * FA_ERR_INDEX when one of the paged cache's kernels read an index that was
- * out of range (of both, the timeout is kept). Reading
+ * FA_ERR_INDEX when a kernel of the paged cache, of packed sequences or of their
+ * positions read an index that was out of range (of both, the timeout is kept). Reading
  * synchronises the device and clears the word. Returns FA_ERR_LAUNCH if the
  * word cannot be read.
  */

@@ -13,7 +13,9 @@
 //
 // Everything the device reads as an index (cu) is checked against the sizes
 // that the host gave before it is used: what fails is clamped and kStatusIndex
-// is raised, so a bad table never becomes a bad address.
+// is raised, so a bad table never becomes a bad address. Nor endless work: a list
+// of borders that fall somewhere stays empty (sequences that overlap could have any
+// number of rows).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,6 +42,7 @@ __device__ __forceinline__ int warp_prefix(int x, int lane) {
 // First row of sequence b and its number of rows.
 struct PackedSeq {
   int row0, n;
+  bool fell;  // ends before it begins
 };
 
 __device__ __forceinline__ PackedSeq packed_seq(const PackedShape& s, int b, int* status) {
@@ -47,6 +50,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const PackedShape& s, int b, int
   PackedSeq q;
   q.row0 = min(max(c0, 0), s.T);
   q.n = min(max(c1, q.row0), s.T) - q.row0;
+  q.fell = c1 < c0;
   if (c0 < 0 || c1 < c0 || c1 > s.T) raise_index(status);
   return q;
 }
@@ -80,7 +84,7 @@ __device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, int unit
   const int lane = static_cast<int>(lane_id());
   int before = 0;
   for (int b0 = 0; b0 < s.B; b0 += 32) {
-    PackedSeq q{0, 0};
+    PackedSeq q{0, 0, false};
     if (b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
     const int own = (q.n + unit - 1) / unit;
     const int end = warp_prefix(own, lane);
@@ -157,15 +161,18 @@ __device__ __forceinline__ int cost_of(const PackedShape& s, const PackedList& l
   return l.keys ? rows_of(s, n, i0, i1).n : keys_of(s, n, i0, i1).n;
 }
 
-// Makes list l, by a block of kThreads.
+// Makes list l, by a block of kThreads. Where borders rise, its entries are no
+// more than l.cap = T / l.unit + B.
 template <int kThreads>
 __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList& l, int* status) {
   constexpr int kWarps = kThreads / 32, kOwn = kBuckets / kThreads;  // buckets per thread, when their beginnings are summed up
   static_assert(kBuckets % kThreads == 0, "buckets are divided evenly");
   __shared__ int bucket[kBuckets];  // heaviest first
   __shared__ int sums[kWarps];
+  __shared__ int bad;  // borders fall
   const int tid = threadIdx.x, warp = warp_id(), lane = static_cast<int>(lane_id());
   for (int i = 0; i < kOwn; ++i) bucket[tid + i * kThreads] = 0;
+  if (tid == 0) bad = 0;
   __syncthreads();
   // Few sequences: a warp takes one at a time, its lanes the entries. Many: it
   // takes up to 32 neighbours at a time, and its lanes their entries end to end
@@ -174,26 +181,33 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
   const int per = min(s.B / kWarps, 32);
   auto each = [&](auto&& f) {
     auto entry = [&](const PackedSeq& q, int i) { f(q, i, kBuckets - 1 - min(cost_of(s, l, q.n, i), kBuckets - 1)); };
-    if (per <= 1) {
+    if (per <= 1) {  // (two sequences a warp at most)
       for (int b = warp; b < s.B; b += kWarps) {
         const PackedSeq q = packed_seq(s, b, status);
+        if (q.fell) bad = 1;
         for (long long i0 = static_cast<long long>(lane) * l.unit; i0 < q.n; i0 += 32LL * l.unit)
           entry(q, static_cast<int>(i0));
       }
       return;
     }
+    int seen = 0;  // entries of this warp so far
     for (int b0 = warp * per; b0 < s.B; b0 += kWarps * per) {
-      PackedSeq q{0, 0};
+      PackedSeq q{0, 0, false};
       if (lane < per && b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
       const int own = (q.n + l.unit - 1) / l.unit;
       const int end = warp_prefix(own, lane), total = __shfl_sync(0xffffffffu, end, 31);
+      if (__any_sync(0xffffffffu, q.fell) || total > l.cap - seen) {
+        bad = 1;
+        return;
+      }
+      seen += total;
       for (int e0 = 0; e0 < total; e0 += 32) {
         const int e = e0 + lane;
         int src = 0;  // its sequence: as many of them end before it
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1)
           if (__shfl_sync(0xffffffffu, end, src + m - 1) <= e) src += m;
-        const PackedSeq of{__shfl_sync(0xffffffffu, q.row0, src), __shfl_sync(0xffffffffu, q.n, src)};
+        const PackedSeq of{__shfl_sync(0xffffffffu, q.row0, src), __shfl_sync(0xffffffffu, q.n, src), false};
         const int i = (e - __shfl_sync(0xffffffffu, end - own, src)) * l.unit;
         if (e < total) entry(of, i);
       }
@@ -215,12 +229,9 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
     bucket[tid * kOwn + i] = before;
     before += own[i];
   }
-  if (tid == kThreads - 1) {
-    // (sequences that overlap could be more than there is room for)
-    if (before > l.cap) raise_index(status);
-    *l.head = PackedHead{min(before, l.cap), 0, {}};
-  }
+  if (tid == kThreads - 1) *l.head = PackedHead{bad ? 0 : before, 0, {}};
   __syncthreads();
+  if (bad) return;
   each([&](const PackedSeq& q, int i, int k) {
     const int at = atomicAdd(&bucket[k], 1);
     if (at < l.cap) l.entries[at] = make_int4(q.row0, q.n, i, 0);

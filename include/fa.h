@@ -403,7 +403,8 @@ size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged
  *   cu      : in,  int32 [B + 1] on the device: sequence b's rows are cu[b] ..
  *             cu[b + 1] - 1, none allowed. Rows outside [cu[0], cu[B]) are no
  *             sequence's: what they hold has no influence, and outputs there
- *             are left as they were.
+ *             are left as they were. (Padding between sequences can be given
+ *             sequences of its own: it then meets no other's rows.)
  *   causal  : != 0: row i of a sequence sees its rows j <= i
  *   window  : W >= 1 (causal only): and of those only j > i - W; 0: none
  *   scale   : finite and >= 0, as in fa_fwd
@@ -415,10 +416,10 @@ size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged
  *             calls in flight at once need two, also as replays of two
  *             captured graphs.
  * d is 64 or 128 and Hq / Hkv at most 128 (FA_ERR_UNSUPPORTED otherwise); T is
- * below 2^30 and T * Hq below 2^31 - 4096. The same inputs give the same bits. The device checks cu:
- * what does not rise or lies outside [0, T] is clamped and raises FA_ERR_INDEX
- * in the device status word; sequences that overlap leave unspecified outputs
- * in their rows.
+ * below 2^30 and T * Hq below 2^31 - 4096. The same inputs give the same bits.
+ * The device checks cu and raises FA_ERR_INDEX in the device status word: a
+ * border outside [0, T] is clamped; where cu falls somewhere, outputs are not
+ * specified and may not be written at all.
  * Values that are not finite stay within their sequence. There they follow the
  * formula as the tensor core evaluates it, tile by tile: an infinity or NaN in
  * v reaches all rows whose tile of 128 keys holds it, seen or not (0 * inf is

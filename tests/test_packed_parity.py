@@ -314,6 +314,21 @@ def test_packed_fwd_too_many_overlapping_rows_for_the_list():
     done(fa.FA_ERR_INDEX)
 
 
+@pytest.mark.parametrize("B,at", [(100, 50), (3000, 2500), (70000, 69999)])
+def test_borders_that_fall_make_no_work(B, at):
+    """Thousands of sequences that each hold all rows would be hours of work: a list of them stays empty."""
+    T = 100000
+    q, out = (torch.ones(T, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    outs, lse = [torch.full_like(q, 3) for _ in range(3)], torch.full((T, 2), 7.0, device="cuda")
+    for cu in ([0, T] * (B // 2), [T // 2] * at + [0] + [T] * (B - at)):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        fa.fa_packed_fwd(q, q, q, cu, out=out, lse=lse, causal=True)
+        done(fa.FA_ERR_INDEX)
+        fa.fa_packed_bwd(q, q, q, q, torch.zeros_like(lse), q, cu, dq=outs[0], dk=outs[1], dv=outs[2])
+        done(fa.FA_ERR_INDEX)
+        assert (out == 1).all() and (lse == 7).all() and all((x == 3).all() for x in outs)
+
+
 def test_packed_fwd_of_nothing():
     for T, B in ((0, 1), (5, 0)):
         q = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda")

@@ -703,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // queries of a key k: [k, k + window); a border cuts the warp's part of a tile
       // that begins before token cut_lo, or from cut_hi on
       const int warp_k0 = it.x0 + (warp & 3) * 32;
-      const int cut_lo = sh.causal ? warp_k0 + 31 - sh.by_group.div(wg * kCols) : -0x7fffffff;
+      const bool single = sh.window == 1 || it.n == 1;  // each query sees one key: dS = 0
+      const int cut_lo = single ? 0x7fffffff : sh.causal ? warp_k0 + 31 - sh.by_group.div(wg * kCols) : -0x7fffffff;
       const int cut_hi = sh.window > 0 ? warp_k0 + sh.window - sh.by_group.div(wg * kCols + kCols - 1) : 0x7fffffff;
       for (; g < end; ++g, i0 += sh.tpt) {
         const float* stat = f.stats(g) + wg * kCols;
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[c / 2] = __fmul2_rn(p[c / 2], __fadd2_rn(pair(x + c), make_float2(d.x, d.y)));
           p[c / 2 + 1] = __fmul2_rn(p[c / 2 + 1], __fadd2_rn(pair(x + c + 2), make_float2(d.z, d.w)));
         }
-        if (cut) keep_bits(p, seen);  // (where a query is not seen, dP may be anything)
+        if (cut) keep_bits(p, single ? 0u : seen);  // (where a query is not seen, dP may be anything)
 #pragma unroll
         for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
         tmem_st16(tDs, pk);
@@ -915,8 +916,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         d = __ldcg(args.neg_d + at);
       }
       const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
-      const int key_hi = sh.causal ? min(n, pos + 1) : n;                  // exclusive
       const int key_lo = sh.window > 0 ? pos - sh.window + 1 : 0;
+      int key_hi = sh.causal ? min(n, pos + 1) : n;  // exclusive
+      // the softmax of a single key is 1 whatever its score: no gradient, rather than dP - D's rounding
+      if (key_hi - max(key_lo, 0) == 1) key_hi = 0;
       // keys that all rows of the warp see: full_lo <= key < full_hi
       const int full_hi = sh.causal ? min(n, i0 + warp_i0 + 1) : n;
       const int full_lo = sh.window > 0 ? i0 + warp_i1 - sh.window + 1 : 0;

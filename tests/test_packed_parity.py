@@ -469,6 +469,20 @@ def test_packed_bwd_what_is_not_finite_stays_in_its_sequence(d, G, causal):
     assert all(x[rows.cu[1]:rows.cu[2]].isnan().all() for x in got)
 
 
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 5), (128, 1), (128, 8)])
+@pytest.mark.parametrize("lens,causal,window", [([1] * 300, False, 0), ([1, 0, 1], True, 0), ([70, 300, 1], True, 1)])
+def test_packed_bwd_where_each_row_sees_one_key(lens, causal, window, d, G):
+    """The softmax of one score does not depend on it: dq and dk are zero, and dv is dO, summed over the group."""
+    rows = Rows(lens, 2 * G, 2, d, seed=d + G)
+    (q, k, v), cu = rows.on_gpu()
+    do = randn(rows.rng, rows.T, 2 * G, d)
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=causal, window=window)
+    dq, dk, dv = fa.fa_packed_bwd(q, k, v, o, lse, do.cuda(), cu, causal=causal, window=window)
+    done()
+    assert not dq.any() and not dk.any()
+    check_bwd(rows, o.cpu(), lse.cpu(), do, (dq, dk, dv), causal, 1 / math.sqrt(d), window)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_packed_bwd_against_differences(d):
     """The loss sum(o dO) of the GPU's own forward, along a direction, against the GPU's gradients.

@@ -764,7 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[c / 2] = __fmul2_rn(p[c / 2], __fadd2_rn(pair(x + c), make_float2(d.x, d.y)));
           p[c / 2 + 1] = __fmul2_rn(p[c / 2 + 1], __fadd2_rn(pair(x + c + 2), make_float2(d.z, d.w)));
         }
-        if (cut) keep_bits(p, single ? 0u : seen);  // (where a query is not seen, dP may be anything)
+        // (where a query is not seen, dP may be anything; `single` formed again: kept in
+        // a register it cost 1.5 us of 274, d = 64)
+        if (cut) keep_bits(p, sh.window == 1 || *reinterpret_cast<const volatile int*>(&it.n) == 1 ? 0u : seen);
 #pragma unroll
         for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
         tmem_st16(tDs, pk);

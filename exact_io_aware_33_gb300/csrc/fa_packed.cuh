@@ -26,8 +26,9 @@ namespace fa {
 
 constexpr int kKeyTile = 128;
 
-// What the device reads of the borders and lists it takes from L2: the dQ kernel
+// What the kernels read of the borders and lists they take from L2: the dQ kernel
 // reads what was written before the kernel ahead of it, which alone has waited.
+// (make_list, after a wait of its own, reads the borders twice, and may cache them.)
 
 // Sum of x over this lane and those before it.
 __device__ __forceinline__ int warp_prefix(int x, int lane) {
@@ -45,8 +46,9 @@ struct PackedSeq {
   bool fell;  // ends before it begins
 };
 
+template <bool kCache = false>
 __device__ __forceinline__ PackedSeq packed_seq(const PackedShape& s, int b, int* status) {
-  const int c0 = __ldcg(s.cu + b), c1 = __ldcg(s.cu + b + 1);
+  const int c0 = kCache ? s.cu[b] : __ldcg(s.cu + b), c1 = kCache ? s.cu[b + 1] : __ldcg(s.cu + b + 1);
   PackedSeq q;
   q.row0 = min(max(c0, 0), s.T);
   q.n = min(max(c1, q.row0), s.T) - q.row0;
@@ -168,7 +170,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
   constexpr int kWarps = kThreads / 32, kOwn = kBuckets / kThreads;  // buckets per thread, when their beginnings are summed up
   static_assert(kBuckets % kThreads == 0, "buckets are divided evenly");
   __shared__ int bucket[kBuckets];  // heaviest first
-  __shared__ int sums[kWarps];
+  __shared__ int sums[32];
   __shared__ int bad;  // borders fall
   const int tid = threadIdx.x, warp = warp_id(), lane = static_cast<int>(lane_id());
   for (int i = 0; i < kOwn; ++i) bucket[tid + i * kThreads] = 0;
@@ -183,7 +185,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
     auto entry = [&](const PackedSeq& q, int i) { f(q, i, kBuckets - 1 - min(cost_of(s, l, q.n, i), kBuckets - 1)); };
     if (per <= 1) {  // (two sequences a warp at most)
       for (int b = warp; b < s.B; b += kWarps) {
-        const PackedSeq q = packed_seq(s, b, status);
+        const PackedSeq q = packed_seq<true>(s, b, status);
         if (q.fell) bad = 1;
         for (long long i0 = static_cast<long long>(lane) * l.unit; i0 < q.n; i0 += 32LL * l.unit)
           entry(q, static_cast<int>(i0));
@@ -193,7 +195,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
     int seen = 0;  // entries of this warp so far
     for (int b0 = warp * per; b0 < s.B; b0 += kWarps * per) {
       PackedSeq q{0, 0, false};
-      if (lane < per && b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
+      if (lane < per && b0 + lane < s.B) q = packed_seq<true>(s, b0 + lane, status);
       const int own = (q.n + l.unit - 1) / l.unit;
       const int end = warp_prefix(own, lane), total = __shfl_sync(0xffffffffu, end, 31);
       if (__any_sync(0xffffffffu, q.fell) || total > l.cap - seen) {
@@ -222,8 +224,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
   const int end = warp_prefix(all, lane);
   if (lane == 31) sums[warp] = end;
   __syncthreads();
-  int before = end - all;
-  for (int w = 0; w < warp; ++w) before += sums[w];
+  int before = end - all + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     bucket[tid * kOwn + i] = before;

@@ -569,11 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_s = [&](int which, int q, int g) {
       const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
       const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-        mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
-      }
+      mma_ss_depth_w<D>(tmem + (which ? C::kColDp : C::kColS), a, b, kIdS, 0u);
       mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
       if (which == 0) mbar_arrive_warp(f.bar(C::kBarS));
     };
@@ -582,11 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_a = [&](int which, int g, bool first) {
       const uint64_t b = which ? cols1 + g % C::kStages1 * kTile : cols0 + g % C::kStages0 * kTile;
       const uint32_t col = C::kApart ? (which ? C::kColP : C::kColDs) : which ? C::kColS : C::kColDp;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts_w(tmem + C::kColA + which * D,
-                 tmem + col + (C::kApart ? kk * 8 : (kk * 16 / kCols) * kCols + kk * 16 % kCols / 2), b + 128 * kk, kIdA,
-                 (!first || kk > 0) ? 1u : 0u);
+      mma_ts_depth_w<!C::kApart>(tmem + C::kColA + which * D, tmem + col, b, kIdA, first ? 0u : 1u);
     };
     auto ready0 = [&](int g) { return f.landed0(g) && f.ready(g); };
     auto ready1 = [&](int g) { return f.landed1(g) && f.ready(g); };
@@ -834,11 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_s = [&](int which, int q, int g) {
       const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
       const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-        mma_ss_w(tmem + (which ? C::kColDp : C::kColS), a + off, b + off, kIdS, kk > 0 ? 1u : 0u);
-      }
+      mma_ss_depth_w<D>(tmem + (which ? C::kColDp : C::kColS), a, b, kIdS, 0u);
       mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
     };
     int g = 0;
@@ -872,9 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint64_t b = cols0 + gs % C::kStages0 * kTile;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts_w(tmem + C::kColA, tmem + C::kColDs + kk * 8, b + 128 * kk, kIdA, (jj > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_depth_w<false>(tmem + C::kColA, tmem + C::kColDs, b, kIdA, jj > 0 ? 1u : 0u);
           mma_commit_w(f.bar(C::kBarDsFree));
           mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
         }

@@ -301,20 +301,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     auto issue_s = [&](int t, int gs) {
       const uint64_t qd = dQ + static_cast<uint64_t>((t * C::kTileBytes) >> 4);
       const uint64_t kd = dK0 + static_cast<uint64_t>(((gs % kS) * C::kTileBytes) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-        mma_ss_w(tmem + t * kBN, qd + off, kd + off, kIdS, kk > 0 ? 1u : 0u);
-      }
+      mma_ss_depth_w<D>(tmem + t * kBN, qd, kd, kIdS, 0u);
       mma_commit_w(bar(C::kBarSFull + t));
     };
     // O_t (+)= P_t V for stream step gs; P_t (bf16 pairs, 64 columns) over S_t or in its own columns
     auto issue_pv = [&](int t, int gs, bool first) {
       const uint64_t vd = dV0 + static_cast<uint64_t>(((gs % kS) * C::kTileBytes) >> 4);
       const uint32_t pcol = C::kSepP ? C::kColP + t * 64 : t * kBN;
-#pragma unroll
-      for (int kk = 0; kk < kBN / 16; ++kk)
-        mma_ts_w(tmem + C::kColO + t * D, tmem + pcol + kk * 8, vd + 128 * kk, kIdO, (!first || kk > 0) ? 1u : 0u);
+      mma_ts_depth_w<false>(tmem + C::kColO + t * D, tmem + pcol, vd, kIdO, first ? 0u : 1u);
     };
     int g = 0;
     int ut[QT] = {};  // S tiles of tile t over all items (its S/P barrier phases)

@@ -474,6 +474,91 @@ __device__ __forceinline__ void mma_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint6
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// All products of a tile's depth, which differ in their operands' beginnings only:
+// one election, and sums in 32 bits (the address field does not carry out of the
+// descriptor's lower word). Less code than as many single calls; the issuing warp
+// is on the way of every hand-off, and shares the instruction cache with the others'
+// hot loops. 8 packed sequences of up to 4096 tokens, 32 / 8 heads, d = 128: forward
+// 178 -> 174.5 us, backward 616 -> 597.
+
+// kDepth / 16 products of K-major operands in 128-byte-swizzled chunks of 128 rows x 64.
+template <int kDepth>
+__device__ __forceinline__ void mma_ss_depth_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  static_assert(kDepth == 64 || kDepth == 128, "one chunk or two");
+  if constexpr (kDepth == 64) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 al, ah, bl, bh, x, y;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u32 x, al, 2;\n\tadd.u32 y, bl, 2;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 4;\n\tadd.u32 y, bl, 4;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 6;\n\tadd.u32 y, bl, 6;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 al, ah, bl, bh, x, y;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u32 x, al, 2;\n\tadd.u32 y, bl, 2;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 4;\n\tadd.u32 y, bl, 4;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 6;\n\tadd.u32 y, bl, 6;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 1024;\n\tadd.u32 y, bl, 1024;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 1026;\n\tadd.u32 y, bl, 1026;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 1028;\n\tadd.u32 y, bl, 1028;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u32 x, al, 1030;\n\tadd.u32 y, bl, 1030;\n\tmov.b64 a, {x, ah};\n\tmov.b64 b, {y, bh};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Eight products, 128 deep: A in tensor memory, its 16-deep parts eight columns
+// apart, or (kSpread) two of them in the first half of every 32 columns; B MN-major.
+template <bool kSpread>
+__device__ __forceinline__ void mma_ts_depth_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  constexpr int kPair = kSpread ? 32 : 16;
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 bl, bh, x, y;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "mov.b64 {bl, bh}, %2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 y, bl, 128;\n\tadd.u32 x, %1, %5;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 256;\n\tadd.u32 x, %1, %6;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 384;\n\tadd.u32 x, %1, %7;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 512;\n\tadd.u32 x, %1, %8;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 640;\n\tadd.u32 x, %1, %9;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 768;\n\tadd.u32 x, %1, %10;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "add.u32 y, bl, 896;\n\tadd.u32 x, %1, %11;\n\tmov.b64 b, {y, bh};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+      "}" ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(8), "n"(kPair), "n"(kPair + 8),
+      "n"(2 * kPair), "n"(2 * kPair + 8), "n"(3 * kPair), "n"(3 * kPair + 8)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"

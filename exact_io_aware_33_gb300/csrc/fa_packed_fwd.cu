@@ -27,12 +27,12 @@
 // last tile's P over, put zeros in their place in shared memory.
 //
 // What bounds it: at d = 128 the tensor core, 4 d flops per visible pair (one
-// sequence of 16384 tokens, 32 / 8 heads, causal: 1.35 ms, 1630 TFLOP/s, 86 % of
+// sequence of 16384 tokens, 32 / 8 heads, causal: 1.34 ms, 1640 TFLOP/s, 86 % of
 // the rate of a large library product), less where items are short: 8 prompts of up
-// to 4096 tokens, 178 us, 71 %. At d = 64 the softmax beside it, one exponential and
+// to 4096 tokens, 174 us, 73 %. At d = 64 the softmax beside it, one exponential and
 // four other instructions per pair: 24 images of up to 1369 tokens, 16 heads,
-// unmasked, 88 us, 40 %; 6 x up to 5001 tokens, 12 / 4 heads, a window of 700, 80 us,
-// 32 %, where two or three of seven key tiles are cut by a border.
+// unmasked, 86.5 us, 41 %; 6 x up to 5001 tokens, 12 / 4 heads, a window of 700, 78 us,
+// 33 %, where two or three of seven key tiles are cut by a border.
 //
 // CTA: softmax warpgroup(s) (thread = row = TMEM lane), an MMA warp, a TMA warp.
 

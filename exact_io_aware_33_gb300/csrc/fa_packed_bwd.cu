@@ -38,8 +38,9 @@
 // What bounds it: 14 d flops per visible pair on the tensor core (10 d of them
 // the algorithm's), which reads up to 128 bytes a clock of operands from shared
 // memory, two exponentials per pair, and the hand-offs between the roles: a step
-// of 128 x 128 takes 2700 (dK, dV) and 1950 (dQ) cycles at d = 128, 2150 and 1600
-// at d = 64, of which the tensor core is at work for 2200, 1600, 1100 and 800.
+// of 128 x 128 takes 2730 (dK, dV) and 1940 (dQ) cycles at d = 128, 2230 and 1630
+// at d = 64 (medians, with time stamps), of which the tensor core is at work for
+// 2200, 1650, 1100 and 820.
 // Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 595 us,
 // 1010 TFLOP/s of the algorithm's; one of 8192, 16 heads: 595, 1155; 24 images of up
 // to 1369 tokens, 16 heads, d = 64, unmasked: 270, 622.

@@ -41,14 +41,18 @@
 // of 128 x 128 takes 2730 (dK, dV) and 1940 (dQ) cycles at d = 128, 2230 and 1630
 // at d = 64 (medians, with time stamps), of which the tensor core is at work for
 // 2200, 1650, 1100 and 820.
-// Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 595 us,
-// 1010 TFLOP/s of the algorithm's; one of 8192, 16 heads: 595, 1155; 24 images of up
-// to 1369 tokens, 16 heads, d = 64, unmasked: 270, 622.
+// Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 589 us,
+// 1020 TFLOP/s of the algorithm's; one of 8192, 16 heads: 589, 1167; 24 images of up
+// to 1369 tokens, 16 heads, d = 64, unmasked: 269, 625.
 
 #include "fa_packed.cuh"
 
 namespace fa {
 namespace {
+
+// Steps and items counted are not negative; said so, their remainders and quotients
+// take fewer instructions (595 -> 589 us, 8 documents of up to 4096 tokens).
+__device__ __forceinline__ uint32_t u32(int x) { return static_cast<uint32_t>(x); }
 
 constexpr int kKT = kKeyTile;  // keys per tile; also rows per tile of query rows
 constexpr int kItems = 4;      // item records kept
@@ -270,14 +274,14 @@ struct Frame {
   __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBarOff + 8u * i; }
   __device__ __forceinline__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(smem + C::kMiscOff); }
   __device__ __forceinline__ Item* items() const { return reinterpret_cast<Item*>(smem + C::kItemOff); }
-  __device__ __forceinline__ uint8_t* ring0(int g) const { return smem + C::kRing0 + g % C::kStages0 * C::kTileBytes; }
-  __device__ __forceinline__ uint8_t* ring1(int g) const { return smem + C::kRing1 + g % C::kStages1 * C::kTileBytes; }
+  __device__ __forceinline__ uint8_t* ring0(int g) const { return smem + C::kRing0 + u32(g) % C::kStages0 * C::kTileBytes; }
+  __device__ __forceinline__ uint8_t* ring1(int g) const { return smem + C::kRing1 + u32(g) % C::kStages1 * C::kTileBytes; }
   // Waits of stream step g on the barriers of its stages.
   __device__ __forceinline__ bool landed0(int g) const { return at_step(C::kBarLoad0, C::kStages0, g); }
   __device__ __forceinline__ bool landed1(int g) const { return at_step(C::kBarLoad1, C::kStages1, g); }
   __device__ __forceinline__ bool ready(int g) const { return at_step(C::kBarReady, C::kStages0, g); }
   __device__ __forceinline__ bool at_step(int b, int stages, int g) const {
-    return mbar_wait_w(bar(b + g % stages), (g / stages) & 1, abort_flag);
+    return mbar_wait_w(bar(b + u32(g) % stages), (u32(g) / stages) & 1, abort_flag);
   }
   // The same for the compute warps. At d = 128 they wait for the tensor core most
   // of the time, and asleep they take no issue slots and shared-memory cycles from
@@ -295,7 +299,7 @@ struct Frame {
   // The g-th phase of a barrier that has one per step.
   __device__ __forceinline__ bool wait(int b, int g) const { return mbar_wait_w(bar(b), g & 1, abort_flag); }
   __device__ __forceinline__ float* stats(int g) const {
-    return reinterpret_cast<float*>(smem + C::kStatOff + g % C::kStatStages * 1024);
+    return reinterpret_cast<float*>(smem + C::kStatOff + u32(g) % C::kStatStages * 1024);
   }
 
   // The dQ kernel does not read what the one before it on the stream writes, so it
@@ -350,9 +354,9 @@ struct Frame {
 
   // Item number k, for a consuming warp that gives it back with give_item.
   __device__ __forceinline__ bool get_item(int k) const {
-    return mbar_wait_w(bar(C::kBarItemFull + k % kItems), (k / kItems) & 1, abort_flag);
+    return mbar_wait_w(bar(C::kBarItemFull + u32(k) % kItems), (u32(k) / kItems) & 1, abort_flag);
   }
-  __device__ __forceinline__ void give_item(int k) const { mbar_arrive_warp(bar(C::kBarItemEmpty + k % kItems)); }
+  __device__ __forceinline__ void give_item(int k) const { mbar_arrive_warp(bar(C::kBarItemEmpty + u32(k) % kItems)); }
 
   // Whether stream step t0 + jj of an item is a tile that reaches past the sequence.
   __device__ __forceinline__ static bool last_tile(const PackedShape& s, const Item& it, int jj) {
@@ -380,13 +384,13 @@ struct Frame {
       const int x1 = min(e.i0 + list.unit, e.n);
       const TileRange r = kKeys ? rows_of(s, e.n, e.i0, x1) : keys_of(s, e.n, e.i0, x1);
       const Item it{0, e.row0, e.n, h, e.i0, r.lo, r.n, 0};
-      if (q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
+      if (q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + u32(q) % kItems), (u32(q) / kItems - 1) & 1, abort_flag);
       if (!ok) break;
-      items()[q % kItems] = it;
-      mbar_arrive(bar(C::kBarItemFull + q % kItems));
+      items()[u32(q) % kItems] = it;
+      mbar_arrive(bar(C::kBarItemFull + u32(q) % kItems));
       auto load_resident = [&]() {
-        const int rb = q % C::kResBufs;
-        if (q >= C::kResBufs) ok = mbar_wait(bar(C::kBarResFree + rb), (q / C::kResBufs - 1) & 1, abort_flag);
+        const int rb = u32(q) % C::kResBufs;
+        if (q >= C::kResBufs) ok = mbar_wait(bar(C::kBarResFree + rb), (u32(q) / C::kResBufs - 1) & 1, abort_flag);
         if (!ok) return;
         const uint32_t res = base + C::kResOff + rb * 2 * C::kTileBytes, res_full = bar(C::kBarResFull + rb);
         mbar_arrive_expect_tx(res_full, res_bytes);
@@ -402,7 +406,7 @@ struct Frame {
         const int row = e.row0 + (it.t0 + jj) * (kKeys ? s.tpt : kKT);
         queue.step(it.ns - jj);
         auto load = [&](int w, int load_bar, int empty_bar, int stages, uint8_t* to) {
-          if (g >= stages) ok = mbar_wait(bar(empty_bar + g % stages), (g / stages - 1) & 1, abort_flag);
+          if (g >= stages) ok = mbar_wait(bar(empty_bar + u32(g) % stages), (u32(g) / stages - 1) & 1, abort_flag);
 #ifdef FA_TEST_SKIP_ARRIVE
           // Test-only build (never in libfa.so): the first item's last tile (Q, or
           // K) is never loaded and nothing more is, so the bounded waits for it
@@ -410,7 +414,7 @@ struct Frame {
           if (w == 0 && jj == it.ns - 1) ok = false;
 #endif
           if (!ok) return;
-          const uint32_t full = bar(load_bar + g % stages);
+          const uint32_t full = bar(load_bar + u32(g) % stages);
           mbar_arrive_expect_tx(full, str_bytes);
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d(smem_u32(to) + c * kChunkBytes, w == 0 ? str0 : str1, full, c * 64, 0, h, row);
@@ -422,10 +426,10 @@ struct Frame {
       }
       ++q;
     }
-    if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
+    if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + u32(q) % kItems), (u32(q) / kItems - 1) & 1, abort_flag);
     if (ok) {
-      items()[q % kItems].end = 1;
-      mbar_arrive(bar(C::kBarItemFull + q % kItems));
+      items()[u32(q) % kItems].end = 1;
+      mbar_arrive(bar(C::kBarItemFull + u32(q) % kItems));
     }
   }
 
@@ -440,8 +444,8 @@ struct Frame {
     const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kColA;
     [[maybe_unused]] uint8_t* stage = smem + C::kOutOff + (warp & 3) * 2048;
     for (int q = 0;; ++q) {
-      if (!get_item(q) || items()[q % kItems].end) break;
-      const Item it = items()[q % kItems];
+      if (!get_item(q) || items()[u32(q) % kItems].end) break;
+      const Item it = items()[u32(q) % kItems];
       give_item(q);
       if (!mbar_wait_sleep_w(bar(C::kBarFinal), q & 1, abort_flag)) break;
       tc_fence_after();
@@ -479,11 +483,11 @@ struct Frame {
       // thread started land before the CTA exits (only the last load of each
       // buffer can still be pending).
       for (int i = max(res_loads - C::kResBufs, 0); i < res_loads; ++i)
-        mbar_wait(bar(C::kBarResFull + i % C::kResBufs), (i / C::kResBufs) & 1, nullptr);
+        mbar_wait(bar(C::kBarResFull + u32(i) % C::kResBufs), (u32(i) / C::kResBufs) & 1, nullptr);
       for (int i = max(stage_loads[0] - C::kStages0, 0); i < stage_loads[0]; ++i)
-        mbar_wait(bar(C::kBarLoad0 + i % C::kStages0), (i / C::kStages0) & 1, nullptr);
+        mbar_wait(bar(C::kBarLoad0 + u32(i) % C::kStages0), (u32(i) / C::kStages0) & 1, nullptr);
       for (int i = max(stage_loads[1] - C::kStages1, 0); i < stage_loads[1]; ++i)
-        mbar_wait(bar(C::kBarLoad1 + i % C::kStages1), (i / C::kStages1) & 1, nullptr);
+        mbar_wait(bar(C::kBarLoad1 + u32(i) % C::kStages1), (u32(i) / C::kStages1) & 1, nullptr);
     }
     if (warp_id() == kMmaWarp) {
       __syncwarp();
@@ -527,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const Item it = f.items()[q % kItems];
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const Item it = f.items()[u32(q) % kItems];
       f.give_item(q);
       for (int jj = 0; jj < it.ns; ++jj, ++g) {
         const int i0 = (it.t0 + jj) * sh.tpt, rows = min(sh.tpt, it.n - i0) * G;
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
         }
-        cp_async_arrive(f.bar(C::kBarReady + g % C::kStages0));
+        cp_async_arrive(f.bar(C::kBarReady + u32(g) % C::kStages0));
       }
     }
     cp_async_wait_all();
@@ -568,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // S^T = K Q^T (which = 0) or dP^T = V dO^T (1) for stream step g, of item q
     auto issue_s = [&](int which, int q, int g) {
-      const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
-      const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
+      const uint64_t a = res + (2 * (u32(q) % C::kResBufs) + which) * kTile;
+      const uint64_t b = which ? rows1 + u32(g) % C::kStages1 * kTile : rows0 + u32(g) % C::kStages0 * kTile;
       mma_ss_depth_w<D>(tmem + (which ? C::kColDp : C::kColS), a, b, kIdS, 0u);
       mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
       if (which == 0) mbar_arrive_warp(f.bar(C::kBarS));
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // dV (+)= P^T dO (which = 1) or dK (+)= dS^T Q (0); where P and dS are not
     // apart, each warpgroup's part of them begins where its part of S or dP did
     auto issue_a = [&](int which, int g, bool first) {
-      const uint64_t b = which ? cols1 + g % C::kStages1 * kTile : cols0 + g % C::kStages0 * kTile;
+      const uint64_t b = which ? cols1 + u32(g) % C::kStages1 * kTile : cols0 + u32(g) % C::kStages0 * kTile;
       const uint32_t col = C::kApart ? (which ? C::kColP : C::kColDs) : which ? C::kColS : C::kColDp;
       mma_ts_depth_w<!C::kApart>(tmem + C::kColA + which * D, tmem + col, b, kIdA, first ? 0u : 1u);
     };
@@ -586,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const int ns = f.items()[q % kItems].ns;
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const int ns = f.items()[u32(q) % kItems].ns;
       f.give_item(q);
       if constexpr (C::kApart) {
         if (warp == kMmaWarp) {
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             issue_s(1, q, gs);
           }
-          if (ok) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
+          if (ok) mma_commit_w(f.bar(C::kBarResFree + u32(q) % C::kResBufs));
         } else {
           // dV and dK; that dS is there says that S^T and dP^T have been computed
           for (int jj = 0; jj < ns && ok; ++jj) {
@@ -616,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_a(1, gs, jj == 0);
             issue_a(0, gs, jj == 0);
             mma_commit_w(f.bar(C::kBarDsFree));
-            mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
-            mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
+            mma_commit_w(f.bar(C::kBarEmpty0 + u32(gs) % C::kStages0));
+            mma_commit_w(f.bar(C::kBarEmpty1 + u32(gs) % C::kStages1));
           }
           if (ok) mma_commit_w(f.bar(C::kBarFinal));
         }
@@ -630,14 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         issue_s(1, q, g);
-        if (ns == 1) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
+        if (ns == 1) mma_commit_w(f.bar(C::kBarResFree + u32(q) % C::kResBufs));
         for (int jj = 0; jj < ns; ++jj) {
           const int gs = g + jj;
           ok = (jj > 0 || q == 0 || f.wait(C::kBarAccFree, q - 1)) && f.wait(C::kBarP, gs);
           if (!ok) break;
           tc_fence_after();
           issue_a(1, gs, jj == 0);
-          mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
+          mma_commit_w(f.bar(C::kBarEmpty1 + u32(gs) % C::kStages1));
           if (jj + 1 < ns) {
             ok = ready0(gs + 1);
             if (!ok) break;
@@ -648,14 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           issue_a(0, gs, jj == 0);
-          mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
+          mma_commit_w(f.bar(C::kBarEmpty0 + u32(gs) % C::kStages0));
           if (jj + 1 < ns) {
             ok = f.landed1(gs + 1);
             if (!ok) break;
             tc_fence_after();
             issue_s(1, q, gs + 1);
             // K and V are free once the item's last S^T and dP^T have completed
-            if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
+            if (jj + 2 == ns) mma_commit_w(f.bar(C::kBarResFree + u32(q) % C::kResBufs));
           } else {
             mma_commit_w(f.bar(C::kBarFinal));
           }
@@ -689,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const Item& it = f.items()[q % kItems];  // (given back at the item's end)
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const Item& it = f.items()[u32(q) % kItems];  // (given back at the item's end)
       int i0 = it.t0 * sh.tpt;
       const int end = g + it.ns;
       // queries of a key k: [k, k + window); a border cuts the warp's part of a tile
@@ -800,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const Item it = f.items()[q % kItems];
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const Item it = f.items()[u32(q) % kItems];
       f.give_item(q);
       for (int jj = 0; jj < it.ns; ++jj, ++g) {
         ok = f.landed0(g);
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_rows(f.ring0(g), kChunkBytes, C::kChunks, it.n - (it.t0 + jj) * kKT, kKT, lane, 32);
           fence_async_smem();
         }
-        mbar_arrive_warp(f.bar(C::kBarReady + g % C::kStages0));
+        mbar_arrive_warp(f.bar(C::kBarReady + u32(g) % C::kStages0));
       }
     }
   } else if (warp == kMmaWarp || warp == kSumWarp) {
@@ -825,16 +829,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // S = Q K^T (which = 0) or dP = dO V^T (1) for stream step g, of item q
     auto issue_s = [&](int which, int q, int g) {
-      const uint64_t a = res + (2 * (q % C::kResBufs) + which) * kTile;
-      const uint64_t b = which ? rows1 + g % C::kStages1 * kTile : rows0 + g % C::kStages0 * kTile;
+      const uint64_t a = res + (2 * (u32(q) % C::kResBufs) + which) * kTile;
+      const uint64_t b = which ? rows1 + u32(g) % C::kStages1 * kTile : rows0 + u32(g) % C::kStages0 * kTile;
       mma_ss_depth_w<D>(tmem + (which ? C::kColDp : C::kColS), a, b, kIdS, 0u);
       mma_commit_w(f.bar(which ? C::kBarDp : C::kBarS));
     };
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const int ns = f.items()[q % kItems].ns;
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const int ns = f.items()[u32(q) % kItems].ns;
       f.give_item(q);
       if (warp == kMmaWarp) {
         // S and dP, each once its predecessor is in registers (both once dP is: 345
@@ -850,9 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           issue_s(1, q, gs);
-          mma_commit_w(f.bar(C::kBarEmpty1 + gs % C::kStages1));
+          mma_commit_w(f.bar(C::kBarEmpty1 + u32(gs) % C::kStages1));
         }
-        if (ok) mma_commit_w(f.bar(C::kBarResFree + q % C::kResBufs));
+        if (ok) mma_commit_w(f.bar(C::kBarResFree + u32(q) % C::kResBufs));
       } else {
         // dQ (+)= dS K; that dS is there says that S has been computed
         for (int jj = 0; jj < ns && ok; ++jj) {
@@ -860,10 +864,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = f.landed0(gs) && f.ready(gs) && (jj > 0 || q == 0 || f.wait(C::kBarAccFree, q - 1)) && f.wait(C::kBarDs, gs);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t b = cols0 + gs % C::kStages0 * kTile;
+          const uint64_t b = cols0 + u32(gs) % C::kStages0 * kTile;
           mma_ts_depth_w<false>(tmem + C::kColA, tmem + C::kColDs, b, kIdA, jj > 0 ? 1u : 0u);
           mma_commit_w(f.bar(C::kBarDsFree));
-          mma_commit_w(f.bar(C::kBarEmpty0 + gs % C::kStages0));
+          mma_commit_w(f.bar(C::kBarEmpty0 + u32(gs) % C::kStages0));
         }
         if (ok) mma_commit_w(f.bar(C::kBarFinal));
       }
@@ -895,8 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     for (int q = 0; ok; ++q) {
       ok = f.get_item(q);
-      if (!ok || f.items()[q % kItems].end) break;
-      const Item& it = f.items()[q % kItems];
+      if (!ok || f.items()[u32(q) % kItems].end) break;
+      const Item& it = f.items()[u32(q) % kItems];
       const int ns = it.ns, n = it.n, i0 = it.x0, pos = i0 + ri;
       float l = -INFINITY, d = 0.f;
       if (ri < sh.tpt && pos < n) {

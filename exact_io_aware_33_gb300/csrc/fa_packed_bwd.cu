@@ -39,7 +39,7 @@
 // the algorithm's), which reads up to 128 bytes a clock of operands from shared
 // memory, two exponentials per pair, and the hand-offs between the roles: a step
 // of 128 x 128 takes 2730 (dK, dV) and 1940 (dQ) cycles at d = 128, 2230 and 1630
-// at d = 64 (medians, with time stamps), of which the tensor core is at work for
+// at d = 64 (medians under time stamps, which cost some), of which the tensor core is at work for
 // 2200, 1650, 1100 and 820.
 // Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 589 us,
 // 1020 TFLOP/s of the algorithm's; one of 8192, 16 heads: 589, 1167; 24 images of up

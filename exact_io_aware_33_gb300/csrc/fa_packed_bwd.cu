@@ -313,7 +313,8 @@ struct Frame {
     if (threadIdx.x == 0) {
       for (int i = C::kBarResFull; i < C::kBarLoad0; ++i) mbar_init(bar(i), 1);
       for (int i = C::kBarLoad0; i < C::kBarS; ++i)
-        mbar_init(bar(i), kKeys && i >= C::kBarReady && i < C::kBarLoad1 ? 32 : 1);  // (dK, dV's helper: each lane's copies)
+        // (dK, dV's helper: each lane's copies, and what the warp wrote itself)
+        mbar_init(bar(i), kKeys && i >= C::kBarReady && i < C::kBarLoad1 ? 33 : 1);
       mbar_init(bar(C::kBarS), kKeys ? 2 : 1);  // dK, dV: and the MMA warp, which passes on that the statistics are written
       mbar_init(bar(C::kBarDp), 1);
       mbar_init(bar(C::kBarP), kComputeWarps);
@@ -553,9 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_rows(f.ring0(g), kChunkBytes, C::kChunks, rows, 128, lane, 32);
           zero_rows(f.ring1(g), kChunkBytes, C::kChunks, rows, 128, lane, 32);
           fence_async_smem();
-          __syncwarp();
         }
+        // The copies arrive when they land, and that orders nothing else the lanes
+        // wrote: the zeros are handed over by an arrival of their own, a release.
         cp_async_arrive(f.bar(C::kBarReady + u32(g) % C::kStages0));
+        mbar_arrive_warp(f.bar(C::kBarReady + u32(g) % C::kStages0));
       }
     }
     cp_async_wait_all();

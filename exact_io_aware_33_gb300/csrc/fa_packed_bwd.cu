@@ -1029,8 +1029,7 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   a.neg_d = stats + rows;
   a.status = status;
   a.scale = p.scale;
-  const float sl2 = p.scale * kLog2e;
-  a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  a.scale_log2 = p.scale * kLog2e;  // (0 too: keys that are not seen are taken out after the exponential)
   auto grid = [&](int i) { return dim3(plan.listed[i] ? plan.slots : plan.cap[i] * s.Hkv); };
   a.list = lists[0];
   a.out[0] = static_cast<__nv_bfloat16*>(b.dk);

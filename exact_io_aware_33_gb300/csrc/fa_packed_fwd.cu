@@ -36,6 +36,9 @@
 //
 // CTA: softmax warpgroup(s) (thread = row = TMEM lane), an MMA warp, a TMA warp.
 
+#include <algorithm>
+#include <limits>
+
 #include "fa_packed.cuh"
 
 namespace fa {
@@ -712,8 +715,9 @@ int launch_packed_fwd(const PackedProblem& p, void* o, float* lse, void* workspa
   }
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  const float sl2 = p.scale * kLog2e;
-  a.scale_log2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  // 0 would make NaN of the -infinity of a masked key. The least there is, 2^-149,
+  // leaves scores below 2^-21: all weights alike, as they are to be.
+  a.scale_log2 = std::max(p.scale * kLog2e, std::numeric_limits<float>::denorm_min());
   return p.d == 64 ? launch_d<64>(p, a, plan, stream) : launch_d<128>(p, a, plan, stream);
 }
 

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 fa = pytest.importorskip("exact_io_aware_33_gb300")
 
-from test_packed_parity import Rows, done, randn  # noqa: E402
+from test_packed_parity import Rows, backward_of, check_bwd, check_fwd, done, forward_for, randn  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,46 @@ def test_rows_past_a_sequence_are_zeros_before_they_are_multiplied(d, G):
     done()
     for got in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], got))
+
+
+# ------------------------------------------------------------------ scales
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_largest_queries_with_the_smallest_scales(d):
+    """The scale takes the queries' size back: powers of two, so the bits are those of queries and a scale of usual size
+    (dq's times the size; at 2^100 its values are still normal numbers)."""
+    rows = Rows([150, 40], 4, 2, d, seed=d)
+    (q, k, v), cu = rows.on_gpu()
+    do = randn(rows.rng, rows.T, 4, d).cuda()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True, scale=0.125)
+    dq, dk, dv = fa.fa_packed_bwd(q, k, v, o, lse, do, cu, causal=True, scale=0.125)
+    done()
+    check_fwd(rows, o, lse, True, 0.125, 0)
+    check_bwd(rows, o, lse, do, (dq, dk, dv), True, 0.125, 0)
+    for size in (2.0 ** 100, 2.0 ** 120):
+        large = (q.float() * size).to(torch.bfloat16)
+        got, got_lse = fa.fa_packed_fwd(large, k, v, cu, causal=True, scale=0.125 / size)
+        done()
+        assert torch.equal(got, o) and torch.equal(got_lse, lse)
+        if size > 2.0 ** 100:                     # (sums of dS q would leave float32's range)
+            continue
+        grads = fa.fa_packed_bwd(large, k, v, o, lse, do, cu, causal=True, scale=0.125 / size)
+        done()
+        assert torch.equal((grads[0].double() * size).to(torch.bfloat16), dq)
+        assert torch.equal(grads[1], dk) and torch.equal(grads[2], dv)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 1e-42])
+def test_scales_of_nothing_weigh_all_keys_alike_whatever_the_queries(d, scale):
+    rows = Rows([150, 40], 4, 2, d, seed=d)
+    rows.q *= 2.0 ** 115                          # (scores times 1e-42: below 1e-5)
+    (q, k, v), cu = rows.on_gpu()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True, scale=scale)
+    done()
+    check_fwd(rows, o, lse, True, scale, 0)
+    o, lse = forward_for(rows, True, 0.0, 0)
+    do = randn(rows.rng, rows.T, 4, d)
+    got = backward_of(rows, o, lse, do, True, 0, scale=0.0)
+    done()
+    check_bwd(rows, o, lse, do, got, True, 0.0, 0)
+    assert not got[0].any() and not got[1].any()

@@ -257,6 +257,7 @@ struct PackedList {
   int4* entries;  // row0, n, i0, -; nullptr: every item has a CTA, no list is made
   int cap;
   int unit;       // tokens per entry
+  int least;      // tokens of the shortest sequence that makes entries
   int keys;       // 0: an entry's tokens are queries (its cost: key tiles), 1: keys (tiles of query rows)
 };
 

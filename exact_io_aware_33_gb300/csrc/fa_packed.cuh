@@ -82,19 +82,19 @@ struct PackedEntry {
 
 // Entry number e when the sequences' entries are laid end to end, found by a
 // whole warp; n = 0 when there are fewer.
-__device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, int unit, int e, int* status) {
+__device__ __forceinline__ PackedEntry find_entry(const PackedShape& s, const PackedList& l, int e, int* status) {
   const int lane = static_cast<int>(lane_id());
   int before = 0;
   for (int b0 = 0; b0 < s.B; b0 += 32) {
     PackedSeq q{0, 0, false};
     if (b0 + lane < s.B) q = packed_seq(s, b0 + lane, status);
-    const int own = (q.n + unit - 1) / unit;
+    const int own = q.n < l.least ? 0 : (q.n + l.unit - 1) / l.unit;
     const int end = warp_prefix(own, lane);
     const uint32_t past = __ballot_sync(0xffffffffu, before + end > e);
     if (past) {
       const int src = __ffs(past) - 1;
       const int first = before + __shfl_sync(0xffffffffu, end - own, src);
-      return PackedEntry{__shfl_sync(0xffffffffu, q.row0, src), __shfl_sync(0xffffffffu, q.n, src), (e - first) * unit};
+      return PackedEntry{__shfl_sync(0xffffffffu, q.row0, src), __shfl_sync(0xffffffffu, q.n, src), (e - first) * l.unit};
     }
     before += __shfl_sync(0xffffffffu, end, 31);
   }
@@ -121,7 +121,7 @@ struct ItemQueue {
     by_head = s.by_head;
     next = static_cast<int>(blockIdx.x);
     if (l.entries == nullptr)
-      own = find_entry(s, l.unit, by_head.div(next), status);
+      own = find_entry(s, l, by_head.div(next), status);
     else
       count = __ldcg(&l.head->count);
   }
@@ -187,6 +187,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
       for (int b = warp; b < s.B; b += kWarps) {
         const PackedSeq q = packed_seq<true>(s, b, status);
         if (q.fell) bad = 1;
+        if (q.n < l.least) continue;
         for (long long i0 = static_cast<long long>(lane) * l.unit; i0 < q.n; i0 += 32LL * l.unit)
           entry(q, static_cast<int>(i0));
       }
@@ -196,7 +197,7 @@ __device__ __forceinline__ void make_list(const PackedShape& s, const PackedList
     for (int b0 = warp * per; b0 < s.B; b0 += kWarps * per) {
       PackedSeq q{0, 0, false};
       if (lane < per && b0 + lane < s.B) q = packed_seq<true>(s, b0 + lane, status);
-      const int own = (q.n + l.unit - 1) / l.unit;
+      const int own = q.n < l.least ? 0 : (q.n + l.unit - 1) / l.unit;
       const int end = warp_prefix(own, lane), total = __shfl_sync(0xffffffffu, end, 31);
       if (__any_sync(0xffffffffu, q.fell) || total > l.cap - seen) {
         bad = 1;

@@ -9,6 +9,11 @@
 // P and dS are rounded to bf16 for the products (2^-9 of a term on average);
 // everything else is fp32.
 //
+// A row that sees one key, its own (a window of 1, a sequence of one token), needs no
+// tiles: it is computed as it is written, beside the row sums, with dO . v - D as sum_c
+// dO_c (v_c - O_c). That is exactly 0 where O is v, as the forward leaves it, where two
+// sums would leave their rounding errors.
+//
 // Three kernels: D; dK and dV, with a key tile resident and the tiles of query
 // rows streamed; dQ, with a tile of query rows resident and the key tiles
 // streamed. S and dP are computed in both, 7 products instead of the 5 of a
@@ -44,6 +49,8 @@
 // Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 589 us,
 // 1020 TFLOP/s of the algorithm's; one of 8192, 16 heads: 589, 1167; 24 images of up
 // to 1369 tokens, 16 heads, d = 64, unmasked: 269, 625.
+
+#include <algorithm>
 
 #include "fa_packed.cuh"
 
@@ -149,8 +156,118 @@ struct SumArgs {
   PackedShape s;
   PackedList lists[2];
   int n_lists;
+  int n_own;  // blocks of own_rows
   int* status;
+  // for own_rows
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *dq, *dk, *dv;
+  long long q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
+  float scale, scale_log2;
 };
+
+// N channels of a lane: N / 2 words, in fp32 and back.
+template <int N>
+struct Channels {
+  float x[N];
+  __device__ __forceinline__ explicit Channels(float f) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = f;
+  }
+  __device__ __forceinline__ Channels(const __nv_bfloat16* at, int lane) {
+    uint32_t w[N / 2];
+    if constexpr (N == 4) {
+      const uint2 u = *reinterpret_cast<const uint2*>(at + lane * N);
+      w[0] = u.x;
+      w[1] = u.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(at + lane * N);
+    }
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) {
+      x[2 * c] = __uint_as_float(w[c] << 16);
+      x[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* at, int lane, float f) const {
+    if constexpr (N == 4)
+      *reinterpret_cast<uint2*>(at + lane * N) = make_uint2(pack_bf16(x[0] * f, x[1] * f), pack_bf16(x[2] * f, x[3] * f));
+    else
+      *reinterpret_cast<uint32_t*>(at + lane * N) = pack_bf16(x[0] * f, x[1] * f);
+  }
+  __device__ __forceinline__ void add(float f, const Channels& y) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = fmaf(f, y.x[c], x[c]);
+  }
+};
+
+__device__ __forceinline__ float warp_total(float x) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
+}
+
+// The gradients of the rows that see their own key alone: all tokens where the
+// window is 1, otherwise the sequences of one token. A warp takes a key head of up
+// to kOwn of them, its lanes the channels.
+constexpr int kOwn = 8;
+constexpr int kSumWarps = kSumThreads / 32;
+
+// Warps' items: below 2^31, as T Hq and B Hkv are.
+__host__ __device__ __forceinline__ int own_items(const PackedShape& s, int count) { return (count + kOwn - 1) / kOwn * s.Hkv; }
+
+template <int D>
+__device__ __forceinline__ void own_rows(const SumArgs& a, const __nv_bfloat16* o, const __nv_bfloat16* dO,
+                                         long long do_stride, const float* lse, int block) {
+  using Part = Channels<D / 32>;
+  const PackedShape& s = a.s;
+  const int lane = static_cast<int>(lane_id()), G = s.by_group.G;
+  int first = 0, count = s.B;
+  if (s.window == 1) {
+    for (int b = block * kSumThreads + static_cast<int>(threadIdx.x); b < s.B; b += a.n_own * kSumThreads)
+      packed_seq<true>(s, b, a.status);  // (reports borders that are wrong)
+    first = min(max(s.cu[0], 0), s.T);
+    count = max(min(s.cu[s.B], s.T) - first, 0);
+  }
+  const int items = own_items(s, count);
+#pragma unroll 1
+  for (int i = block * kSumWarps + warp_id(); i < items; i += a.n_own * kSumWarps) {
+    const int set = s.by_head.div(i), h = i - set * s.Hkv, mine = set * kOwn + lane;
+    int token = -1;
+    if (lane < kOwn && mine < count) {
+      if (s.window == 1) {
+        token = first + mine;
+      } else {
+        const PackedSeq q = packed_seq<true>(s, mine, a.status);
+        if (q.n == 1) token = q.row0;
+      }
+    }
+#pragma unroll 1
+    for (uint32_t left = __ballot_sync(0xffffffffu, token >= 0); left; left &= left - 1) {
+      const long long t = __shfl_sync(0xffffffffu, token, __ffs(left) - 1);
+      const Part k(a.k + t * a.k_stride + static_cast<long long>(h) * D, lane);
+      const Part v(a.v + t * a.v_stride + static_cast<long long>(h) * D, lane);
+      Part dk(0.f), dv(0.f);
+#pragma unroll 1
+      for (int g = 0; g < G; ++g) {
+        const long long head = static_cast<long long>(h) * G + g, row = t * s.Hq + head;
+        const Part q(a.q + t * a.q_stride + head * D, lane), out(o + row * D, lane), grad(dO + t * do_stride + head * D, lane);
+        float score = 0.f, diff = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          score = fmaf(q.x[c], k.x[c], score);
+          diff = fmaf(grad.x[c], v.x[c] - out.x[c], diff);
+        }
+        const float p = ex2(fmaf(warp_total(score), a.scale_log2, -kLog2e * lse[row]));
+        const float ds = p * warp_total(diff);
+        k.store(a.dq + t * a.dq_stride + head * D, lane, ds * a.scale);
+        dk.add(ds, q);
+        dv.add(p, grad);
+      }
+      dk.store(a.dk + t * a.dk_stride + static_cast<long long>(h) * D, lane, a.scale);
+      dv.store(a.dv + t * a.dv_stride + static_cast<long long>(h) * D, lane, 1.f);
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kSumThreads, 4) packed_rowsum_kernel(const __nv_bfloat16* __restrict__ o,
@@ -162,9 +279,13 @@ __global__ void __launch_bounds__(kSumThreads, 4) packed_rowsum_kernel(const __n
   constexpr int kLanes = D / 8, kUnroll = 2;
   grid_dep_wait();
   grid_dep_launch();
-  const int block = static_cast<int>(blockIdx.x) - args.n_lists;
-  if (block < 0) {
+  if (static_cast<int>(blockIdx.x) < args.n_lists) {
     make_list<kSumThreads>(args.s, args.lists[blockIdx.x], args.status);
+    return;
+  }
+  const int block = static_cast<int>(blockIdx.x) - args.n_lists - args.n_own;
+  if (block < 0) {
+    own_rows<D>(args, o, dO, do_stride, lse, block + args.n_own);
     return;
   }
   const GroupDiv group = args.s.by_group;
@@ -703,8 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // queries of a key k: [k, k + window); a border cuts the warp's part of a tile
       // that begins before token cut_lo, or from cut_hi on
       const int warp_k0 = it.x0 + (warp & 3) * 32;
-      const bool single = sh.window == 1 || it.n == 1;  // each query sees one key: dS = 0
-      const int cut_lo = single ? 0x7fffffff : sh.causal ? warp_k0 + 31 - sh.by_group.div(wg * kCols) : -0x7fffffff;
+      const int cut_lo = sh.causal ? warp_k0 + 31 - sh.by_group.div(wg * kCols) : -0x7fffffff;
       const int cut_hi = sh.window > 0 ? warp_k0 + sh.window - sh.by_group.div(wg * kCols + kCols - 1) : 0x7fffffff;
       for (; g < end; ++g, i0 += sh.tpt) {
         const float* stat = f.stats(g) + wg * kCols;
@@ -764,9 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[c / 2] = __fmul2_rn(p[c / 2], __fadd2_rn(pair(x + c), make_float2(d.x, d.y)));
           p[c / 2 + 1] = __fmul2_rn(p[c / 2 + 1], __fadd2_rn(pair(x + c + 2), make_float2(d.z, d.w)));
         }
-        // (where a query is not seen, dP may be anything; `single` formed again: kept in
-        // a register it cost 1.5 us of 274, d = 64)
-        if (cut) keep_bits(p, sh.window == 1 || *reinterpret_cast<const volatile int*>(&it.n) == 1 ? 0u : seen);
+        if (cut) keep_bits(p, seen);  // (where a query is not seen, dP may be anything)
 #pragma unroll
         for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(p[c].x, p[c].y);
         tmem_st16(tDs, pk);
@@ -913,9 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float2 l2 = make_float2(l, l), d2 = make_float2(d, d);
       const int key_lo = sh.window > 0 ? pos - sh.window + 1 : 0;
-      int key_hi = sh.causal ? min(n, pos + 1) : n;  // exclusive
-      // the softmax of a single key is 1 whatever its score: no gradient, rather than dP - D's rounding
-      if (key_hi - max(key_lo, 0) == 1) key_hi = 0;
+      const int key_hi = sh.causal ? min(n, pos + 1) : n;  // exclusive
       // keys that all rows of the warp see: full_lo <= key < full_hi
       const int full_hi = sh.causal ? min(n, i0 + warp_i0 + 1) : n;
       const int full_lo = sh.window > 0 ? i0 + warp_i1 - sh.window + 1 : 0;
@@ -1012,17 +1128,34 @@ int launch_d(const PackedBwd& b, const BwdPlan& plan, const PackedList (&lists)[
   if (!ensure_smem_attr(reinterpret_cast<const void*>(dkv), kDkvBytes, kSlot) ||
       !ensure_smem_attr(reinterpret_cast<const void*>(dq), kDqBytes, kSlot + 1))
     return -3;
+  const bool all_own = s.window == 1;
   const long long rows = static_cast<long long>(s.T) * s.Hq, per = kSumThreads / (D / 8) * 2;
   SumArgs sum{};
   sum.s = s;
   sum.status = status;
   for (const PackedList& l : lists)
-    if (l.entries != nullptr) sum.lists[sum.n_lists++] = l;
-  cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per + sum.n_lists)),
-                                    dim3(kSumThreads), 0, stream, static_cast<const __nv_bfloat16*>(b.o),
+    if (l.entries != nullptr && !all_own) sum.lists[sum.n_lists++] = l;
+  sum.n_own = std::min((own_items(s, all_own ? s.T : s.B) + kSumWarps - 1) / kSumWarps, device_sm_count() * 4);
+  sum.q = static_cast<const __nv_bfloat16*>(p.q);
+  sum.k = static_cast<const __nv_bfloat16*>(p.k);
+  sum.v = static_cast<const __nv_bfloat16*>(p.v);
+  sum.dq = static_cast<__nv_bfloat16*>(b.dq);
+  sum.dk = static_cast<__nv_bfloat16*>(b.dk);
+  sum.dv = static_cast<__nv_bfloat16*>(b.dv);
+  sum.q_stride = p.q_stride;
+  sum.k_stride = p.k_stride;
+  sum.v_stride = p.v_stride;
+  sum.dq_stride = b.dq_stride;
+  sum.dk_stride = b.dk_stride;
+  sum.dv_stride = b.dv_stride;
+  sum.scale = p.scale;
+  sum.scale_log2 = p.scale * kLog2e;
+  const long long sum_blocks = (all_own ? 0 : (rows + per - 1) / per) + sum.n_lists + sum.n_own;
+  cudaError_t e = launch_overlapped(packed_rowsum_kernel<D>, dim3(static_cast<unsigned>(sum_blocks)), dim3(kSumThreads), 0, stream, static_cast<const __nv_bfloat16*>(b.o),
                                     static_cast<const __nv_bfloat16*>(b.dO), b.do_stride, b.lse, stats, stats + rows,
                                     GroupDiv::of(s.Hq), rows, sum);
   if (e != cudaSuccess) return -3;
+  if (all_own) return cudaGetLastError() == cudaSuccess ? 0 : -3;
   BwdArgs a{};
   a.s = s;
   a.neg_lse = stats;
@@ -1056,7 +1189,7 @@ int launch_packed_bwd(const PackedBwd& b, void* workspace, cudaStream_t stream) 
   const BwdPlan plan = bwd_plan(s.B, s.T, s.Hq, s.Hkv, sms);
   PackedList lists[2];
   for (int i = 0; i < 2; ++i) {
-    lists[i] = PackedList{nullptr, nullptr, plan.cap[i], plan.unit[i], i == 0 ? 1 : 0};
+    lists[i] = PackedList{nullptr, nullptr, plan.cap[i], plan.unit[i], 2, i == 0 ? 1 : 0};
     if (plan.listed[i]) {
       lists[i].head = reinterpret_cast<PackedHead*>(static_cast<char*>(workspace) + plan.head[i]);
       lists[i].entries = reinterpret_cast<int4*>(lists[i].head + 1);

@@ -707,7 +707,7 @@ int launch_packed_fwd(const PackedProblem& p, void* o, float* lse, void* workspa
   a.status = device_status_word();
   if (!a.status || sms <= 0) return -3;
   const FwdPlan plan = fwd_plan(s.B, s.T, s.Hq, s.Hkv, p.d, sms);
-  a.list = PackedList{static_cast<PackedHead*>(workspace), nullptr, plan.cap, plan.unit, 0};
+  a.list = PackedList{static_cast<PackedHead*>(workspace), nullptr, plan.cap, plan.unit, 1, 0};
   if (plan.listed) {
     a.list.entries = reinterpret_cast<int4*>(a.list.head + 1);
     const int rc = launch_packed_plan(s, a.list, stream);

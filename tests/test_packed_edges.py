@@ -1,6 +1,8 @@
 """Packed sequences on the GPU where calls are legal and rare: hand-offs under load, values, scales and lengths at the
 ends of their ranges. Against the float64 oracle, with the bounds of test_packed_parity.py, or for equal bits."""
 
+import math
+
 import numpy as np
 import pytest
 
@@ -41,7 +43,9 @@ def test_rows_past_a_sequence_are_zeros_before_they_are_multiplied(d, G):
 @pytest.mark.parametrize("d", [64, 128])
 def test_the_largest_queries_with_the_smallest_scales(d):
     """The scale takes the queries' size back: powers of two, so the bits are those of queries and a scale of usual size
-    (dq's times the size; at 2^100 its values are still normal numbers)."""
+    (dq's times the size). At 2^100 dq is no normal number where it is below 2^-26, as where a row sees one key and dq
+    is the rounding of nothing: to the nearest multiple of 2^-133 it errs by up to 2^-134, which is 2^-34 times the size,
+    and the other side by up to 2^-9 of 2^-26: together less than 2^-33."""
     rows = Rows([150, 40], 4, 2, d, seed=d)
     (q, k, v), cu = rows.on_gpu()
     do = randn(rows.rng, rows.T, 4, d).cuda()
@@ -59,7 +63,8 @@ def test_the_largest_queries_with_the_smallest_scales(d):
             continue
         grads = fa.fa_packed_bwd(large, k, v, o, lse, do, cu, causal=True, scale=0.125 / size)
         done()
-        assert torch.equal((grads[0].double() * size).to(torch.bfloat16), dq)
+        err = (grads[0].double() * size - dq.double()).abs()
+        assert (err <= torch.where(dq.double().abs() <= 2.0 ** -26, 2.0 ** -33, 0.0)).all()
         assert torch.equal(grads[1], dk) and torch.equal(grads[2], dv)
 
 
@@ -78,3 +83,45 @@ def test_scales_of_nothing_weigh_all_keys_alike_whatever_the_queries(d, scale):
     done()
     check_bwd(rows, o, lse, do, got, True, 0.0, 0)
     assert not got[0].any() and not got[1].any()
+
+
+# ------------------------------------------------------------------ rows that see one key
+ONE_KEY = [([40, 1, 200, 1, 1, 129], True, 0), ([40, 1, 200, 1, 1, 129], True, 1), ([300, 1, 70, 1], False, 0), ([1] * 300, False, 0)]
+
+
+@pytest.mark.parametrize("lens,causal,window", ONE_KEY)
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 3), (128, 1), (128, 8)])
+def test_gradients_that_are_not_finite_where_a_row_sees_one_key(lens, causal, window, d, G):
+    """dS = P (dO . v - D) is NaN there as elsewhere: an infinity less itself, or a NaN."""
+    rows = Rows(lens, 2 * G, 2, d, seed=d + G)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, causal, scale, window)
+    do = randn(rows.rng, rows.T, 2 * G, d)
+    hurt = [b for b in range(len(lens)) if b % 2 == 1 or lens[b] == 200]
+    alone = [int(rows.cu[b]) for b in hurt if causal or lens[b] == 1]     # rows that see their own key alone
+    for i, t in enumerate(alone):
+        do[t, ::G, i % d] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    dq, dk, dv = backward_of(rows, o, lse, do, causal, window)
+    done()
+    for t in alone:
+        assert dq[t, ::G].isnan().all() and dk[t].isnan().all(), t
+        assert not dv[t].isfinite().all()
+    check_bwd(rows, o, lse, do, (dq, dk, dv), causal, scale, window,
+              which=[b for b in range(len(lens)) if not rows.cu[b] in alone])
+
+
+@pytest.mark.parametrize("lens,causal,window", ONE_KEY + [([33, 0, 100, 7] * 60, True, 0)])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 3), (128, 1), (128, 8)])
+def test_gradients_of_attention_in_parts(lens, causal, window, d, G):
+    """o and lse of rows that see more keys than this call's, as where a row's keys are divided among calls: rows that
+    see one key here have a gradient too."""
+    rows = Rows(lens, 2 * G, 2, d, seed=d + G, trail=3)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, causal, scale, window)
+    part = torch.from_numpy(rows.rng.uniform(0.2, 0.9, lse.shape)).float()         # of a row's weight, here
+    o = (part[..., None] * o.float() + (1 - part[..., None]) * randn(rows.rng, *o.shape).float()).to(torch.bfloat16)
+    lse = lse - part.log()
+    do = randn(rows.rng, rows.T, 2 * G, d)
+    got = backward_of(rows, o, lse, do, causal, window)
+    done()
+    check_bwd(rows, o, lse, do, got, causal, scale, window)

@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         ok = mbar_wait_w(bar(C::kBarOFinal + t), qt & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      const float inv_l = l > 0.f ? 1.0f / l : 0.f;
+      const float inv_l = l == 0.f ? 0.f : 1.0f / l;  // (NaN stays NaN)
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-      const float lse_row = l > 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
+      const float lse_row = l == 0.f ? -INFINITY : (m_use + log2f(l)) * kLn2;
       const float2 il2 = make_float2(inv_l, inv_l);
       // Each warp swizzles its 32 rows, 64 columns at a time, into its staging
       // block. At d = 128, where they are all the sequence's and whole tokens, one

@@ -125,3 +125,21 @@ def test_gradients_of_attention_in_parts(lens, causal, window, d, G):
     got = backward_of(rows, o, lse, do, causal, window)
     done()
     check_bwd(rows, o, lse, do, got, causal, scale, window)
+
+
+# ------------------------------------------------------------------ NaN
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 150)])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 3), (128, 1), (128, 8)])
+def test_a_key_of_nan_reaches_the_lse_of_the_rows_that_see_it(causal, window, d, G):
+    rows = Rows([100, 400, 60], 2 * G, 2, d, seed=d + G)
+    at = 100 + 210
+    rows.k[at, 1, 3] = float("nan")               # of the second key head
+    (q, k, v), cu = rows.on_gpu()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=causal, window=window)
+    done()
+    t = torch.arange(rows.T, device="cuda")
+    seen = (t >= (at if causal else 100)) & (t < (min(at + window, 500) if window else 500))
+    want = torch.zeros(rows.T, 2 * G, dtype=torch.bool, device="cuda")
+    want[:, G:] = seen[:, None]
+    assert torch.equal(lse.isnan(), want) and not lse.isinf().any()
+    assert torch.equal(o.isnan().all(-1), want) and torch.equal(o.isnan().any(-1), want)

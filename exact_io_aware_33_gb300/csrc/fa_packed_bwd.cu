@@ -391,6 +391,7 @@ struct Frame {
   uint8_t* smem;
   uint32_t base, tmem;
   volatile int* abort_flag;
+  volatile int* loaded;  // stream steps that the TMA warp has started
 
   __device__ __forceinline__ uint32_t bar(int i) const { return base + C::kBarOff + 8u * i; }
   __device__ __forceinline__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(smem + C::kMiscOff); }
@@ -431,6 +432,7 @@ struct Frame {
     base = smem_u32(raw);  // 1 KiB aligned, as the array is declared (there is no room to align it here)
     smem = raw;
     abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    loaded = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 8);
     if (threadIdx.x == 0) {
       for (int i = C::kBarResFull; i < C::kBarLoad0; ++i) mbar_init(bar(i), 1);
       for (int i = C::kBarLoad0; i < C::kBarS; ++i)
@@ -451,6 +453,7 @@ struct Frame {
       mbar_init(bar(C::kBarDrain), 1);
       mbar_init(bar(C::kBarDrain + 1), 1);
       *abort_flag = 0;
+      *loaded = 0;
       mbar_fence_init();
     }
     if (warp_id() == kMmaWarp) {
@@ -544,6 +547,7 @@ struct Frame {
         };
         load(1, C::kBarLoad1, C::kBarEmpty1, C::kStages1, ring1(g));
         if (ok) load(0, C::kBarLoad0, C::kBarEmpty0, C::kStages0, ring0(g));
+        *loaded = g + 1;
         if (C::kResBufs == 1 && jj == 0 && ok) load_resident();
       }
       ++q;
@@ -569,7 +573,8 @@ struct Frame {
       if (!get_item(q) || items()[u32(q) % kItems].end) break;
       const Item it = items()[u32(q) % kItems];
       give_item(q);
-      if (!mbar_wait_sleep_w(bar(C::kBarFinal), q & 1, abort_flag)) break;
+      // (a whole item: with a token of 128 heads a step, a million tokens are more than a second)
+      if (!mbar_wait_long_w(bar(C::kBarFinal), q & 1, abort_flag, loaded)) break;
       tc_fence_after();
       body(it, [&](int which, float factor, auto&& row_at) {
         [[maybe_unused]] __nv_bfloat16* mine = C::kStaged ? nullptr : row_at(lane);

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
   auto bar = [&](int i) -> uint32_t { return base + C::kBarOff + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+  volatile int* loaded = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 8);  // stream steps started
   Item* items = reinterpret_cast<Item*>(smem + C::kItemOff);
   const PackedShape& sh = args.s;
   const int G = sh.by_group.G;
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     }
     mbar_init(bar(C::kBarDrain), 1);
     *abort_flag = 0;
+    *loaded = 0;
     mbar_fence_init();
   }
   if (warp == C::kMmaWarp) {
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
             tma_load_4d(base + C::kVOff + st * C::kTileBytes + c * kChunkBytes, &tmV, bar(C::kBarVFull + st), c * 64, 0,
                         h, key_row);
           kv_issued = 2 * g + 2;
+          *loaded = g + 1;
         }
       }
       if (ok && q >= kItems) ok = mbar_wait(bar(C::kBarItemEmpty + q % kItems), (q / kItems - 1) & 1, abort_flag);
@@ -421,7 +424,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
     int ut = 0, qt = 0;  // S tiles and items of this query tile so far
     for (int q = 0; ok; ++q) {
       // (the record is given back at the item's end: what the loop does not need is read again there)
-      ok = mbar_wait_w(bar(C::kBarItemFull + q % kItems), (q / kItems) & 1, abort_flag);
+      if constexpr (QT == 1)
+        ok = mbar_wait_w(bar(C::kBarItemFull + q % kItems), (q / kItems) & 1, abort_flag);
+      else  // (a whole item, where this tile of the last one held no rows)
+        ok = mbar_wait_long_w(bar(C::kBarItemFull + q % kItems), (q / kItems) & 1, abort_flag, loaded);
       if (!ok) break;
       const Item& it = items[q % kItems];
       if (it.end) break;

@@ -3,9 +3,10 @@
 // memory matrix descriptors the tensor core reads operands through.
 //
 // Every wait in this file is bounded: it gives up after a fixed wall-clock
-// budget (read from %globaltimer) or as soon as another role of the CTA has
-// raised the CTA's abort flag, and reports that to the caller, which then
-// winds down instead of spinning forever.
+// budget (read from %globaltimer; of mbar_wait_long: one without progress) or
+// as soon as another role of the CTA has raised the CTA's abort flag, and
+// reports that to the caller, which then winds down instead of spinning
+// forever.
 #pragma once
 
 #include <cstdint>
@@ -144,6 +145,27 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint32_t bar, uint32_t parity, v
     if (abort != nullptr && *abort) return false;
     if (global_ns() - t0 > kWaitBudgetNs) {
       if (abort != nullptr) *abort = 1;
+      return false;
+    }
+  }
+}
+
+// mbar_wait_sleep for a wait that may last as long as many steps of other roles.
+// *progress counts these: while it moves, the budget begins anew.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               const volatile int* progress) {
+  if (mbar_try_suspend(bar, parity)) return true;
+  unsigned long long t0 = global_ns();
+  int seen = *progress;
+  while (true) {
+    if (mbar_try_suspend(bar, parity)) return true;
+    if (*abort) return false;
+    const int now = *progress;
+    if (now != seen) {
+      seen = now;
+      t0 = global_ns();
+    } else if (global_ns() - t0 > kWaitBudgetNs) {
+      *abort = 1;
       return false;
     }
   }
@@ -577,6 +599,12 @@ __device__ __forceinline__ bool mbar_wait_w(uint32_t bar, uint32_t parity, volat
 // mbar_wait_sleep by all 32 lanes of a warp, with one verdict for all.
 __device__ __forceinline__ bool mbar_wait_sleep_w(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait_sleep(bar, parity, abort));
+}
+
+// mbar_wait_long by all 32 lanes of a warp, with one verdict for all.
+__device__ __forceinline__ bool mbar_wait_long_w(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                 const volatile int* progress) {
+  return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort, progress));
 }
 
 // ---------------------------------------------------------------- math

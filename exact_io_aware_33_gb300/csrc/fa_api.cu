@@ -517,6 +517,15 @@ bool rows_meet(const void* a, long long as, long long aw, const void* b, long lo
   return ahead < 2 * aw || ahead + 2 * bw > 2 * as;
 }
 
+// Whether T rows of aw 16-bit elements, as elements apart, share bytes with the `bytes` from b on.
+bool rows_meet_bytes(const void* a, long long as, long long aw, int T, const void* b, long long bytes) {
+  const long long a0 = static_cast<long long>(reinterpret_cast<uintptr_t>(a)), b0 = static_cast<long long>(reinterpret_cast<uintptr_t>(b));
+  if (a0 + 2 * ((T - 1) * as + aw) <= b0 || b0 + bytes <= a0) return false;
+  if (b0 < a0) return true;
+  const long long off = (b0 - a0) % (2 * as);  // behind the row before it
+  return off < 2 * aw || off + bytes > 2 * as;
+}
+
 // SMs of the current device, looked up once; a GB300's where there is none.
 int paged_sms() {
   const int sms = fa::device_sm_count();
@@ -701,6 +710,10 @@ int fa_packed_bwd(const void* q, long long q_stride, const void* k, long long k_
   for (int i = 0; i < 3; ++i) {
     for (const Rows& r : in)
       if (meet(out[i], r)) return FA_ERR_INVALID;
+    const long long width = static_cast<long long>(out[i].heads) * d;
+    if (rows_meet_bytes(out[i].at, out[i].stride, width, T, lse, 4LL * T * Hq) ||
+        rows_meet_bytes(out[i].at, out[i].stride, width, T, cu, 4LL * (B + 1)))
+      return FA_ERR_INVALID;
     for (int j = 0; j < i; ++j)
       if (meet(out[i], out[j])) return FA_ERR_INVALID;
   }

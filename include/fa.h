@@ -410,7 +410,8 @@ size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged
  *   scale   : finite and >= 0, as in fa_fwd
  *   o       : out, bf16 [T, Hq, d] contiguous; must not meet q, k or v
  *             (FA_ERR_INVALID)
- *   lse     : out, fp32 [T, Hq], natural-log log-sum-exp
+ *   lse     : out, fp32 [T, Hq], natural-log log-sum-exp; must not meet any of
+ *             the others (not checked)
  *   workspace : at least fa_packed_fwd_workspace_bytes(...) bytes (0: may be
  *             NULL), 256-byte aligned; nothing in it outlives the call. Two
  *             calls in flight at once need two, also as replays of two
@@ -441,8 +442,8 @@ size_t fa_packed_fwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d);
  *             key head, added up in fp32
  *   workspace : at least fa_packed_bwd_workspace_bytes(...) bytes, 256-byte
  *             aligned, as for the forward
- * Outputs must not meet an input or each other (FA_ERR_INVALID); rows outside
- * the sequences are left as they were. No sum's order depends on timing: the
+ * Outputs must not meet an input or each other (FA_ERR_INVALID), nor the
+ * workspace, which is not checked; rows outside the sequences are left as they were. No sum's order depends on timing: the
  * same inputs give the same bits. Otherwise as fa_packed_fwd, the device's
  * checks included.
  */
@@ -461,8 +462,9 @@ size_t fa_packed_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int d);
  *              elements apart (at least heads * d, a multiple of 8); either may
  *              be NULL with no heads
  *   q_out, k_out : out, the same shapes; each may be its input itself (with the
- *              same stride) and must not meet an input or the other output
- *              otherwise (FA_ERR_INVALID)
+ *              same stride) and must not meet q, k or the other output
+ *              otherwise (FA_ERR_INVALID); nor the positions or the tables,
+ *              which is not checked
  *   positions: in,  int32 [num_axes, T] on the device
  *   axis_of  : in,  rot / 2 axis numbers, in HOST memory, read during the call
  *   cos, sin : in,  fp32 [max_pos, rot / 2]: the angles of each position

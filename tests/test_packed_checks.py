@@ -1,0 +1,28 @@
+"""Host checks of the packed calls that tests/test_oracle_packed.py does not make (no device touched)."""
+
+import pytest
+
+import exact_io_aware_33_gb300 as fa
+from test_oracle_packed import P, _bwd, _far, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=_far(5)), dict(lse=_far(5) + 4096), dict(lse=_far(6) - 16), dict(lse=_far(7) + 8 * 512 - 4),
+    dict(cu=_far(5) + 512), dict(cu=_far(6) - 4), dict(cu=_far(7) + 8 * 512 - 4),
+    # in a row, or across the end of the gap between two
+    dict(dqs=1024, lse=_far(5) + 2048 + 1024 - 4), dict(dqs=1024, lse=_far(5) + 2048 - 64),
+    dict(dks=1024, cu=_far(6) + 2048 + 512 - 4), dict(dvs=1024, cu=_far(7) + 2048 - 8)])
+def test_gradients_that_meet_the_statistics_or_the_borders_are_refused(lib, kw):  # noqa: F811
+    assert _bwd(lib, **kw) == fa.FA_ERR_INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lse=_far(5) - 128), dict(lse=_far(5) + 8 * 1024), dict(cu=_far(6) - 16), dict(cu=_far(6) + 8 * 512),
+    # between two rows (128 bytes of lse, 16 of cu), or behind the last one's
+    dict(dqs=1024, lse=_far(5) + 1024), dict(dqs=1024, lse=_far(5) + 2048 - 128), dict(dks=1024, cu=_far(6) + 2048 - 16),
+    dict(dvs=1024, cu=_far(7) + 7 * 2048 + 512)])
+def test_gradients_beside_the_statistics_or_the_borders_are_not(lib, kw):  # noqa: F811
+    # the code that a call which passes its checks gives where there is no device to launch on
+    if fa.fa_get_last_device_status() != fa.FA_ERR_LAUNCH:
+        pytest.skip("would launch on pointers that are none")
+    assert _bwd(lib, **kw) == fa.FA_ERR_LAUNCH

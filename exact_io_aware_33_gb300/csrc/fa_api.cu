@@ -630,6 +630,9 @@ int check_packed(int B, int T, int Hq, int Hkv, int d) {
   return FA_OK;
 }
 
+// The kernels scale scores in units of log2.
+bool packed_scale_ok(float scale) { return scale >= 0.f && std::isfinite(scale * 1.4426950408889634f); }
+
 // row_stride_ok for rows that a tensor map names (strides below 2^40 bytes).
 bool map_stride_ok(long long stride, int heads, int d) { return row_stride_ok(stride, heads, d) && stride < (1LL << 38); }
 
@@ -656,7 +659,7 @@ int fa_packed_fwd(const void* q, long long q_stride, const void* k, long long k_
                   float scale, void* o, float* lse, void* workspace, size_t ws_bytes, void* cuda_stream) {
   int rc = check_packed(B, T, Hq, Hkv, d);
   if (rc != FA_OK) return rc;
-  if (!std::isfinite(scale) || scale < 0.f || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
+  if (!packed_scale_ok(scale) || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
   if (B == 0 || T == 0) return FA_OK;
   if (!fa::aligned16(q) || !fa::aligned16(k) || !fa::aligned16(v) || !fa::aligned16(o) || !aligned4(lse) ||
       !aligned4(cu) || !map_stride_ok(q_stride, Hq, d) || !map_stride_ok(k_stride, Hkv, d) ||
@@ -688,7 +691,7 @@ int fa_packed_bwd(const void* q, long long q_stride, const void* k, long long k_
                   void* workspace, size_t ws_bytes, void* cuda_stream) {
   int rc = check_packed(B, T, Hq, Hkv, d);
   if (rc != FA_OK) return rc;
-  if (!std::isfinite(scale) || scale < 0.f || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
+  if (!packed_scale_ok(scale) || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID;
   if (B == 0 || T == 0) return FA_OK;
   struct Rows {
     const void* at;

@@ -407,7 +407,7 @@ size_t fa_paged_attn_workspace_bytes(const fa_paged_cache* cache, const fa_paged
  *             sequences of its own: it then meets no other's rows.)
  *   causal  : != 0: row i of a sequence sees its rows j <= i
  *   window  : W >= 1 (causal only): and of those only j > i - W; 0: none
- *   scale   : finite and >= 0, as in fa_fwd
+ *   scale   : >= 0, and finite times log2(e): below 2.35e38
  *   o       : out, bf16 [T, Hq, d] contiguous; must not meet q, k or v
  *             (FA_ERR_INVALID)
  *   lse     : out, fp32 [T, Hq], natural-log log-sum-exp; must not meet any of

@@ -3,7 +3,7 @@
 import pytest
 
 import exact_io_aware_33_gb300 as fa
-from test_oracle_packed import P, _bwd, _far, lib  # noqa: F401
+from test_oracle_packed import _bwd, _far, _fwd, _rope, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("kw", [
@@ -26,3 +26,23 @@ def test_gradients_beside_the_statistics_or_the_borders_are_not(lib, kw):  # noq
     if fa.fa_get_last_device_status() != fa.FA_ERR_LAUNCH:
         pytest.skip("would launch on pointers that are none")
     assert _bwd(lib, **kw) == fa.FA_ERR_LAUNCH
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_scales_whose_product_with_log2_e_is_no_number_are_refused(lib, call):  # noqa: F811
+    # scores are scaled in units of log2: 3.4e38 / 1.4427 is the largest scale
+    for scale in (2.4e38, 3.4e38):
+        assert call(lib, scale=scale) == fa.FA_ERR_INVALID
+
+
+# What a call that passes its checks gives where there is no device to launch on.
+@pytest.mark.parametrize("call,kw", [
+    (_fwd, dict()), (_fwd, dict(scale=2.3e38)), (_fwd, dict(scale=0.0)), (_fwd, dict(d=64, qs=256, ks=128, vs=128)),
+    (_bwd, dict()), (_bwd, dict(scale=2.3e38)), (_bwd, dict(scale=0.0)),
+    (_bwd, dict(d=64, qs=256, ks=128, vs=128, dos=256, dqs=256, dks=128, dvs=128)),
+    (_rope, dict()), (_rope, dict(rot=64, d=64, qs=256, qos=256, ks=128, kos=128)), (_rope, dict(rot=64, d=256, qs=1024,
+                                                                                    qos=1024, ks=512, kos=512))])
+def test_calls_as_they_are_meant_pass_their_checks(lib, call, kw):  # noqa: F811
+    if fa.fa_get_last_device_status() != fa.FA_ERR_LAUNCH:
+        pytest.skip("would launch on pointers that are none")
+    assert call(lib, **kw) == fa.FA_ERR_LAUNCH

@@ -50,7 +50,7 @@ def cxx() -> str:
     path = shutil.which("g++") or shutil.which("c++")
     if path:
         return path
-    raise RuntimeError("g++ not found: the paged cache's binding is built with it")
+    raise RuntimeError("g++ not found: the Python binding of the paged cache and of packed sequences is built with it")
 
 
 def _headers():
@@ -179,7 +179,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, out_dir:
             for old in (BINDING, stamp_file):  # one that is there does not fit what was built
                 if os.path.exists(old):
                     os.remove(old)
-            print(f"{lib} is built, the paged cache's Python binding is not:\n{why}", file=sys.stderr, flush=True)
+            print(f"{lib} is built, the Python binding of the paged cache and of packed sequences is not:\n{why}", file=sys.stderr, flush=True)
     return lib
 
 

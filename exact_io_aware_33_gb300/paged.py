@@ -40,7 +40,7 @@ def _load():
         try:
             from . import _paged_native as native
         except ImportError as e:
-            raise ImportError(f"the paged cache's binding is not built ({e}); run "
+            raise ImportError(f"the Python binding of the paged cache and of packed sequences is not built ({e}); run "
                               "`python -m exact_io_aware_33_gb300.build` or __graft_entry__.build() first") from e
         native.set_fail(_check)
         _lib, _native, _current = lib, native, t._C._cuda_getDevice

@@ -1,5 +1,9 @@
 """Host checks of the packed calls that tests/test_oracle_packed.py does not make (no device touched)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 
 import exact_io_aware_33_gb300 as fa
@@ -46,3 +50,24 @@ def test_calls_as_they_are_meant_pass_their_checks(lib, call, kw):  # noqa: F811
     if fa.fa_get_last_device_status() != fa.FA_ERR_LAUNCH:
         pytest.skip("would launch on pointers that are none")
     assert call(lib, **kw) == fa.FA_ERR_LAUNCH
+
+
+def test_packed_calls_say_what_is_missing_where_there_is_no_binding():
+    code = """
+import sys
+import torch
+import exact_io_aware_33_gb300 as fa
+sys.modules["exact_io_aware_33_gb300._paged_native"] = None    # an import that fails
+q, cu = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+for call in (lambda: fa.fa_packed_fwd(q, q, q, cu), lambda: fa.fa_packed_bwd_workspace_bytes(1, 1, 1, 1, 64),
+             lambda: fa.fa_rope_axes(q, q, cu[None, :1], (q, q), sections=(32,)), lambda: fa.PagedCache.empty(1, 1, 16, 64)):
+    try:
+        call()
+    except ImportError as e:
+        assert "packed sequences" in str(e) and "paged cache" in str(e) and "build()" in str(e), e
+    else:
+        raise AssertionError("no ImportError")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr

@@ -143,3 +143,42 @@ def test_a_key_of_nan_reaches_the_lse_of_the_rows_that_see_it(causal, window, d,
     want[:, G:] = seen[:, None]
     assert torch.equal(lse.isnan(), want) and not lse.isinf().any()
     assert torch.equal(o.isnan().all(-1), want) and torch.equal(o.isnan().any(-1), want)
+
+
+# ------------------------------------------------------------------ lengths, streams
+@pytest.mark.parametrize("lens,Hq,Hkv,d,causal,window", [
+    ([2600], 2, 1, 64, True, 0), ([2600], 2, 1, 128, True, 0), ([2311, 40], 1, 1, 64, False, 0), ([2311, 40], 3, 1, 128, False, 0),
+    ([3001], 2, 2, 64, True, 900), ([3001], 4, 1, 128, True, 900)])
+def test_gradients_of_long_sequences(lens, Hq, Hkv, d, causal, window):
+    rows = Rows(lens, Hq, Hkv, d, seed=d + Hq)
+    scale = 1 / math.sqrt(d)
+    o, lse = forward_for(rows, causal, scale, window)
+    do = randn(rows.rng, rows.T, Hq, d)
+    got = backward_of(rows, o, lse, do, causal, window)
+    done()
+    check_bwd(rows, o, lse, do, got, causal, scale, window)
+
+
+@pytest.mark.parametrize("lens", [[200, 130], [200, 3, 0, 130] * 50])
+def test_a_call_on_a_stream_against_the_oracle(lens):
+    rows = Rows(lens, 4, 2, 64, seed=6)
+    (q, k, v), cu = rows.on_gpu()
+    do = randn(rows.rng, rows.T, 4, 64)
+    dog = do.cuda()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    o, lse = fa.fa_packed_fwd(q, k, v, cu, causal=True, stream=s)
+    grads = fa.fa_packed_bwd(q, k, v, o, lse, dog, cu, causal=True, stream=s)
+    done()
+    check_fwd(rows, o, lse, True, 0.125, 0)
+    check_bwd(rows, o, lse, do, grads, True, 0.125, 0)
+
+
+def test_borders_that_fall_and_rise_again_write_nothing_where_there_is_a_list():
+    rows = Rows([700] * 4, 2, 2, 64, seed=5)
+    (q, k, v), _ = rows.on_gpu()
+    cu = torch.tensor([0, 2800] * 300, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((2800, 2), 7.0, device="cuda")
+    fa.fa_packed_fwd(q, k, v, cu, causal=True, out=out, lse=lse)
+    done(fa.FA_ERR_INDEX)
+    assert (out == 7).all() and (lse == 7).all()

@@ -46,9 +46,13 @@
 // of 128 x 128 takes 2730 (dK, dV) and 1940 (dQ) cycles at d = 128, 2230 and 1630
 // at d = 64 (medians under time stamps, which cost some), of which the tensor core is at work for
 // 2200, 1650, 1100 and 820.
-// Measured: 8 documents of up to 4096 tokens, 32 / 8 heads, d = 128: 589 us,
-// 1020 TFLOP/s of the algorithm's; one of 8192, 16 heads: 589, 1167; 24 images of up
-// to 1369 tokens, 16 heads, d = 64, unmasked: 269, 625.
+// Measured (a CUDA graph of the call, replayed back to back; one call after another from
+// Python the d = 128 ones take 5 to 7 % more, under the power limit): 8 documents of up to
+// 4096 tokens, 32 / 8 heads, d = 128: 588 us, 1020 TFLOP/s of the algorithm's; one of 8192,
+// 16 heads: 589, 1167; 24 images of up to 1369 tokens, 16 heads, d = 64, unmasked: 269, 625.
+// dK and dV's work is divided by key tiles and key heads only. Where one key head serves
+// many heads, the first keys' item is what the call takes: one sequence of 11585 tokens,
+// 8 / 1 heads, 1178 us, 583 TFLOP/s; one of 8192, 32 / 1, 3184 us, 432 (d = 128, causal).
 
 #include <algorithm>
 
@@ -58,7 +62,7 @@ namespace fa {
 namespace {
 
 // Steps and items counted are not negative; said so, their remainders and quotients
-// take fewer instructions (595 -> 589 us, 8 documents of up to 4096 tokens).
+// take fewer instructions (269.5 us instead of 270.6, 24 images of up to 1369 tokens).
 __device__ __forceinline__ uint32_t u32(int x) { return static_cast<uint32_t>(x); }
 
 constexpr int kKT = kKeyTile;  // keys per tile; also rows per tile of query rows
@@ -147,9 +151,10 @@ struct Cfg {
 // -D = -rowsum(dO O) and -LSE in log2 units for every row and head, read as they
 // lie and laid out so that the rows of a tile are contiguous; d / 8 lanes per row.
 // Bound by memory: 4 d + 12 bytes a row (37 us for 12400 tokens of 32 heads, d =
-// 128, 207 MB). Many threads with two rows each keep more loads in flight than
-// fewer with four or eight (46 and 67 us). The first blocks make the lists of the two kernels that
-// follow, under the others' loads (before them, it was 4 to 5 us of the call).
+// 128, 207 MB). Many threads with two rows each keep more loads in flight than fewer
+// with four or eight (the call: 588 us, 605 and 662). The first blocks make the lists of
+// the two kernels that follow, and the next ones compute the rows of own_rows, under the
+// others' loads.
 constexpr int kSumThreads = 512;
 
 struct SumArgs {
@@ -208,7 +213,11 @@ __device__ __forceinline__ float warp_total(float x) {
 
 // The gradients of the rows that see their own key alone: all tokens where the
 // window is 1, otherwise the sequences of one token. A warp takes a key head of up
-// to kOwn of them, its lanes the channels.
+// to kOwn of them, its lanes the channels. Bound by the latency of a warp's chain of
+// loads and sums, a head at a time: 4096 sequences of one token, 12 / 4 heads, d = 64,
+// 24.6 us for the call (6 x up to 5001 tokens with a window of 1: 68 us for 204 MB).
+// Found out by the row sums' own threads instead, which rows these are cost 10 us of
+// 590 and 10 of 269 in calls that have none, and by the tile kernels 8 of 269.
 constexpr int kOwn = 8;
 constexpr int kSumWarps = kSumThreads / 32;
 
@@ -407,9 +416,8 @@ struct Frame {
   }
   // The same for the compute warps. At d = 128 they wait for the tensor core most
   // of the time, and asleep they take no issue slots and shared-memory cycles from
-  // it (655 us instead of 669 when it was put in, 8 documents of up to 4096 tokens,
-  // 32 / 8 heads); at d = 64 they are what is waited for (232 instead of 240, 8 x
-  // 2048 tokens, 12 heads).
+  // it (588 us instead of 599, 8 documents of up to 4096 tokens, 32 / 8 heads); at d =
+  // 64 they are what is waited for (269 instead of 280, 24 images of up to 1369).
   __device__ __forceinline__ bool wait_calm(int b, int g) const {
     return D == 64 ? mbar_wait_w(bar(b), g & 1, abort_flag) : mbar_wait_sleep_w(bar(b), g & 1, abort_flag);
   }
@@ -651,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kHelpWarp) {
     // ------------------------------------------------------------ statistics
     // Each step's 128 -LSE and -D are copied without being waited for: they arrive
-    // on the stage's barrier themselves (waited for here, they were what a step
-    // took: 3400 cycles instead of 2100 where they came from memory). Rows that are
-    // none get zeros: their queries and dO are zeros too, so P = 1 adds nothing.
+    // on the stage's barrier themselves (588 us instead of 592, 8 documents of up to
+    // 4096 tokens; as much as a load from memory takes each step, where L2 does not
+    // hold them). Rows that are none get zeros: their queries and dO are zeros too, so P = 1 adds nothing.
     bool ok = true;
     int g = 0;
     for (int q = 0; ok; ++q) {
@@ -967,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ns = f.items()[u32(q) % kItems].ns;
       f.give_item(q);
       if (warp == kMmaWarp) {
-        // S and dP, each once its predecessor is in registers (both once dP is: 345
-        // us instead of 295 when it was put in, 8 x up to 4096 tokens, 32 heads, d = 128)
+        // S and dP, each once its predecessor is in registers (both once dP is: 668
+        // us instead of 588 for the call, 8 documents of up to 4096 tokens, 32 / 8 heads)
         ok = f.resident(q);
         for (int jj = 0; jj < ns && ok; ++jj) {
           const int gs = g + jj;

@@ -26,12 +26,14 @@
 // which is NaN for what is not finite: the softmax warps, before they hand the
 // last tile's P over, put zeros in their place in shared memory.
 //
-// What bounds it: at d = 128 the tensor core, 4 d flops per visible pair (one
-// sequence of 16384 tokens, 32 / 8 heads, causal: 1.34 ms, 1640 TFLOP/s, 86 % of
-// the rate of a large library product), less where items are short: 8 prompts of up
-// to 4096 tokens, 174 us, 73 %. At d = 64 the softmax beside it, one exponential and
-// four other instructions per pair: 24 images of up to 1369 tokens, 16 heads,
-// unmasked, 86.5 us, 41 %; 6 x up to 5001 tokens, 12 / 4 heads, a window of 700, 78 us,
+// What bounds it (times of a CUDA graph of the call, replayed back to back; one call
+// after another from Python the d = 128 ones take 3 to 5 % more): at d = 128 the tensor
+// core, 4 d flops per visible pair (one sequence of 16384 tokens, 32 / 8 heads, causal:
+// 1.28 to 1.35 ms as the power limit allows, 1630 to 1715 TFLOP/s, 86 to 90 % of the rate
+// of a large library product), less where items are short: 8 prompts of up to 4096
+// tokens, 173 us, 73 %. At d = 64 no unit, but the chain of hand-offs from role to role
+// (tensor core 39 % busy, issue slots 52 %): 24 images of up to 1369 tokens, 16 heads,
+// unmasked, 86.6 us, 41 %; 6 x up to 5001 tokens, 12 / 4 heads, a window of 700, 78 us,
 // 33 %, where two or three of seven key tiles are cut by a border.
 //
 // CTA: softmax warpgroup(s) (thread = row = TMEM lane), an MMA warp, a TMA warp.
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         // masks, by words of 32 keys, where a border of some row of the warp cuts the
         // tile. (Little code, here and below, rather than few instructions: the hot
         // loops of all roles share the instruction cache. A comparison per key and
-        // border took 83 instead of 80 us, 6 x up to 5001 tokens, window 700, d = 64.)
+        // border took 4 % more, 6 x up to 5001 tokens, window 700, d = 64.)
         if (key0 + kBN > full_hi || key0 < full_lo) {
           const int hi = key_hi - key0, lo = key_lo - key0;
 #pragma unroll
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
         // settled: this S was committed after the tile's previous P.V (P over
         // S), or that P.V's completion was waited for above (P apart).
         if (u > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1  // (unrolled: 180 instead of 177 us, 8 prompts of up to 4096 tokens, d = 128)
+#pragma unroll 1  // (unrolled: 176 instead of 173 us, 8 prompts of up to 4096 tokens, d = 128)
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + c * 32, o);
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtasPerSm)
       // block. At d = 128, where they are all the sequence's and whole tokens, one
       // tensor copy takes them from there while the warp goes on (an SM's own stores
       // move 32 bytes a clock: 2000 cycles an item; 8 prompts of up to 4096 tokens,
-      // 32 / 8 heads: 189 -> 183 us. At d = 64 the other CTA has the tensor core
+      // 32 / 8 heads: 173 us, not 180. At d = 64 the other CTA has the tensor core
       // meanwhile, and nothing was gained.) Otherwise the warp writes them back as
       // four whole lines per instruction.
       const int i0 = it.i0 + t * sh.tpt;

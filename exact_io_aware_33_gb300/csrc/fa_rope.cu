@@ -14,9 +14,10 @@
 // keeps the angles of 16 channels (8 pairs) in registers and takes them
 // through up to kHeads heads of its token, whose loads are all in flight at once;
 // eight neighbouring threads cover 128-byte lines.
-// Measured: 32768 tokens, 32 + 8 heads, d = 128, three axes: 105 us, 96 % of the
-// rate of a plain copy; 10007 tokens, 16 + 16 heads, d = 64, interleaved: 16.5
-// us, 75 % (a launch of 16 us ends before its loads run at full rate for long).
+// Measured: 32768 tokens, 32 + 8 heads, d = 128, three axes: 104.6 us, 97 % of the
+// rate of a plain copy; 10007 tokens, 16 + 16 heads, d = 64, interleaved: 16.5 us one
+// call after another, 75 % (a launch of 16 us ends before its loads run at full rate
+// for long), 12.6 as replays of a graph, whose 85 MB stay in L2.
 
 #include "fa_paged.cuh"
 

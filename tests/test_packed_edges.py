@@ -182,3 +182,23 @@ def test_borders_that_fall_and_rise_again_write_nothing_where_there_is_a_list():
     fa.fa_packed_fwd(q, k, v, cu, causal=True, out=out, lse=lse)
     done(fa.FA_ERR_INDEX)
     assert (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("window", [0, 1])
+@pytest.mark.parametrize("bad", [[0, 1, 2, 200], [-4, 1, 2, 110], [0, 60, 50], [109, 300, 400], [0, 110, 0, 110, 109, 110], [-1, 0, 1]])
+def test_borders_out_of_range_where_rows_see_one_key(bad, window):
+    """Reported, and clamped: what lies outside the rows there are is neither read nor written."""
+    rows = Rows([110], 4, 2, 64, seed=4)
+    (q, k, v), _ = rows.on_gpu()
+    o, lse = (x.cuda() for x in forward_for(rows, True, 0.125, 0))
+    cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    outs = [torch.full((130, h, 64), 7.0, dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2)]
+    fa.fa_packed_bwd(q, k, v, o, lse, o, cu, causal=True, window=window, dq=outs[0][:110], dk=outs[1][:110], dv=outs[2][:110])
+    done(fa.FA_ERR_INDEX)
+    assert all((x[110:] == 7).all() for x in outs)
+    if bad == sorted(bad):                        # the rows that the clamped borders leave
+        cu = cu.clamp(0, 110)
+        want = fa.fa_packed_bwd(q, k, v, o, lse, o, cu, causal=True, window=window)
+        done()
+        at = slice(int(cu[0]), int(cu[-1]))
+        assert all(torch.equal(a[at], b[at]) for a, b in zip(outs, want))
